@@ -254,7 +254,7 @@ int tf_topk_bf16_noalloc(const void *logits, int64_t rows, int64_t cols, int64_t
  * TF_TOPK_* status (ERR_ARG for temperature or top_p, ERR_K, ERR_SHAPE for
  * rows < 0, ERR_NULL, ERR_ALIGN: val 2-byte, the others 4-byte aligned).
  */
-#define TF_TOPK_ERR_ARG 9 /* tf_topk_nucleus_bf16: temperature or top_p out of range */
+#define TF_TOPK_ERR_ARG 9 /* temperature, top_p, target_bytes, score, groups or scale out of range */
 int tf_topk_nucleus_bf16(const uint16_t *val, const int32_t *count, int64_t rows, int32_t k, float temperature,
                          float top_p, float *out_prob, int32_t *out_keep, void *stream);
 
@@ -364,6 +364,136 @@ int tf_topk_head_bf16(const void *hidden, const void *weight, int32_t rows, int3
  * split ticket, and the fp32 partial sums of two tiles that a CTA may share
  * with a neighbour); 0 for invalid arguments. */
 size_t tf_topk_head_bf16_workspace(int32_t rows, int32_t k);
+
+/*
+ * The head's loss: softmax cross entropy of an LM head's logits against one
+ * target column per row, without storing the logits (training or scoring the
+ * head that tf_topk_head_bf16 serves):
+ *   x[r][v] = sum over d of hidden[r][d] * weight[v][d]     (bf16 in, fp32 sum, not rounded)
+ *   lse[r]  = log( sum over v of exp(x[r][v]) )
+ *   loss[r] = lse[r] - x[r][target[r]]
+ * A row whose target is ignore_index has loss 0 and lse 0; any other target
+ * outside [0, vocab) gives NaN in both (and no gradient).  The losses are per
+ * row: their mean or sum is the caller's.
+ *
+ *   hidden, weight  device, bf16; row r at hidden + r * hidden_stride, column
+ *                   v of the vocabulary at weight + v * weight_stride
+ *                   (elements); 16-byte aligned, the strides multiples of 8
+ *                   and at least dim.
+ *   rows            0..TF_TOPK_HEAD_LOSS_MAX_ROWS (0: a no-op).
+ *   dim             >= 8, a multiple of 8.   vocab  1..2^31 - 1025.
+ *   target          device, [rows], int32 or int64 (target_bytes 4 or 8).
+ *   workspace       device, at least tf_topk_head_loss_bf16_workspace(rows,
+ *                   dim, vocab) bytes, owned by the caller; its contents on
+ *                   entry do not matter.  Calls that overlap on the GPU must
+ *                   not share it.
+ *   out_loss, out_lse  device float [rows].
+ * Asynchronous on `stream`; allocates nothing; the same inputs give the same
+ * bits.  Returns a TF_TOPK_* status: ERR_SHAPE, ERR_ARG (target_bytes),
+ * ERR_NULL, ERR_ALIGN, ERR_SCRATCH (workspace too small), ERR_DEVICE or
+ * ERR_CUDA.
+ */
+#define TF_TOPK_HEAD_LOSS_MAX_ROWS 1048576
+int tf_topk_head_loss_bf16(const void *hidden, int64_t hidden_stride, const void *weight, int64_t weight_stride,
+                           int64_t rows, int32_t dim, int64_t vocab, const void *target, int32_t target_bytes,
+                           int64_t ignore_index, void *workspace, size_t workspace_bytes, float *out_loss,
+                           float *out_lse, void *stream);
+
+/* Workspace bytes tf_topk_head_loss_bf16 needs on the current device; 0 for invalid arguments. */
+size_t tf_topk_head_loss_bf16_workspace(int64_t rows, int32_t dim, int64_t vocab);
+
+/*
+ * Gradient of the head's loss.  With g[r] the gradient of loss[r] and
+ *   G[r][v] = g[r] * (exp(x[r][v] - lse[r]) - [v == target[r]])
+ * for the rows that count (target neither ignore_index nor out of range):
+ *   grad_hidden = G weight,   grad_weight = G^T hidden   (fp32 sums, rounded to bf16).
+ * The logits are computed again, in pieces of the vocabulary; G of a piece is
+ * held in the workspace, rounded to bf16 relative to the largest |g|.  Rows
+ * that do not count get zeros in grad_hidden, and whatever their hidden
+ * states hold (NaN too) reaches nothing.
+ *
+ *   hidden .. ignore_index  as for tf_topk_head_loss_bf16 (rows 0: grad_weight is 0).
+ *   lse             device float [rows], as tf_topk_head_loss_bf16 wrote it.
+ *   grad_loss       device float [rows].
+ *   workspace       device; any size from tf_topk_head_loss_grad_bf16_workspace
+ *                   (rows, dim, vocab, 1) on works, and up to (.., 0) more room
+ *                   means wider and fewer pieces.  Calls that overlap on the
+ *                   GPU must not share it.
+ *   out_grad_hidden device bf16 [rows][dim], out_grad_weight device bf16
+ *                   [vocab][dim], both packed, 16-byte aligned; either may be
+ *                   NULL (a frozen head, or frozen states) and is then not
+ *                   computed.  Neither may overlap an input.
+ * Asynchronous on `stream`; allocates nothing; the same inputs and workspace
+ * size give the same bits.  Returns the statuses of tf_topk_head_loss_bf16.
+ */
+int tf_topk_head_loss_grad_bf16(const void *hidden, int64_t hidden_stride, const void *weight, int64_t weight_stride,
+                                int64_t rows, int32_t dim, int64_t vocab, const void *target, int32_t target_bytes,
+                                int64_t ignore_index, const float *lse, const float *grad_loss, void *workspace,
+                                size_t workspace_bytes, void *out_grad_hidden, void *out_grad_weight, void *stream);
+
+/* Workspace bytes of tf_topk_head_loss_grad_bf16 on the current device: the
+ * recommended size, or with `least` nonzero the smallest it accepts; 0 for
+ * invalid arguments. */
+size_t tf_topk_head_loss_grad_bf16_workspace(int64_t rows, int32_t dim, int64_t vocab, int32_t least);
+
+/*
+ * Expert routing: each token's best k experts with their weights.
+ *   score   s[e] = 1 / (1 + exp(-x[e]))  or  softmax(x)[e], over the experts
+ *           within reach: a logit of NaN or -inf puts its expert out of reach
+ *           (not in the softmax, never chosen); +inf stands for the largest
+ *           finite float.
+ *   choice  c[e] = s[e] + bias[e]; the bias moves the choice only.  An expert
+ *           whose choice is NaN or -inf is not chosen.
+ *   groups  `groups` runs of experts / groups consecutive experts; a group's
+ *           value is the sum of its best group_best choices, and only the
+ *           experts of the best groups_kept groups remain (ties: the lower
+ *           group; a group without a choice comes last).
+ *   chosen  the k largest remaining choices, best first; ties go to the lower
+ *           expert.  Without a bias the order is that of the logits.
+ *   weight  scale * s, with renormalize divided by the sum over the chosen.
+ * The choice is decided as by the formula in 64 bits.  Places beyond the
+ * experts that remain hold index -1 and weight 0.
+ *
+ *   logits       device, [tokens] rows of `experts` elements of `dtype`
+ *                (TF_TOPK_DTYPE_*), row_stride elements apart, aligned to the
+ *                element size.
+ *   experts      1..TF_TOPK_ROUTE_MAX_EXPERTS;  k  1..TF_TOPK_ROUTE_MAX_K.
+ *   bias         device float [experts], or NULL.
+ *   score        TF_TOPK_ROUTE_SOFTMAX or TF_TOPK_ROUTE_SIGMOID.
+ *   groups       1..TF_TOPK_ROUTE_MAX_GROUPS, a divisor of experts;
+ *                groups_kept 1..groups; group_best 1 or 2.
+ *   scale        finite.
+ *   out_idx      device int32 [tokens][k]; out_weight device float [tokens][k].
+ *   load         device int32 [experts], or NULL: grows by the tokens that
+ *                each expert was chosen for.
+ * Asynchronous on `stream`; allocates nothing; the same inputs give the same
+ * bits.  Returns a TF_TOPK_* status: ERR_DTYPE, ERR_K, ERR_SHAPE, ERR_ARG
+ * (score, groups, scale), ERR_NULL, ERR_ALIGN, ERR_DEVICE or ERR_CUDA.
+ */
+#define TF_TOPK_ROUTE_SOFTMAX 0
+#define TF_TOPK_ROUTE_SIGMOID 1
+#define TF_TOPK_ROUTE_MAX_EXPERTS 1024
+#define TF_TOPK_ROUTE_MAX_K 32
+#define TF_TOPK_ROUTE_MAX_GROUPS 32
+int tf_topk_route(const void *logits, int32_t dtype, int64_t tokens, int32_t experts, int64_t row_stride, int32_t k,
+                  const float *bias, int32_t score, int32_t groups, int32_t groups_kept, int32_t group_best,
+                  int32_t renormalize, float scale, int32_t *out_idx, float *out_weight, int32_t *load, void *stream);
+
+/*
+ * Gradient of the routing weights for the logits, the choice held fixed.
+ *   idx          device int32 [tokens][k], as tf_topk_route wrote it (negative
+ *                or out-of-range entries are skipped).
+ *   grad_weight  device float [tokens][k]; entries at skipped places are not used.
+ *   score, renormalize, scale  as in the forward call.
+ *   out_grad_logits  device, [tokens][experts] elements of `dtype`, packed; every
+ *                element is written (zero where nothing flows).  Must not
+ *                overlap the logits.
+ * The bias has no gradient (it moves the choice only).  Asynchronous on
+ * `stream`; allocates nothing.  Returns the statuses of tf_topk_route.
+ */
+int tf_topk_route_grad(const void *logits, int32_t dtype, int64_t tokens, int32_t experts, int64_t row_stride,
+                       int32_t k, const int32_t *idx, const float *grad_weight, int32_t score, int32_t renormalize,
+                       float scale, void *out_grad_logits, void *stream);
 
 /* Human-readable text for a TF_TOPK_* status (static storage). */
 const char *tf_topk_strerror(int status);

@@ -14,7 +14,8 @@ from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
-SOURCES = [PKG / "csrc" / "tf_topk.cu", PKG / "csrc" / "tf_topk_head.cu", PKG / "csrc" / "tf_topk_f32.cu"]
+SOURCES = [PKG / "csrc" / "tf_topk.cu", PKG / "csrc" / "tf_topk_head.cu", PKG / "csrc" / "tf_topk_f32.cu",
+           PKG / "csrc" / "tf_topk_head_loss.cu", PKG / "csrc" / "tf_topk_route.cu"]
 HEADERS = [ROOT / "include" / "tf_topk.h"]
 LIBRARY = PKG / "libtf_topk.so"
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"

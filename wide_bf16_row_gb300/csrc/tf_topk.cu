@@ -3136,6 +3136,15 @@ int run_select(const void *logits, int32_t dtype, int64_t rows, int64_t cols, in
 // Shared with the head entry points (a separate translation unit).
 int tf_topk_internal_fail_cuda(int cuda_error) { return fail_cuda(static_cast<cudaError_t>(cuda_error)); }
 uint32_t tf_topk_internal_head_fault_take();
+uint32_t tf_topk_internal_head_loss_fault_take();
+
+// The current device's SM count, or the status that bars it (the other
+// translation units' launches).
+int tf_topk_internal_device(int *sm_count)
+{
+    int dev = 0;
+    return device_setup(&dev, sm_count);
+}
 
 extern "C" {
 
@@ -3216,6 +3225,8 @@ int tf_topk_device_fault(void)
     if (e != cudaSuccess) return -fail_cuda(e);
     const uint32_t fh = tf_topk_internal_head_fault_take();
     if (f == 0) f = fh;
+    const uint32_t fl = tf_topk_internal_head_loss_fault_take();
+    if (f == 0) f = fl;
     if (f != 0) {
         const uint32_t zero = 0;
         e = cudaMemcpyToSymbol(g_fault, &zero, sizeof zero);
@@ -3244,16 +3255,16 @@ const char *tf_topk_strerror(int status)
     switch (status) {
     case TF_TOPK_OK: return "ok";
     case TF_TOPK_ERR_NULL: return "a required pointer is NULL";
-    case TF_TOPK_ERR_SHAPE: return "invalid shape (rows, cols or row_stride)";
+    case TF_TOPK_ERR_SHAPE: return "invalid shape (rows, columns or strides)";
     case TF_TOPK_ERR_K: return "k out of range (1..TF_TOPK_MAX_K)";
     case TF_TOPK_ERR_ALIGN: return "misaligned pointer";
     case TF_TOPK_ERR_PLAN: return "unknown plan code";
     case TF_TOPK_ERR_DEVICE: return "current device is not compute capability 10.3 (sm_103a)";
     case TF_TOPK_ERR_CUDA: return "CUDA runtime error (see tf_topk_last_cuda_error)";
-    case TF_TOPK_ERR_ARG: return "temperature or top_p out of range";
+    case TF_TOPK_ERR_ARG: return "an argument is out of range (temperature, top_p, target_bytes, score, groups or scale)";
     case TF_TOPK_ERR_DTYPE: return "unknown logit format (TF_TOPK_DTYPE_*)";
-    case TF_TOPK_ERR_SCRATCH: return "the launch needs more scratch slots than the static area of "
-                                     "tf_topk_bf16_noalloc holds (TF_TOPK_NOALLOC_MAX_CTAS)";
+    case TF_TOPK_ERR_SCRATCH: return "the workspace is too small, or the launch needs more scratch slots than the "
+                                     "static area of tf_topk_bf16_noalloc holds (TF_TOPK_NOALLOC_MAX_CTAS)";
     default: return "unknown status";
     }
 }

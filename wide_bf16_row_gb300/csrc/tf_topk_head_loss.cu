@@ -1,0 +1,1197 @@
+// The head's loss and its gradient for GB300 (sm_103a): softmax cross entropy
+// of an LM head's logits against one target column per row, without storing
+// the logits.
+//
+// What is computed, for rows n, vocabulary columns v and dims d:
+//   x[n][v]  = sum_d hidden[n][d] * weight[v][d]        (bf16 in, fp32 sum)
+//   lse[n]   = log sum_v exp(x[n][v])
+//   loss[n]  = lse[n] - x[n][target[n]]
+// and, for a gradient g[n] of loss[n]:
+//   G[n][v]  = g[n] * (exp(x[n][v] - lse[n]) - [v == target[n]])
+//   d_hidden = G weight,   d_weight = G^T hidden.
+// Rows whose target is ignored take no part.
+//
+// One kernel shape serves the four products: pair_product_kernel, persistent,
+// a pair of CTAs (cluster of two, tcgen05.mma cta_group::2) per tile of 256
+// rows x up to 256 columns.  Each CTA of the pair holds half of the tile's
+// rows (M) and loads half of its columns (N); its 128 accumulator lanes are
+// its rows.  Warp roles, per CTA:
+//   warp 0     TMA producer: per ring stage one CTA's halves of A and B, 64
+//              steps of the summed dimension K, 128-byte swizzle;
+//   warp 1     TMEM allocation; in the leading CTA also the MMA issuer, into
+//              one of two accumulators of 256 columns, so that the epilogue
+//              of a tile overlaps the products of the next;
+//   warps 2-9  epilogue, a thread per row and half of the tile's columns.
+// The modes differ in the operands and the epilogue:
+//   kLse   A = hidden, B = weight: per row and half tile the running maximum
+//          and the sum of exp2, the target's column left out;
+//   kProb  the same product, turned into G (bf16) for a piece of the
+//          vocabulary;
+//   kHidden  A = G, B = weight with K = the vocabulary (B is stored with N
+//          contiguous): fp32 sums that grow from piece to piece;
+//   kWeight  A = G^T, B = hidden with K = the rows (both stored with M and N
+//          contiguous): the piece's rows of d_weight.
+//
+// The tensor cores truncate their running fp32 sums, which biases a logit of
+// 12 by about -2.6e-5 at 2048 dims (measured against 64 bits; the fp32 FMA
+// sum is unbiased).  In lse that is spread over many small logits, but in
+// loss it would be the target's alone, so the target's logit is summed by
+// FMA in head_loss_rows_kernel and
+//   loss = log(1 + exp(rest - x_t)),  rest = log sum over v != t of exp(x_v),
+// which also keeps the digits of a loss near 0.
+//
+// No wait is unbounded: every mbarrier wait gives up after kWaitLimit polls,
+// records a fault code, and the CTA winds down.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <float.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+#include <mutex>
+
+#include "tf_topk.h"
+
+int tf_topk_internal_fail_cuda(int cuda_error);
+int tf_topk_internal_device(int *sm_count);
+
+namespace {
+
+constexpr int kTileRows = 256;                       // rows (M) of a pair's tile
+constexpr int kTileCols = 256;                       // columns (N) of the widest tile
+constexpr int kHalf = 128;                           // one CTA's share of either
+constexpr int kStepK = 64;                           // K per ring stage: one 128-byte swizzle row of bf16
+constexpr int kStages = 6;
+constexpr uint32_t kShare = kHalf * kStepK * 2;      // 16 KB: one CTA's share of an operand per stage
+constexpr int kEpiWarps = 8;
+constexpr int kPairThreads = 32 * (2 + kEpiWarps);
+constexpr int kTmemCols = 2 * kTileCols;
+constexpr int kChunk = 32;                           // accumulator columns an epilogue thread takes at a time
+constexpr int kGroupRows = 16;                       // row tiles that share the sweep over the columns
+constexpr uint32_t kWaitLimit = 1u << 20;
+constexpr uint32_t kFaultWait = 1;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+enum Mode { kLse, kProb, kHidden, kWeight };
+
+__device__ uint32_t g_head_loss_fault;
+
+struct __align__(16) PairSmem {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    uint32_t abort;
+};
+
+// Rows that count, as the prepare kernel finds them.
+struct RowHeader {
+    int32_t count;
+    float grad_scale; // largest finite |g|, or 1
+};
+
+struct PairArgs {
+    const RowHeader *header;  // null: every row counts, in its own place
+    const int32_t *order;     // [count] the row at each place (null: the same)
+    const void *target;       // int64 or int32 [rows]
+    int32_t target64;
+    int32_t rows;             // all rows
+    int32_t dim;
+    int32_t vocab;
+    int32_t begin, cols;      // the piece of the vocabulary [begin, begin + cols)
+    int32_t width;            // columns of a tile
+    int32_t pad_rows;         // row pitch of `partial`
+    int32_t splits;           // kHidden: shares of K, each with sums of its own
+    int32_t first;            // kHidden: the sums start here
+    int32_t pitch;            // row pitch of G
+    float2 *partial;          // kLse: [2 * column tiles][pad_rows]: reference exponent, sum
+    const float *lse;         // kProb [rows]
+    const float *grad;        // kProb [rows]
+    __nv_bfloat16 *prob;      // kProb: G [pad_rows][pitch]
+    float *sums;              // kHidden: [splits][pad_rows][dim]
+    __nv_bfloat16 *d_weight;  // kWeight: [vocab][dim]
+};
+
+// ---------------------------------------------------------------- PTX helpers
+
+__device__ __forceinline__ uint32_t saddr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(bar)), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(bar)), "r"(bytes) : "memory");
+}
+
+// Address of the same shared-memory object in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr(p)), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// Bounded wait for the phase with this parity; gives up after kWaitLimit
+// polls (recording the fault) or once another warp of this CTA has.
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort)
+{
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(saddr(bar)), "r"(parity)
+                     : "memory");
+        if (ok) return true;
+        if (*abort) return false;
+    }
+    atomicCAS(&g_head_loss_fault, 0u, kFaultWait);
+    *abort = 1;
+    return false;
+}
+
+// One box of a tensor map into this CTA's shared memory; its bytes count on
+// the leading CTA's barrier.
+__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int32_t x, int32_t y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(saddr(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+// Shared-memory matrix descriptors of tiles written by TMA with the 128-byte
+// swizzle (start address >> 4, leading byte offset at bit 16, stride byte
+// offset at bit 32, version 1 at bit 46, swizzle mode 2 at bit 61).  K-major:
+// eight 128-byte rows of 64 K steps are 1024 bytes apart (stride); the
+// leading offset is not used.  MN-major: a 128-byte row holds 64 rows or
+// columns of one K step, eight K steps are 1024 bytes apart (stride), and the
+// next 64 rows or columns follow a whole box later (leading).
+constexpr uint64_t kDescK = (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+constexpr uint64_t kDescMN =
+    ((uint64_t)((kStepK * 128) >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+
+__device__ __forceinline__ uint64_t desc_at(const void *p, uint64_t bits) { return bits | ((saddr(p) & 0x3FFFFu) >> 4); }
+
+// Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator (bit 4),
+// bf16 A and B (bits 7 and 10), A or B with M or N contiguous (bits 15 and
+// 16), N / 8 at bit 17, M / 16 at bit 24.
+__device__ __forceinline__ uint32_t instruction_desc(bool a_mn, bool b_mn, uint32_t n)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((n >> 3) << 17) |
+           ((uint32_t)(kTileRows >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+                 : "memory");
+}
+
+// Arrive on this barrier in both CTAs of the pair once every tcgen05
+// operation this thread issued before has completed.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     saddr(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// This warp's 32 accumulator lanes (lane = thread), kChunk columns from `taddr`.
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[kChunk])
+{
+    uint32_t r[kChunk];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependents_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ int64_t target_of(const void *target, int target64, int row)
+{
+    return target64 ? static_cast<const int64_t *>(target)[row] : (int64_t)static_cast<const int32_t *>(target)[row];
+}
+
+// ---------------------------------------------------------------- the products
+
+__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// A tile of the persistent schedule and its share [k0, k1) of the K steps.
+struct Unit {
+    int m, n, split, k0, k1;
+};
+
+template <int kMode> struct Shape {
+    int m_tiles, n_tiles, k_steps, splits;
+    __device__ Shape(const PairArgs &a, int count)
+    {
+        const int row_tiles = max(1, ceil_div(count, kTileRows));
+        splits = 1;
+        if (kMode == kLse || kMode == kProb) {
+            m_tiles = row_tiles;
+            n_tiles = ceil_div(a.cols, a.width);
+            k_steps = ceil_div(a.dim, kStepK);
+        } else if (kMode == kHidden) {
+            m_tiles = row_tiles;
+            n_tiles = ceil_div(a.dim, kTileCols);
+            k_steps = ceil_div(a.cols, kStepK);
+            splits = min(a.splits, k_steps);
+        } else {
+            m_tiles = ceil_div(a.cols, kTileRows);
+            n_tiles = ceil_div(a.dim, kTileCols);
+            k_steps = max(1, ceil_div(count, kStepK));
+        }
+    }
+    __device__ int64_t units() const { return (int64_t)m_tiles * n_tiles * splits; }
+    __device__ Unit at(int64_t u) const
+    {
+        Unit t;
+        if (kMode == kLse || kMode == kProb) {
+            // groups of kGroupRows row tiles; in a group the row tile moves
+            // first, so that the pairs at work share the weight's tiles
+            const int64_t per_group = (int64_t)kGroupRows * n_tiles;
+            const int g = (int)(u / per_group);
+            const int64_t r = u - g * per_group;
+            const int in_group = min(kGroupRows, m_tiles - g * kGroupRows);
+            t.m = g * kGroupRows + (int)(r % in_group);
+            t.n = (int)(r / in_group);
+            t.split = 0;
+        } else {
+            t.n = (int)(u % n_tiles);
+            const int64_t r = u / n_tiles;
+            t.m = (int)(r % m_tiles);
+            t.split = (int)(r / m_tiles);
+        }
+        t.k0 = (int)((int64_t)k_steps * t.split / splits);
+        t.k1 = (int)((int64_t)k_steps * (t.split + 1) / splits);
+        return t;
+    }
+};
+
+template <int kMode>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    pair_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, PairArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *ring_a = ring, *ring_b = ring + (size_t)kStages * kShare;
+    PairSmem &sm = *reinterpret_cast<PairSmem *>(ring + 2 * (size_t)kStages * kShare);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = blockIdx.x & 1; // in the pair; rank 0 leads
+    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    constexpr bool kAisMN = kMode == kWeight, kBisMN = kMode == kHidden || kMode == kWeight;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sm.acc_full[b], 1);
+            mbar_init(&sm.acc_empty[b], 2 * kEpiWarps);
+        }
+        mbar_init(&sm.drain, 1);
+        sm.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b) : "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sm.tmem_base)),
+                     "n"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    grid_dependency_wait(); // the inputs may come from the kernel before on the stream
+
+    const int count = a.header ? a.header->count : a.rows;
+    const Shape<kMode> shape(a, count);
+    const int64_t units = shape.units();
+    const int half_cols = kMode == kLse || kMode == kProb ? a.width / 2 : kHalf; // one CTA's share of B
+    volatile uint32_t *abort = &sm.abort;
+
+    if (warp == 0) {
+        // ---- TMA producer
+        if (lane == 0) {
+            const uint32_t bytes = 2 * (kShare + (uint32_t)half_cols * kStepK * 2); // both CTAs'
+            uint32_t it = 0;
+            bool ok = true;
+            for (int64_t u = pair; u < units && ok; u += pairs) {
+                const Unit t = shape.at(u);
+                const int row = t.m * kTileRows + (int)rank * kHalf;
+                for (int k = t.k0; k < t.k1; ++k, ++it) {
+                    const uint32_t s = it % kStages, ph = it / kStages;
+                    if (*abort || (ph > 0 && !mbar_wait(&sm.empty[s], (ph - 1) & 1, abort))) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_expect_tx(&sm.full[s], bytes);
+                    const uint32_t bar = peer_addr(&sm.full[s], 0);
+                    uint8_t *da = ring_a + (size_t)s * kShare, *db = ring_b + (size_t)s * kShare;
+                    if (!kAisMN) {
+                        tma_load(da, &map_a, k * kStepK, row, bar);
+                    } else {
+                        tma_load(da, &map_a, row, k * kStepK, bar);
+                        tma_load(da + kShare / 2, &map_a, row + 64, k * kStepK, bar);
+                    }
+                    if (!kBisMN) {
+                        tma_load(db, &map_b, k * kStepK, a.begin + t.n * a.width + (int)rank * half_cols, bar);
+                    } else {
+                        const int col = t.n * kTileCols + (int)rank * kHalf;
+                        const int y = (kMode == kHidden ? a.begin : 0) + k * kStepK;
+                        tma_load(db, &map_b, col, y, bar);
+                        tma_load(db + kShare / 2, &map_b, col + 64, y, bar);
+                    }
+                }
+            }
+            // both CTAs' copies land before the pair leaves: the last fill of
+            // each stage (the leader's barrier counts both CTAs' bytes)
+            if (rank == 0)
+                for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0u; j < it; ++j)
+                    mbar_wait(&sm.full[j % kStages], (j / kStages) & 1, abort);
+        }
+    } else if (warp == 1) {
+        // ---- MMA issuer (the leading CTA's)
+        if (rank == 0 && lane == 0) {
+            const uint32_t idesc = instruction_desc(kAisMN, kBisMN, (uint32_t)half_cols * 2);
+            uint32_t it = 0, tile = 0;
+            bool ok = true;
+            for (int64_t u = pair; u < units && ok; u += pairs, ++tile) {
+                const Unit t = shape.at(u);
+                const uint32_t buf = tile & 1, use = tile >> 1;
+                if (use > 0 && !mbar_wait(&sm.acc_empty[buf], (use - 1) & 1, abort)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + buf * kTileCols;
+                for (int k = t.k0; k < t.k1; ++k, ++it) {
+                    const uint32_t s = it % kStages, ph = it / kStages;
+                    if (!mbar_wait(&sm.full[s], ph & 1, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = desc_at(ring_a + (size_t)s * kShare, kAisMN ? kDescMN : kDescK);
+                    const uint64_t bd = desc_at(ring_b + (size_t)s * kShare, kBisMN ? kDescMN : kDescK);
+                    // 16 K steps: 32 bytes along a K-major row, 16 whole rows of an MN-major box
+                    constexpr uint64_t step_a = kAisMN ? (16 * 128) >> 4 : 32 >> 4;
+                    constexpr uint64_t step_b = kBisMN ? (16 * 128) >> 4 : 32 >> 4;
+#pragma unroll
+                    for (int kk = 0; kk < kStepK / 16; ++kk)
+                        mma_pair(d, ad + kk * step_a, bd + kk * step_b, idesc, k != t.k0 || kk != 0);
+                    mma_commit_pair(&sm.empty[s]);
+                }
+                if (!ok) break;
+                mma_commit_pair(&sm.acc_full[buf]);
+            }
+            // every product is done before the TMEM is freed
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                             saddr(&sm.drain))
+                         : "memory");
+            mbar_wait(&sm.drain, 0, abort);
+        }
+    } else {
+        // ---- epilogue
+        const int q = warp & 3, h = (warp - 2) >> 2;
+        const uint32_t acc_empty0 = peer_addr(&sm.acc_empty[0], 0), acc_empty1 = peer_addr(&sm.acc_empty[1], 0);
+        uint32_t tile = 0;
+        for (int64_t u = pair; u < units; u += pairs, ++tile) {
+            const Unit t = shape.at(u);
+            const uint32_t buf = tile & 1, use = tile >> 1;
+            const int row = t.m * kTileRows + (int)rank * kHalf + 32 * q + lane; // M index of this thread
+            // what the thread needs of its row, fetched while the products run
+            int at = -1; // the target's column of the piece
+            float lse2 = 0.0f, g = 0.0f;
+            if ((kMode == kLse || kMode == kProb) && row < count) {
+                const int r = a.order ? a.order[row] : row;
+                const int64_t target = target_of(a.target, a.target64, r);
+                if (target >= a.begin && target < (int64_t)a.begin + a.cols) at = (int)(target - a.begin);
+                if (kMode == kProb) {
+                    lse2 = a.lse[r] * kLog2e;
+                    g = a.grad[r] / a.header->grad_scale;
+                }
+            }
+            const bool ready = mbar_wait(&sm.acc_full[buf], use & 1, abort);
+            if (!__all_sync(0xFFFFFFFFu, ready)) break;
+            tc_fence_after();
+            const uint32_t lanes = tmem + buf * kTileCols + ((uint32_t)(32 * q) << 16);
+            // columns of the tile that this thread takes
+            const int c0 = h * half_cols, chunks = half_cols / kChunk;
+            if (kMode == kLse) {
+                float ref = 0.0f, top = -INFINITY, sum = 0.0f; // reference exponent (base 2), its logit, sum of exp2
+                for (int c = 0; c < chunks; ++c) {
+                    float x[kChunk];
+                    tmem_load(lanes + c0 + c * kChunk, x);
+                    const int col = t.n * a.width + c0 + c * kChunk; // of the piece
+                    const int left = a.cols - col;
+                    if (left < kChunk)
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i)
+                            if (i >= left) x[i] = -INFINITY;
+                    const int hit = at - col;
+                    if (__any_sync(0xFFFFFFFFu, (uint32_t)hit < (uint32_t)kChunk))
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i)
+                            if (i == hit) x[i] = -INFINITY;
+                    float m = x[0];
+#pragma unroll
+                    for (int i = 1; i < kChunk; ++i) m = fmaxf(m, x[i]);
+                    if (m > top) {
+                        // an infinite maximum keeps reference 0: inf and NaN then show in the sum
+                        const float next = fabsf(m) < INFINITY ? m * kLog2e : 0.0f;
+                        sum *= top > -INFINITY ? exp2_fast(ref - next) : 1.0f;
+                        ref = next;
+                        top = m;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) sum += exp2_fast(fmaf(x[i], kLog2e, -ref));
+                }
+                if (row < count)
+                    a.partial[(size_t)(2 * t.n + h) * a.pad_rows + row] =
+                        make_float2(top == -INFINITY ? -INFINITY : ref, sum);
+            } else if (kMode == kProb) {
+                for (int c = 0; c < chunks; ++c) {
+                    float x[kChunk];
+                    tmem_load(lanes + c0 + c * kChunk, x);
+                    const int col = t.n * a.width + c0 + c * kChunk;
+                    const int left = row < count ? a.cols - col : 0;
+                    const int hit = at - col;
+                    uint32_t out[kChunk / 2];
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) {
+                        x[i] = exp2_fast(fmaf(x[i], kLog2e, -lse2));
+                        if (i == hit) x[i] -= 1.0f;
+                        x[i] = i < left ? x[i] * g : 0.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kChunk / 2; ++i) out[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+                    uint4 *dst = reinterpret_cast<uint4 *>(a.prob + (size_t)row * a.pitch + col);
+#pragma unroll
+                    for (int i = 0; i < kChunk / 8; ++i)
+                        dst[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+                }
+            } else if (kMode == kHidden) {
+                for (int c = 0; c < chunks; ++c) {
+                    float x[kChunk];
+                    tmem_load(lanes + c0 + c * kChunk, x);
+                    const int col = t.n * kTileCols + c0 + c * kChunk;
+                    if (row < count) {
+                        float4 *dst = reinterpret_cast<float4 *>(
+                            a.sums + ((size_t)t.split * a.pad_rows + row) * a.dim + col);
+#pragma unroll
+                        for (int i = 0; i < kChunk / 4; ++i)
+                            if (col + 4 * i < a.dim) {
+                                float4 v = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                                if (!a.first) {
+                                    const float4 o = dst[i];
+                                    v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+                                }
+                                dst[i] = v;
+                            }
+                    }
+                }
+            } else {
+                const float scale = a.header->grad_scale;
+                for (int c = 0; c < chunks; ++c) {
+                    float x[kChunk];
+                    tmem_load(lanes + c0 + c * kChunk, x);
+                    const int col = t.n * kTileCols + c0 + c * kChunk;
+                    if (row < a.cols) {
+                        uint4 *dst =
+                            reinterpret_cast<uint4 *>(a.d_weight + ((size_t)a.begin + row) * a.dim + col);
+#pragma unroll
+                        for (int i = 0; i < kChunk / 8; ++i)
+                            if (col + 8 * i < a.dim)
+                                dst[i] = make_uint4(pack_bf16(x[8 * i] * scale, x[8 * i + 1] * scale),
+                                                    pack_bf16(x[8 * i + 2] * scale, x[8 * i + 3] * scale),
+                                                    pack_bf16(x[8 * i + 4] * scale, x[8 * i + 5] * scale),
+                                                    pack_bf16(x[8 * i + 6] * scale, x[8 * i + 7] * scale));
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(buf ? acc_empty1 : acc_empty0);
+        }
+    }
+    __syncwarp();
+    grid_dependents_go();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync(); // neither CTA leaves while the other may still reach its shared memory
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- rows before and after
+
+constexpr int kPrepareThreads = 1024;
+
+// One CTA: the rows that count, in their order (order[j] the row at place j,
+// place[r] its place or -1), and the largest finite |g|, by which every g is
+// divided before G is rounded to bf16: with one g for all rows (a mean) the
+// target's entry of G is then exactly p - 1, and no g leaves bf16's range.
+__global__ void __launch_bounds__(kPrepareThreads)
+    head_loss_prepare_kernel(const void *target, int target64, int64_t ignore, const float *grad, int rows, int vocab,
+                             RowHeader *header, int32_t *order, int32_t *place)
+{
+    __shared__ int warp_sum[32];
+    __shared__ float warp_max[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dependency_wait();
+    int base = 0;
+    float top = 0.0f;
+    for (int r0 = 0; r0 < rows; r0 += kPrepareThreads) {
+        const int r = r0 + tid;
+        bool counts = false;
+        if (r < rows) {
+            const int64_t t = target_of(target, target64, r);
+            counts = t != ignore && t >= 0 && t < vocab;
+            if (counts && grad) {
+                const float g = fabsf(grad[r]);
+                if (g < INFINITY) top = fmaxf(top, g);
+            }
+        }
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, counts);
+        if (lane == 0) warp_sum[warp] = __popc(mask);
+        __syncthreads();
+        int before = base, total = 0;
+        for (int w = 0; w < 32; ++w) {
+            const int n = warp_sum[w];
+            if (w < warp) before += n;
+            total += n;
+        }
+        const int at = before + __popc(mask & ((1u << lane) - 1u));
+        if (r < rows) {
+            place[r] = counts ? at : -1;
+            if (counts) order[at] = r;
+        }
+        base += total;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    if (lane == 0) warp_max[warp] = top;
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 0; w < 32; ++w) top = fmaxf(top, warp_max[w]);
+        header->count = base;
+        header->grad_scale = top > 0.0f ? top : 1.0f;
+    }
+    grid_dependents_go();
+}
+
+// The hidden rows that count, packed, with zero rows up to the next whole
+// tile (the products sum over whole K steps of rows).
+__global__ void __launch_bounds__(256)
+    head_loss_gather_kernel(const __nv_bfloat16 *hidden, int64_t stride, int dim, const RowHeader *header,
+                            const int32_t *order, __nv_bfloat16 *packed)
+{
+    grid_dependency_wait();
+    const int count = header->count;
+    const int end = max(1, ceil_div(count, kTileRows)) * kTileRows;
+    const int vecs = dim / 8;
+    for (int j = blockIdx.x; j < end; j += gridDim.x) {
+        uint4 *dst = reinterpret_cast<uint4 *>(packed + (size_t)j * dim);
+        if (j < count) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(hidden + (size_t)order[j] * stride);
+            for (int i = threadIdx.x; i < vecs; i += blockDim.x) dst[i] = src[i];
+        } else {
+            for (int i = threadIdx.x; i < vecs; i += blockDim.x) dst[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    grid_dependents_go();
+}
+
+constexpr int kRowsThreads = 128;
+constexpr int kRowsPerCta = 4; // neighbours of `partial` share its 32-byte sectors
+
+__device__ __forceinline__ float2 join(float2 p, float2 q)
+{
+    // exp2 sums over two reference exponents; -inf: no term yet
+    if (q.x == -INFINITY && !isnan(q.y)) return p;
+    if (p.x == -INFINITY && !isnan(p.y)) return q;
+    const float top = fmaxf(p.x, q.x);
+    return make_float2(top, p.y * exp2f(p.x - top) + q.y * exp2f(q.x - top));
+}
+
+// The rows' losses: four rows per CTA.  The partial sums of a row joined, the
+// target's logit by FMA, and both into loss and lse.
+__global__ void __launch_bounds__(kRowsThreads)
+    head_loss_rows_kernel(const float2 *__restrict__ partial, int parts, int pad_rows, const int32_t *place,
+                          const __nv_bfloat16 *__restrict__ hidden, int64_t hidden_stride,
+                          const __nv_bfloat16 *__restrict__ weight, int64_t weight_stride, int dim, int vocab,
+                          const void *target, int target64, int64_t ignore, int rows, float *loss, float *lse)
+{
+    __shared__ float2 part[kRowsThreads / 32][kRowsPerCta];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dependency_wait();
+    const int r0 = blockIdx.x * kRowsPerCta;
+    // thread = (row tid % 4, every 32nd part)
+    {
+        const int r = r0 + (tid & 3);
+        const int j = r < rows ? (place ? place[r] : r) : -1;
+        float2 mine = make_float2(-INFINITY, 0.0f);
+        if (j >= 0)
+            for (int p = tid >> 2; p < parts; p += kRowsThreads / 4) mine = join(mine, partial[(size_t)p * pad_rows + j]);
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+            const float2 other = make_float2(__shfl_xor_sync(0xFFFFFFFFu, mine.x, d), __shfl_xor_sync(0xFFFFFFFFu, mine.y, d));
+            mine = join(mine, other);
+        }
+        if (lane < 4) part[warp][lane] = mine;
+    }
+    __syncthreads();
+    // warp = row
+    const int r = r0 + warp;
+    if (r < rows) {
+        const int64_t t = target_of(target, target64, r);
+        if (t == ignore) {
+            if (lane == 0) loss[r] = 0.0f, lse[r] = 0.0f;
+        } else if (t < 0 || t >= vocab) {
+            if (lane == 0) loss[r] = NAN, lse[r] = NAN;
+        } else {
+            const uint4 *hv = reinterpret_cast<const uint4 *>(hidden + (size_t)r * hidden_stride);
+            const uint4 *wv = reinterpret_cast<const uint4 *>(weight + (size_t)t * weight_stride);
+            float dot = 0.0f;
+            for (int i = lane; i < dim / 8; i += 32) {
+                const uint4 p = hv[i], w = wv[i];
+                const uint32_t pa[4] = {p.x, p.y, p.z, p.w}, wa[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    dot = fmaf(__uint_as_float(pa[k] << 16), __uint_as_float(wa[k] << 16), dot);
+                    dot = fmaf(__uint_as_float(pa[k] & 0xFFFF0000u), __uint_as_float(wa[k] & 0xFFFF0000u), dot);
+                }
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
+            if (lane == 0) {
+                float2 all = part[0][warp];
+                for (int w = 1; w < kRowsThreads / 32; ++w) all = join(all, part[w][warp]);
+                // a vocabulary of one column leaves no other: rest = -inf
+                const float rest = all.x == -INFINITY && !isnan(all.y) ? -INFINITY : (all.x + log2f(all.y)) * kLn2;
+                const float above = rest - dot;
+                const float tail = log1pf(expf(-fabsf(above)));
+                loss[r] = fmaxf(above, 0.0f) + tail;
+                lse[r] = fmaxf(rest, dot) + tail;
+                if (isnan(above)) loss[r] = lse[r] = above;
+            }
+        }
+    }
+    grid_dependents_go();
+}
+
+// d_hidden: the shares' sums of a row added up, scaled back and rounded;
+// zeros for the rows that do not count.
+__global__ void __launch_bounds__(256)
+    head_loss_hidden_kernel(const float *__restrict__ sums, int splits, int pad_rows, int dim, const RowHeader *header,
+                            const int32_t *place, int rows, __nv_bfloat16 *d_hidden)
+{
+    grid_dependency_wait();
+    const float scale = header->grad_scale;
+    const int vecs = dim / 8;
+    for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+        const int j = place[r];
+        uint4 *dst = reinterpret_cast<uint4 *>(d_hidden + (size_t)r * dim);
+        for (int i = threadIdx.x; i < vecs; i += blockDim.x) {
+            float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (j >= 0)
+                for (int s = 0; s < splits; ++s) {
+                    const float4 *src = reinterpret_cast<const float4 *>(sums + ((size_t)s * pad_rows + j) * dim) + 2 * i;
+                    const float4 p = src[0], q = src[1];
+                    v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+                    v[4] += q.x, v[5] += q.y, v[6] += q.z, v[7] += q.w;
+                }
+            dst[i] = make_uint4(pack_bf16(v[0] * scale, v[1] * scale), pack_bf16(v[2] * scale, v[3] * scale),
+                                pack_bf16(v[4] * scale, v[5] * scale), pack_bf16(v[6] * scale, v[7] * scale));
+        }
+    }
+    grid_dependents_go();
+}
+
+// ---------------------------------------------------------------- host side
+
+constexpr size_t kPairSmemBytes = 1024 + 2 * (size_t)kStages * kShare + sizeof(PairSmem);
+static_assert(kPairSmemBytes <= 227 * 1024, "the pair kernel's shared memory fits one CTA");
+
+constexpr int kMaxDevices = 64;
+struct LossDevice {
+    std::atomic<bool> ready{false};
+    int pairs = 0; // CTA pairs that fit the device at a time
+};
+LossDevice g_loss_dev[kMaxDevices];
+std::mutex g_loss_mutex;
+PFN_cuTensorMapEncodeTiled_v12000 g_loss_encode = nullptr;
+
+template <int kMode> cudaError_t allow_smem()
+{
+    return cudaFuncSetAttribute(pair_product_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)kPairSmemBytes);
+}
+
+// Per device, once: the kernels' shared memory limits, the pairs the device
+// holds, and the driver's tensor-map encoder.
+int loss_setup(int *pairs, int *sm_count)
+{
+    int st = tf_topk_internal_device(sm_count);
+    if (st != TF_TOPK_OK) return st;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return tf_topk_internal_fail_cuda((int)e);
+    LossDevice &d = g_loss_dev[dev];
+    if (!d.ready.load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lock(g_loss_mutex);
+        if (!d.ready.load(std::memory_order_relaxed)) {
+            e = allow_smem<kLse>();
+            if (e == cudaSuccess) e = allow_smem<kProb>();
+            if (e == cudaSuccess) e = allow_smem<kHidden>();
+            if (e == cudaSuccess) e = allow_smem<kWeight>();
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)(*sm_count / 2 * 2), 1, 1);
+            cfg.blockDim = dim3(kPairThreads, 1, 1);
+            cfg.dynamicSmemBytes = kPairSmemBytes;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, pair_product_kernel<kLse>, &cfg);
+            if (e != cudaSuccess) return tf_topk_internal_fail_cuda((int)e);
+            d.pairs = n < 1 ? 1 : n;
+            if (!g_loss_encode) {
+                void *fn = nullptr;
+                cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+                e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+                if (e != cudaSuccess) return tf_topk_internal_fail_cuda((int)e);
+                if (q != cudaDriverEntryPointSuccess || !fn) return TF_TOPK_ERR_DEVICE;
+                g_loss_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+            }
+            d.ready.store(true, std::memory_order_release);
+        }
+    }
+    *pairs = d.pairs;
+    return TF_TOPK_OK;
+}
+
+// A 2-D bf16 tensor map, boxes of 64 x box_rows with the 128-byte swizzle;
+// coordinates past either extent read as zero.
+bool encode_map(CUtensorMap *map, const void *p, int64_t inner, int64_t outer, int64_t stride, int box_rows)
+{
+    cuuint64_t gdim[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+    cuuint64_t gstride[1] = {(cuuint64_t)stride * 2};
+    cuuint32_t box[2] = {(cuuint32_t)kStepK, (cuuint32_t)box_rows};
+    cuuint32_t estride[2] = {1, 1};
+    return g_loss_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), gdim, gstride, box, estride,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaLaunchConfig_t config(int grid, int threads, size_t smem, cudaStream_t stream, cudaLaunchAttribute *attr)
+{
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <int kMode>
+cudaError_t launch_product(const CUtensorMap &ma, const CUtensorMap &mb, const PairArgs &a, int64_t most_units,
+                           int pairs, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr[1];
+    const int64_t n = most_units < pairs ? most_units : pairs;
+    const cudaLaunchConfig_t cfg = config((int)(2 * n), kPairThreads, kPairSmemBytes, stream, attr);
+    return cudaLaunchKernelEx(&cfg, pair_product_kernel<kMode>, ma, mb, a);
+}
+
+int64_t pad_rows_of(int64_t rows) { return (rows + kTileRows - 1) / kTileRows * kTileRows; }
+
+// Carves a workspace into 256-byte aligned parts.
+struct Carver {
+    uintptr_t at;
+    explicit Carver(const void *p) : at((reinterpret_cast<uintptr_t>(p) + 255) & ~(uintptr_t)255) {}
+    template <typename T> T *take(int64_t n)
+    {
+        T *p = reinterpret_cast<T *>(at);
+        at += ((size_t)n * sizeof(T) + 255) & ~(size_t)255;
+        return p;
+    }
+};
+
+// Columns of a tile for the forward product: the widest tile moves the
+// fewest bytes through shared memory, a narrower one may fill the last round
+// of the pairs better.  A round costs about its width plus 32 columns.
+int tile_width(int64_t rows, int64_t vocab, int pairs)
+{
+    const int64_t m = pad_rows_of(rows) / kTileRows;
+    int best = kTileCols;
+    int64_t cost = INT64_MAX;
+    for (int w = kTileCols; w >= 64; w -= 64) {
+        const int64_t units = m * ((vocab + w - 1) / w);
+        const int64_t c = (units + pairs - 1) / pairs * (w + 32);
+        if (c < cost) {
+            cost = c;
+            best = w;
+        }
+    }
+    return best;
+}
+
+struct LossSpace {
+    RowHeader *header;
+    int32_t *order, *place;
+    __nv_bfloat16 *packed;
+    float2 *partial;
+    size_t bytes;
+};
+
+// Rows are packed when they fill more than one row tile (then every ignored
+// row saves its share of the product).
+LossSpace loss_space(const void *p, int64_t rows, int64_t dim, int64_t parts)
+{
+    Carver c(p);
+    LossSpace s = {};
+    if (rows > kTileRows) {
+        s.header = c.take<RowHeader>(1);
+        s.order = c.take<int32_t>(rows);
+        s.place = c.take<int32_t>(rows);
+        s.packed = c.take<__nv_bfloat16>(pad_rows_of(rows) * dim);
+    }
+    s.partial = c.take<float2>(parts * pad_rows_of(rows));
+    s.bytes = (size_t)(c.at - (reinterpret_cast<uintptr_t>(p))) + 256;
+    return s;
+}
+
+struct GradSpace {
+    RowHeader *header;
+    int32_t *order, *place;
+    __nv_bfloat16 *packed;
+    float *sums;
+    __nv_bfloat16 *prob;
+    int splits;
+    int64_t piece; // columns of a piece
+    size_t bytes;
+};
+
+constexpr int64_t kProbBytes = 256ll << 20; // G of a piece, where the caller has the room
+
+// Shares of K that the hidden states' gradient is summed in: enough tiles for
+// every pair to have work, four shares at most where the rows alone give it.
+int hidden_splits(int64_t rows, int64_t dim, int pairs)
+{
+    const int64_t tiles = pad_rows_of(rows) / kTileRows * ((dim + kTileCols - 1) / kTileCols);
+    int64_t s = (4 * (int64_t)pairs + tiles - 1) / tiles;
+    return (int)(s < 1 ? 1 : s > 32 ? 32 : s);
+}
+
+GradSpace grad_space(const void *p, int64_t rows, int64_t dim, int64_t vocab, int pairs, bool hidden, int64_t piece)
+{
+    Carver c(p);
+    GradSpace s = {};
+    s.piece = piece;
+    s.splits = hidden_splits(rows, dim, pairs);
+    const int64_t pad = pad_rows_of(rows);
+    s.header = c.take<RowHeader>(1);
+    s.order = c.take<int32_t>(rows);
+    s.place = c.take<int32_t>(rows);
+    s.packed = c.take<__nv_bfloat16>(pad * dim);
+    if (hidden) s.sums = c.take<float>((int64_t)s.splits * pad * dim);
+    s.prob = c.take<__nv_bfloat16>(pad * piece);
+    s.bytes = (size_t)(c.at - (reinterpret_cast<uintptr_t>(p))) + 256;
+    return s;
+}
+
+int64_t whole_piece(int64_t vocab) { return (vocab + kTileCols - 1) / kTileCols * kTileCols; }
+
+// The recommended columns of a piece: G of kProbBytes, at least one tile.
+int64_t good_piece(int64_t rows, int64_t vocab)
+{
+    int64_t cols = kProbBytes / (2 * pad_rows_of(rows)) / kTileCols * kTileCols;
+    if (cols < kTileCols) cols = kTileCols;
+    const int64_t all = whole_piece(vocab);
+    if (cols >= all) return all;
+    const int64_t pieces = (all + cols - 1) / cols; // of equal width
+    return ((all + pieces - 1) / pieces + kTileCols - 1) / kTileCols * kTileCols;
+}
+
+bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+bool bad_shape(int64_t rows, int32_t dim, int64_t vocab)
+{
+    return rows < 0 || rows > TF_TOPK_HEAD_LOSS_MAX_ROWS || dim < 8 || dim % 8 != 0 || vocab < 1 ||
+           vocab > (int64_t)INT32_MAX - 1024;
+}
+
+bool bad_stride(int64_t stride, int64_t dim, int64_t n)
+{
+    // 16-byte rows whose byte offsets stay below the tensor maps' 2^40
+    return stride < dim || stride % 8 != 0 || stride >= (1ll << 39) || (n > 0 && stride > INT64_MAX / 4 / n);
+}
+
+int run_loss(const void *hidden, int64_t hidden_stride, const void *weight, int64_t weight_stride, int64_t rows,
+             int32_t dim, int64_t vocab, const void *target, int32_t target_bytes, int64_t ignore, void *workspace,
+             size_t workspace_bytes, float *loss, float *lse, void *stream)
+{
+    if (bad_shape(rows, dim, vocab) || bad_stride(hidden_stride, dim, rows) || bad_stride(weight_stride, dim, vocab))
+        return TF_TOPK_ERR_SHAPE;
+    if (rows == 0) return TF_TOPK_OK;
+    if (target_bytes != 4 && target_bytes != 8) return TF_TOPK_ERR_ARG;
+    if (!hidden || !weight || !target || !workspace || !loss || !lse) return TF_TOPK_ERR_NULL;
+    if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(target, (size_t)target_bytes) || !aligned(loss, 4) ||
+        !aligned(lse, 4))
+        return TF_TOPK_ERR_ALIGN;
+    int pairs = 0, sms = 0;
+    const int st = loss_setup(&pairs, &sms);
+    if (st != TF_TOPK_OK) return st;
+    const int width = tile_width(rows, vocab, pairs);
+    const int64_t tiles = (vocab + width - 1) / width;
+    const LossSpace s = loss_space(workspace, rows, dim, 2 * tiles);
+    if (s.bytes > workspace_bytes) return TF_TOPK_ERR_SCRATCH;
+    const cudaStream_t strm = static_cast<cudaStream_t>(stream);
+    CUtensorMap ma, mb;
+    const bool packed = s.packed != nullptr;
+    if (!encode_map(&ma, packed ? s.packed : hidden, dim, packed ? pad_rows_of(rows) : rows, packed ? dim : hidden_stride,
+                    kHalf) ||
+        !encode_map(&mb, weight, dim, vocab, weight_stride, width / 2))
+        return tf_topk_internal_fail_cuda((int)cudaErrorInvalidValue);
+    cudaLaunchAttribute attr[1];
+    cudaError_t e = cudaSuccess;
+    if (packed) {
+        cudaLaunchConfig_t cfg = config(1, kPrepareThreads, 0, strm, attr);
+        e = cudaLaunchKernelEx(&cfg, head_loss_prepare_kernel, target, (int)(target_bytes == 8), ignore,
+                               (const float *)nullptr, (int)rows, (int)vocab, s.header, s.order, s.place);
+        cfg = config((int)(rows < 4 * sms ? rows : 4 * sms), 256, 0, strm, attr);
+        if (e == cudaSuccess)
+            e = cudaLaunchKernelEx(&cfg, head_loss_gather_kernel, static_cast<const __nv_bfloat16 *>(hidden),
+                                   hidden_stride, (int)dim, (const RowHeader *)s.header, (const int32_t *)s.order,
+                                   s.packed);
+    }
+    PairArgs a = {};
+    a.header = s.header;
+    a.order = s.order;
+    a.target = target;
+    a.target64 = target_bytes == 8;
+    a.rows = (int32_t)rows;
+    a.dim = dim;
+    a.vocab = (int32_t)vocab;
+    a.begin = 0;
+    a.cols = (int32_t)vocab;
+    a.width = width;
+    a.pad_rows = (int32_t)pad_rows_of(rows);
+    a.partial = s.partial;
+    if (e == cudaSuccess) e = launch_product<kLse>(ma, mb, a, tiles * (pad_rows_of(rows) / kTileRows), pairs, strm);
+    const cudaLaunchConfig_t cfg =
+        config((int)((rows + kRowsPerCta - 1) / kRowsPerCta), kRowsThreads, 0, strm, attr);
+    if (e == cudaSuccess)
+        e = cudaLaunchKernelEx(&cfg, head_loss_rows_kernel, (const float2 *)s.partial, (int)(2 * tiles), a.pad_rows,
+                               (const int32_t *)s.place, static_cast<const __nv_bfloat16 *>(hidden), hidden_stride,
+                               static_cast<const __nv_bfloat16 *>(weight), weight_stride, (int)dim, (int)vocab, target,
+                               (int)(target_bytes == 8), ignore, (int)rows, loss, lse);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? TF_TOPK_OK : tf_topk_internal_fail_cuda((int)e);
+}
+
+int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int64_t weight_stride, int64_t rows,
+             int32_t dim, int64_t vocab, const void *target, int32_t target_bytes, int64_t ignore, const float *lse,
+             const float *grad_loss, void *workspace, size_t workspace_bytes, void *d_hidden, void *d_weight,
+             void *stream)
+{
+    if (bad_shape(rows, dim, vocab) || bad_stride(hidden_stride, dim, rows) || bad_stride(weight_stride, dim, vocab))
+        return TF_TOPK_ERR_SHAPE;
+    if (rows == 0) { // nothing flows to the weight
+        if (!d_weight) return TF_TOPK_OK;
+        if (!aligned(d_weight, 16)) return TF_TOPK_ERR_ALIGN;
+        int sms = 0;
+        const int st = tf_topk_internal_device(&sms);
+        if (st != TF_TOPK_OK) return st;
+        const cudaError_t e =
+            cudaMemsetAsync(d_weight, 0, (size_t)vocab * dim * 2, static_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? TF_TOPK_OK : tf_topk_internal_fail_cuda((int)e);
+    }
+    if (target_bytes != 4 && target_bytes != 8) return TF_TOPK_ERR_ARG;
+    if (!hidden || !weight || !target || !lse || !grad_loss || !workspace || (!d_hidden && !d_weight))
+        return TF_TOPK_ERR_NULL;
+    if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(d_hidden, 16) || !aligned(d_weight, 16) ||
+        !aligned(target, (size_t)target_bytes) || !aligned(lse, 4) || !aligned(grad_loss, 4))
+        return TF_TOPK_ERR_ALIGN;
+    int pairs = 0, sms = 0;
+    const int st = loss_setup(&pairs, &sms);
+    if (st != TF_TOPK_OK) return st;
+    // the widest pieces the workspace holds, up to the recommended ones
+    int64_t piece = good_piece(rows, vocab);
+    if (grad_space(workspace, rows, dim, vocab, pairs, d_hidden != nullptr, piece).bytes > workspace_bytes) {
+        const size_t least = grad_space(workspace, rows, dim, vocab, pairs, d_hidden != nullptr, kTileCols).bytes;
+        if (least > workspace_bytes) return TF_TOPK_ERR_SCRATCH;
+        piece = kTileCols + (int64_t)((workspace_bytes - least) / (2 * (size_t)pad_rows_of(rows))) / kTileCols * kTileCols;
+    }
+    const GradSpace s = grad_space(workspace, rows, dim, vocab, pairs, d_hidden != nullptr, piece);
+    const int64_t pad = pad_rows_of(rows);
+    const cudaStream_t strm = static_cast<cudaStream_t>(stream);
+    CUtensorMap packed_k, packed_n, weight_k, weight_n, prob_k, prob_m;
+    if (!encode_map(&packed_k, s.packed, dim, pad, dim, kHalf) || !encode_map(&packed_n, s.packed, dim, pad, dim, kStepK) ||
+        !encode_map(&weight_k, weight, dim, vocab, weight_stride, kHalf) ||
+        !encode_map(&weight_n, weight, dim, vocab, weight_stride, kStepK) ||
+        !encode_map(&prob_k, s.prob, piece, pad, piece, kHalf) || !encode_map(&prob_m, s.prob, piece, pad, piece, kStepK))
+        return tf_topk_internal_fail_cuda((int)cudaErrorInvalidValue);
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config(1, kPrepareThreads, 0, strm, attr);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, head_loss_prepare_kernel, target, (int)(target_bytes == 8), ignore,
+                                       grad_loss, (int)rows, (int)vocab, s.header, s.order, s.place);
+    cfg = config((int)(pad < 4 * sms ? pad : 4 * sms), 256, 0, strm, attr);
+    if (e == cudaSuccess)
+        e = cudaLaunchKernelEx(&cfg, head_loss_gather_kernel, static_cast<const __nv_bfloat16 *>(hidden), hidden_stride,
+                               (int)dim, (const RowHeader *)s.header, (const int32_t *)s.order, s.packed);
+    PairArgs a = {};
+    a.header = s.header;
+    a.order = s.order;
+    a.target = target;
+    a.target64 = target_bytes == 8;
+    a.rows = (int32_t)rows;
+    a.dim = dim;
+    a.vocab = (int32_t)vocab;
+    a.width = kTileCols;
+    a.pad_rows = (int32_t)pad;
+    a.pitch = (int32_t)piece;
+    a.lse = lse;
+    a.grad = grad_loss;
+    a.prob = s.prob;
+    a.sums = s.sums;
+    a.d_weight = static_cast<__nv_bfloat16 *>(d_weight);
+    const int64_t row_tiles = pad / kTileRows, dim_tiles = (dim + kTileCols - 1) / kTileCols;
+    // every share of the sums starts in the first piece, the widest
+    const int64_t steps = ((vocab < piece ? vocab : piece) + kStepK - 1) / kStepK;
+    a.splits = (int32_t)(s.splits < steps ? s.splits : steps);
+    for (int64_t begin = 0; begin < vocab && e == cudaSuccess; begin += piece) {
+        a.begin = (int32_t)begin;
+        a.cols = (int32_t)(vocab - begin < piece ? vocab - begin : piece);
+        a.first = begin == 0;
+        const int64_t col_tiles = (a.cols + kTileCols - 1) / kTileCols;
+        e = launch_product<kProb>(packed_k, weight_k, a, row_tiles * col_tiles, pairs, strm);
+        if (e == cudaSuccess && d_hidden)
+            e = launch_product<kHidden>(prob_k, weight_n, a, row_tiles * dim_tiles * a.splits, pairs, strm);
+        if (e == cudaSuccess && d_weight)
+            e = launch_product<kWeight>(prob_m, packed_n, a, col_tiles * dim_tiles, pairs, strm);
+    }
+    if (e == cudaSuccess && d_hidden) {
+        cfg = config((int)(rows < 8 * sms ? rows : 8 * sms), 256, 0, strm, attr);
+        e = cudaLaunchKernelEx(&cfg, head_loss_hidden_kernel, (const float *)s.sums, (int)a.splits, a.pad_rows, (int)dim,
+                               (const RowHeader *)s.header, (const int32_t *)s.place, (int)rows,
+                               static_cast<__nv_bfloat16 *>(d_hidden));
+    }
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? TF_TOPK_OK : tf_topk_internal_fail_cuda((int)e);
+}
+
+} // namespace
+
+// This file's fault word, read and cleared (tf_topk_device_fault reports it).
+uint32_t tf_topk_internal_head_loss_fault_take()
+{
+    uint32_t f = 0;
+    if (cudaMemcpyFromSymbol(&f, g_head_loss_fault, sizeof f) != cudaSuccess) return 0;
+    if (f) {
+        const uint32_t zero = 0;
+        cudaMemcpyToSymbol(g_head_loss_fault, &zero, sizeof zero);
+    }
+    return f;
+}
+
+extern "C" {
+
+int tf_topk_head_loss_bf16(const void *hidden, int64_t hidden_stride, const void *weight, int64_t weight_stride,
+                           int64_t rows, int32_t dim, int64_t vocab, const void *target, int32_t target_bytes,
+                           int64_t ignore_index, void *workspace, size_t workspace_bytes, float *out_loss,
+                           float *out_lse, void *stream)
+{
+    return run_loss(hidden, hidden_stride, weight, weight_stride, rows, dim, vocab, target, target_bytes, ignore_index,
+                    workspace, workspace_bytes, out_loss, out_lse, stream);
+}
+
+size_t tf_topk_head_loss_bf16_workspace(int64_t rows, int32_t dim, int64_t vocab)
+{
+    int pairs = 0, sms = 0;
+    if (rows < 1 || bad_shape(rows, dim, vocab) || loss_setup(&pairs, &sms) != TF_TOPK_OK) return 0;
+    const int width = tile_width(rows, vocab, pairs);
+    return loss_space(nullptr, rows, dim, 2 * ((vocab + width - 1) / width)).bytes + 256;
+}
+
+int tf_topk_head_loss_grad_bf16(const void *hidden, int64_t hidden_stride, const void *weight, int64_t weight_stride,
+                                int64_t rows, int32_t dim, int64_t vocab, const void *target, int32_t target_bytes,
+                                int64_t ignore_index, const float *lse, const float *grad_loss, void *workspace,
+                                size_t workspace_bytes, void *out_grad_hidden, void *out_grad_weight, void *stream)
+{
+    return run_grad(hidden, hidden_stride, weight, weight_stride, rows, dim, vocab, target, target_bytes, ignore_index,
+                    lse, grad_loss, workspace, workspace_bytes, out_grad_hidden, out_grad_weight, stream);
+}
+
+size_t tf_topk_head_loss_grad_bf16_workspace(int64_t rows, int32_t dim, int64_t vocab, int32_t least)
+{
+    int pairs = 0, sms = 0;
+    if (rows < 1 || bad_shape(rows, dim, vocab) || loss_setup(&pairs, &sms) != TF_TOPK_OK) return 0;
+    return grad_space(nullptr, rows, dim, vocab, pairs, true, least ? kTileCols : good_piece(rows, vocab)).bytes + 256;
+}
+
+} // extern "C"

@@ -7,9 +7,11 @@ not been built, every entry point raises -- there is no fallback.
 Tensor-level calls: ``topk_bf16`` (bf16 rows, k <= 64, any launch plan),
 ``select_topk`` (bf16 / fp16 / fp32 rows, k <= 1024), ``merge_bf16``
 (per-shard lists into each row's top k), ``nucleus_bf16`` (top-p
-probabilities over the lists) and ``head_topk_bf16`` (the draft head's
-product and the top-k in one kernel).  The raw C entry points are exposed under
-their C names.
+probabilities over the lists), ``head_topk_bf16`` (the draft head's
+product and the top-k in one kernel), ``head_loss_bf16`` and
+``head_loss_grad_bf16`` (the head's cross entropy and its gradient without the
+logits), ``route_experts`` and ``route_experts_grad`` (each token's experts and
+their weights).  The raw C entry points are exposed under their C names.
 """
 from __future__ import annotations
 
@@ -84,6 +86,23 @@ def library() -> ctypes.CDLL:
                                           c_p, c_p, c_p]
         lib.tf_topk_head_bf16_workspace.restype = ctypes.c_size_t
         lib.tf_topk_head_bf16_workspace.argtypes = [c_i32, c_i32]
+        c_size = ctypes.c_size_t
+        lib.tf_topk_head_loss_bf16.restype = ctypes.c_int
+        lib.tf_topk_head_loss_bf16.argtypes = [c_p, c_i64, c_p, c_i64, c_i64, c_i32, c_i64, c_p, c_i32, c_i64, c_p,
+                                               c_size, c_p, c_p, c_p]
+        lib.tf_topk_head_loss_bf16_workspace.restype = c_size
+        lib.tf_topk_head_loss_bf16_workspace.argtypes = [c_i64, c_i32, c_i64]
+        lib.tf_topk_head_loss_grad_bf16.restype = ctypes.c_int
+        lib.tf_topk_head_loss_grad_bf16.argtypes = [c_p, c_i64, c_p, c_i64, c_i64, c_i32, c_i64, c_p, c_i32, c_i64,
+                                                    c_p, c_p, c_p, c_size, c_p, c_p, c_p]
+        lib.tf_topk_head_loss_grad_bf16_workspace.restype = c_size
+        lib.tf_topk_head_loss_grad_bf16_workspace.argtypes = [c_i64, c_i32, c_i64, c_i32]
+        lib.tf_topk_route.restype = ctypes.c_int
+        lib.tf_topk_route.argtypes = [c_p, c_i32, c_i64, c_i32, c_i64, c_i32, c_p, c_i32, c_i32, c_i32, c_i32, c_i32,
+                                      ctypes.c_float, c_p, c_p, c_p, c_p]
+        lib.tf_topk_route_grad.restype = ctypes.c_int
+        lib.tf_topk_route_grad.argtypes = [c_p, c_i32, c_i64, c_i32, c_i64, c_i32, c_p, c_p, c_i32, c_i32,
+                                           ctypes.c_float, c_p, c_p]
         lib.tf_topk_strerror.restype = ctypes.c_char_p
         lib.tf_topk_strerror.argtypes = [ctypes.c_int]
         lib.tf_topk_last_cuda_error.restype = ctypes.c_int
@@ -360,6 +379,256 @@ def head_topk_bf16(hidden, weight, k: int, *, out=None, workspace=None, stream=N
     _check(_on_device(dev, tf_topk_head_bf16, hidden.data_ptr(), weight.data_ptr(), rows, dim, vocab, k,
                       workspace.data_ptr(), workspace.numel(), out[0].data_ptr(), out[1].data_ptr(),
                       out[2].data_ptr(), out[3].data_ptr(), _stream_handle(stream, dev)))
+    return out
+
+
+def tf_topk_head_loss_bf16(hidden: int, hidden_stride: int, weight: int, weight_stride: int, rows: int, dim: int,
+                           vocab: int, target: int, target_bytes: int, ignore_index: int, workspace: int,
+                           workspace_bytes: int, out_loss: int, out_lse: int, stream: int | None) -> int:
+    """The C entry point of the head's loss with raw pointers; returns the status code."""
+    return library().tf_topk_head_loss_bf16(hidden, hidden_stride, weight, weight_stride, rows, dim, vocab, target,
+                                            target_bytes, ignore_index, workspace, workspace_bytes, out_loss, out_lse,
+                                            stream)
+
+
+def tf_topk_head_loss_bf16_workspace(rows: int, dim: int, vocab: int) -> int:
+    """Workspace bytes tf_topk_head_loss_bf16 needs on the current device (0 for bad arguments)."""
+    return library().tf_topk_head_loss_bf16_workspace(rows, dim, vocab)
+
+
+def tf_topk_head_loss_grad_bf16(hidden: int, hidden_stride: int, weight: int, weight_stride: int, rows: int, dim: int,
+                                vocab: int, target: int, target_bytes: int, ignore_index: int, lse: int,
+                                grad_loss: int, workspace: int, workspace_bytes: int, out_grad_hidden: int | None,
+                                out_grad_weight: int | None, stream: int | None) -> int:
+    """The C entry point of the head loss's gradient with raw pointers; returns the status code."""
+    return library().tf_topk_head_loss_grad_bf16(hidden, hidden_stride, weight, weight_stride, rows, dim, vocab,
+                                                 target, target_bytes, ignore_index, lse, grad_loss, workspace,
+                                                 workspace_bytes, out_grad_hidden, out_grad_weight, stream)
+
+
+def tf_topk_head_loss_grad_bf16_workspace(rows: int, dim: int, vocab: int, least: bool = False) -> int:
+    """Workspace bytes tf_topk_head_loss_grad_bf16 makes good use of on the
+    current device, or the least it accepts (0 for bad arguments)."""
+    return library().tf_topk_head_loss_grad_bf16_workspace(rows, dim, vocab, int(least))
+
+
+def _head_inputs(hidden, weight, target):
+    """(rows, dim, vocab, hidden row stride, weight row stride) of a head's loss, checked."""
+    import torch
+
+    for name, t in (("hidden", hidden), ("weight", weight)):
+        if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+            raise TypeError(f"expected bf16 bits, got {t.dtype}")
+        if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must be a 2-D CUDA tensor with contiguous columns")
+    rows, dim = hidden.shape
+    vocab = weight.shape[0]
+    if weight.shape[1] != dim:
+        raise ValueError("hidden and weight disagree on dim")
+    if target.dtype not in (torch.int64, torch.int32):
+        raise TypeError(f"target must be int64 or int32, got {target.dtype}")
+    dev = hidden.device
+    if target.dim() != 1 or target.shape[0] != rows or not target.is_contiguous():
+        raise ValueError("target must be a contiguous [rows] tensor")
+    if weight.device != dev or target.device != dev:
+        raise ValueError("hidden, weight and target must be on one device")
+    round_up = -(-dim // 8) * 8  # the stride of a single row is free
+    return (rows, dim, vocab, hidden.stride(0) if rows > 1 else round_up, weight.stride(0) if vocab > 1 else round_up)
+
+
+def _check_out(t, shape, dtype, dev, name):
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the inputs' device")
+
+
+def _empty(shape, dtype, dev, stream):
+    """A fresh tensor whose memory belongs to the stream the call runs on: what
+    is freed there may still be in use by the work queued before it, and what a
+    call frees at its end (a workspace) is reused by the work after it."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _workspace(workspace, need: int, dev, stream):
+    """A caller's workspace, checked, or a fresh one of ``need`` bytes."""
+    import torch
+
+    if workspace is None:
+        return _empty((max(need, 8),), torch.uint8, dev, stream)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace
+
+
+def head_loss_bf16(hidden, weight, target, *, ignore_index: int = -100, out=None, workspace=None, stream=None):
+    """Softmax cross entropy of the head's logits ``hidden @ weight.T`` (bf16
+    in, fp32 sums, not rounded) against one target column per row, without
+    storing the logits.
+
+    ``hidden``: CUDA bf16 (or int16 bits) [rows, dim], ``weight`` [vocab, dim],
+    both with contiguous columns, dim and row strides multiples of 8;
+    ``target``: int64 or int32 [rows].
+    Returns ``(loss float32[rows], lse float32[rows])``: per row, 0 and 0 where
+    the target is ``ignore_index``, NaN where it is any other value outside the
+    vocabulary.  ``loss`` is not reduced; ``lse`` is what
+    ``head_loss_grad_bf16`` takes.  ``out`` may supply those two tensors and
+    ``workspace`` a CUDA tensor of at least
+    ``tf_topk_head_loss_bf16_workspace(rows, dim, vocab)`` bytes.
+    """
+    import torch
+
+    rows, dim, vocab, hs, ws = _head_inputs(hidden, weight, target)
+    dev = hidden.device
+    if out is None:
+        out = (_empty((rows,), torch.float32, dev, stream), _empty((rows,), torch.float32, dev, stream))
+    else:
+        for t, name in zip(out, ("loss", "lse")):
+            _check_out(t, (rows,), torch.float32, dev, name)
+    need = _on_device(dev, tf_topk_head_loss_bf16_workspace, rows, dim, vocab) if workspace is None else 0
+    space = _workspace(workspace, need, dev, stream)
+    _check(_on_device(dev, tf_topk_head_loss_bf16, hidden.data_ptr(), hs, weight.data_ptr(), ws, rows, dim, vocab,
+                      target.data_ptr(), target.element_size(), ignore_index, space.data_ptr(), space.nbytes,
+                      out[0].data_ptr(), out[1].data_ptr(), _stream_handle(stream, dev)))
+    return out
+
+
+def head_loss_grad_bf16(hidden, weight, target, lse, grad_loss, *, ignore_index: int = -100, hidden_grad: bool = True,
+                        weight_grad: bool = True, out=None, workspace=None, stream=None):
+    """Gradient of ``head_loss_bf16``: with ``grad_loss`` float32 [rows] the
+    gradient of its losses and ``lse`` as it returned it, gives
+    ``(grad_hidden bf16[rows, dim], grad_weight bf16[vocab, dim])``.
+
+    The logits are computed again, in pieces of the vocabulary.  A gradient
+    that is not wanted (``hidden_grad`` / ``weight_grad`` False) is not
+    computed and None in its place.  Rows that do not count get zeros and
+    reach nothing, whatever they hold.  ``out`` may supply the two tensors
+    (None for one not wanted) and ``workspace`` a CUDA tensor of any size from
+    ``tf_topk_head_loss_grad_bf16_workspace(rows, dim, vocab, True)`` bytes on.
+    """
+    import torch
+
+    rows, dim, vocab, hs, ws = _head_inputs(hidden, weight, target)
+    dev = hidden.device
+    _check_out(lse, (rows,), torch.float32, dev, "lse")
+    _check_out(grad_loss, (rows,), torch.float32, dev, "grad_loss")
+    if not hidden_grad and not weight_grad:
+        return None, None
+    if out is None:
+        out = (_empty((rows, dim), torch.bfloat16, dev, stream) if hidden_grad else None,
+               _empty((vocab, dim), torch.bfloat16, dev, stream) if weight_grad else None)
+    else:
+        for t, shape, want, name in ((out[0], (rows, dim), hidden_grad, "grad_hidden"),
+                                     (out[1], (vocab, dim), weight_grad, "grad_weight")):
+            if want:
+                _check_out(t, shape, torch.bfloat16, dev, name)
+    need = (_on_device(dev, tf_topk_head_loss_grad_bf16_workspace, rows, dim, vocab) if workspace is None else 0)
+    space = _workspace(workspace, need, dev, stream)
+    _check(_on_device(dev, tf_topk_head_loss_grad_bf16, hidden.data_ptr(), hs, weight.data_ptr(), ws, rows, dim, vocab,
+                      target.data_ptr(), target.element_size(), ignore_index, lse.data_ptr(), grad_loss.data_ptr(),
+                      space.data_ptr(), space.nbytes, out[0].data_ptr() if hidden_grad else None,
+                      out[1].data_ptr() if weight_grad else None, _stream_handle(stream, dev)))
+    return (out[0] if hidden_grad else None, out[1] if weight_grad else None)
+
+
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
+ROUTE_MAX_EXPERTS, ROUTE_MAX_K, ROUTE_MAX_GROUPS = 1024, 32, 32
+
+
+def tf_topk_route(logits: int, dtype: int, tokens: int, experts: int, row_stride: int, k: int, bias: int | None,
+                  score: int, groups: int, groups_kept: int, group_best: int, renormalize: int, scale: float,
+                  out_idx: int, out_weight: int, load: int | None, stream: int | None) -> int:
+    """The C entry point of expert routing with raw pointers; returns the status code."""
+    return library().tf_topk_route(logits, dtype, tokens, experts, row_stride, k, bias, score, groups, groups_kept,
+                                   group_best, renormalize, scale, out_idx, out_weight, load, stream)
+
+
+def tf_topk_route_grad(logits: int, dtype: int, tokens: int, experts: int, row_stride: int, k: int, idx: int,
+                       grad_weight: int, score: int, renormalize: int, scale: float, out_grad_logits: int,
+                       stream: int | None) -> int:
+    """The C entry point of the routing gradient with raw pointers; returns the status code."""
+    return library().tf_topk_route_grad(logits, dtype, tokens, experts, row_stride, k, idx, grad_weight, score,
+                                        renormalize, scale, out_grad_logits, stream)
+
+
+def _router_logits(logits, score: str):
+    """(dtype code, tokens, experts, row stride, score code) of a router's logits, checked."""
+    import torch
+
+    code = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}.get(logits.dtype)
+    if code is None:
+        raise TypeError(f"logits must be bfloat16, float16 or float32, got {logits.dtype}")
+    if score not in ROUTE_SCORES:
+        raise ValueError(f"score must be one of {tuple(ROUTE_SCORES)}, got {score!r}")
+    if not logits.is_cuda or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a 2-D CUDA tensor with contiguous columns")
+    tokens, experts = logits.shape
+    return code, tokens, experts, logits.stride(0) if tokens > 1 else experts, ROUTE_SCORES[score]
+
+
+def route_experts(logits, k: int, *, bias=None, score: str = "softmax", groups: int = 1, groups_kept: int | None = None,
+                  group_best: int = 2, renormalize: bool = True, scale: float = 1.0, load=None, out=None, stream=None):
+    """Each token's best ``k`` experts, best first (ties to the lower expert),
+    with their weights.
+
+    ``logits``: CUDA bf16 / fp16 / fp32 [tokens, experts], contiguous columns.
+    Scores are the sigmoid or the softmax of the logits; an expert whose logit
+    is NaN or -inf is out of reach.  ``bias`` (float32 [experts]) moves the
+    choice only.  With ``groups`` > 1 only the experts of the ``groups_kept``
+    best groups remain, a group's value being the sum of its best
+    ``group_best`` (1 or 2) choices.  Weights are the chosen scores, with
+    ``renormalize`` over their sum, times ``scale``.
+    Returns ``(idx int32[tokens, k], weight float32[tokens, k])``; places that
+    no expert is left for hold -1 and 0.  ``load`` (int32 [experts]), if given,
+    grows by the tokens each expert was chosen for.  ``out`` may supply idx and
+    weight.
+    """
+    import torch
+
+    code, tokens, experts, stride, how = _router_logits(logits, score)
+    dev = logits.device
+    if bias is not None:
+        _check_out(bias, (experts,), torch.float32, dev, "bias")
+    if load is not None:
+        _check_out(load, (experts,), torch.int32, dev, "load")
+    if out is None:
+        out = (_empty((tokens, k), torch.int32, dev, stream), _empty((tokens, k), torch.float32, dev, stream))
+    else:
+        _check_out(out[0], (tokens, k), torch.int32, dev, "idx")
+        _check_out(out[1], (tokens, k), torch.float32, dev, "weight")
+    _check(_on_device(dev, tf_topk_route, logits.data_ptr(), code, tokens, experts, stride, k,
+                      None if bias is None else bias.data_ptr(), how, groups,
+                      groups if groups_kept is None else groups_kept, group_best, int(renormalize), scale,
+                      out[0].data_ptr(), out[1].data_ptr(), None if load is None else load.data_ptr(),
+                      _stream_handle(stream, dev)))
+    return out
+
+
+def route_experts_grad(logits, idx, grad_weight, *, score: str = "softmax", renormalize: bool = True,
+                       scale: float = 1.0, out=None, stream=None):
+    """Gradient of ``route_experts``'s weights for the logits, the choice held
+    fixed: ``idx`` int32 [tokens, k] as it returned it, ``grad_weight`` float32
+    [tokens, k], the other arguments as in its call.  Returns the gradient
+    [tokens, experts] in the logits' dtype (zero where nothing flows)."""
+    import torch
+
+    code, tokens, experts, stride, how = _router_logits(logits, score)
+    dev = logits.device
+    if idx.dim() != 2 or idx.shape[0] != tokens:
+        raise ValueError("idx must be [tokens, k]")
+    k = idx.shape[1]
+    _check_out(idx, (tokens, k), torch.int32, dev, "idx")
+    _check_out(grad_weight, (tokens, k), torch.float32, dev, "grad_weight")
+    if out is None:
+        out = _empty((tokens, experts), logits.dtype, dev, stream)
+    else:
+        _check_out(out, (tokens, experts), logits.dtype, dev, "out")
+    _check(_on_device(dev, tf_topk_route_grad, logits.data_ptr(), code, tokens, experts, stride, k, idx.data_ptr(),
+                      grad_weight.data_ptr(), how, int(renormalize), scale, out.data_ptr(),
+                      _stream_handle(stream, dev)))
     return out
 
 
