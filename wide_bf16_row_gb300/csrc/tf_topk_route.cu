@@ -46,12 +46,13 @@ constexpr int kRouteThreads = 32 * kRouteWarps;
 constexpr int kMaxExperts = TF_TOPK_ROUTE_MAX_EXPERTS;
 constexpr int kMaxRouteK = TF_TOPK_ROUTE_MAX_K;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-// Errors of the 32-bit scores, rounded up: a score is within 2e-6 of its
-// value (exp2 of a rounded product, a sum of at most kMaxExperts of them, a
-// reciprocal: under 8 * 2^-23 for a score of at most 1, with |x| s(1 - s) <=
-// 0.23 and |x| exp(-|x|) <= 0.37 bounding the share of the rounded exponent),
-// and adding the bias rounds by 2^-24 of the sum.
-constexpr float kScoreError = 2e-6f;
+template <int P> constexpr int kRouteCtas = P <= 8 ? 4 : P <= 16 ? 2 : 1; // CTAs an SM holds at a time
+// Errors of the 32-bit scores, rounded up: a score is within 4e-6 of its
+// value (exp2 of a rounded product, with |x| s(1 - s) <= 0.23 and |x| exp(-|x|)
+// <= 0.37 bounding the share of the rounded exponent; a sum of 32 lanes' at
+// most 32 terms, 36 * 2^-24; a reciprocal and a product, 4 * 2^-24), and
+// adding the bias rounds by 2^-24 of the sum.
+constexpr float kScoreError = 4e-6f;
 constexpr float kSumError = 1.2e-7f;
 
 static_assert(kMaxRouteK <= 32, "a lane per chosen expert");
@@ -61,6 +62,7 @@ struct RouteArgs {
     int64_t tokens, row_stride;
     int32_t experts, k, softmax, groups, kept, best, renorm;
     float scale;
+    bool vec; // rows are whole vectors (load_row)
     const float *bias;
     int32_t *idx;
     float *weight;
@@ -257,123 +259,252 @@ __device__ __noinline__ int choose_in_64_bits(const T *row, const RouteArgs &a)
     return chosen;
 }
 
-// The chosen scores of one row (lane i holds the i-th, or `on` false) divided
-// by their sum; where the scores themselves underflow, through their
-// logarithms.
-__device__ __forceinline__ float share_of(float s, float x, bool on, bool softmax)
+// Sum and maximum over the W lanes (a power of two) that hold one token.
+template <int W> __device__ __forceinline__ float lanes_sum(float v)
 {
-    if (softmax) { // exp(x_i) / sum over the chosen exp(x_j): the row's other experts cancel
-        const float top = warp_max(on ? x : -INFINITY);
-        const float q = on ? expf(x - top) : 0.0f;
-        const float total = warp_sum(q);
-        return on ? q / total : 0.0f;
-    }
-    const float total = warp_sum(on ? s : 0.0f);
-    if (total >= 1e-30f) return on ? s / total : 0.0f;
-    const float log_s = fminf(x, 0.0f) - log1pf(expf(-fabsf(x)));
-    const float top = warp_max(on ? log_s : -INFINITY);
-    const float q = on ? expf(log_s - top) : 0.0f;
-    const float sum = warp_sum(q);
-    return on ? q / sum : 0.0f;
+#pragma unroll
+    for (int d = W / 2; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+    return v;
+}
+template <int W> __device__ __forceinline__ float lanes_max(float v)
+{
+#pragma unroll
+    for (int d = W / 2; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+    return v;
 }
 
+// The chosen scores of a token (a lane each, or `on` false) divided by their
+// sum; where the scores themselves underflow, through their logarithms.
+template <int W> __device__ __forceinline__ float share_of(float s, float x, bool on, bool softmax)
+{
+    float log_s = x;
+    if (!softmax) {
+        const float total = lanes_sum<W>(on ? s : 0.0f);
+        if (__all_sync(kAll, total >= 1e-30f)) return on ? s / total : 0.0f;
+        log_s = fminf(x, 0.0f) - log1pf(expf(-fabsf(x)));
+    }
+    // softmax: the row's other experts cancel
+    const float top = lanes_max<W>(on ? log_s : -INFINITY);
+    const float q = on ? expf(log_s - top) : 0.0f;
+    const float total = lanes_sum<W>(q);
+    return on ? q / total : 0.0f;
+}
+
+// A lane's P logits of a row, its experts lane * P ..: -inf past the last
+// expert and for NaN, +inf as the largest finite float.  `vec`: rows and the
+// expert count are whole 16-byte (or, where a lane holds less, P-element)
+// vectors.
 template <typename T, int P>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(const T *__restrict__ logits, RouteArgs a)
+__device__ __forceinline__ void load_row(const T *row, int experts, int lane, bool vec, float (&x)[P])
+{
+    constexpr int kBytes = P * (int)sizeof(T) < 16 ? P * (int)sizeof(T) : 16;
+    constexpr int kEach = kBytes / (int)sizeof(T); // elements per vector
+    if (vec) {
+#pragma unroll
+        for (int v = 0; v < P / kEach; ++v) {
+            const int e = lane * P + v * kEach;
+            alignas(16) T part[kEach];
+            if (e < experts) {
+                if (kBytes == 16) *reinterpret_cast<uint4 *>(part) = *reinterpret_cast<const uint4 *>(row + e);
+                else if (kBytes == 8) *reinterpret_cast<uint2 *>(part) = *reinterpret_cast<const uint2 *>(row + e);
+                else if (kBytes == 4) *reinterpret_cast<uint32_t *>(part) = *reinterpret_cast<const uint32_t *>(row + e);
+                else *reinterpret_cast<uint16_t *>(part) = *reinterpret_cast<const uint16_t *>(row + e);
+            }
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) x[v * kEach + j] = e < experts ? load_logit(&part[j]) : -INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < P; ++j) x[j] = lane * P + j < experts ? load_logit(row + lane * P + j) : -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < P; ++j) x[j] = in_reach(x[j]) ? fminf(x[j], FLT_MAX) : -INFINITY;
+}
+
+// Largest and second largest (in that order) of two such pairs.
+__device__ __forceinline__ void join_best_two(float &m1, float &m2, float o1, float o2)
+{
+    m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+    m1 = fmaxf(m1, o1);
+}
+
+__device__ __forceinline__ float group_value(float m1, float m2, int best)
+{
+    return best > 1 && m2 > -INFINITY ? m1 + m2 : m1;
+}
+
+// One warp per token.  The choice: every lane's best one, the k-th largest of
+// those (k rounds of a warp maximum) bounds the k-th choice from below, so
+// the few experts at or above the bound (less the margin within which 32 bits
+// do not decide) are ranked against one another; more than 32 of them (heavy
+// ties) take the k + 1 best one by one.
+template <typename T, int P>
+__global__ void __launch_bounds__(kRouteThreads, kRouteCtas<P>) route_kernel(const T *__restrict__ logits, RouteArgs a)
 {
     __shared__ int32_t count[kMaxExperts];
+    __shared__ uint64_t found[kRouteWarps][32], sorted[kRouteWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (a.load) {
         for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) count[e] = 0;
         __syncthreads();
     }
     grid_dependency_wait();
-    for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.tokens; t += (int64_t)gridDim.x * kRouteWarps) {
-        const T *row = logits + t * a.row_stride;
-        float x[P], s[P];
-        float top = -INFINITY;
+    float bias[P];
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            const int e = lane * P + j;
-            x[j] = e < a.experts ? fminf(load_logit(row + e), FLT_MAX) : -INFINITY;
-            if (e < a.experts && isnan(load_logit(row + e))) x[j] = -INFINITY;
-            top = fmaxf(top, x[j]);
-        }
-        float total = 1.0f;
+    for (int j = 0; j < P; ++j) bias[j] = a.bias && lane * P + j < a.experts ? a.bias[lane * P + j] : 0.0f;
+    const int per = a.experts / a.groups;
+    // lanes that hold one group, when whole lanes do and their count is a power of two
+    const int group_lanes = per % P == 0 && ((per / P) & (per / P - 1)) == 0 ? per / P : 0;
+    const int64_t step = (int64_t)gridDim.x * kRouteWarps;
+    int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+    float next[P];
+    if (t < a.tokens) load_row<T, P>(logits + t * a.row_stride, a.experts, lane, a.vec, next);
+    for (; t < a.tokens; t += step) {
+        const T *row = logits + t * a.row_stride;
+        float x[P], c[P]; // logits, choices
+#pragma unroll
+        for (int j = 0; j < P; ++j) x[j] = next[j];
+        if (t + step < a.tokens) load_row<T, P>(logits + (t + step) * a.row_stride, a.experts, lane, a.vec, next);
+        float top = 0.0f, total = 1.0f;
         if (a.softmax) {
-            top = warp_max(top);
-            float sum = 0.0f;
+            float m = x[0], sum = 0.0f;
+#pragma unroll
+            for (int j = 1; j < P; ++j) m = fmaxf(m, x[j]);
+            top = fmaxf(warp_max(m), -FLT_MAX); // finite: exp(-inf - top) is 0
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                s[j] = in_reach(x[j]) ? __expf(x[j] - top) : 0.0f;
-                sum += s[j];
+                c[j] = __expf(x[j] - top);
+                sum += c[j];
             }
             total = warp_sum(sum);
+            const float inverse = __fdividef(1.0f, total);
 #pragma unroll
-            for (int j = 0; j < P; ++j) s[j] = s[j] / total;
+            for (int j = 0; j < P; ++j) c[j] *= inverse;
         } else {
 #pragma unroll
-            for (int j = 0; j < P; ++j) s[j] = __frcp_rn(1.0f + __expf(-x[j]));
+            for (int j = 0; j < P; ++j) c[j] = __fdividef(1.0f, 1.0f + __expf(-x[j]));
         }
-        // the order that decides: the biased scores, or the logits alone
-        uint32_t key[P];
-        float c[P];
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-            c[j] = s[j] + (a.bias && in_reach(x[j]) ? a.bias[lane * P + j] : 0.0f);
-            const float v = a.bias ? c[j] : x[j];
-            key[j] = in_reach(x[j]) && c[j] > -INFINITY ? order_key(v) : 0u;
+            c[j] += bias[j];
+            if (!(x[j] > -INFINITY && c[j] > -INFINITY)) x[j] = c[j] = -INFINITY;
         }
         bool again = false; // too close to call in 32 bits
-        if (a.groups > 1) {
-            const int per = a.experts / a.groups;
+        if (a.groups > 1 && group_lanes) {
+            float m1 = c[0], m2 = -INFINITY;
+#pragma unroll
+            for (int j = 1; j < P; ++j) join_best_two(m1, m2, c[j], -INFINITY);
+            for (int d = 1; d < group_lanes; d <<= 1)
+                join_best_two(m1, m2, __shfl_xor_sync(kAll, m1, d), __shfl_xor_sync(kAll, m2, d));
+            const float v = group_value(m1, m2, a.best);
+            int rank = 0;
+            const int mine = lane / group_lanes;
+            for (int g = 0; g < a.groups; ++g) {
+                const float o = __shfl_sync(kAll, v, g * group_lanes);
+                rank += o > v || (o == v && g < mine);
+            }
+            const bool on = mine < a.groups;
+            const uint32_t edge = __ballot_sync(kAll, on && rank == a.kept - 1), past = __ballot_sync(kAll, on && rank == a.kept);
+            const float last = __shfl_sync(kAll, v, __ffs(edge) - 1), cut = __shfl_sync(kAll, v, __ffs(past) - 1);
+            const float size = fabsf(m1) + (m2 > -INFINITY ? fabsf(m2) : 0.0f);
+            const float most = __uint_as_float(__reduce_max_sync(kAll, on && m1 > -INFINITY ? __float_as_uint(size) : 0u));
+            // two scores, their biases and their sum on either side of the cut
+            if (cut > -INFINITY) again = !(last - cut > 4.0f * kScoreError + 4.0f * kSumError * most);
+            if (!on || rank >= a.kept)
+#pragma unroll
+                for (int j = 0; j < P; ++j) x[j] = c[j] = -INFINITY;
+        } else if (a.groups > 1) {
             uint32_t mine = 0;
-            float size = 0.0f; // of the largest terms added up
+            float most = 0.0f;
             for (int g = 0; g < a.groups; ++g) {
                 uint32_t members[P];
 #pragma unroll
                 for (int j = 0; j < P; ++j)
-                    members[j] = key[j] && (lane * P + j) / per == g ? order_key(c[j]) : 0u;
+                    members[j] = c[j] > -INFINITY && (lane * P + j) / per == g ? order_key(c[j]) : 0u;
                 int e;
                 const uint32_t first = take_best<P>(members, lane, e);
                 const uint32_t second = a.best > 1 && first ? take_best<P>(members, lane, e) : 0u;
                 const float u = first ? key_value(first) : 0.0f, w = second ? key_value(second) : 0.0f;
                 if (lane == g) mine = first ? order_key(u + w) : 0u;
-                size = fmaxf(size, fabsf(u) + fabsf(w));
+                most = fmaxf(most, fabsf(u) + fabsf(w));
             }
             uint32_t last, cut;
             const uint32_t keep = best_groups<uint32_t>(mine, a.groups, a.kept, lane, last, cut);
-            // two scores, their biases and their sum on either side of the cut
-            if (cut) again = !(key_value(last) - key_value(cut) > 4.0f * kScoreError + 4.0f * kSumError * size);
+            if (cut) again = !(key_value(last) - key_value(cut) > 4.0f * kScoreError + 4.0f * kSumError * most);
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 const int e = lane * P + j;
-                if (e < a.experts && !((keep >> (e / per)) & 1u)) key[j] = 0;
+                if (e < a.experts && !((keep >> (e / per)) & 1u)) x[j] = c[j] = -INFINITY;
             }
         }
-        int chosen = -1;
-        float value = 0.0f;
+        if (!a.bias) // the order is that of the logits, exactly
+#pragma unroll
+            for (int j = 0; j < P; ++j) c[j] = x[j];
+        // the bound: the k-th largest of the lanes' best
+        float m = c[0];
+#pragma unroll
+        for (int j = 1; j < P; ++j) m = fmaxf(m, c[j]);
+        uint32_t left = m > -INFINITY ? order_key(m) : 0u, bound = 0;
         for (int i = 0; i < a.k; ++i) {
-            int e;
-            const uint32_t best = take_best<P>(key, lane, e);
-            if (best == 0) break;
-            if (lane == i) {
-                chosen = e;
-                value = key_value(best);
+            bound = __reduce_max_sync(kAll, left);
+            if (bound == 0) break;
+            const uint32_t ties = __ballot_sync(kAll, left == bound);
+            if (lane == __ffs(ties) - 1) left = 0;
+        }
+        float least = bound ? key_value(bound) : -FLT_MAX;
+        if (bound && a.bias && fabsf(least) < INFINITY)
+            least -= 2.1f * kScoreError + 3.0f * kSumError * fabsf(least);
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const bool in = c[j] >= least;
+            const uint32_t mask = __ballot_sync(kAll, in);
+            const int at = n + __popc(mask & ((1u << lane) - 1u));
+            if (in && at < 32) found[warp][at] = ((uint64_t)order_key(c[j]) << 32) | (uint32_t)~(lane * P + j);
+            n += __popc(mask);
+        }
+        int chosen = -1, after = -1; // this place's expert and the one behind it
+        float value = 0.0f, after_value = 0.0f;
+        if (n <= 32) {
+            __syncwarp();
+            const uint64_t mine = lane < n ? found[warp][lane] : 0ull;
+            int rank = 0;
+            for (int i = 0; i < n; ++i) rank += found[warp][i] > mine;
+            if (lane < n) sorted[warp][rank] = mine;
+            __syncwarp();
+            if (lane < n) {
+                const uint64_t best = sorted[warp][lane];
+                chosen = (int)~(uint32_t)best;
+                value = key_value((uint32_t)(best >> 32));
+            }
+            if (lane + 1 < n) {
+                const uint64_t best = sorted[warp][lane + 1];
+                after = (int)~(uint32_t)best;
+                after_value = key_value((uint32_t)(best >> 32));
+            }
+        } else {
+            uint32_t key[P];
+#pragma unroll
+            for (int j = 0; j < P; ++j) key[j] = c[j] > -INFINITY ? order_key(c[j]) : 0u;
+            for (int i = 0; i <= a.k; ++i) {
+                int e;
+                const uint32_t best = take_best<P>(key, lane, e);
+                if (lane == i) {
+                    chosen = e;
+                    value = key_value(best);
+                }
+                if (lane == i - 1) {
+                    after = e;
+                    after_value = key_value(best);
+                }
+                if (best == 0) break;
             }
         }
         if (a.bias) {
-            int past; // the neighbour past the cut
-            const float past_value = key_value(take_best<P>(key, lane, past));
-            int en = __shfl_down_sync(kAll, chosen, 1);
-            float vn = __shfl_down_sync(kAll, value, 1);
-            if (lane == a.k - 1) {
-                en = past;
-                vn = past_value;
-            }
             bool close = false;
-            if (lane < a.k && chosen >= 0 && en >= 0 &&
-                !(value - vn > 2.0f * kScoreError + kSumError * (fabsf(value) + fabsf(vn))))
-                close = load_logit(row + chosen) != load_logit(row + en) || a.bias[chosen] != a.bias[en];
+            if (lane < a.k && chosen >= 0 && after >= 0 &&
+                !(value - after_value > 2.0f * kScoreError + kSumError * (fabsf(value) + fabsf(after_value))))
+                close = load_logit(row + chosen) != load_logit(row + after) || a.bias[chosen] != a.bias[after];
             again = again || __any_sync(kAll, close);
         }
         if (again) chosen = choose_in_64_bits<T, P>(row, a);
@@ -381,12 +512,13 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const T *__restric
         const bool on = lane < a.k && chosen >= 0;
         const float xi = on ? fminf(load_logit(row + chosen), FLT_MAX) : 0.0f;
         const float si = !on ? 0.0f : a.softmax ? expf(xi - top) / total : 1.0f / (1.0f + expf(-xi));
-        const float w = a.renorm ? share_of(si, xi, on, a.softmax != 0) : si;
+        const float w = a.renorm ? share_of<32>(si, xi, on, a.softmax != 0) : si;
         if (lane < a.k) {
             a.idx[t * a.k + lane] = on ? chosen : -1;
             a.weight[t * a.k + lane] = on ? w * a.scale : 0.0f;
         }
         if (a.load && on) atomicAdd(&count[chosen], 1);
+        __syncwarp(); // the lists are read before the next token's are written
     }
     grid_dependents_go();
     if (a.load) {
@@ -400,6 +532,7 @@ struct RouteGradArgs {
     int64_t tokens, row_stride;
     int32_t experts, k, softmax, renorm;
     float scale;
+    bool vec, vec_row; // the gradient's and the logits' rows are whole vectors
     const int32_t *idx;
     const float *grad;
 };
@@ -408,75 +541,137 @@ __device__ __forceinline__ void store_grad(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_grad(__half *p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void store_grad(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Gradient of the weights for the logits, one warp per token:
+// A lane's P values of a row (as load_row holds them).
+template <typename T, int P>
+__device__ __forceinline__ void store_row(T *row, int experts, int lane, bool vec, const float (&x)[P])
+{
+    constexpr int kBytes = P * (int)sizeof(T) < 16 ? P * (int)sizeof(T) : 16;
+    constexpr int kEach = kBytes / (int)sizeof(T);
+    if (vec) {
+#pragma unroll
+        for (int v = 0; v < P / kEach; ++v) {
+            const int e = lane * P + v * kEach;
+            alignas(16) T part[kEach];
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) store_grad(&part[j], x[v * kEach + j]);
+            if (e < experts) {
+                if (kBytes == 16) *reinterpret_cast<uint4 *>(row + e) = *reinterpret_cast<const uint4 *>(part);
+                else if (kBytes == 8) *reinterpret_cast<uint2 *>(row + e) = *reinterpret_cast<const uint2 *>(part);
+                else if (kBytes == 4) *reinterpret_cast<uint32_t *>(row + e) = *reinterpret_cast<const uint32_t *>(part);
+                else *reinterpret_cast<uint16_t *>(row + e) = *reinterpret_cast<const uint16_t *>(part);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+            if (lane * P + j < experts) store_grad(row + lane * P + j, x[j]);
+    }
+}
+
+// An expert named twice for a token (a list this library never writes) adds
+// up, in the lanes' order, in its first lane; false in the others.
+template <int W> __device__ __forceinline__ bool add_twins(float &d, bool on, int expert, int k)
+{
+    const int lane = threadIdx.x & 31, first = lane & ~(W - 1);
+    const uint32_t twins = __match_any_sync(kAll, on ? first * kMaxExperts + expert : -1 - lane);
+    if (__any_sync(kAll, (twins & (twins - 1)) != 0)) {
+        float sum = 0.0f;
+        for (int i = 0; i < k; ++i) {
+            const float o = __shfl_sync(kAll, d, first + i);
+            if ((twins >> (first + i)) & 1u) sum += o;
+        }
+        d = sum;
+    }
+    return on && lane == __ffs(twins) - 1;
+}
+
+// Gradient of the weights for the logits:
 //   per chosen score  g_i = scale * dw_i, renormalised: (g_i - sum_j g_j r_j) / S
 //                     with r_j = s_j / S, S the chosen scores' sum;
 //   sigmoid  dx_i = g_i s_i (1 - s_i), others 0;
 //   softmax  dx_e = s_e (g_e - sum_j g_j s_j), g_e = 0 for the others -- and
 //            with renormalised weights that sum is 0, so only the chosen
-//            experts' logits are read.
-template <typename T>
+//            experts' logits count.
+// This kernel: all but the plain softmax.  W lanes per token, 32 / W tokens
+// per warp; their rows are cleared, then the chosen experts' values stored.
+template <typename T, int W>
 __global__ void __launch_bounds__(kRouteThreads)
 route_grad_kernel(const T *__restrict__ logits, T *__restrict__ out, RouteGradArgs a)
+{
+    constexpr int kTokens = 32 / W;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, place = lane & (W - 1);
+    grid_dependency_wait();
+    const int64_t step = (int64_t)gridDim.x * kRouteWarps * kTokens;
+    for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWarps + warp) * kTokens; t0 < a.tokens; t0 += step) {
+        const int64_t t = t0 + lane / W;
+        const int64_t cells = (a.tokens - t0 < kTokens ? a.tokens - t0 : kTokens) * a.experts;
+        T *rows = out + t0 * a.experts;
+        if (a.vec) {
+            uint4 *v = reinterpret_cast<uint4 *>(rows);
+            for (int i = lane; i < (int)(cells * (int)sizeof(T) / 16); i += 32) v[i] = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int i = lane; i < (int)cells; i += 32) store_grad(rows + i, 0.0f);
+        }
+        const bool mine = place < a.k && t < a.tokens;
+        const int e = mine ? a.idx[t * a.k + place] : -1;
+        const float g_in = mine ? a.grad[t * a.k + place] : 0.0f;
+        float x = e >= 0 && e < a.experts ? load_logit(logits + t * a.row_stride + e) : -INFINITY;
+        const bool on = in_reach(x);
+        x = fminf(x, FLT_MAX);
+        const float g = on ? a.scale * g_in : 0.0f;
+        const float below = on && !a.softmax ? 1.0f / (1.0f + expf(x)) : 1.0f; // 1 - s
+        const float s = on && !a.softmax ? 1.0f / (1.0f + expf(-x)) : 0.0f;
+        float d;
+        if (a.renorm) {
+            const float r = share_of<W>(s, x, on, a.softmax != 0);
+            const float dot = lanes_sum<W>(on ? g * r : 0.0f);
+            d = on ? r * (g - dot) * below : 0.0f;
+        } else {
+            d = g * below * s;
+        }
+        __syncwarp(); // the rows are cleared
+        if (add_twins<W>(d, on, e, a.k)) store_grad(out + t * a.experts + e, d);
+    }
+    grid_dependents_go();
+}
+
+// The plain softmax (no renormalising): every expert within reach has a
+// gradient.  One warp per token, the row's exponentials in registers.
+template <typename T, int P>
+__global__ void __launch_bounds__(kRouteThreads)
+route_softmax_grad_kernel(const T *__restrict__ logits, T *__restrict__ out, RouteGradArgs a)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
     for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.tokens; t += (int64_t)gridDim.x * kRouteWarps) {
         const T *row = logits + t * a.row_stride;
         T *dst = out + t * a.experts;
-        int e = lane < a.k ? a.idx[t * a.k + lane] : -1;
-        float x = e >= 0 && e < a.experts ? load_logit(row + e) : -INFINITY;
+        const int e = lane < a.k ? a.idx[t * a.k + lane] : -1;
+        const float g_in = lane < a.k ? a.grad[t * a.k + lane] : 0.0f;
+        float s[P];
+        load_row<T, P>(row, a.experts, lane, a.vec_row, s);
+        float top = s[0], sum = 0.0f;
+#pragma unroll
+        for (int j = 1; j < P; ++j) top = fmaxf(top, s[j]);
+        top = fmaxf(warp_max(top), -FLT_MAX);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            s[j] = expf(s[j] - top);
+            sum += s[j];
+        }
+        const float total = fmaxf(warp_sum(sum), FLT_MIN); // no expert within reach: all 0
+        const float x = e >= 0 && e < a.experts ? load_logit(row + e) : -INFINITY;
         const bool on = in_reach(x);
-        x = fminf(x, FLT_MAX);
-        float g = on ? a.scale * a.grad[t * a.k + lane] : 0.0f;
-        float d; // the chosen expert's gradient
-        const float below = on && !a.softmax ? 1.0f / (1.0f + expf(x)) : 1.0f; // 1 - s
-        float dot = 0.0f, top = 0.0f, total = 1.0f;
-        if (a.renorm) {
-            const float s = on && !a.softmax ? 1.0f / (1.0f + expf(-x)) : 0.0f;
-            const float r = share_of(s, x, on, a.softmax != 0);
-            dot = warp_sum(on ? g * r : 0.0f);
-            d = r * (g - dot) * below;
-        } else if (!a.softmax) {
-            d = on ? g * below / (1.0f + expf(-x)) : 0.0f;
-        } else {
-            float m = -INFINITY;
-            for (int i = lane; i < a.experts; i += 32) {
-                const float y = load_logit(row + i);
-                if (in_reach(y)) m = fmaxf(m, fminf(y, FLT_MAX));
-            }
-            top = warp_max(m);
-            float sum = 0.0f;
-            for (int i = lane; i < a.experts; i += 32) {
-                const float y = load_logit(row + i);
-                if (in_reach(y)) sum += expf(fminf(y, FLT_MAX) - top);
-            }
-            total = warp_sum(sum);
-            const float s = on ? expf(x - top) / total : 0.0f;
-            dot = warp_sum(on ? g * s : 0.0f);
-            d = on ? s * (g - dot) : 0.0f;
-        }
-        if (a.softmax && !a.renorm) {
-            for (int i = lane; i < a.experts; i += 32) {
-                const float y = load_logit(row + i);
-                store_grad(dst + i, in_reach(y) ? -dot * (expf(fminf(y, FLT_MAX) - top) / total) : 0.0f);
-            }
-        } else {
-            for (int i = lane; i < a.experts; i += 32) store_grad(dst + i, 0.0f);
-        }
-        __syncwarp(); // the chosen experts' values replace those of the pass above
-        // an expert named twice (a list this library never writes) adds up
-        const uint32_t twins = __match_any_sync(kAll, on ? e : -1 - lane);
-        if (__any_sync(kAll, on && (twins & (twins - 1)) != 0)) {
-            const float extra = a.softmax && !a.renorm && on ? -dot * (expf(x - top) / total) : 0.0f;
-            float sum = 0.0f; // each twin's own part, the shared part once
-            for (int i = 0; i < a.k; ++i) {
-                const float o = __shfl_sync(kAll, d - extra, i);
-                if ((twins >> i) & 1u) sum += o;
-            }
-            d = sum + extra;
-        }
-        if (on && lane == __ffs(twins) - 1) store_grad(dst + e, d);
+        const float own = on ? expf(fminf(x, FLT_MAX) - top) / total : 0.0f;
+        const float g = on ? a.scale * g_in : 0.0f;
+        const float dot = warp_sum(g * own);
+#pragma unroll
+        for (int j = 0; j < P; ++j) s[j] = -dot * (s[j] / total);
+        store_row<T, P>(dst, a.experts, lane, a.vec, s);
+        __syncwarp(); // the chosen experts' values replace the row's
+        float d = g;
+        const bool first = add_twins<32>(d, on, e, a.k);
+        if (first) store_grad(dst + e, own * (d - dot));
     }
     grid_dependents_go();
 }
@@ -496,10 +691,11 @@ template <typename T> RouteKernel<T> route_kernel_for(int experts)
                        : route_kernel<T, 32>;
 }
 
-int64_t route_grid(int64_t tokens, int sm_count)
+// CTAs for a warp per token (or group of tokens), `each` per SM at most.
+int64_t route_grid(int64_t warps, int sm_count, int each)
 {
-    const int64_t need = (tokens + kRouteWarps - 1) / kRouteWarps;
-    const int64_t most = (int64_t)sm_count * 8;
+    const int64_t need = (warps + kRouteWarps - 1) / kRouteWarps;
+    const int64_t most = (int64_t)sm_count * each;
     return need < most ? need : most;
 }
 
@@ -516,19 +712,57 @@ cudaLaunchConfig_t route_config(int64_t grid, cudaStream_t stream, cudaLaunchAtt
     return cfg;
 }
 
-template <typename T> cudaError_t launch_route(const void *logits, const RouteArgs &a, int sm_count, void *stream)
+// Whether a lane's experts can be read as whole vectors.
+bool whole_vectors(const void *logits, size_t size, int experts, int64_t row_stride)
 {
+    int per = 1;
+    while (32 * per < experts) per *= 2;
+    const size_t bytes = per * size < 16 ? per * size : 16;
+    return (reinterpret_cast<uintptr_t>(logits) & (bytes - 1)) == 0 && experts * size % bytes == 0 &&
+           (size_t)row_stride * size % bytes == 0;
+}
+
+template <typename T> cudaError_t launch_route(const void *logits, RouteArgs a, int sm_count, void *stream)
+{
+    a.vec = whole_vectors(logits, sizeof(T), a.experts, a.row_stride);
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = route_config(route_grid(a.tokens, sm_count), static_cast<cudaStream_t>(stream), attr);
+    const int each = a.experts <= 256 ? kRouteCtas<8> : a.experts <= 512 ? kRouteCtas<16> : kRouteCtas<32>;
+    const cudaLaunchConfig_t cfg =
+        route_config(route_grid(a.tokens, sm_count, each), static_cast<cudaStream_t>(stream), attr);
     return cudaLaunchKernelEx(&cfg, route_kernel_for<T>(a.experts), static_cast<const T *>(logits), a);
 }
 
-template <typename T>
-cudaError_t launch_route_grad(const void *logits, void *out, const RouteGradArgs &a, int sm_count, void *stream)
+template <typename T> using RouteGradKernel = void (*)(const T *, T *, RouteGradArgs);
+
+template <typename T> RouteGradKernel<T> softmax_grad_kernel_for(int experts)
 {
+    const int per = (experts + 31) / 32;
+    return per <= 1 ? route_softmax_grad_kernel<T, 1>
+           : per <= 2 ? route_softmax_grad_kernel<T, 2>
+           : per <= 4 ? route_softmax_grad_kernel<T, 4>
+           : per <= 8 ? route_softmax_grad_kernel<T, 8>
+           : per <= 16 ? route_softmax_grad_kernel<T, 16>
+                       : route_softmax_grad_kernel<T, 32>;
+}
+
+template <typename T>
+cudaError_t launch_route_grad(const void *logits, void *out, RouteGradArgs a, int sm_count, void *stream)
+{
+    RouteGradKernel<T> kernel;
+    int tokens_per_warp = 1;
+    if (a.softmax && !a.renorm) {
+        a.vec = whole_vectors(out, sizeof(T), a.experts, a.experts);
+        a.vec_row = whole_vectors(logits, sizeof(T), a.experts, a.row_stride);
+        kernel = softmax_grad_kernel_for<T>(a.experts);
+    } else {
+        a.vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && a.experts * sizeof(T) % 16 == 0;
+        kernel = a.k <= 8 ? route_grad_kernel<T, 8> : a.k <= 16 ? route_grad_kernel<T, 16> : route_grad_kernel<T, 32>;
+        tokens_per_warp = a.k <= 8 ? 4 : a.k <= 16 ? 2 : 1;
+    }
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = route_config(route_grid(a.tokens, sm_count), static_cast<cudaStream_t>(stream), attr);
-    return cudaLaunchKernelEx(&cfg, route_grad_kernel<T>, static_cast<const T *>(logits), static_cast<T *>(out), a);
+    const int64_t warps = (a.tokens + tokens_per_warp - 1) / tokens_per_warp;
+    const cudaLaunchConfig_t cfg = route_config(route_grid(warps, sm_count, 8), static_cast<cudaStream_t>(stream), attr);
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<const T *>(logits), static_cast<T *>(out), a);
 }
 
 bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
