@@ -47,12 +47,14 @@ constexpr int kMaxExperts = TF_TOPK_ROUTE_MAX_EXPERTS;
 constexpr int kMaxRouteK = TF_TOPK_ROUTE_MAX_K;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 template <int P> constexpr int kRouteCtas = P <= 8 ? 4 : P <= 16 ? 2 : 1; // CTAs an SM holds at a time
-// Errors of the 32-bit scores, rounded up: a score is within 4e-6 of its
-// value (exp2 of a rounded product, with |x| s(1 - s) <= 0.23 and |x| exp(-|x|)
-// <= 0.37 bounding the share of the rounded exponent; a sum of 32 lanes' at
-// most 32 terms, 36 * 2^-24; a reciprocal and a product, 4 * 2^-24), and
-// adding the bias rounds by 2^-24 of the sum.
-constexpr float kScoreError = 4e-6f;
+// Errors of the 32-bit scores, rounded up (u = 2^-24).  Sigmoid: exp2 of a
+// rounded product, |x| s(1 - s) <= 0.23 bounding the share of the rounded
+// exponent and s(1 - s) <= 1/4 that of exp2's 2 ulp; a sum and a reciprocal
+// of at most 1: under 6 u.  Softmax: |x| exp(-|x|) <= 0.37, a sum of 32 lanes'
+// at most 32 terms (36 u), a reciprocal, a product: under 45 u.  Adding the
+// bias rounds by u of the sum.
+constexpr float kSigmoidError = 5e-7f;
+constexpr float kSoftmaxError = 4e-6f;
 constexpr float kSumError = 1.2e-7f;
 
 static_assert(kMaxRouteK <= 32, "a lane per chosen expert");
@@ -280,14 +282,14 @@ template <int W> __device__ __forceinline__ float share_of(float s, float x, boo
     float log_s = x;
     if (!softmax) {
         const float total = lanes_sum<W>(on ? s : 0.0f);
-        if (__all_sync(kAll, total >= 1e-30f)) return on ? s / total : 0.0f;
+        if (__all_sync(kAll, total >= 1e-30f)) return on ? __fdividef(s, total) : 0.0f;
         log_s = fminf(x, 0.0f) - log1pf(expf(-fabsf(x)));
     }
     // softmax: the row's other experts cancel
     const float top = lanes_max<W>(on ? log_s : -INFINITY);
-    const float q = on ? expf(log_s - top) : 0.0f;
+    const float q = on ? __expf(log_s - top) : 0.0f;
     const float total = lanes_sum<W>(q);
-    return on ? q / total : 0.0f;
+    return on ? __fdividef(q, total) : 0.0f;
 }
 
 // A lane's P logits of a row, its experts lane * P ..: -inf past the last
@@ -333,192 +335,324 @@ __device__ __forceinline__ float group_value(float m1, float m2, int best)
     return best > 1 && m2 > -INFINITY ? m1 + m2 : m1;
 }
 
-// One warp per token.  The choice: every lane's best one, the k-th largest of
-// those (k rounds of a warp maximum) bounds the k-th choice from below, so
-// the few experts at or above the bound (less the margin within which 32 bits
-// do not decide) are ranked against one another; more than 32 of them (heavy
-// ties) take the k + 1 best one by one.
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float reciprocal_fast(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float sigmoid_fast(float x) { return reciprocal_fast(1.0f + exp2_fast(-kLog2e * x)); }
+
+// Short keys: an order key whose low bits give way to the expert (lower
+// experts larger), so that a warp maximum names the choice and its expert at
+// once, and no two are equal.  What the cut bits held decides later, where
+// two neighbours come close.
+template <int P> struct ShortKey {
+    static constexpr uint32_t kMask = 32 * P - 1;
+    // the part of a value that the cut bits may hold
+    static constexpr float kCut = (float)(32 * P) / (float)(1 << 23);
+    __device__ static uint32_t make(float v, int expert) { return (order_key(v) & ~kMask) | (kMask - expert); }
+    __device__ static float value(uint32_t key) { return key_value(key & ~kMask); }
+    __device__ static int expert(uint32_t key) { return (int)(kMask - (key & kMask)); }
+};
+
+__device__ __forceinline__ void order_pair(uint32_t &a, uint32_t &b)
+{
+    const uint32_t hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+
+// A lane's D largest keys in descending order (D = P up to 4).
+template <int P> struct LaneList {
+    static constexpr int D = P < 4 ? P : 4;
+    uint32_t at[D];
+
+    __device__ static void sort4(uint32_t (&k)[4])
+    {
+        order_pair(k[0], k[1]);
+        order_pair(k[2], k[3]);
+        order_pair(k[0], k[2]);
+        order_pair(k[1], k[3]);
+        order_pair(k[1], k[2]);
+    }
+    __device__ explicit LaneList(const uint32_t (&key)[P])
+    {
+#pragma unroll
+        for (int i = 0; i < D; ++i) at[i] = key[i];
+        if constexpr (P == 2) order_pair(at[0], at[1]);
+        if constexpr (P >= 4) sort4(at);
+#pragma unroll
+        for (int b = 4; b + 3 < P; b += 4) {
+            uint32_t o[4] = {key[b], key[b + 1], key[b + 2], key[b + 3]};
+            sort4(o);
+            // the four largest of two descending fours: bitonic, then sorted
+#pragma unroll
+            for (int i = 0; i < 4; ++i) at[i] = max(at[i], o[3 - i]);
+            order_pair(at[0], at[2]);
+            order_pair(at[1], at[3]);
+            order_pair(at[0], at[1]);
+            order_pair(at[2], at[3]);
+        }
+    }
+    // The warp's largest key, taken out of its lane's list.
+    __device__ uint32_t take(const uint32_t (&key)[P])
+    {
+        const uint32_t best = __reduce_max_sync(kAll, at[0]);
+        if (at[0] == best) {
+#pragma unroll
+            for (int i = 0; i + 1 < D; ++i) at[i] = at[i + 1];
+            at[D - 1] = 0;
+            if (D < P && at[0] == 0) // the list ran out: the next one of the lane
+#pragma unroll
+                for (int j = 0; j < P; ++j)
+                    if (key[j] < best) at[0] = max(at[0], key[j]);
+        }
+        return best;
+    }
+};
+
+// The k best experts of a row by the logits alone, from whole keys.
+template <typename T, int P>
+__device__ __noinline__ int choose_by_logits(const T *row, const RouteArgs &a)
+{
+    const int lane = threadIdx.x & 31;
+    float x[P];
+    load_row<T, P>(row, a.experts, lane, a.vec, x);
+    uint32_t key[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) key[j] = x[j] > -INFINITY ? order_key(x[j]) : 0u;
+    int chosen = -1;
+    for (int i = 0; i < a.k; ++i) {
+        int e;
+        if (take_best<P>(key, lane, e) == 0) break;
+        if (lane == i) chosen = e;
+    }
+    return chosen;
+}
+
+// The order of up to 32 experts, one per lane (lanes < n), that short keys
+// could not settle: by the logits, or with a bias by the choices, in 64 bits
+// where 32 leave neighbours closer than their error.  `c` is the lane's choice
+// in 32 bits.  Lane i gets the i-th.
+template <typename T, int P>
+__device__ __noinline__ int settle(const T *row, const RouteArgs &a, int expert, float c, int n, int *place)
+{
+    const int lane = threadIdx.x & 31;
+    const bool mine = lane < n;
+    int rank = 0;
+    bool close = false;
+    const float error = 2.0f * (a.softmax ? kSoftmaxError : kSigmoidError);
+    for (int i = 0; i < n; ++i) {
+        const float o = __shfl_sync(kAll, c, i);
+        const int oe = __shfl_sync(kAll, expert, i);
+        rank += o > c || (o == c && oe < expert);
+        close |= mine && oe != expert && !(fabsf(o - c) > error + kSumError * (fabsf(o) + fabsf(c)));
+    }
+    if (a.bias && __any_sync(kAll, close)) {
+        const float x = mine ? fminf(load_logit(row + expert), FLT_MAX) : 0.0f;
+        double d;
+        if (a.softmax) {
+            float y[P];
+            load_row<T, P>(row, a.experts, lane, a.vec, y);
+            float top = y[0];
+#pragma unroll
+            for (int j = 1; j < P; ++j) top = fmaxf(top, y[j]);
+            top = warp_max(top);
+            double sum = 0;
+#pragma unroll 1
+            for (int j = 0; j < P; ++j) {
+                const int e = lane * P + j;
+                const float z = e < a.experts ? load_logit(row + e) : -INFINITY;
+                if (in_reach(z)) sum += exp((double)fminf(z, FLT_MAX) - top);
+            }
+            sum = warp_sum64(sum);
+            d = exp((double)x - top) / sum;
+        } else {
+            d = 1.0 / (1.0 + exp(-(double)x));
+        }
+        if (mine) d += (double)a.bias[expert];
+        rank = 0;
+        for (int i = 0; i < n; ++i) {
+            const double o = __shfl_sync(kAll, d, i);
+            const int oe = __shfl_sync(kAll, expert, i);
+            rank += o > d || (o == d && oe < expert);
+        }
+    }
+    if (mine) place[rank] = expert;
+    __syncwarp();
+    const int chosen = mine ? place[lane] : -1;
+    __syncwarp();
+    return chosen;
+}
+
+// One warp per token.  A lane sorts its best few experts' short keys; k warp
+// maxima over the lanes' best then name the choices in order.  It is bound by
+// the instructions of the scan over E logits (two special-function ones per
+// sigmoid) and of the k rounds, not by the row's bytes.
 template <typename T, int P>
 __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<P>) route_kernel(const T *__restrict__ logits, RouteArgs a)
 {
     __shared__ int32_t count[kMaxExperts];
-    __shared__ uint64_t found[kRouteWarps][32], sorted[kRouteWarps][32];
+    __shared__ int32_t place[kRouteWarps][32];
+    using Key = ShortKey<P>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (a.load) {
         for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) count[e] = 0;
         __syncthreads();
     }
     grid_dependency_wait();
-    float bias[P];
+    float bias[P]; // -inf where no choice can come of it
 #pragma unroll
-    for (int j = 0; j < P; ++j) bias[j] = a.bias && lane * P + j < a.experts ? a.bias[lane * P + j] : 0.0f;
+    for (int j = 0; j < P; ++j) {
+        bias[j] = a.bias && lane * P + j < a.experts ? a.bias[lane * P + j] : 0.0f;
+        bias[j] = bias[j] > -INFINITY ? bias[j] : -INFINITY;
+    }
     const int per = a.experts / a.groups;
     // lanes that hold one group, when whole lanes do and their count is a power of two
     const int group_lanes = per % P == 0 && ((per / P) & (per / P - 1)) == 0 ? per / P : 0;
+    const bool scored = a.bias || a.groups > 1; // else the logits alone decide
+    // errors of a choice: of the score, and relative to the sum with the bias
+    const float error = !scored ? 0.0f : a.softmax ? kSoftmaxError : kSigmoidError;
+    const float part = scored ? kSumError + 2.0f * Key::kCut : 0.0f;
     const int64_t step = (int64_t)gridDim.x * kRouteWarps;
     int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
     float next[P];
     if (t < a.tokens) load_row<T, P>(logits + t * a.row_stride, a.experts, lane, a.vec, next);
     for (; t < a.tokens; t += step) {
         const T *row = logits + t * a.row_stride;
-        float x[P], c[P]; // logits, choices
+        float c[P];
 #pragma unroll
-        for (int j = 0; j < P; ++j) x[j] = next[j];
+        for (int j = 0; j < P; ++j) c[j] = next[j];
         if (t + step < a.tokens) load_row<T, P>(logits + (t + step) * a.row_stride, a.experts, lane, a.vec, next);
-        float top = 0.0f, total = 1.0f;
-        if (a.softmax) {
-            float m = x[0], sum = 0.0f;
+        float top = 0.0f, inverse = 1.0f;
+        if (a.softmax && (scored || !a.renorm)) {
+            float m = c[0], sum = 0.0f, q[P];
 #pragma unroll
-            for (int j = 1; j < P; ++j) m = fmaxf(m, x[j]);
+            for (int j = 1; j < P; ++j) m = fmaxf(m, c[j]);
             top = fmaxf(warp_max(m), -FLT_MAX); // finite: exp(-inf - top) is 0
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                c[j] = __expf(x[j] - top);
-                sum += c[j];
+                q[j] = exp2_fast(kLog2e * (c[j] - top));
+                sum += q[j];
             }
-            total = warp_sum(sum);
-            const float inverse = __fdividef(1.0f, total);
+            inverse = reciprocal_fast(warp_sum(sum));
+            if (scored)
 #pragma unroll
-            for (int j = 0; j < P; ++j) c[j] *= inverse;
-        } else {
+                for (int j = 0; j < P; ++j) c[j] = c[j] > -INFINITY ? fmaf(q[j], inverse, bias[j]) : -INFINITY;
+        } else if (scored) {
 #pragma unroll
-            for (int j = 0; j < P; ++j) c[j] = __fdividef(1.0f, 1.0f + __expf(-x[j]));
+            for (int j = 0; j < P; ++j) c[j] = c[j] > -INFINITY ? sigmoid_fast(c[j]) + bias[j] : -INFINITY;
         }
+        uint32_t key[P];
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            c[j] += bias[j];
-            if (!(x[j] > -INFINITY && c[j] > -INFINITY)) x[j] = c[j] = -INFINITY;
-        }
+        for (int j = 0; j < P; ++j) key[j] = c[j] > -INFINITY ? Key::make(c[j], lane * P + j) : 0u;
         bool again = false; // too close to call in 32 bits
-        if (a.groups > 1 && group_lanes) {
-            float m1 = c[0], m2 = -INFINITY;
-#pragma unroll
-            for (int j = 1; j < P; ++j) join_best_two(m1, m2, c[j], -INFINITY);
-            for (int d = 1; d < group_lanes; d <<= 1)
-                join_best_two(m1, m2, __shfl_xor_sync(kAll, m1, d), __shfl_xor_sync(kAll, m2, d));
-            const float v = group_value(m1, m2, a.best);
-            int rank = 0;
-            const int mine = lane / group_lanes;
-            for (int g = 0; g < a.groups; ++g) {
-                const float o = __shfl_sync(kAll, v, g * group_lanes);
-                rank += o > v || (o == v && g < mine);
-            }
-            const bool on = mine < a.groups;
-            const uint32_t edge = __ballot_sync(kAll, on && rank == a.kept - 1), past = __ballot_sync(kAll, on && rank == a.kept);
-            const float last = __shfl_sync(kAll, v, __ffs(edge) - 1), cut = __shfl_sync(kAll, v, __ffs(past) - 1);
-            const float size = fabsf(m1) + (m2 > -INFINITY ? fabsf(m2) : 0.0f);
-            const float most = __uint_as_float(__reduce_max_sync(kAll, on && m1 > -INFINITY ? __float_as_uint(size) : 0u));
-            // two scores, their biases and their sum on either side of the cut
-            if (cut > -INFINITY) again = !(last - cut > 4.0f * kScoreError + 4.0f * kSumError * most);
-            if (!on || rank >= a.kept)
-#pragma unroll
-                for (int j = 0; j < P; ++j) x[j] = c[j] = -INFINITY;
-        } else if (a.groups > 1) {
+        if (a.groups > 1 && !group_lanes) {
             uint32_t mine = 0;
             float most = 0.0f;
             for (int g = 0; g < a.groups; ++g) {
                 uint32_t members[P];
 #pragma unroll
-                for (int j = 0; j < P; ++j)
-                    members[j] = c[j] > -INFINITY && (lane * P + j) / per == g ? order_key(c[j]) : 0u;
+                for (int j = 0; j < P; ++j) members[j] = (lane * P + j) / per == g ? key[j] : 0u;
                 int e;
                 const uint32_t first = take_best<P>(members, lane, e);
                 const uint32_t second = a.best > 1 && first ? take_best<P>(members, lane, e) : 0u;
-                const float u = first ? key_value(first) : 0.0f, w = second ? key_value(second) : 0.0f;
+                const float u = first ? Key::value(first) : 0.0f, w = second ? Key::value(second) : 0.0f;
                 if (lane == g) mine = first ? order_key(u + w) : 0u;
                 most = fmaxf(most, fabsf(u) + fabsf(w));
             }
             uint32_t last, cut;
             const uint32_t keep = best_groups<uint32_t>(mine, a.groups, a.kept, lane, last, cut);
-            if (cut) again = !(key_value(last) - key_value(cut) > 4.0f * kScoreError + 4.0f * kSumError * most);
+            if (cut) again = !(key_value(last) - key_value(cut) > 4.0f * error + 4.0f * part * most);
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 const int e = lane * P + j;
-                if (e < a.experts && !((keep >> (e / per)) & 1u)) x[j] = c[j] = -INFINITY;
+                if (e < a.experts && !((keep >> (e / per)) & 1u)) key[j] = 0;
             }
         }
-        if (!a.bias) // the order is that of the logits, exactly
+        LaneList<P> list(key);
+        if (a.groups > 1 && group_lanes) {
+            float m1 = c[0], m2 = -INFINITY; // whole values: a cut between groups must not hang on short keys
 #pragma unroll
-            for (int j = 0; j < P; ++j) c[j] = x[j];
-        // the bound: the k-th largest of the lanes' best
-        float m = c[0];
+            for (int j = 1; j < P; ++j) {
+                m2 = fmaxf(m2, fminf(m1, c[j]));
+                m1 = fmaxf(m1, c[j]);
+            }
+            for (int d = 1; d < group_lanes; d <<= 1)
+                join_best_two(m1, m2, __shfl_xor_sync(kAll, m1, d), __shfl_xor_sync(kAll, m2, d));
+            const bool any = m1 > -INFINITY && lane < a.groups * group_lanes;
+            const uint32_t mine = any ? order_key(group_value(m1, m2, a.best)) : 0u;
+            uint32_t left = mine, last = 0;
+            for (int g = 0; g < a.kept; ++g) { // equal values go at once; the cut is then not clear
+                last = __reduce_max_sync(kAll, left);
+                if (left == last) left = 0;
+            }
+            const uint32_t cut = __reduce_max_sync(kAll, left);
+            const bool keep = mine >= last;
+            if (cut) {
+                const float size = any ? fabsf(m1) + (m2 > -INFINITY ? fabsf(m2) : 0.0f) : 0.0f;
+                const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
+                again = !(key_value(last) - key_value(cut) > 4.0f * error + 4.0f * kSumError * most);
+            }
+            // equal values among the kept ones: more groups than asked for
+            again = again || __popc(__ballot_sync(kAll, keep && any)) > a.kept * group_lanes;
+            if (!keep)
 #pragma unroll
-        for (int j = 1; j < P; ++j) m = fmaxf(m, c[j]);
-        uint32_t left = m > -INFINITY ? order_key(m) : 0u, bound = 0;
+                for (int i = 0; i < LaneList<P>::D; ++i) list.at[i] = 0;
+        }
+        uint32_t mine = 0, prev = 0;
         for (int i = 0; i < a.k; ++i) {
-            bound = __reduce_max_sync(kAll, left);
-            if (bound == 0) break;
-            const uint32_t ties = __ballot_sync(kAll, left == bound);
-            if (lane == __ffs(ties) - 1) left = 0;
+            prev = list.take(key);
+            if (lane == i) mine = prev;
         }
-        float least = bound ? key_value(bound) : -FLT_MAX;
-        if (bound && a.bias && fabsf(least) < INFINITY)
-            least -= 2.1f * kScoreError + 3.0f * kSumError * fabsf(least);
-        int n = 0;
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-            const bool in = c[j] >= least;
-            const uint32_t mask = __ballot_sync(kAll, in);
-            const int at = n + __popc(mask & ((1u << lane) - 1u));
-            if (in && at < 32) found[warp][at] = ((uint64_t)order_key(c[j]) << 32) | (uint32_t)~(lane * P + j);
-            n += __popc(mask);
-        }
-        int chosen = -1, after = -1; // this place's expert and the one behind it
-        float value = 0.0f, after_value = 0.0f;
-        if (n <= 32) {
-            __syncwarp();
-            const uint64_t mine = lane < n ? found[warp][lane] : 0ull;
-            int rank = 0;
-            for (int i = 0; i < n; ++i) rank += found[warp][i] > mine;
-            if (lane < n) sorted[warp][rank] = mine;
-            __syncwarp();
-            if (lane < n) {
-                const uint64_t best = sorted[warp][lane];
-                chosen = (int)~(uint32_t)best;
-                value = key_value((uint32_t)(best >> 32));
-            }
-            if (lane + 1 < n) {
-                const uint64_t best = sorted[warp][lane + 1];
-                after = (int)~(uint32_t)best;
-                after_value = key_value((uint32_t)(best >> 32));
-            }
-        } else {
-            uint32_t key[P];
-#pragma unroll
-            for (int j = 0; j < P; ++j) key[j] = c[j] > -INFINITY ? order_key(c[j]) : 0u;
-            for (int i = 0; i <= a.k; ++i) {
-                int e;
-                const uint32_t best = take_best<P>(key, lane, e);
-                if (lane == i) {
-                    chosen = e;
-                    value = key_value(best);
+        int chosen = lane < a.k && mine ? Key::expert(mine) : -1;
+        // neighbours that the short keys do not settle, the one behind the k-th among them
+        const auto close = [&](uint32_t p, uint32_t q) {
+            const float u = Key::value(p), w = Key::value(q);
+            return p && q && !(u - w > 2.0f * error + part * (fabsf(u) + fabsf(w)));
+        };
+        const uint32_t below = __shfl_down_sync(kAll, mine, 1);
+        uint32_t past = list.take(key);
+        const bool over = close(prev, past);
+        if (!again && __any_sync(kAll, over || (lane < a.k - 1 && close(mine, below)))) {
+            int n = a.k;
+            if (over) { // everything that could still belong before the cut
+                while (n < 32) {
+                    if (lane == n) chosen = Key::expert(past);
+                    ++n;
+                    prev = past;
+                    past = list.take(key);
+                    if (!close(prev, past)) break;
                 }
-                if (lane == i - 1) {
-                    after = e;
-                    after_value = key_value(best);
-                }
-                if (best == 0) break;
+                again = n == 32 && close(prev, past);
+            }
+            if (!again) {
+                const int found = __popc(__ballot_sync(kAll, chosen >= 0));
+                float mine_c = chosen >= 0 ? fminf(load_logit(row + chosen), FLT_MAX) : 0.0f; // the logits decide
+                if (a.bias && chosen >= 0)
+                    mine_c = (a.softmax ? exp2_fast(kLog2e * (mine_c - top)) * inverse : sigmoid_fast(mine_c)) + a.bias[chosen];
+                chosen = settle<T, P>(row, a, chosen, mine_c, min(n, found), place[warp]);
             }
         }
-        if (a.bias) {
-            bool close = false;
-            if (lane < a.k && chosen >= 0 && after >= 0 &&
-                !(value - after_value > 2.0f * kScoreError + kSumError * (fabsf(value) + fabsf(after_value))))
-                close = load_logit(row + chosen) != load_logit(row + after) || a.bias[chosen] != a.bias[after];
-            again = again || __any_sync(kAll, close);
-        }
-        if (again) chosen = choose_in_64_bits<T, P>(row, a);
+        if (again) chosen = scored ? choose_in_64_bits<T, P>(row, a) : choose_by_logits<T, P>(row, a);
         // weights of the chosen
         const bool on = lane < a.k && chosen >= 0;
-        const float xi = on ? fminf(load_logit(row + chosen), FLT_MAX) : 0.0f;
-        const float si = !on ? 0.0f : a.softmax ? expf(xi - top) / total : 1.0f / (1.0f + expf(-xi));
-        const float w = a.renorm ? share_of<32>(si, xi, on, a.softmax != 0) : si;
+        const float x = on ? fminf(load_logit(row + chosen), FLT_MAX) : 0.0f;
+        float w = !on ? 0.0f : a.softmax ? exp2_fast(kLog2e * (x - top)) * inverse : sigmoid_fast(x);
+        if (a.renorm) w = share_of<32>(w, x, on, a.softmax != 0);
         if (lane < a.k) {
             a.idx[t * a.k + lane] = on ? chosen : -1;
-            a.weight[t * a.k + lane] = on ? w * a.scale : 0.0f;
+            a.weight[t * a.k + lane] = w * a.scale;
         }
         if (a.load && on) atomicAdd(&count[chosen], 1);
-        __syncwarp(); // the lists are read before the next token's are written
     }
     grid_dependents_go();
     if (a.load) {
