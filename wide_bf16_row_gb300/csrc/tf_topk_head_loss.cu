@@ -30,7 +30,9 @@
 //   kHidden  A = G, B = weight with K = the vocabulary (B is stored with N
 //          contiguous): fp32 sums that grow from piece to piece;
 //   kWeight  A = G^T, B = hidden with K = the rows (both stored with M and N
-//          contiguous): the piece's rows of d_weight.
+//          contiguous): the piece's rows of d_weight;
+//   kGrads kHidden's tiles, then kWeight's, in one launch, so that the second
+//          fill the last round of the first.
 //
 // The tensor cores truncate their running fp32 sums, which biases a logit of
 // 12 by about -2.6e-5 at 2048 dims (measured against 64 bits; the fp32 FMA
@@ -65,8 +67,9 @@ constexpr int kTileRows = 256;                       // rows (M) of a pair's til
 constexpr int kTileCols = 256;                       // columns (N) of the widest tile
 constexpr int kHalf = 128;                           // one CTA's share of either
 constexpr int kStepK = 64;                           // K per ring stage: one 128-byte swizzle row of bf16
-constexpr int kStages = 6;
-constexpr uint32_t kShare = kHalf * kStepK * 2;      // 16 KB: one CTA's share of an operand per stage
+constexpr uint32_t kShare = kHalf * kStepK * 2;      // 16 KB: one CTA's whole share of an operand per stage
+constexpr int kMaxStages = 16;
+constexpr uint32_t kRingBytes = 200 * 1024;          // leaves an SM room for the small kernels queued behind
 constexpr int kEpiWarps = 8;
 constexpr int kPairThreads = 32 * (2 + kEpiWarps);
 constexpr int kTmemCols = 2 * kTileCols;
@@ -77,12 +80,12 @@ constexpr uint32_t kFaultWait = 1;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-enum Mode { kLse, kProb, kHidden, kWeight };
+enum Mode { kLse, kProb, kHidden, kWeight, kGrads };
 
 __device__ uint32_t g_head_loss_fault;
 
 struct __align__(16) PairSmem {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
     uint32_t tmem_base;
@@ -93,6 +96,7 @@ struct __align__(16) PairSmem {
 struct RowHeader {
     int32_t count;
     float grad_scale; // largest finite |g|, or 1
+    int32_t splits;   // shares of K that the hidden states' gradient is summed in
 };
 
 struct PairArgs {
@@ -105,9 +109,11 @@ struct PairArgs {
     int32_t vocab;
     int32_t begin, cols;      // the piece of the vocabulary [begin, begin + cols)
     int32_t width;            // columns of a tile
+    int32_t stages;           // of the ring
+    int32_t row_box;          // few rows: rows of A that the leading CTA loads (the peer none), a multiple of 8
     int32_t pad_rows;         // row pitch of `partial`
-    int32_t splits;           // kHidden: shares of K, each with sums of its own
     int32_t first;            // kHidden: the sums start here
+    int32_t whole;            // kWeight: rows of d_weight are whole 32-byte sectors
     int32_t pitch;            // row pitch of G
     float2 *partial;          // kLse: [2 * column tiles][pad_rows]: reference exponent, sum
     const float *lse;         // kProb [rows]
@@ -256,6 +262,23 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// A whole 32-byte sector per thread: threads of a warp write rows of their
+// own, and 16-byte pieces of a sector cost the L2 twice (measured on G of
+// 3686 x 98592: 1062 us with 16-byte stores, 940 with these, 905 without any).
+__device__ __forceinline__ void store32(void *p, const uint32_t *v)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+// Adds four floats to memory in the L2, without waiting for the old ones.
+__device__ __forceinline__ void add16(float *p, const float *v)
+{
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3])
+                 : "memory");
+}
+
 __device__ __forceinline__ int64_t target_of(const void *target, int target64, int row)
 {
     return target64 ? static_cast<const int64_t *>(target)[row] : (int64_t)static_cast<const int32_t *>(target)[row];
@@ -265,73 +288,139 @@ __device__ __forceinline__ int64_t target_of(const void *target, int target64, i
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// Shares of K that the hidden states' gradient is summed in, `most` at most,
+// so that its tiles come out in nearly whole rounds of the pairs; every share
+// more costs its sums' traffic, taken as a fiftieth of a round.  One warp, a
+// lane per candidate.
+__device__ __forceinline__ int best_splits(int row_tiles, int dim, int pairs, int most)
+{
+    const int s = (threadIdx.x & 31) + 1;
+    const int64_t tiles = (int64_t)row_tiles * ceil_div(dim, kTileCols);
+    const float rounds = (float)((tiles * s + pairs - 1) / pairs) / (float)s;
+    float cost = s <= most ? rounds * (1.0f + 0.02f * (float)s) : 3e38f;
+    int best = s;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const float o = __shfl_xor_sync(0xFFFFFFFFu, cost, d);
+        const int os = __shfl_xor_sync(0xFFFFFFFFu, best, d);
+        if (o < cost || (o == cost && os < best)) {
+            cost = o;
+            best = os;
+        }
+    }
+    return best;
+}
+
 // A tile of the persistent schedule and its share [k0, k1) of the K steps.
 struct Unit {
     int m, n, split, k0, k1;
 };
 
 template <int kMode> struct Shape {
-    int m_tiles, n_tiles, k_steps, splits;
+    int m_tiles, n_tiles, k_steps, splits; // kGrads: the weight's
+    int h_tiles, h_steps;                  // the hidden states' row tiles and K steps
+    int64_t h_units;
     __device__ Shape(const PairArgs &a, int count)
     {
         const int row_tiles = max(1, ceil_div(count, kTileRows));
         splits = 1;
+        h_tiles = h_steps = 0;
+        h_units = 0;
         if (kMode == kLse || kMode == kProb) {
             m_tiles = row_tiles;
             n_tiles = ceil_div(a.cols, a.width);
             k_steps = ceil_div(a.dim, kStepK);
-        } else if (kMode == kHidden) {
-            m_tiles = row_tiles;
-            n_tiles = ceil_div(a.dim, kTileCols);
-            k_steps = ceil_div(a.cols, kStepK);
-            splits = min(a.splits, k_steps);
         } else {
             m_tiles = ceil_div(a.cols, kTileRows);
             n_tiles = ceil_div(a.dim, kTileCols);
             k_steps = max(1, ceil_div(count, kStepK));
+            if (kMode != kWeight) {
+                h_tiles = row_tiles;
+                h_steps = ceil_div(a.cols, kStepK);
+                splits = min(a.header->splits, h_steps);
+                h_units = (int64_t)h_tiles * n_tiles * splits;
+            }
         }
     }
-    __device__ int64_t units() const { return (int64_t)m_tiles * n_tiles * splits; }
+    __device__ int64_t units() const { return h_units + (kMode == kHidden ? 0 : (int64_t)m_tiles * n_tiles); }
+    // Whether a unit is a tile of d_weight.
+    __device__ bool of_weight(int64_t u) const { return kMode == kWeight || (kMode == kGrads && u >= h_units); }
     __device__ Unit at(int64_t u) const
     {
         Unit t;
-        if (kMode == kLse || kMode == kProb) {
-            // groups of kGroupRows row tiles; in a group the row tile moves
-            // first, so that the pairs at work share the weight's tiles
-            const int64_t per_group = (int64_t)kGroupRows * n_tiles;
-            const int g = (int)(u / per_group);
-            const int64_t r = u - g * per_group;
-            const int in_group = min(kGroupRows, m_tiles - g * kGroupRows);
-            t.m = g * kGroupRows + (int)(r % in_group);
-            t.n = (int)(r / in_group);
-            t.split = 0;
-        } else {
-            t.n = (int)(u % n_tiles);
-            const int64_t r = u / n_tiles;
-            t.m = (int)(r % m_tiles);
-            t.split = (int)(r / m_tiles);
+        if (kMode == kHidden || (kMode == kGrads && u < h_units)) {
+            t.m = (int)(u % h_tiles);
+            const int64_t r = u / h_tiles;
+            t.n = (int)(r % n_tiles);
+            t.split = (int)(r / n_tiles);
+            t.k0 = (int)((int64_t)h_steps * t.split / splits);
+            t.k1 = (int)((int64_t)h_steps * (t.split + 1) / splits);
+            return t;
         }
-        t.k0 = (int)((int64_t)k_steps * t.split / splits);
-        t.k1 = (int)((int64_t)k_steps * (t.split + 1) / splits);
+        // groups of kGroupRows row tiles; in a group the row tile moves
+        // first, so that the pairs at work share the tiles of B
+        u -= h_units;
+        const int64_t per_group = (int64_t)kGroupRows * n_tiles;
+        const int g = (int)(u / per_group);
+        const int64_t r = u - g * per_group;
+        const int in_group = min(kGroupRows, m_tiles - g * kGroupRows);
+        t.m = g * kGroupRows + (int)(r % in_group);
+        t.n = (int)(r / in_group);
+        t.split = 0;
+        t.k0 = 0;
+        t.k1 = k_steps;
         return t;
     }
 };
 
-template <int kMode>
+// The products of one tile: `steps` ring stages from `s` on into accumulator
+// `d`.  False when a wait gave up.
+template <bool kAMN, bool kBMN>
+__device__ __forceinline__ bool issue_tile(PairSmem &sm, uint32_t d, uint32_t idesc, int steps, uint32_t &s,
+                                           uint32_t &parity, uint32_t stages, const uint8_t *ring_a, uint32_t share_a,
+                                           const uint8_t *ring_b, uint32_t share_b, volatile uint32_t *abort)
+{
+    // 16 K steps: 32 bytes along a K-major row, 16 whole rows of an MN-major box
+    constexpr uint64_t step_a = kAMN ? (16 * 128) >> 4 : 32 >> 4;
+    constexpr uint64_t step_b = kBMN ? (16 * 128) >> 4 : 32 >> 4;
+    for (int k = 0; k < steps; ++k) {
+        if (!mbar_wait(&sm.full[s], parity, abort)) return false;
+        tc_fence_after();
+        const uint64_t ad = desc_at(ring_a + s * share_a, kAMN ? kDescMN : kDescK);
+        const uint64_t bd = desc_at(ring_b + s * share_b, kBMN ? kDescMN : kDescK);
+#pragma unroll
+        for (int kk = 0; kk < kStepK / 16; ++kk)
+            mma_pair(d, ad + kk * step_a, bd + kk * step_b, idesc, k != 0 || kk != 0);
+        mma_commit_pair(&sm.empty[s]);
+        if (++s == stages) s = 0, parity ^= 1;
+    }
+    return true;
+}
+
+template <int kMode, bool kFew>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    pair_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, PairArgs a)
+    pair_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                        const __grid_constant__ CUtensorMap map_wa, const __grid_constant__ CUtensorMap map_wb, PairArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t *ring_a = ring, *ring_b = ring + (size_t)kStages * kShare;
-    PairSmem &sm = *reinterpret_cast<PairSmem *>(ring + 2 * (size_t)kStages * kShare);
+    // Rows of A that are not loaded leave whatever the ring holds in their
+    // lanes of the accumulator, which nothing reads; the MMA reads on from a
+    // short share of A into what follows it in the ring.
+    const int half_cols = kMode == kLse || kMode == kProb ? a.width / 2 : kHalf; // one CTA's share of B
+    // (Whole shares have the ring's shape at compile time: the issuing thread
+    // keeps up better, 615 against 631 us on 800 x 2048 x 248320.)
+    const uint32_t share_a = kFew ? (uint32_t)a.row_box * kStepK * 2 : kShare;
+    const uint32_t share_b = kFew ? (uint32_t)half_cols * kStepK * 2 : kShare;
+    const uint32_t stages = kFew ? (uint32_t)a.stages : kRingBytes / (2 * kShare);
+    uint8_t *ring_a = ring, *ring_b = ring + stages * share_a;
+    PairSmem &sm = *reinterpret_cast<PairSmem *>(ring + stages * (share_a + share_b));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = blockIdx.x & 1; // in the pair; rank 0 leads
     const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    constexpr bool kAisMN = kMode == kWeight, kBisMN = kMode == kHidden || kMode == kWeight;
 
     if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(&sm.full[s], 1);
             mbar_init(&sm.empty[s], 1);
         }
@@ -357,82 +446,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     grid_dependency_wait(); // the inputs may come from the kernel before on the stream
+    if (kMode == kLse) grid_dependents_go(); // the rows' kernel may take its place beside this one
 
     const int count = a.header ? a.header->count : a.rows;
     const Shape<kMode> shape(a, count);
     const int64_t units = shape.units();
-    const int half_cols = kMode == kLse || kMode == kProb ? a.width / 2 : kHalf; // one CTA's share of B
     volatile uint32_t *abort = &sm.abort;
 
     if (warp == 0) {
         // ---- TMA producer
         if (lane == 0) {
-            const uint32_t bytes = 2 * (kShare + (uint32_t)half_cols * kStepK * 2); // both CTAs'
-            uint32_t it = 0;
+            // both CTAs' bytes; of few rows only the leading CTA has any
+            const uint32_t bytes = (kFew ? share_a : 2 * share_a) + 2 * (uint32_t)half_cols * kStepK * 2;
+            const bool has_a = !kFew || rank == 0;
+            uint32_t s = 0, turn = 0; // ring stage, times round the ring
             bool ok = true;
             for (int64_t u = pair; u < units && ok; u += pairs) {
                 const Unit t = shape.at(u);
+                const bool weight = shape.of_weight(u);
                 const int row = t.m * kTileRows + (int)rank * kHalf;
-                for (int k = t.k0; k < t.k1; ++k, ++it) {
-                    const uint32_t s = it % kStages, ph = it / kStages;
-                    if (*abort || (ph > 0 && !mbar_wait(&sm.empty[s], (ph - 1) & 1, abort))) {
+                for (int k = t.k0; k < t.k1; ++k) {
+                    if (*abort || (turn > 0 && !mbar_wait(&sm.empty[s], (turn - 1) & 1, abort))) {
                         ok = false;
                         break;
                     }
                     if (rank == 0) mbar_expect_tx(&sm.full[s], bytes);
                     const uint32_t bar = peer_addr(&sm.full[s], 0);
-                    uint8_t *da = ring_a + (size_t)s * kShare, *db = ring_b + (size_t)s * kShare;
-                    if (!kAisMN) {
-                        tma_load(da, &map_a, k * kStepK, row, bar);
-                    } else {
-                        tma_load(da, &map_a, row, k * kStepK, bar);
-                        tma_load(da + kShare / 2, &map_a, row + 64, k * kStepK, bar);
-                    }
-                    if (!kBisMN) {
+                    uint8_t *da = ring_a + s * share_a, *db = ring_b + s * share_b;
+                    if (kMode == kLse || kMode == kProb) {
+                        if (has_a) tma_load(da, &map_a, k * kStepK, row, bar);
                         tma_load(db, &map_b, k * kStepK, a.begin + t.n * a.width + (int)rank * half_cols, bar);
                     } else {
                         const int col = t.n * kTileCols + (int)rank * kHalf;
-                        const int y = (kMode == kHidden ? a.begin : 0) + k * kStepK;
-                        tma_load(db, &map_b, col, y, bar);
-                        tma_load(db + kShare / 2, &map_b, col + 64, y, bar);
+                        if (!weight) {
+                            if (has_a) tma_load(da, &map_a, k * kStepK, row, bar);
+                            tma_load(db, &map_b, col, a.begin + k * kStepK, bar);
+                            tma_load(db + kShare / 2, &map_b, col + 64, a.begin + k * kStepK, bar);
+                        } else {
+                            tma_load(da, &map_wa, row, k * kStepK, bar);
+                            tma_load(da + kShare / 2, &map_wa, row + 64, k * kStepK, bar);
+                            tma_load(db, &map_wb, col, k * kStepK, bar);
+                            tma_load(db + kShare / 2, &map_wb, col + 64, k * kStepK, bar);
+                        }
                     }
+                    if (++s == stages) s = 0, ++turn;
                 }
             }
             // both CTAs' copies land before the pair leaves: the last fill of
             // each stage (the leader's barrier counts both CTAs' bytes)
             if (rank == 0)
-                for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0u; j < it; ++j)
-                    mbar_wait(&sm.full[j % kStages], (j / kStages) & 1, abort);
+                for (uint32_t j = 0; j < stages; ++j) {
+                    const uint32_t filled = j < s ? turn + 1 : turn; // times stage j was filled
+                    if (filled) mbar_wait(&sm.full[j], (filled - 1) & 1, abort);
+                }
         }
     } else if (warp == 1) {
         // ---- MMA issuer (the leading CTA's)
         if (rank == 0 && lane == 0) {
-            const uint32_t idesc = instruction_desc(kAisMN, kBisMN, (uint32_t)half_cols * 2);
-            uint32_t it = 0, tile = 0;
-            bool ok = true;
-            for (int64_t u = pair; u < units && ok; u += pairs, ++tile) {
+            const uint32_t cols = (uint32_t)half_cols * 2;
+            uint32_t s = 0, parity = 0, tile = 0;
+            for (int64_t u = pair; u < units; u += pairs, ++tile) {
                 const Unit t = shape.at(u);
                 const uint32_t buf = tile & 1, use = tile >> 1;
                 if (use > 0 && !mbar_wait(&sm.acc_empty[buf], (use - 1) & 1, abort)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * kTileCols;
-                for (int k = t.k0; k < t.k1; ++k, ++it) {
-                    const uint32_t s = it % kStages, ph = it / kStages;
-                    if (!mbar_wait(&sm.full[s], ph & 1, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t ad = desc_at(ring_a + (size_t)s * kShare, kAisMN ? kDescMN : kDescK);
-                    const uint64_t bd = desc_at(ring_b + (size_t)s * kShare, kBisMN ? kDescMN : kDescK);
-                    // 16 K steps: 32 bytes along a K-major row, 16 whole rows of an MN-major box
-                    constexpr uint64_t step_a = kAisMN ? (16 * 128) >> 4 : 32 >> 4;
-                    constexpr uint64_t step_b = kBisMN ? (16 * 128) >> 4 : 32 >> 4;
-#pragma unroll
-                    for (int kk = 0; kk < kStepK / 16; ++kk)
-                        mma_pair(d, ad + kk * step_a, bd + kk * step_b, idesc, k != t.k0 || kk != 0);
-                    mma_commit_pair(&sm.empty[s]);
-                }
+                const int steps = t.k1 - t.k0;
+                bool ok;
+                if (kMode == kLse || kMode == kProb)
+                    ok = issue_tile<false, false>(sm, d, instruction_desc(false, false, cols), steps, s, parity, stages,
+                                                  ring_a, share_a, ring_b, share_b, abort);
+                else if (!shape.of_weight(u))
+                    ok = issue_tile<false, true>(sm, d, instruction_desc(false, true, cols), steps, s, parity, stages,
+                                                 ring_a, share_a, ring_b, share_b, abort);
+                else
+                    ok = issue_tile<true, true>(sm, d, instruction_desc(true, true, cols), steps, s, parity, stages,
+                                                ring_a, share_a, ring_b, share_b, abort);
                 if (!ok) break;
                 mma_commit_pair(&sm.acc_full[buf]);
             }
@@ -447,6 +536,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int q = warp & 3, h = (warp - 2) >> 2;
         const uint32_t acc_empty0 = peer_addr(&sm.acc_empty[0], 0), acc_empty1 = peer_addr(&sm.acc_empty[1], 0);
         uint32_t tile = 0;
+        // kLse: reference exponent (base 2), its logit, sum of exp2; with few
+        // rows over all of the pair's tiles
+        float ref = 0.0f, top = -INFINITY, sum = 0.0f;
+        // few rows: the warps that have none (but for kProb's zeros) skip the tile
+        const bool no_rows = kFew && kMode != kProb && (int)rank * kHalf + 32 * q >= count;
         for (int64_t u = pair; u < units; u += pairs, ++tile) {
             const Unit t = shape.at(u);
             const uint32_t buf = tile & 1, use = tile >> 1;
@@ -468,9 +562,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             tc_fence_after();
             const uint32_t lanes = tmem + buf * kTileCols + ((uint32_t)(32 * q) << 16);
             // columns of the tile that this thread takes
-            const int c0 = h * half_cols, chunks = half_cols / kChunk;
+            const int c0 = h * half_cols, chunks = no_rows ? 0 : half_cols / kChunk;
             if (kMode == kLse) {
-                float ref = 0.0f, top = -INFINITY, sum = 0.0f; // reference exponent (base 2), its logit, sum of exp2
+                if (!kFew) ref = 0.0f, top = -INFINITY, sum = 0.0f;
                 for (int c = 0; c < chunks; ++c) {
                     float x[kChunk];
                     tmem_load(lanes + c0 + c * kChunk, x);
@@ -498,7 +592,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) sum += exp2_fast(fmaf(x[i], kLog2e, -ref));
                 }
-                if (row < count)
+                if (row < count && !kFew)
                     a.partial[(size_t)(2 * t.n + h) * a.pad_rows + row] =
                         make_float2(top == -INFINITY ? -INFINITY : ref, sum);
             } else if (kMode == kProb) {
@@ -517,29 +611,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     }
 #pragma unroll
                     for (int i = 0; i < kChunk / 2; ++i) out[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-                    uint4 *dst = reinterpret_cast<uint4 *>(a.prob + (size_t)row * a.pitch + col);
+                    __nv_bfloat16 *dst = a.prob + (size_t)row * a.pitch + col;
 #pragma unroll
-                    for (int i = 0; i < kChunk / 8; ++i)
-                        dst[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+                    for (int i = 0; i < kChunk / 16; ++i) store32(dst + 16 * i, out + 8 * i);
                 }
-            } else if (kMode == kHidden) {
+            } else if (!shape.of_weight(u)) {
                 for (int c = 0; c < chunks; ++c) {
                     float x[kChunk];
                     tmem_load(lanes + c0 + c * kChunk, x);
                     const int col = t.n * kTileCols + c0 + c * kChunk;
                     if (row < count) {
-                        float4 *dst = reinterpret_cast<float4 *>(
-                            a.sums + ((size_t)t.split * a.pad_rows + row) * a.dim + col);
+                        float *dst = a.sums + ((size_t)t.split * a.pad_rows + row) * a.dim + col;
+                        if (a.first) {
 #pragma unroll
-                        for (int i = 0; i < kChunk / 4; ++i)
-                            if (col + 4 * i < a.dim) {
-                                float4 v = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                                if (!a.first) {
-                                    const float4 o = dst[i];
-                                    v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-                                }
-                                dst[i] = v;
-                            }
+                            for (int i = 0; i < kChunk / 8; ++i)
+                                if (col + 8 * i < a.dim) store32(dst + 8 * i, reinterpret_cast<const uint32_t *>(x) + 8 * i);
+                        } else { // one addition per element and launch: the order is the pieces'
+#pragma unroll
+                            for (int i = 0; i < kChunk / 4; ++i)
+                                if (col + 4 * i < a.dim) add16(dst + 4 * i, x + 4 * i);
+                        }
                     }
                 }
             } else {
@@ -549,15 +640,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     tmem_load(lanes + c0 + c * kChunk, x);
                     const int col = t.n * kTileCols + c0 + c * kChunk;
                     if (row < a.cols) {
-                        uint4 *dst =
-                            reinterpret_cast<uint4 *>(a.d_weight + ((size_t)a.begin + row) * a.dim + col);
+                        __nv_bfloat16 *dst = a.d_weight + ((size_t)a.begin + row) * a.dim + col;
+                        uint32_t out[kChunk / 2];
 #pragma unroll
-                        for (int i = 0; i < kChunk / 8; ++i)
-                            if (col + 8 * i < a.dim)
-                                dst[i] = make_uint4(pack_bf16(x[8 * i] * scale, x[8 * i + 1] * scale),
-                                                    pack_bf16(x[8 * i + 2] * scale, x[8 * i + 3] * scale),
-                                                    pack_bf16(x[8 * i + 4] * scale, x[8 * i + 5] * scale),
-                                                    pack_bf16(x[8 * i + 6] * scale, x[8 * i + 7] * scale));
+                        for (int i = 0; i < kChunk / 2; ++i) out[i] = pack_bf16(x[2 * i] * scale, x[2 * i + 1] * scale);
+                        if (a.whole) {
+#pragma unroll
+                            for (int i = 0; i < kChunk / 16; ++i)
+                                if (col + 16 * i < a.dim) store32(dst + 16 * i, out + 8 * i);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kChunk / 8; ++i)
+                                if (col + 8 * i < a.dim)
+                                    *reinterpret_cast<uint4 *>(dst + 8 * i) =
+                                        make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+                        }
                     }
                 }
             }
@@ -565,9 +662,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(buf ? acc_empty1 : acc_empty0);
         }
+        if (kMode == kLse && kFew) {
+            const int row = (int)rank * kHalf + 32 * q + lane;
+            if (row < count)
+                a.partial[(size_t)(2 * pair + h) * a.pad_rows + row] =
+                    make_float2(top == -INFINITY ? -INFINITY : ref, sum);
+        }
     }
     __syncwarp();
-    grid_dependents_go();
+    if (kMode != kLse) grid_dependents_go();
     tc_fence_before();
     __syncthreads();
     cluster_sync(); // neither CTA leaves while the other may still reach its shared memory
@@ -587,7 +690,7 @@ constexpr int kPrepareThreads = 1024;
 // target's entry of G is then exactly p - 1, and no g leaves bf16's range.
 __global__ void __launch_bounds__(kPrepareThreads)
     head_loss_prepare_kernel(const void *target, int target64, int64_t ignore, const float *grad, int rows, int vocab,
-                             RowHeader *header, int32_t *order, int32_t *place)
+                             int dim, int pairs, int most_splits, RowHeader *header, int32_t *order, int32_t *place)
 {
     __shared__ int warp_sum[32];
     __shared__ float warp_max[32];
@@ -627,10 +730,16 @@ __global__ void __launch_bounds__(kPrepareThreads)
     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
     if (lane == 0) warp_max[warp] = top;
     __syncthreads();
-    if (tid == 0) {
-        for (int w = 0; w < 32; ++w) top = fmaxf(top, warp_max[w]);
-        header->count = base;
-        header->grad_scale = top > 0.0f ? top : 1.0f;
+    if (warp == 0) {
+        top = warp_max[lane];
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        const int splits = best_splits(max(1, ceil_div(base, kTileRows)), dim, pairs, most_splits);
+        if (lane == 0) {
+            header->count = base;
+            header->grad_scale = top > 0.0f ? top : 1.0f;
+            header->splits = splits;
+        }
     }
     grid_dependents_go();
 }
@@ -657,37 +766,67 @@ __global__ void __launch_bounds__(256)
     grid_dependents_go();
 }
 
-constexpr int kRowsThreads = 128;
+constexpr int kRowsThreads = 256;
 constexpr int kRowsPerCta = 4; // neighbours of `partial` share its 32-byte sectors
 
+// exp2 sums over two reference exponents; (-inf, 0) is none yet.  The floor
+// keeps -inf - -inf away.
 __device__ __forceinline__ float2 join(float2 p, float2 q)
 {
-    // exp2 sums over two reference exponents; -inf: no term yet
-    if (q.x == -INFINITY && !isnan(q.y)) return p;
-    if (p.x == -INFINITY && !isnan(p.y)) return q;
-    const float top = fmaxf(p.x, q.x);
-    return make_float2(top, p.y * exp2f(p.x - top) + q.y * exp2f(q.x - top));
+    const float top = fmaxf(fmaxf(p.x, q.x), -FLT_MAX);
+    return make_float2(fmaxf(p.x, q.x), p.y * exp2_fast(p.x - top) + q.y * exp2_fast(q.x - top));
 }
 
-// The rows' losses: four rows per CTA.  The partial sums of a row joined, the
-// target's logit by FMA, and both into loss and lse.
+// The rows' losses: four rows per CTA.  The target's logit by FMA (while the
+// products still run), the partial sums of a row joined, and both into loss
+// and lse.
 __global__ void __launch_bounds__(kRowsThreads)
-    head_loss_rows_kernel(const float2 *__restrict__ partial, int parts, int pad_rows, const int32_t *place,
-                          const __nv_bfloat16 *__restrict__ hidden, int64_t hidden_stride,
-                          const __nv_bfloat16 *__restrict__ weight, int64_t weight_stride, int dim, int vocab,
-                          const void *target, int target64, int64_t ignore, int rows, float *loss, float *lse)
+    head_loss_rows_kernel(const float2 *__restrict__ partial, int parts, int pad_rows, const int32_t *place, const __nv_bfloat16 *__restrict__ hidden,
+                          int64_t hidden_stride, const __nv_bfloat16 *__restrict__ weight, int64_t weight_stride,
+                          int dim, int vocab, const void *target, int target64, int64_t ignore, int rows, float *loss,
+                          float *lse)
 {
     __shared__ float2 part[kRowsThreads / 32][kRowsPerCta];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    grid_dependency_wait();
     const int r0 = blockIdx.x * kRowsPerCta;
-    // thread = (row tid % 4, every 32nd part)
+    // warps 0-3 = row: the target's logit.  The kernel before let this one start
+    // only once the kernels before it had ended, so the inputs are there.
+    const int r = r0 + warp;
+    const int64_t t = warp < kRowsPerCta && r < rows ? target_of(target, target64, r) : ignore;
+    float dot = 0.0f;
+    if (t != ignore && t >= 0 && t < vocab) {
+        const uint4 *hv = reinterpret_cast<const uint4 *>(hidden + (size_t)r * hidden_stride);
+        const uint4 *wv = reinterpret_cast<const uint4 *>(weight + (size_t)t * weight_stride);
+#pragma unroll 4
+        for (int i = lane; i < dim / 8; i += 32) {
+            const uint4 p = hv[i], w = wv[i];
+            const uint32_t pa[4] = {p.x, p.y, p.z, p.w}, wa[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                dot = fmaf(__uint_as_float(pa[k] << 16), __uint_as_float(wa[k] << 16), dot);
+                dot = fmaf(__uint_as_float(pa[k] & 0xFFFF0000u), __uint_as_float(wa[k] & 0xFFFF0000u), dot);
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
+    grid_dependency_wait();
     {
-        const int r = r0 + (tid & 3);
-        const int j = r < rows ? (place ? place[r] : r) : -1;
+        // thread = (row tid % 4, every 64th part)
+        const int rr = r0 + (tid & 3);
+        const int j = rr < rows ? (place ? place[rr] : rr) : -1;
         float2 mine = make_float2(-INFINITY, 0.0f);
-        if (j >= 0)
-            for (int p = tid >> 2; p < parts; p += kRowsThreads / 4) mine = join(mine, partial[(size_t)p * pad_rows + j]);
+        constexpr int kAhead = 8; // loads in flight
+        for (int p = tid >> 2; j >= 0 && p < parts; p += kAhead * kRowsThreads / 4) {
+            float2 v[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int q = p + i * (kRowsThreads / 4);
+                v[i] = q < parts ? partial[(size_t)q * pad_rows + j] : make_float2(-INFINITY, 0.0f);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) mine = join(mine, v[i]);
+        }
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
             const float2 other = make_float2(__shfl_xor_sync(0xFFFFFFFFu, mine.x, d), __shfl_xor_sync(0xFFFFFFFFu, mine.y, d));
@@ -696,40 +835,20 @@ __global__ void __launch_bounds__(kRowsThreads)
         if (lane < 4) part[warp][lane] = mine;
     }
     __syncthreads();
-    // warp = row
-    const int r = r0 + warp;
-    if (r < rows) {
-        const int64_t t = target_of(target, target64, r);
+    if (warp < kRowsPerCta && r < rows && lane == 0) {
         if (t == ignore) {
-            if (lane == 0) loss[r] = 0.0f, lse[r] = 0.0f;
+            loss[r] = lse[r] = 0.0f;
         } else if (t < 0 || t >= vocab) {
-            if (lane == 0) loss[r] = NAN, lse[r] = NAN;
+            loss[r] = lse[r] = NAN;
         } else {
-            const uint4 *hv = reinterpret_cast<const uint4 *>(hidden + (size_t)r * hidden_stride);
-            const uint4 *wv = reinterpret_cast<const uint4 *>(weight + (size_t)t * weight_stride);
-            float dot = 0.0f;
-            for (int i = lane; i < dim / 8; i += 32) {
-                const uint4 p = hv[i], w = wv[i];
-                const uint32_t pa[4] = {p.x, p.y, p.z, p.w}, wa[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    dot = fmaf(__uint_as_float(pa[k] << 16), __uint_as_float(wa[k] << 16), dot);
-                    dot = fmaf(__uint_as_float(pa[k] & 0xFFFF0000u), __uint_as_float(wa[k] & 0xFFFF0000u), dot);
-                }
-            }
-#pragma unroll
-            for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
-            if (lane == 0) {
-                float2 all = part[0][warp];
-                for (int w = 1; w < kRowsThreads / 32; ++w) all = join(all, part[w][warp]);
-                // a vocabulary of one column leaves no other: rest = -inf
-                const float rest = all.x == -INFINITY && !isnan(all.y) ? -INFINITY : (all.x + log2f(all.y)) * kLn2;
-                const float above = rest - dot;
-                const float tail = log1pf(expf(-fabsf(above)));
-                loss[r] = fmaxf(above, 0.0f) + tail;
-                lse[r] = fmaxf(rest, dot) + tail;
-                if (isnan(above)) loss[r] = lse[r] = above;
-            }
+            float2 all = part[0][warp];
+            for (int w = 1; w < kRowsThreads / 32; ++w) all = join(all, part[w][warp]);
+            // a vocabulary of one column leaves no other: rest = -inf
+            const float rest = all.x == -INFINITY && all.y == 0.0f ? -INFINITY : (all.x + log2f(all.y)) * kLn2;
+            const float above = rest - dot;
+            const float tail = log1pf(expf(-fabsf(above)));
+            loss[r] = isnan(above) ? above : fmaxf(above, 0.0f) + tail;
+            lse[r] = isnan(above) ? above : fmaxf(rest, dot) + tail;
         }
     }
     grid_dependents_go();
@@ -738,11 +857,12 @@ __global__ void __launch_bounds__(kRowsThreads)
 // d_hidden: the shares' sums of a row added up, scaled back and rounded;
 // zeros for the rows that do not count.
 __global__ void __launch_bounds__(256)
-    head_loss_hidden_kernel(const float *__restrict__ sums, int splits, int pad_rows, int dim, const RowHeader *header,
+    head_loss_hidden_kernel(const float *__restrict__ sums, int pad_rows, int dim, const RowHeader *header,
                             const int32_t *place, int rows, __nv_bfloat16 *d_hidden)
 {
     grid_dependency_wait();
     const float scale = header->grad_scale;
+    const int splits = header->splits;
     const int vecs = dim / 8;
     for (int r = blockIdx.x; r < rows; r += gridDim.x) {
         const int j = place[r];
@@ -750,6 +870,7 @@ __global__ void __launch_bounds__(256)
         for (int i = threadIdx.x; i < vecs; i += blockDim.x) {
             float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             if (j >= 0)
+#pragma unroll 4
                 for (int s = 0; s < splits; ++s) {
                     const float4 *src = reinterpret_cast<const float4 *>(sums + ((size_t)s * pad_rows + j) * dim) + 2 * i;
                     const float4 p = src[0], q = src[1];
@@ -765,7 +886,7 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- host side
 
-constexpr size_t kPairSmemBytes = 1024 + 2 * (size_t)kStages * kShare + sizeof(PairSmem);
+constexpr size_t kPairSmemBytes = 1024 + (size_t)kRingBytes + sizeof(PairSmem);
 static_assert(kPairSmemBytes <= 227 * 1024, "the pair kernel's shared memory fits one CTA");
 
 constexpr int kMaxDevices = 64;
@@ -777,10 +898,17 @@ LossDevice g_loss_dev[kMaxDevices];
 std::mutex g_loss_mutex;
 PFN_cuTensorMapEncodeTiled_v12000 g_loss_encode = nullptr;
 
+template <int kMode> constexpr bool kHasFew = kMode != kWeight && kMode != kGrads;
+
 template <int kMode> cudaError_t allow_smem()
 {
-    return cudaFuncSetAttribute(pair_product_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)kPairSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(pair_product_kernel<kMode, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kPairSmemBytes);
+    if constexpr (kHasFew<kMode>)
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(pair_product_kernel<kMode, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)kPairSmemBytes);
+    return e;
 }
 
 // Per device, once: the kernels' shared memory limits, the pairs the device
@@ -800,6 +928,7 @@ int loss_setup(int *pairs, int *sm_count)
             if (e == cudaSuccess) e = allow_smem<kProb>();
             if (e == cudaSuccess) e = allow_smem<kHidden>();
             if (e == cudaSuccess) e = allow_smem<kWeight>();
+            if (e == cudaSuccess) e = allow_smem<kGrads>();
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3((unsigned)(*sm_count / 2 * 2), 1, 1);
             cfg.blockDim = dim3(kPairThreads, 1, 1);
@@ -812,7 +941,7 @@ int loss_setup(int *pairs, int *sm_count)
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             int n = 0;
-            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, pair_product_kernel<kLse>, &cfg);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, pair_product_kernel<kLse, false>, &cfg);
             if (e != cudaSuccess) return tf_topk_internal_fail_cuda((int)e);
             d.pairs = n < 1 ? 1 : n;
             if (!g_loss_encode) {
@@ -857,14 +986,30 @@ cudaLaunchConfig_t config(int grid, int threads, size_t smem, cudaStream_t strea
     return cfg;
 }
 
-template <int kMode>
-cudaError_t launch_product(const CUtensorMap &ma, const CUtensorMap &mb, const PairArgs &a, int64_t most_units,
-                           int pairs, cudaStream_t stream)
+// The ring of a product with up to kHalf rows: only the leading CTA loads
+// rows of A, as many as there are (in eights), and the stages take what is
+// left (15 x 2048 x 98592: 80 us, with whole shares of A 128).
+bool set_ring(PairArgs &a, int mode, int64_t rows)
 {
+    if (mode == kWeight || mode == kGrads || rows > kHalf) return false;
+    a.row_box = (int32_t)((rows + 7) / 8 * 8);
+    const int cols = mode == kHidden ? kHalf : a.width / 2;
+    const int fit = (int)(kRingBytes / ((uint32_t)(a.row_box + cols) * kStepK * 2));
+    a.stages = fit < kMaxStages ? fit : kMaxStages;
+    return true;
+}
+
+template <int kMode>
+cudaError_t launch_product(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &wa, const CUtensorMap &wb,
+                           PairArgs &a, int64_t most_units, int pairs, cudaStream_t stream)
+{
+    const bool few = set_ring(a, kMode, a.rows);
     cudaLaunchAttribute attr[1];
     const int64_t n = most_units < pairs ? most_units : pairs;
     const cudaLaunchConfig_t cfg = config((int)(2 * n), kPairThreads, kPairSmemBytes, stream, attr);
-    return cudaLaunchKernelEx(&cfg, pair_product_kernel<kMode>, ma, mb, a);
+    if constexpr (kHasFew<kMode>)
+        if (few) return cudaLaunchKernelEx(&cfg, pair_product_kernel<kMode, true>, ma, mb, wa, wb, a);
+    return cudaLaunchKernelEx(&cfg, pair_product_kernel<kMode, false>, ma, mb, wa, wb, a);
 }
 
 int64_t pad_rows_of(int64_t rows) { return (rows + kTileRows - 1) / kTileRows * kTileRows; }
@@ -938,13 +1083,12 @@ struct GradSpace {
 
 constexpr int64_t kProbBytes = 256ll << 20; // G of a piece, where the caller has the room
 
-// Shares of K that the hidden states' gradient is summed in: enough tiles for
-// every pair to have work, four shares at most where the rows alone give it.
-int hidden_splits(int64_t rows, int64_t dim, int pairs)
+// Shares the workspace holds sums for: few tiles want many.
+int most_splits(int64_t rows, int64_t dim, int pairs)
 {
     const int64_t tiles = pad_rows_of(rows) / kTileRows * ((dim + kTileCols - 1) / kTileCols);
-    int64_t s = (4 * (int64_t)pairs + tiles - 1) / tiles;
-    return (int)(s < 1 ? 1 : s > 32 ? 32 : s);
+    const int64_t s = (2 * (int64_t)pairs + tiles - 1) / tiles;
+    return (int)(s < 4 ? 4 : s > 32 ? 32 : s);
 }
 
 GradSpace grad_space(const void *p, int64_t rows, int64_t dim, int64_t vocab, int pairs, bool hidden, int64_t piece)
@@ -952,7 +1096,7 @@ GradSpace grad_space(const void *p, int64_t rows, int64_t dim, int64_t vocab, in
     Carver c(p);
     GradSpace s = {};
     s.piece = piece;
-    s.splits = hidden_splits(rows, dim, pairs);
+    s.splits = most_splits(rows, dim, pairs);
     const int64_t pad = pad_rows_of(rows);
     s.header = c.take<RowHeader>(1);
     s.order = c.take<int32_t>(rows);
@@ -966,15 +1110,28 @@ GradSpace grad_space(const void *p, int64_t rows, int64_t dim, int64_t vocab, in
 
 int64_t whole_piece(int64_t vocab) { return (vocab + kTileCols - 1) / kTileCols * kTileCols; }
 
-// The recommended columns of a piece: G of kProbBytes, at least one tile.
-int64_t good_piece(int64_t rows, int64_t vocab)
+// The recommended columns of a piece: G of up to kProbBytes, at least one
+// tile, and the width (from half of that on) at which the tiles of G come out
+// in the fewest rounds of the pairs, a launch costing about as much as half a
+// round.
+int64_t good_piece(int64_t rows, int64_t vocab, int pairs)
 {
-    int64_t cols = kProbBytes / (2 * pad_rows_of(rows)) / kTileCols * kTileCols;
-    if (cols < kTileCols) cols = kTileCols;
-    const int64_t all = whole_piece(vocab);
-    if (cols >= all) return all;
-    const int64_t pieces = (all + cols - 1) / cols; // of equal width
-    return ((all + pieces - 1) / pieces + kTileCols - 1) / kTileCols * kTileCols;
+    const int64_t row_tiles = pad_rows_of(rows) / kTileRows, all = whole_piece(vocab) / kTileCols;
+    int64_t most = kProbBytes / (2 * pad_rows_of(rows)) / kTileCols;
+    if (most < 1) most = 1;
+    if (most >= all) return all * kTileCols; // one piece
+    int64_t best = most;
+    double least = 1e300;
+    for (int64_t t = most; t >= 1 && 2 * t >= most; --t) {
+        const int64_t whole = all / t, rest = all % t;
+        const double cost = (double)(whole * ((row_tiles * t + pairs - 1) / pairs) + (row_tiles * rest + pairs - 1) / pairs) +
+                            0.5 * (double)(whole + (rest > 0));
+        if (cost < least) {
+            least = cost;
+            best = t;
+        }
+    }
+    return best * kTileCols;
 }
 
 bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
@@ -1013,8 +1170,9 @@ int run_loss(const void *hidden, int64_t hidden_stride, const void *weight, int6
     const cudaStream_t strm = static_cast<cudaStream_t>(stream);
     CUtensorMap ma, mb;
     const bool packed = s.packed != nullptr;
+    const int box = rows <= kHalf ? (int)((rows + 7) / 8 * 8) : kHalf; // rows of A a CTA loads (set_ring)
     if (!encode_map(&ma, packed ? s.packed : hidden, dim, packed ? pad_rows_of(rows) : rows, packed ? dim : hidden_stride,
-                    kHalf) ||
+                    box) ||
         !encode_map(&mb, weight, dim, vocab, weight_stride, width / 2))
         return tf_topk_internal_fail_cuda((int)cudaErrorInvalidValue);
     cudaLaunchAttribute attr[1];
@@ -1022,7 +1180,8 @@ int run_loss(const void *hidden, int64_t hidden_stride, const void *weight, int6
     if (packed) {
         cudaLaunchConfig_t cfg = config(1, kPrepareThreads, 0, strm, attr);
         e = cudaLaunchKernelEx(&cfg, head_loss_prepare_kernel, target, (int)(target_bytes == 8), ignore,
-                               (const float *)nullptr, (int)rows, (int)vocab, s.header, s.order, s.place);
+                               (const float *)nullptr, (int)rows, (int)vocab, (int)dim, pairs, 1, s.header, s.order,
+                               s.place);
         cfg = config((int)(rows < 4 * sms ? rows : 4 * sms), 256, 0, strm, attr);
         if (e == cudaSuccess)
             e = cudaLaunchKernelEx(&cfg, head_loss_gather_kernel, static_cast<const __nv_bfloat16 *>(hidden),
@@ -1042,12 +1201,15 @@ int run_loss(const void *hidden, int64_t hidden_stride, const void *weight, int6
     a.width = width;
     a.pad_rows = (int32_t)pad_rows_of(rows);
     a.partial = s.partial;
-    if (e == cudaSuccess) e = launch_product<kLse>(ma, mb, a, tiles * (pad_rows_of(rows) / kTileRows), pairs, strm);
+    const int64_t units = tiles * (pad_rows_of(rows) / kTileRows);
+    if (e == cudaSuccess) e = launch_product<kLse>(ma, mb, ma, mb, a, units, pairs, strm);
+    // parts of a row's sum: two halves per tile, or per pair with few rows
+    const int parts = (int)(2 * (rows > kHalf ? tiles : units < pairs ? units : pairs));
     const cudaLaunchConfig_t cfg =
         config((int)((rows + kRowsPerCta - 1) / kRowsPerCta), kRowsThreads, 0, strm, attr);
     if (e == cudaSuccess)
-        e = cudaLaunchKernelEx(&cfg, head_loss_rows_kernel, (const float2 *)s.partial, (int)(2 * tiles), a.pad_rows,
-                               (const int32_t *)s.place, static_cast<const __nv_bfloat16 *>(hidden), hidden_stride,
+        e = cudaLaunchKernelEx(&cfg, head_loss_rows_kernel, (const float2 *)s.partial,
+                               parts, a.pad_rows, (const int32_t *)s.place, static_cast<const __nv_bfloat16 *>(hidden), hidden_stride,
                                static_cast<const __nv_bfloat16 *>(weight), weight_stride, (int)dim, (int)vocab, target,
                                (int)(target_bytes == 8), ignore, (int)rows, loss, lse);
     if (e == cudaSuccess) e = cudaGetLastError();
@@ -1081,7 +1243,7 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
     const int st = loss_setup(&pairs, &sms);
     if (st != TF_TOPK_OK) return st;
     // the widest pieces the workspace holds, up to the recommended ones
-    int64_t piece = good_piece(rows, vocab);
+    int64_t piece = good_piece(rows, vocab, pairs);
     if (grad_space(workspace, rows, dim, vocab, pairs, d_hidden != nullptr, piece).bytes > workspace_bytes) {
         const size_t least = grad_space(workspace, rows, dim, vocab, pairs, d_hidden != nullptr, kTileCols).bytes;
         if (least > workspace_bytes) return TF_TOPK_ERR_SCRATCH;
@@ -1091,15 +1253,20 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
     const int64_t pad = pad_rows_of(rows);
     const cudaStream_t strm = static_cast<cudaStream_t>(stream);
     CUtensorMap packed_k, packed_n, weight_k, weight_n, prob_k, prob_m;
-    if (!encode_map(&packed_k, s.packed, dim, pad, dim, kHalf) || !encode_map(&packed_n, s.packed, dim, pad, dim, kStepK) ||
+    const int box = rows <= kHalf ? (int)((rows + 7) / 8 * 8) : kHalf; // rows of A a CTA loads (set_ring)
+    if (!encode_map(&packed_k, s.packed, dim, pad, dim, box) || !encode_map(&packed_n, s.packed, dim, pad, dim, kStepK) ||
         !encode_map(&weight_k, weight, dim, vocab, weight_stride, kHalf) ||
         !encode_map(&weight_n, weight, dim, vocab, weight_stride, kStepK) ||
-        !encode_map(&prob_k, s.prob, piece, pad, piece, kHalf) || !encode_map(&prob_m, s.prob, piece, pad, piece, kStepK))
+        !encode_map(&prob_k, s.prob, piece, pad, piece, box) || !encode_map(&prob_m, s.prob, piece, pad, piece, kStepK))
         return tf_topk_internal_fail_cuda((int)cudaErrorInvalidValue);
+    // every share of the sums starts in the first piece, the widest
+    const int64_t steps = ((vocab < piece ? vocab : piece) + kStepK - 1) / kStepK;
+    const int splits = (int)(s.splits < steps ? s.splits : steps);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = config(1, kPrepareThreads, 0, strm, attr);
     cudaError_t e = cudaLaunchKernelEx(&cfg, head_loss_prepare_kernel, target, (int)(target_bytes == 8), ignore,
-                                       grad_loss, (int)rows, (int)vocab, s.header, s.order, s.place);
+                                       grad_loss, (int)rows, (int)vocab, (int)dim, pairs, splits, s.header, s.order,
+                                       s.place);
     cfg = config((int)(pad < 4 * sms ? pad : 4 * sms), 256, 0, strm, attr);
     if (e == cudaSuccess)
         e = cudaLaunchKernelEx(&cfg, head_loss_gather_kernel, static_cast<const __nv_bfloat16 *>(hidden), hidden_stride,
@@ -1120,24 +1287,27 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
     a.prob = s.prob;
     a.sums = s.sums;
     a.d_weight = static_cast<__nv_bfloat16 *>(d_weight);
+    a.whole = dim % 16 == 0 && aligned(d_weight, 32);
     const int64_t row_tiles = pad / kTileRows, dim_tiles = (dim + kTileCols - 1) / kTileCols;
-    // every share of the sums starts in the first piece, the widest
-    const int64_t steps = ((vocab < piece ? vocab : piece) + kStepK - 1) / kStepK;
-    a.splits = (int32_t)(s.splits < steps ? s.splits : steps);
     for (int64_t begin = 0; begin < vocab && e == cudaSuccess; begin += piece) {
         a.begin = (int32_t)begin;
         a.cols = (int32_t)(vocab - begin < piece ? vocab - begin : piece);
         a.first = begin == 0;
         const int64_t col_tiles = (a.cols + kTileCols - 1) / kTileCols;
-        e = launch_product<kProb>(packed_k, weight_k, a, row_tiles * col_tiles, pairs, strm);
-        if (e == cudaSuccess && d_hidden)
-            e = launch_product<kHidden>(prob_k, weight_n, a, row_tiles * dim_tiles * a.splits, pairs, strm);
+        const int64_t hidden_units = row_tiles * dim_tiles * splits, weight_units = col_tiles * dim_tiles;
+        e = launch_product<kProb>(packed_k, weight_k, packed_k, weight_k, a, row_tiles * col_tiles, pairs, strm);
+        if (e != cudaSuccess) break;
+        if (d_hidden && d_weight && rows > kHalf) {
+            e = launch_product<kGrads>(prob_k, weight_n, prob_m, packed_n, a, hidden_units + weight_units, pairs, strm);
+            continue;
+        }
+        if (d_hidden) e = launch_product<kHidden>(prob_k, weight_n, prob_m, packed_n, a, hidden_units, pairs, strm);
         if (e == cudaSuccess && d_weight)
-            e = launch_product<kWeight>(prob_m, packed_n, a, col_tiles * dim_tiles, pairs, strm);
+            e = launch_product<kWeight>(prob_k, weight_n, prob_m, packed_n, a, weight_units, pairs, strm);
     }
     if (e == cudaSuccess && d_hidden) {
         cfg = config((int)(rows < 8 * sms ? rows : 8 * sms), 256, 0, strm, attr);
-        e = cudaLaunchKernelEx(&cfg, head_loss_hidden_kernel, (const float *)s.sums, (int)a.splits, a.pad_rows, (int)dim,
+        e = cudaLaunchKernelEx(&cfg, head_loss_hidden_kernel, (const float *)s.sums, a.pad_rows, (int)dim,
                                (const RowHeader *)s.header, (const int32_t *)s.place, (int)rows,
                                static_cast<__nv_bfloat16 *>(d_hidden));
     }
@@ -1191,7 +1361,7 @@ size_t tf_topk_head_loss_grad_bf16_workspace(int64_t rows, int32_t dim, int64_t 
 {
     int pairs = 0, sms = 0;
     if (rows < 1 || bad_shape(rows, dim, vocab) || loss_setup(&pairs, &sms) != TF_TOPK_OK) return 0;
-    return grad_space(nullptr, rows, dim, vocab, pairs, true, least ? kTileCols : good_piece(rows, vocab)).bytes + 256;
+    return grad_space(nullptr, rows, dim, vocab, pairs, true, least ? kTileCols : good_piece(rows, vocab, pairs)).bytes + 256;
 }
 
 } // extern "C"
