@@ -169,6 +169,37 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     return false;
 }
 
+// As mbar_wait, by a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile uint32_t *abort)
+{
+    const bool ok = mbar_wait(bar, parity, abort);
+    return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// Whether the phase with this parity has completed (no wait).
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(saddr(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
+// One lane of a converged warp, always the same.  The loops around TMA and
+// MMA instructions run in the whole warp and only these instructions in the
+// one lane: their operands then come from uniform registers (issued from a
+// divergent lane, an MMA took 60 cycles and the 64-step loop 530, more than
+// the products it issued).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // One box of a tensor map into this CTA's shared memory; its bytes count on
 // the leading CTA's barrier.
 __device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int32_t x, int32_t y, uint32_t bar)
@@ -383,16 +414,23 @@ __device__ __forceinline__ bool issue_tile(PairSmem &sm, uint32_t d, uint32_t id
     // 16 K steps: 32 bytes along a K-major row, 16 whole rows of an MN-major box
     constexpr uint64_t step_a = kAMN ? (16 * 128) >> 4 : 32 >> 4;
     constexpr uint64_t step_b = kBMN ? (16 * 128) >> 4 : 32 >> 4;
+    bool ready = false;
     for (int k = 0; k < steps; ++k) {
-        if (!mbar_wait(&sm.full[s], parity, abort)) return false;
-        tc_fence_after();
-        const uint64_t ad = desc_at(ring_a + s * share_a, kAMN ? kDescMN : kDescK);
-        const uint64_t bd = desc_at(ring_b + s * share_b, kBMN ? kDescMN : kDescK);
-#pragma unroll
-        for (int kk = 0; kk < kStepK / 16; ++kk)
-            mma_pair(d, ad + kk * step_a, bd + kk * step_b, idesc, k != 0 || kk != 0);
-        mma_commit_pair(&sm.empty[s]);
+        if (!ready && !mbar_wait_warp(&sm.full[s], parity, abort)) return false;
+        const uint32_t here = s;
         if (++s == stages) s = 0, parity ^= 1;
+        const bool next = mbar_test(&sm.full[s], parity); // answered while the products are issued
+        tc_fence_after();
+        const uint64_t ad = desc_at(ring_a + here * share_a, kAMN ? kDescMN : kDescK);
+        const uint64_t bd = desc_at(ring_b + here * share_b, kBMN ? kDescMN : kDescK);
+        if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kStepK / 16; ++kk)
+                mma_pair(d, ad + kk * step_a, bd + kk * step_b, idesc, k != 0 || kk != 0);
+            mma_commit_pair(&sm.empty[here]);
+        }
+        __syncwarp();
+        ready = __all_sync(0xFFFFFFFFu, next);
     }
     return true;
 }
@@ -455,40 +493,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
     if (warp == 0) {
         // ---- TMA producer
-        if (lane == 0) {
+        {
             // both CTAs' bytes; of few rows only the leading CTA has any
             const uint32_t bytes = (kFew ? share_a : 2 * share_a) + 2 * (uint32_t)half_cols * kStepK * 2;
             const bool has_a = !kFew || rank == 0;
-            uint32_t s = 0, turn = 0; // ring stage, times round the ring
+            const uint32_t full0 = peer_addr(&sm.full[0], 0); // the leading CTA's barriers
+            uint32_t s = 0, turn = 0;                         // ring stage, times round the ring
             bool ok = true;
             for (int64_t u = pair; u < units && ok; u += pairs) {
                 const Unit t = shape.at(u);
                 const bool weight = shape.of_weight(u);
                 const int row = t.m * kTileRows + (int)rank * kHalf;
+                const int col = t.n * kTileCols + (int)rank * kHalf;
+                const int voc = a.begin + t.n * a.width + (int)rank * half_cols;
                 for (int k = t.k0; k < t.k1; ++k) {
-                    if (*abort || (turn > 0 && !mbar_wait(&sm.empty[s], (turn - 1) & 1, abort))) {
-                        ok = false;
-                        break;
-                    }
-                    if (rank == 0) mbar_expect_tx(&sm.full[s], bytes);
-                    const uint32_t bar = peer_addr(&sm.full[s], 0);
-                    uint8_t *da = ring_a + s * share_a, *db = ring_b + s * share_b;
-                    if (kMode == kLse || kMode == kProb) {
-                        if (has_a) tma_load(da, &map_a, k * kStepK, row, bar);
-                        tma_load(db, &map_b, k * kStepK, a.begin + t.n * a.width + (int)rank * half_cols, bar);
-                    } else {
-                        const int col = t.n * kTileCols + (int)rank * kHalf;
-                        if (!weight) {
-                            if (has_a) tma_load(da, &map_a, k * kStepK, row, bar);
-                            tma_load(db, &map_b, col, a.begin + k * kStepK, bar);
-                            tma_load(db + kShare / 2, &map_b, col + 64, a.begin + k * kStepK, bar);
+                    ok = *abort == 0 && (turn == 0 || mbar_wait(&sm.empty[s], (turn - 1) & 1, abort));
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        if (rank == 0) mbar_expect_tx(&sm.full[s], bytes);
+                        const uint32_t bar = full0 + s * (uint32_t)sizeof(uint64_t);
+                        uint8_t *da = ring_a + s * share_a, *db = ring_b + s * share_b;
+                        const int kx = k * kStepK;
+                        if (kMode == kLse || kMode == kProb) {
+                            if (has_a) tma_load(da, &map_a, kx, row, bar);
+                            tma_load(db, &map_b, kx, voc, bar);
+                        } else if (!weight) {
+                            if (has_a) tma_load(da, &map_a, kx, row, bar);
+                            tma_load(db, &map_b, col, a.begin + kx, bar);
+                            tma_load(db + kShare / 2, &map_b, col + 64, a.begin + kx, bar);
                         } else {
-                            tma_load(da, &map_wa, row, k * kStepK, bar);
-                            tma_load(da + kShare / 2, &map_wa, row + 64, k * kStepK, bar);
-                            tma_load(db, &map_wb, col, k * kStepK, bar);
-                            tma_load(db + kShare / 2, &map_wb, col + 64, k * kStepK, bar);
+                            tma_load(da, &map_wa, row, kx, bar);
+                            tma_load(da + kShare / 2, &map_wa, row + 64, kx, bar);
+                            tma_load(db, &map_wb, col, kx, bar);
+                            tma_load(db + kShare / 2, &map_wb, col + 64, kx, bar);
                         }
                     }
+                    __syncwarp();
                     if (++s == stages) s = 0, ++turn;
                 }
             }
@@ -502,13 +543,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
     } else if (warp == 1) {
         // ---- MMA issuer (the leading CTA's)
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             const uint32_t cols = (uint32_t)half_cols * 2;
             uint32_t s = 0, parity = 0, tile = 0;
             for (int64_t u = pair; u < units; u += pairs, ++tile) {
                 const Unit t = shape.at(u);
                 const uint32_t buf = tile & 1, use = tile >> 1;
-                if (use > 0 && !mbar_wait(&sm.acc_empty[buf], (use - 1) & 1, abort)) break;
+                if (use > 0 && !mbar_wait_warp(&sm.acc_empty[buf], (use - 1) & 1, abort)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * kTileCols;
                 const int steps = t.k1 - t.k0;
@@ -523,12 +564,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     ok = issue_tile<true, true>(sm, d, instruction_desc(true, true, cols), steps, s, parity, stages,
                                                 ring_a, share_a, ring_b, share_b, abort);
                 if (!ok) break;
-                mma_commit_pair(&sm.acc_full[buf]);
+                if (elect_one()) mma_commit_pair(&sm.acc_full[buf]);
+                __syncwarp();
             }
             // every product is done before the TMEM is freed
-            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                             saddr(&sm.drain))
-                         : "memory");
+            if (elect_one())
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                 saddr(&sm.drain))
+                             : "memory");
+            __syncwarp();
             mbar_wait(&sm.drain, 0, abort);
         }
     } else {
