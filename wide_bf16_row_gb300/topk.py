@@ -412,32 +412,46 @@ def tf_topk_head_loss_grad_bf16_workspace(rows: int, dim: int, vocab: int, least
     return library().tf_topk_head_loss_grad_bf16_workspace(rows, dim, vocab, int(least))
 
 
+_torch = None
+
+
+def _need_torch():
+    """The torch module (imported on the first tensor-level call)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _head_inputs(hidden, weight, target):
     """(rows, dim, vocab, hidden row stride, weight row stride) of a head's loss, checked."""
-    import torch
-
+    torch = _torch or _need_torch()
     for name, t in (("hidden", hidden), ("weight", weight)):
-        if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        if t.dtype is not torch.bfloat16 and t.dtype not in (torch.int16, torch.uint16):
             raise TypeError(f"expected bf16 bits, got {t.dtype}")
-        if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name} must be a 2-D CUDA tensor with contiguous columns")
+        if not t.is_cuda or t.dim() != 2:
+            raise ValueError(f"{name} must be a 2-D CUDA tensor")
     rows, dim = hidden.shape
-    vocab = weight.shape[0]
-    if weight.shape[1] != dim:
+    vocab, width = weight.shape
+    hs, ws = hidden.stride(), weight.stride()
+    if width != dim:
         raise ValueError("hidden and weight disagree on dim")
-    if target.dtype not in (torch.int64, torch.int32):
+    if dim > 1 and (hs[1] != 1 or ws[1] != 1):
+        raise ValueError("hidden and weight must have contiguous columns")
+    if target.dtype is not torch.int64 and target.dtype is not torch.int32:
         raise TypeError(f"target must be int64 or int32, got {target.dtype}")
-    dev = hidden.device
-    if target.dim() != 1 or target.shape[0] != rows or not target.is_contiguous():
+    if target.shape != (rows,) or not target.is_contiguous():
         raise ValueError("target must be a contiguous [rows] tensor")
+    dev = hidden.device
     if weight.device != dev or target.device != dev:
         raise ValueError("hidden, weight and target must be on one device")
     round_up = -(-dim // 8) * 8  # the stride of a single row is free
-    return (rows, dim, vocab, hidden.stride(0) if rows > 1 else round_up, weight.stride(0) if vocab > 1 else round_up)
+    return rows, dim, vocab, hs[0] if rows > 1 else round_up, ws[0] if vocab > 1 else round_up
 
 
 def _check_out(t, shape, dtype, dev, name):
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.device != dev:
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.device != dev:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the inputs' device")
 
 
@@ -445,20 +459,17 @@ def _empty(shape, dtype, dev, stream):
     """A fresh tensor whose memory belongs to the stream the call runs on: what
     is freed there may still be in use by the work queued before it, and what a
     call frees at its end (a workspace) is reused by the work after it."""
-    import torch
-
+    torch = _torch or _need_torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _workspace(workspace, need: int, dev, stream):
-    """A caller's workspace, checked, or a fresh one of ``need`` bytes."""
-    import torch
-
+def _workspace(workspace, need, args, dev, stream):
+    """A caller's workspace, checked, or a fresh one of need(*args) bytes."""
     if workspace is None:
-        return _empty((max(need, 8),), torch.uint8, dev, stream)
+        return _empty((need(*args) or 8,), _torch.uint8, dev, stream)
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     return workspace
@@ -479,21 +490,24 @@ def head_loss_bf16(hidden, weight, target, *, ignore_index: int = -100, out=None
     ``workspace`` a CUDA tensor of at least
     ``tf_topk_head_loss_bf16_workspace(rows, dim, vocab)`` bytes.
     """
-    import torch
-
     rows, dim, vocab, hs, ws = _head_inputs(hidden, weight, target)
-    dev = hidden.device
+    torch, dev = _torch, hidden.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return head_loss_bf16(hidden, weight, target, ignore_index=ignore_index, out=out, workspace=workspace,
+                                  stream=stream)
     if out is None:
-        out = (_empty((rows,), torch.float32, dev, stream), _empty((rows,), torch.float32, dev, stream))
+        loss, lse = _empty((rows,), torch.float32, dev, stream), _empty((rows,), torch.float32, dev, stream)
     else:
-        for t, name in zip(out, ("loss", "lse")):
-            _check_out(t, (rows,), torch.float32, dev, name)
-    need = _on_device(dev, tf_topk_head_loss_bf16_workspace, rows, dim, vocab) if workspace is None else 0
-    space = _workspace(workspace, need, dev, stream)
-    _check(_on_device(dev, tf_topk_head_loss_bf16, hidden.data_ptr(), hs, weight.data_ptr(), ws, rows, dim, vocab,
-                      target.data_ptr(), target.element_size(), ignore_index, space.data_ptr(), space.nbytes,
-                      out[0].data_ptr(), out[1].data_ptr(), _stream_handle(stream, dev)))
-    return out
+        loss, lse = out
+        _check_out(loss, (rows,), torch.float32, dev, "loss")
+        _check_out(lse, (rows,), torch.float32, dev, "lse")
+    lib = _lib or library()
+    space = _workspace(workspace, lib.tf_topk_head_loss_bf16_workspace, (rows, dim, vocab), dev, stream)
+    _check(lib.tf_topk_head_loss_bf16(hidden.data_ptr(), hs, weight.data_ptr(), ws, rows, dim, vocab,
+                                      target.data_ptr(), target.element_size(), ignore_index, space.data_ptr(),
+                                      space.nbytes, loss.data_ptr(), lse.data_ptr(), _stream_handle(stream, dev)))
+    return loss, lse
 
 
 def head_loss_grad_bf16(hidden, weight, target, lse, grad_loss, *, ignore_index: int = -100, hidden_grad: bool = True,
@@ -509,29 +523,34 @@ def head_loss_grad_bf16(hidden, weight, target, lse, grad_loss, *, ignore_index:
     (None for one not wanted) and ``workspace`` a CUDA tensor of any size from
     ``tf_topk_head_loss_grad_bf16_workspace(rows, dim, vocab, True)`` bytes on.
     """
-    import torch
-
     rows, dim, vocab, hs, ws = _head_inputs(hidden, weight, target)
-    dev = hidden.device
+    torch, dev = _torch, hidden.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return head_loss_grad_bf16(hidden, weight, target, lse, grad_loss, ignore_index=ignore_index,
+                                       hidden_grad=hidden_grad, weight_grad=weight_grad, out=out, workspace=workspace,
+                                       stream=stream)
     _check_out(lse, (rows,), torch.float32, dev, "lse")
     _check_out(grad_loss, (rows,), torch.float32, dev, "grad_loss")
     if not hidden_grad and not weight_grad:
         return None, None
     if out is None:
-        out = (_empty((rows, dim), torch.bfloat16, dev, stream) if hidden_grad else None,
-               _empty((vocab, dim), torch.bfloat16, dev, stream) if weight_grad else None)
+        dh = _empty((rows, dim), torch.bfloat16, dev, stream) if hidden_grad else None
+        dw = _empty((vocab, dim), torch.bfloat16, dev, stream) if weight_grad else None
     else:
-        for t, shape, want, name in ((out[0], (rows, dim), hidden_grad, "grad_hidden"),
-                                     (out[1], (vocab, dim), weight_grad, "grad_weight")):
-            if want:
-                _check_out(t, shape, torch.bfloat16, dev, name)
-    need = (_on_device(dev, tf_topk_head_loss_grad_bf16_workspace, rows, dim, vocab) if workspace is None else 0)
-    space = _workspace(workspace, need, dev, stream)
-    _check(_on_device(dev, tf_topk_head_loss_grad_bf16, hidden.data_ptr(), hs, weight.data_ptr(), ws, rows, dim, vocab,
-                      target.data_ptr(), target.element_size(), ignore_index, lse.data_ptr(), grad_loss.data_ptr(),
-                      space.data_ptr(), space.nbytes, out[0].data_ptr() if hidden_grad else None,
-                      out[1].data_ptr() if weight_grad else None, _stream_handle(stream, dev)))
-    return (out[0] if hidden_grad else None, out[1] if weight_grad else None)
+        dh, dw = out[0] if hidden_grad else None, out[1] if weight_grad else None
+        if hidden_grad:
+            _check_out(dh, (rows, dim), torch.bfloat16, dev, "grad_hidden")
+        if weight_grad:
+            _check_out(dw, (vocab, dim), torch.bfloat16, dev, "grad_weight")
+    lib = _lib or library()
+    space = _workspace(workspace, lib.tf_topk_head_loss_grad_bf16_workspace, (rows, dim, vocab, 0), dev, stream)
+    _check(lib.tf_topk_head_loss_grad_bf16(hidden.data_ptr(), hs, weight.data_ptr(), ws, rows, dim, vocab,
+                                           target.data_ptr(), target.element_size(), ignore_index, lse.data_ptr(),
+                                           grad_loss.data_ptr(), space.data_ptr(), space.nbytes,
+                                           dh.data_ptr() if hidden_grad else None,
+                                           dw.data_ptr() if weight_grad else None, _stream_handle(stream, dev)))
+    return dh, dw
 
 
 ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
@@ -554,19 +573,27 @@ def tf_topk_route_grad(logits: int, dtype: int, tokens: int, experts: int, row_s
                                         renormalize, scale, out_grad_logits, stream)
 
 
+_logit_codes = None
+
+
 def _router_logits(logits, score: str):
     """(dtype code, tokens, experts, row stride, score code) of a router's logits, checked."""
-    import torch
-
-    code = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}.get(logits.dtype)
+    global _logit_codes
+    if _logit_codes is None:
+        torch = _need_torch()
+        _logit_codes = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
+    code, how = _logit_codes.get(logits.dtype), ROUTE_SCORES.get(score)
     if code is None:
         raise TypeError(f"logits must be bfloat16, float16 or float32, got {logits.dtype}")
-    if score not in ROUTE_SCORES:
+    if how is None:
         raise ValueError(f"score must be one of {tuple(ROUTE_SCORES)}, got {score!r}")
-    if not logits.is_cuda or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError("logits must be a 2-D CUDA tensor with contiguous columns")
+    if not logits.is_cuda or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D CUDA tensor")
     tokens, experts = logits.shape
-    return code, tokens, experts, logits.stride(0) if tokens > 1 else experts, ROUTE_SCORES[score]
+    stride = logits.stride()
+    if experts > 1 and stride[1] != 1:
+        raise ValueError("logits must have contiguous columns")
+    return code, tokens, experts, stride[0] if tokens > 1 else experts, how
 
 
 def route_experts(logits, k: int, *, bias=None, score: str = "softmax", groups: int = 1, groups_kept: int | None = None,
@@ -586,25 +613,30 @@ def route_experts(logits, k: int, *, bias=None, score: str = "softmax", groups: 
     grows by the tokens each expert was chosen for.  ``out`` may supply idx and
     weight.
     """
-    import torch
-
     code, tokens, experts, stride, how = _router_logits(logits, score)
-    dev = logits.device
+    torch, dev = _torch, logits.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return route_experts(logits, k, bias=bias, score=score, groups=groups, groups_kept=groups_kept,
+                                 group_best=group_best, renormalize=renormalize, scale=scale, load=load, out=out,
+                                 stream=stream)
     if bias is not None:
         _check_out(bias, (experts,), torch.float32, dev, "bias")
     if load is not None:
         _check_out(load, (experts,), torch.int32, dev, "load")
     if out is None:
-        out = (_empty((tokens, k), torch.int32, dev, stream), _empty((tokens, k), torch.float32, dev, stream))
+        # a bad k is the library's to refuse
+        shape = (tokens, k if k > 0 else 0)
+        idx, weight = _empty(shape, torch.int32, dev, stream), _empty(shape, torch.float32, dev, stream)
     else:
-        _check_out(out[0], (tokens, k), torch.int32, dev, "idx")
-        _check_out(out[1], (tokens, k), torch.float32, dev, "weight")
-    _check(_on_device(dev, tf_topk_route, logits.data_ptr(), code, tokens, experts, stride, k,
-                      None if bias is None else bias.data_ptr(), how, groups,
-                      groups if groups_kept is None else groups_kept, group_best, int(renormalize), scale,
-                      out[0].data_ptr(), out[1].data_ptr(), None if load is None else load.data_ptr(),
-                      _stream_handle(stream, dev)))
-    return out
+        idx, weight = out
+        _check_out(idx, (tokens, k), torch.int32, dev, "idx")
+        _check_out(weight, (tokens, k), torch.float32, dev, "weight")
+    _check((_lib or library()).tf_topk_route(
+        logits.data_ptr(), code, tokens, experts, stride, k, None if bias is None else bias.data_ptr(), how, groups,
+        groups if groups_kept is None else groups_kept, group_best, bool(renormalize), scale, idx.data_ptr(),
+        weight.data_ptr(), None if load is None else load.data_ptr(), _stream_handle(stream, dev)))
+    return idx, weight
 
 
 def route_experts_grad(logits, idx, grad_weight, *, score: str = "softmax", renormalize: bool = True,
@@ -613,10 +645,12 @@ def route_experts_grad(logits, idx, grad_weight, *, score: str = "softmax", reno
     fixed: ``idx`` int32 [tokens, k] as it returned it, ``grad_weight`` float32
     [tokens, k], the other arguments as in its call.  Returns the gradient
     [tokens, experts] in the logits' dtype (zero where nothing flows)."""
-    import torch
-
     code, tokens, experts, stride, how = _router_logits(logits, score)
-    dev = logits.device
+    torch, dev = _torch, logits.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return route_experts_grad(logits, idx, grad_weight, score=score, renormalize=renormalize, scale=scale,
+                                      out=out, stream=stream)
     if idx.dim() != 2 or idx.shape[0] != tokens:
         raise ValueError("idx must be [tokens, k]")
     k = idx.shape[1]
@@ -626,9 +660,9 @@ def route_experts_grad(logits, idx, grad_weight, *, score: str = "softmax", reno
         out = _empty((tokens, experts), logits.dtype, dev, stream)
     else:
         _check_out(out, (tokens, experts), logits.dtype, dev, "out")
-    _check(_on_device(dev, tf_topk_route_grad, logits.data_ptr(), code, tokens, experts, stride, k, idx.data_ptr(),
-                      grad_weight.data_ptr(), how, int(renormalize), scale, out.data_ptr(),
-                      _stream_handle(stream, dev)))
+    _check((_lib or library()).tf_topk_route_grad(
+        logits.data_ptr(), code, tokens, experts, stride, k, idx.data_ptr(), grad_weight.data_ptr(), how,
+        bool(renormalize), scale, out.data_ptr(), _stream_handle(stream, dev)))
     return out
 
 
