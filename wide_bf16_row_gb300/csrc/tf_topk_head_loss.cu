@@ -69,11 +69,13 @@ constexpr int kHalf = 128;                           // one CTA's share of eithe
 constexpr int kStepK = 64;                           // K per ring stage: one 128-byte swizzle row of bf16
 constexpr uint32_t kShare = kHalf * kStepK * 2;      // 16 KB: one CTA's whole share of an operand per stage
 constexpr int kMaxStages = 16;
-constexpr uint32_t kRingBytes = 200 * 1024;          // leaves an SM room for the small kernels queued behind
+constexpr uint32_t kRingBytes = 192 * 1024;
 constexpr int kEpiWarps = 8;
 constexpr int kPairThreads = 32 * (2 + kEpiWarps);
 constexpr int kTmemCols = 2 * kTileCols;
 constexpr int kChunk = 32;                           // accumulator columns an epilogue thread takes at a time
+constexpr uint32_t kStagingWarp = 32 * kChunk * 4;   // an epilogue warp's outgoing chunk of fp32 (or two of bf16)
+constexpr uint32_t kStagingBytes = kEpiWarps * kStagingWarp;
 constexpr int kGroupRows = 16;                       // row tiles that share the sweep over the columns
 constexpr uint32_t kWaitLimit = 1u << 20;
 constexpr uint32_t kFaultWait = 1;
@@ -113,14 +115,9 @@ struct PairArgs {
     int32_t row_box;          // few rows: rows of A that the leading CTA loads (the peer none), a multiple of 8
     int32_t pad_rows;         // row pitch of `partial`
     int32_t first;            // kHidden: the sums start here
-    int32_t whole;            // kWeight: rows of d_weight are whole 32-byte sectors
-    int32_t pitch;            // row pitch of G
     float2 *partial;          // kLse: [2 * column tiles][pad_rows]: reference exponent, sum
     const float *lse;         // kProb [rows]
     const float *grad;        // kProb [rows]
-    __nv_bfloat16 *prob;      // kProb: G [pad_rows][pitch]
-    float *sums;              // kHidden: [splits][pad_rows][dim]
-    __nv_bfloat16 *d_weight;  // kWeight: [vocab][dim]
 };
 
 // ---------------------------------------------------------------- PTX helpers
@@ -293,21 +290,48 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// A whole 32-byte sector per thread: threads of a warp write rows of their
-// own, and 16-byte pieces of a sector cost the L2 twice (measured on G of
-// 3686 x 98592: 1062 us with 16-byte stores, 940 with these, 905 without any).
-__device__ __forceinline__ void store32(void *p, const uint32_t *v)
+// A warp's chunk of 32 rows goes out by TMA from shared memory: the warp
+// writes its rows there (16-byte pieces swizzled as the tensor map expects,
+// so that eight lanes meet eight bank groups), and one lane sends the box.
+// (G of 3686 x 98592: 1062 us with 16-byte stores by row, 940 with 32-byte
+// ones, 905 without any.)  The map cuts what lies past its extents.
+__device__ __forceinline__ void send_box(const CUtensorMap *map, const void *box, int32_t x, int32_t y)
 {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                 "r"(saddr(box)), "r"(x), "r"(y)
                  : "memory");
 }
-// Adds four floats to memory in the L2, without waiting for the old ones.
-__device__ __forceinline__ void add16(float *p, const float *v)
+// The same, added to what is there (fp32, in the L2).
+__device__ __forceinline__ void add_box(const CUtensorMap *map, const void *box, int32_t x, int32_t y)
 {
-    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-                 "f"(v[3])
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                 "r"(saddr(box)), "r"(x), "r"(y)
                  : "memory");
+}
+__device__ __forceinline__ void box_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All but the last `kLeft` boxes of this thread have been read from shared memory.
+template <int kLeft> __device__ __forceinline__ void box_read_wait()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ void box_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// This lane's row of a 64-byte swizzled box: 32 bf16.
+__device__ __forceinline__ void put_row_bf16(uint8_t *box, int lane, const uint32_t (&v)[kChunk / 2])
+{
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4 *>(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
+// This lane's row of a 128-byte swizzled box: 32 fp32.
+__device__ __forceinline__ void put_row_f32(uint8_t *box, int lane, const float (&v)[kChunk])
+{
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<float4 *>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+            make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
 }
 
 __device__ __forceinline__ int64_t target_of(const void *target, int target64, int row)
@@ -438,7 +462,9 @@ __device__ __forceinline__ bool issue_tile(PairSmem &sm, uint32_t d, uint32_t id
 template <int kMode, bool kFew>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                        const __grid_constant__ CUtensorMap map_wa, const __grid_constant__ CUtensorMap map_wb, PairArgs a)
+                        const __grid_constant__ CUtensorMap map_wa, const __grid_constant__ CUtensorMap map_wb,
+                        const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_wout,
+                        PairArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -452,7 +478,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t share_b = kFew ? (uint32_t)half_cols * kStepK * 2 : kShare;
     const uint32_t stages = kFew ? (uint32_t)a.stages : kRingBytes / (2 * kShare);
     uint8_t *ring_a = ring, *ring_b = ring + stages * share_a;
-    PairSmem &sm = *reinterpret_cast<PairSmem *>(ring + stages * (share_a + share_b));
+    uint8_t *staging = ring + kRingBytes; // 1024-byte aligned
+    PairSmem &sm = *reinterpret_cast<PairSmem *>(staging + (kMode == kLse ? 0 : kStagingBytes));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = blockIdx.x & 1; // in the pair; rank 0 leads
     const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -579,6 +606,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // ---- epilogue
         const int q = warp & 3, h = (warp - 2) >> 2;
         const uint32_t acc_empty0 = peer_addr(&sm.acc_empty[0], 0), acc_empty1 = peer_addr(&sm.acc_empty[1], 0);
+        uint8_t *box = staging + (warp - 2) * kStagingWarp; // this warp's
+        uint32_t sent = 0;                                  // bf16 boxes alternate between its halves
+        const auto send_bf16 = [&](const CUtensorMap *map, const uint32_t (&v)[kChunk / 2], int x, int y, bool any) {
+            uint8_t *half = box + (sent & 1) * (kStagingWarp / 2);
+            if (elect_one()) box_read_wait<1>();
+            __syncwarp();
+            put_row_bf16(half, lane, v);
+            fence_async_proxy();
+            __syncwarp();
+            if (elect_one()) {
+                if (any) send_box(map, half, x, y);
+                box_commit();
+            }
+            __syncwarp();
+            ++sent;
+        };
         uint32_t tile = 0;
         // kLse: reference exponent (base 2), its logit, sum of exp2; with few
         // rows over all of the pair's tiles
@@ -607,6 +650,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const uint32_t lanes = tmem + buf * kTileCols + ((uint32_t)(32 * q) << 16);
             // columns of the tile that this thread takes
             const int c0 = h * half_cols, chunks = no_rows ? 0 : half_cols / kChunk;
+            if (kMode == kGrads) { // boxes of the other kind may still be on their way out
+                if (elect_one()) box_read_wait<0>();
+                __syncwarp();
+            }
             if (kMode == kLse) {
                 if (!kFew) ref = 0.0f, top = -INFINITY, sum = 0.0f;
                 for (int c = 0; c < chunks; ++c) {
@@ -655,27 +702,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     }
 #pragma unroll
                     for (int i = 0; i < kChunk / 2; ++i) out[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-                    __nv_bfloat16 *dst = a.prob + (size_t)row * a.pitch + col;
-#pragma unroll
-                    for (int i = 0; i < kChunk / 16; ++i) store32(dst + 16 * i, out + 8 * i);
+                    send_bf16(&map_out, out, col, row - lane, true);
                 }
             } else if (!shape.of_weight(u)) {
                 for (int c = 0; c < chunks; ++c) {
                     float x[kChunk];
                     tmem_load(lanes + c0 + c * kChunk, x);
                     const int col = t.n * kTileCols + c0 + c * kChunk;
-                    if (row < count) {
-                        float *dst = a.sums + ((size_t)t.split * a.pad_rows + row) * a.dim + col;
-                        if (a.first) {
-#pragma unroll
-                            for (int i = 0; i < kChunk / 8; ++i)
-                                if (col + 8 * i < a.dim) store32(dst + 8 * i, reinterpret_cast<const uint32_t *>(x) + 8 * i);
-                        } else { // one addition per element and launch: the order is the pieces'
-#pragma unroll
-                            for (int i = 0; i < kChunk / 4; ++i)
-                                if (col + 4 * i < a.dim) add16(dst + 4 * i, x + 4 * i);
-                        }
+                    const bool any = row - lane < count && col < a.dim; // rows past the count get sums nothing reads
+                    if (elect_one()) box_read_wait<0>();
+                    __syncwarp();
+                    put_row_f32(box, lane, x);
+                    fence_async_proxy();
+                    __syncwarp();
+                    if (elect_one() && any) {
+                        const int y = t.split * a.pad_rows + row - lane;
+                        if (a.first) send_box(&map_out, box, col, y);
+                        else add_box(&map_out, box, col, y); // once per element and launch: the order is the pieces'
+                        box_commit();
                     }
+                    __syncwarp();
                 }
             } else {
                 const float scale = a.header->grad_scale;
@@ -683,29 +729,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     float x[kChunk];
                     tmem_load(lanes + c0 + c * kChunk, x);
                     const int col = t.n * kTileCols + c0 + c * kChunk;
-                    if (row < a.cols) {
-                        __nv_bfloat16 *dst = a.d_weight + ((size_t)a.begin + row) * a.dim + col;
-                        uint32_t out[kChunk / 2];
+                    uint32_t out[kChunk / 2];
 #pragma unroll
-                        for (int i = 0; i < kChunk / 2; ++i) out[i] = pack_bf16(x[2 * i] * scale, x[2 * i + 1] * scale);
-                        if (a.whole) {
-#pragma unroll
-                            for (int i = 0; i < kChunk / 16; ++i)
-                                if (col + 16 * i < a.dim) store32(dst + 16 * i, out + 8 * i);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < kChunk / 8; ++i)
-                                if (col + 8 * i < a.dim)
-                                    *reinterpret_cast<uint4 *>(dst + 8 * i) =
-                                        make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
-                        }
-                    }
+                    for (int i = 0; i < kChunk / 2; ++i) out[i] = pack_bf16(x[2 * i] * scale, x[2 * i + 1] * scale);
+                    send_bf16(&map_wout, out, col, a.begin + row - lane, col < a.dim && row - lane < a.cols);
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(buf ? acc_empty1 : acc_empty0);
         }
+        if (kMode != kLse) box_wait(); // what this lane sent is written
         if (kMode == kLse && kFew) {
             const int row = (int)rank * kHalf + 32 * q + lane;
             if (row < count)
@@ -930,7 +964,8 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- host side
 
-constexpr size_t kPairSmemBytes = 1024 + (size_t)kRingBytes + sizeof(PairSmem);
+constexpr size_t kPairSmemBytes = 1024 + (size_t)kRingBytes + kStagingBytes + sizeof(PairSmem);
+constexpr size_t kLseSmemBytes = kPairSmemBytes - kStagingBytes; // leaves an SM room for the rows' kernel
 static_assert(kPairSmemBytes <= 227 * 1024, "the pair kernel's shared memory fits one CTA");
 
 constexpr int kMaxDevices = 64;
@@ -976,7 +1011,7 @@ int loss_setup(int *pairs, int *sm_count)
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3((unsigned)(*sm_count / 2 * 2), 1, 1);
             cfg.blockDim = dim3(kPairThreads, 1, 1);
-            cfg.dynamicSmemBytes = kPairSmemBytes;
+            cfg.dynamicSmemBytes = kPairSmemBytes; // kLse's is less
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
             attr[0].val.clusterDim.x = 2;
@@ -1016,6 +1051,20 @@ bool encode_map(CUtensorMap *map, const void *p, int64_t inner, int64_t outer, i
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The map of an output: boxes of kChunk x 32, bf16 (64-byte swizzle) or fp32
+// (128-byte swizzle); what lies past either extent is not written.
+bool encode_out(CUtensorMap *map, const void *p, bool f32, int64_t inner, int64_t outer)
+{
+    cuuint64_t gdim[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+    cuuint64_t gstride[1] = {(cuuint64_t)inner * (f32 ? 4 : 2)};
+    cuuint32_t box[2] = {(cuuint32_t)kChunk, 32};
+    cuuint32_t estride[2] = {1, 1};
+    return g_loss_encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                         const_cast<void *>(p), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaLaunchConfig_t config(int grid, int threads, size_t smem, cudaStream_t stream, cudaLaunchAttribute *attr)
 {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1029,6 +1078,11 @@ cudaLaunchConfig_t config(int grid, int threads, size_t smem, cudaStream_t strea
     cfg.numAttrs = 1;
     return cfg;
 }
+
+// Tensor maps of a product: operands and output, and those of kGrads' second kind.
+struct PairMaps {
+    CUtensorMap a, b, wa, wb, out, wout;
+};
 
 // The ring of a product with up to kHalf rows: only the leading CTA loads
 // rows of A, as many as there are (in eights), and the stages take what is
@@ -1044,16 +1098,15 @@ bool set_ring(PairArgs &a, int mode, int64_t rows)
 }
 
 template <int kMode>
-cudaError_t launch_product(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &wa, const CUtensorMap &wb,
-                           PairArgs &a, int64_t most_units, int pairs, cudaStream_t stream)
+cudaError_t launch_product(const PairMaps &m, PairArgs &a, int64_t most_units, int pairs, cudaStream_t stream)
 {
     const bool few = set_ring(a, kMode, a.rows);
     cudaLaunchAttribute attr[1];
     const int64_t n = most_units < pairs ? most_units : pairs;
-    const cudaLaunchConfig_t cfg = config((int)(2 * n), kPairThreads, kPairSmemBytes, stream, attr);
+    const cudaLaunchConfig_t cfg = config((int)(2 * n), kPairThreads, kMode == kLse ? kLseSmemBytes : kPairSmemBytes, stream, attr);
     if constexpr (kHasFew<kMode>)
-        if (few) return cudaLaunchKernelEx(&cfg, pair_product_kernel<kMode, true>, ma, mb, wa, wb, a);
-    return cudaLaunchKernelEx(&cfg, pair_product_kernel<kMode, false>, ma, mb, wa, wb, a);
+        if (few) return cudaLaunchKernelEx(&cfg, pair_product_kernel<kMode, true>, m.a, m.b, m.wa, m.wb, m.out, m.wout, a);
+    return cudaLaunchKernelEx(&cfg, pair_product_kernel<kMode, false>, m.a, m.b, m.wa, m.wb, m.out, m.wout, a);
 }
 
 int64_t pad_rows_of(int64_t rows) { return (rows + kTileRows - 1) / kTileRows * kTileRows; }
@@ -1212,12 +1265,12 @@ int run_loss(const void *hidden, int64_t hidden_stride, const void *weight, int6
     const LossSpace s = loss_space(workspace, rows, dim, 2 * tiles);
     if (s.bytes > workspace_bytes) return TF_TOPK_ERR_SCRATCH;
     const cudaStream_t strm = static_cast<cudaStream_t>(stream);
-    CUtensorMap ma, mb;
+    PairMaps m = {};
     const bool packed = s.packed != nullptr;
     const int box = rows <= kHalf ? (int)((rows + 7) / 8 * 8) : kHalf; // rows of A a CTA loads (set_ring)
-    if (!encode_map(&ma, packed ? s.packed : hidden, dim, packed ? pad_rows_of(rows) : rows, packed ? dim : hidden_stride,
+    if (!encode_map(&m.a, packed ? s.packed : hidden, dim, packed ? pad_rows_of(rows) : rows, packed ? dim : hidden_stride,
                     box) ||
-        !encode_map(&mb, weight, dim, vocab, weight_stride, width / 2))
+        !encode_map(&m.b, weight, dim, vocab, weight_stride, width / 2))
         return tf_topk_internal_fail_cuda((int)cudaErrorInvalidValue);
     cudaLaunchAttribute attr[1];
     cudaError_t e = cudaSuccess;
@@ -1246,7 +1299,7 @@ int run_loss(const void *hidden, int64_t hidden_stride, const void *weight, int6
     a.pad_rows = (int32_t)pad_rows_of(rows);
     a.partial = s.partial;
     const int64_t units = tiles * (pad_rows_of(rows) / kTileRows);
-    if (e == cudaSuccess) e = launch_product<kLse>(ma, mb, ma, mb, a, units, pairs, strm);
+    if (e == cudaSuccess) e = launch_product<kLse>(m, a, units, pairs, strm);
     // parts of a row's sum: two halves per tile, or per pair with few rows
     const int parts = (int)(2 * (rows > kHalf ? tiles : units < pairs ? units : pairs));
     const cudaLaunchConfig_t cfg =
@@ -1296,12 +1349,16 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
     const GradSpace s = grad_space(workspace, rows, dim, vocab, pairs, d_hidden != nullptr, piece);
     const int64_t pad = pad_rows_of(rows);
     const cudaStream_t strm = static_cast<cudaStream_t>(stream);
-    CUtensorMap packed_k, packed_n, weight_k, weight_n, prob_k, prob_m;
     const int box = rows <= kHalf ? (int)((rows + 7) / 8 * 8) : kHalf; // rows of A a CTA loads (set_ring)
-    if (!encode_map(&packed_k, s.packed, dim, pad, dim, box) || !encode_map(&packed_n, s.packed, dim, pad, dim, kStepK) ||
-        !encode_map(&weight_k, weight, dim, vocab, weight_stride, kHalf) ||
-        !encode_map(&weight_n, weight, dim, vocab, weight_stride, kStepK) ||
-        !encode_map(&prob_k, s.prob, piece, pad, piece, box) || !encode_map(&prob_m, s.prob, piece, pad, piece, kStepK))
+    PairMaps prob = {}, grads = {};
+    if (!encode_map(&prob.a, s.packed, dim, pad, dim, box) || !encode_map(&prob.b, weight, dim, vocab, weight_stride, kHalf) ||
+        !encode_out(&prob.out, s.prob, false, piece, pad) ||
+        (d_hidden && (!encode_map(&grads.a, s.prob, piece, pad, piece, box) ||
+                      !encode_map(&grads.b, weight, dim, vocab, weight_stride, kStepK) ||
+                      !encode_out(&grads.out, s.sums, true, dim, pad * s.splits))) ||
+        (d_weight && (!encode_map(&grads.wa, s.prob, piece, pad, piece, kStepK) ||
+                      !encode_map(&grads.wb, s.packed, dim, pad, dim, kStepK) ||
+                      !encode_out(&grads.wout, d_weight, false, dim, vocab))))
         return tf_topk_internal_fail_cuda((int)cudaErrorInvalidValue);
     // every share of the sums starts in the first piece, the widest
     const int64_t steps = ((vocab < piece ? vocab : piece) + kStepK - 1) / kStepK;
@@ -1325,13 +1382,8 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
     a.vocab = (int32_t)vocab;
     a.width = kTileCols;
     a.pad_rows = (int32_t)pad;
-    a.pitch = (int32_t)piece;
     a.lse = lse;
     a.grad = grad_loss;
-    a.prob = s.prob;
-    a.sums = s.sums;
-    a.d_weight = static_cast<__nv_bfloat16 *>(d_weight);
-    a.whole = dim % 16 == 0 && aligned(d_weight, 32);
     const int64_t row_tiles = pad / kTileRows, dim_tiles = (dim + kTileCols - 1) / kTileCols;
     for (int64_t begin = 0; begin < vocab && e == cudaSuccess; begin += piece) {
         a.begin = (int32_t)begin;
@@ -1339,15 +1391,15 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
         a.first = begin == 0;
         const int64_t col_tiles = (a.cols + kTileCols - 1) / kTileCols;
         const int64_t hidden_units = row_tiles * dim_tiles * splits, weight_units = col_tiles * dim_tiles;
-        e = launch_product<kProb>(packed_k, weight_k, packed_k, weight_k, a, row_tiles * col_tiles, pairs, strm);
+        e = launch_product<kProb>(prob, a, row_tiles * col_tiles, pairs, strm);
         if (e != cudaSuccess) break;
         if (d_hidden && d_weight && rows > kHalf) {
-            e = launch_product<kGrads>(prob_k, weight_n, prob_m, packed_n, a, hidden_units + weight_units, pairs, strm);
+            e = launch_product<kGrads>(grads, a, hidden_units + weight_units, pairs, strm);
             continue;
         }
-        if (d_hidden) e = launch_product<kHidden>(prob_k, weight_n, prob_m, packed_n, a, hidden_units, pairs, strm);
+        if (d_hidden) e = launch_product<kHidden>(grads, a, hidden_units, pairs, strm);
         if (e == cudaSuccess && d_weight)
-            e = launch_product<kWeight>(prob_k, weight_n, prob_m, packed_n, a, weight_units, pairs, strm);
+            e = launch_product<kWeight>(grads, a, weight_units, pairs, strm);
     }
     if (e == cudaSuccess && d_hidden) {
         cfg = config((int)(rows < 8 * sms ? rows : 8 * sms), 256, 0, strm, attr);
