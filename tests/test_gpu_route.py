@@ -106,6 +106,37 @@ def test_groups(dtype, score, best, experts, groups, kept, k, with_bias):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups,kept,k,with_bias", [
+    (256, 8, 4, 8, True), (256, 1, 1, 8, False), (128, 8, 3, 7, False), (100, 1, 1, 5, True), (64, 4, 2, 6, True),
+    (60, 1, 1, 4, False), (32, 2, 1, 3, True), (4, 1, 1, 8, True), (240, 5, 2, 1, False), (256, 16, 15, 8, True)])
+def test_enough_tokens_for_four_lanes_each(dtype, score, experts, groups, kept, k, with_bias):
+    """At least eight tokens per SM: the kernel that gives a token four lanes, with masked experts, empty rows and a
+    ragged last warp."""
+    bias = _bias(experts, 3) if with_bias else None
+    x = _logits(1301, experts, dtype, seed=experts + groups, masked=0.1)
+    check(x, k, bias, score, groups, kept, 2 - k % 2, renorm=k != 8 or with_bias, scale=1.5)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_ties_and_extremes_with_four_lanes_each(score):
+    import torch
+    x = torch.zeros(1301, 64, device="cuda")
+    check(x, 6, None, score)
+    check(x, 6, torch.zeros(64, device="cuda"), score, 4, 2, 2)
+    coarse = (_logits(1301, 64, "fp32", 5) * 2).round() / 2
+    check(coarse, 6, None, score, 4, 2, 2)
+    check(coarse, 6, torch.full((64,), 0.25, device="cuda"), score)
+    far = _logits(1301, 64, "fp32", 6) * 200
+    far[:, ::5] = float("inf")
+    far[:, 1::7] = -float("inf")
+    far[1::2] -= 3000
+    check(far, 8, None, score)
+    check(far, 8, None, score, renorm=False)
+    check(far, 8, _bias(64, 9, 5.0), score, 4, 3, 2)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_masked(dtype, score, renorm):
     """Experts out of reach, rows that have fewer than k or none."""

@@ -323,6 +323,16 @@ __device__ __forceinline__ void load_row(const T *row, int experts, int lane, bo
     for (int j = 0; j < P; ++j) x[j] = in_reach(x[j]) ? fminf(x[j], FLT_MAX) : -INFINITY;
 }
 
+// A lane's biases; -inf where no choice can come of one.
+template <int P> __device__ __forceinline__ void load_bias(const RouteArgs &a, int lane, float (&bias)[P])
+{
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        bias[j] = a.bias && lane * P + j < a.experts ? a.bias[lane * P + j] : 0.0f;
+        bias[j] = bias[j] > -INFINITY ? bias[j] : -INFINITY;
+    }
+}
+
 // Largest and second largest (in that order) of two such pairs.
 __device__ __forceinline__ void join_best_two(float &m1, float &m2, float o1, float o2)
 {
@@ -359,6 +369,12 @@ template <int P> struct ShortKey {
     // the part of a value that the cut bits may hold
     static constexpr float kCut = (float)(32 * P) / (float)(1 << 23);
     __device__ static uint32_t make(float v, int expert) { return (order_key(v) & ~kMask) | (kMask - expert); }
+    // of a choice that is no -0, -inf included
+    __device__ static uint32_t make_plain(float v, int expert)
+    {
+        const uint32_t b = __float_as_uint(v);
+        return ((b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) & ~kMask) | (kMask - expert);
+    }
     __device__ static float value(uint32_t key) { return key_value(key & ~kMask); }
     __device__ static int expert(uint32_t key) { return (int)(kMask - (key & kMask)); }
 };
@@ -493,28 +509,21 @@ __device__ __noinline__ int settle(const T *row, const RouteArgs &a, int expert,
     return chosen;
 }
 
-// One warp per token.  A lane sorts its best few experts' short keys; k warp
-// maxima over the lanes' best then name the choices in order.  It is bound by
-// the instructions of the scan over E logits (two special-function ones per
-// sigmoid) and of the k rounds, not by the row's bytes.
+// What of a row's softmax the weights need.
+struct RowSoftmax {
+    float top, inverse; // exp(x - top) * inverse
+};
+
+// The choice of one row by a whole warp, from its logits (load_row) in `c`
+// (overwritten): lane i < k gets the i-th expert or -1.  A lane sorts its best
+// few experts' short keys; k warp maxima over the lanes' best then name the
+// choices in order.
 template <typename T, int P>
-__global__ void __launch_bounds__(kRouteThreads, kRouteCtas<P>) route_kernel(const T *__restrict__ logits, RouteArgs a)
+__device__ __forceinline__ int choose_row(const T *row, const RouteArgs &a, float (&c)[P], const float (&bias)[P],
+                                          int32_t *place, RowSoftmax &soft)
 {
-    __shared__ int32_t count[kMaxExperts];
-    __shared__ int32_t place[kRouteWarps][32];
     using Key = ShortKey<P>;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (a.load) {
-        for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) count[e] = 0;
-        __syncthreads();
-    }
-    grid_dependency_wait();
-    float bias[P]; // -inf where no choice can come of it
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-        bias[j] = a.bias && lane * P + j < a.experts ? a.bias[lane * P + j] : 0.0f;
-        bias[j] = bias[j] > -INFINITY ? bias[j] : -INFINITY;
-    }
+    const int lane = threadIdx.x & 31;
     const int per = a.experts / a.groups;
     // lanes that hold one group, when whole lanes do and their count is a power of two
     const int group_lanes = per % P == 0 && ((per / P) & (per / P - 1)) == 0 ? per / P : 0;
@@ -522,6 +531,137 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<P>) route_kernel(con
     // errors of a choice: of the score, and relative to the sum with the bias
     const float error = !scored ? 0.0f : a.softmax ? kSoftmaxError : kSigmoidError;
     const float part = scored ? kSumError + 2.0f * Key::kCut : 0.0f;
+    soft = {0.0f, 1.0f};
+    float &top = soft.top, &inverse = soft.inverse;
+    if (a.softmax && (scored || !a.renorm)) {
+        float m = c[0], sum = 0.0f, q[P];
+#pragma unroll
+        for (int j = 1; j < P; ++j) m = fmaxf(m, c[j]);
+        top = fmaxf(warp_max(m), -FLT_MAX); // finite: exp(-inf - top) is 0
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            q[j] = exp2_fast(kLog2e * (c[j] - top));
+            sum += q[j];
+        }
+        inverse = reciprocal_fast(warp_sum(sum));
+        if (scored)
+#pragma unroll
+            for (int j = 0; j < P; ++j) c[j] = c[j] > -INFINITY ? fmaf(q[j], inverse, bias[j]) : -INFINITY;
+    } else if (scored) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) c[j] = c[j] > -INFINITY ? sigmoid_fast(c[j]) + bias[j] : -INFINITY;
+    }
+    uint32_t key[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) key[j] = c[j] > -INFINITY ? Key::make(c[j], lane * P + j) : 0u;
+    bool again = false; // too close to call in 32 bits
+    if (a.groups > 1 && !group_lanes) {
+        uint32_t mine = 0;
+        float most = 0.0f;
+        for (int g = 0; g < a.groups; ++g) {
+            uint32_t members[P];
+#pragma unroll
+            for (int j = 0; j < P; ++j) members[j] = (lane * P + j) / per == g ? key[j] : 0u;
+            int e;
+            const uint32_t first = take_best<P>(members, lane, e);
+            const uint32_t second = a.best > 1 && first ? take_best<P>(members, lane, e) : 0u;
+            const float u = first ? Key::value(first) : 0.0f, w = second ? Key::value(second) : 0.0f;
+            if (lane == g) mine = first ? order_key(u + w) : 0u;
+            most = fmaxf(most, fabsf(u) + fabsf(w));
+        }
+        uint32_t last, cut;
+        const uint32_t keep = best_groups<uint32_t>(mine, a.groups, a.kept, lane, last, cut);
+        if (cut) again = !(key_value(last) - key_value(cut) > 4.0f * error + 4.0f * part * most);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const int e = lane * P + j;
+            if (e < a.experts && !((keep >> (e / per)) & 1u)) key[j] = 0;
+        }
+    }
+    LaneList<P> list(key);
+    if (a.groups > 1 && group_lanes) {
+        float m1 = c[0], m2 = -INFINITY; // whole values: a cut between groups must not hang on short keys
+#pragma unroll
+        for (int j = 1; j < P; ++j) {
+            m2 = fmaxf(m2, fminf(m1, c[j]));
+            m1 = fmaxf(m1, c[j]);
+        }
+        for (int d = 1; d < group_lanes; d <<= 1)
+            join_best_two(m1, m2, __shfl_xor_sync(kAll, m1, d), __shfl_xor_sync(kAll, m2, d));
+        const bool any = m1 > -INFINITY && lane < a.groups * group_lanes;
+        const uint32_t mine = any ? order_key(group_value(m1, m2, a.best)) : 0u;
+        uint32_t left = mine, last = 0;
+        for (int g = 0; g < a.kept; ++g) { // equal values go at once; the cut is then not clear
+            last = __reduce_max_sync(kAll, left);
+            if (left == last) left = 0;
+        }
+        const uint32_t cut = __reduce_max_sync(kAll, left);
+        const bool keep = mine >= last;
+        if (cut) {
+            const float size = any ? fabsf(m1) + (m2 > -INFINITY ? fabsf(m2) : 0.0f) : 0.0f;
+            const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
+            again = !(key_value(last) - key_value(cut) > 4.0f * error + 4.0f * kSumError * most);
+        }
+        // equal values among the kept ones: more groups than asked for
+        again = again || __popc(__ballot_sync(kAll, keep && any)) > a.kept * group_lanes;
+        if (!keep)
+#pragma unroll
+            for (int i = 0; i < LaneList<P>::D; ++i) list.at[i] = 0;
+    }
+    uint32_t mine = 0, prev = 0;
+    for (int i = 0; i < a.k; ++i) {
+        prev = list.take(key);
+        if (lane == i) mine = prev;
+    }
+    int chosen = lane < a.k && mine ? Key::expert(mine) : -1;
+    // neighbours that the short keys do not settle, the one behind the k-th among them
+    const auto close = [&](uint32_t p, uint32_t q) {
+        const float u = Key::value(p), w = Key::value(q);
+        return p && q && !(u - w > 2.0f * error + part * (fabsf(u) + fabsf(w)));
+    };
+    const uint32_t below = __shfl_down_sync(kAll, mine, 1);
+    uint32_t past = list.take(key);
+    const bool over = close(prev, past);
+    if (!again && __any_sync(kAll, over || (lane < a.k - 1 && close(mine, below)))) {
+        int n = a.k;
+        if (over) { // everything that could still belong before the cut
+            while (n < 32) {
+                if (lane == n) chosen = Key::expert(past);
+                ++n;
+                prev = past;
+                past = list.take(key);
+                if (!close(prev, past)) break;
+            }
+            again = n == 32 && close(prev, past);
+        }
+        if (!again) {
+            const int found = __popc(__ballot_sync(kAll, chosen >= 0));
+            float mine_c = chosen >= 0 ? fminf(load_logit(row + chosen), FLT_MAX) : 0.0f; // the logits decide
+            if (a.bias && chosen >= 0)
+                mine_c = (a.softmax ? exp2_fast(kLog2e * (mine_c - top)) * inverse : sigmoid_fast(mine_c)) + a.bias[chosen];
+            chosen = settle<T, P>(row, a, chosen, mine_c, min(n, found), place);
+        }
+    }
+    if (again) chosen = scored ? choose_in_64_bits<T, P>(row, a) : choose_by_logits<T, P>(row, a);
+    return chosen;
+}
+
+// One warp per token: bound by the instructions of the scan over E logits (two
+// special-function ones per sigmoid) and of the k rounds, not by the row's
+// bytes.  For what route_quad_kernel does not take.
+template <typename T, int P>
+__global__ void __launch_bounds__(kRouteThreads, kRouteCtas<P>) route_kernel(const T *__restrict__ logits, RouteArgs a)
+{
+    __shared__ int32_t count[kMaxExperts];
+    __shared__ int32_t place[kRouteWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (a.load) {
+        for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) count[e] = 0;
+        __syncthreads();
+    }
+    grid_dependency_wait();
+    float bias[P];
+    load_bias<P>(a, lane, bias);
     const int64_t step = (int64_t)gridDim.x * kRouteWarps;
     int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
     float next[P];
@@ -532,127 +672,332 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<P>) route_kernel(con
 #pragma unroll
         for (int j = 0; j < P; ++j) c[j] = next[j];
         if (t + step < a.tokens) load_row<T, P>(logits + (t + step) * a.row_stride, a.experts, lane, a.vec, next);
-        float top = 0.0f, inverse = 1.0f;
-        if (a.softmax && (scored || !a.renorm)) {
-            float m = c[0], sum = 0.0f, q[P];
-#pragma unroll
-            for (int j = 1; j < P; ++j) m = fmaxf(m, c[j]);
-            top = fmaxf(warp_max(m), -FLT_MAX); // finite: exp(-inf - top) is 0
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                q[j] = exp2_fast(kLog2e * (c[j] - top));
-                sum += q[j];
-            }
-            inverse = reciprocal_fast(warp_sum(sum));
-            if (scored)
-#pragma unroll
-                for (int j = 0; j < P; ++j) c[j] = c[j] > -INFINITY ? fmaf(q[j], inverse, bias[j]) : -INFINITY;
-        } else if (scored) {
-#pragma unroll
-            for (int j = 0; j < P; ++j) c[j] = c[j] > -INFINITY ? sigmoid_fast(c[j]) + bias[j] : -INFINITY;
-        }
-        uint32_t key[P];
-#pragma unroll
-        for (int j = 0; j < P; ++j) key[j] = c[j] > -INFINITY ? Key::make(c[j], lane * P + j) : 0u;
-        bool again = false; // too close to call in 32 bits
-        if (a.groups > 1 && !group_lanes) {
-            uint32_t mine = 0;
-            float most = 0.0f;
-            for (int g = 0; g < a.groups; ++g) {
-                uint32_t members[P];
-#pragma unroll
-                for (int j = 0; j < P; ++j) members[j] = (lane * P + j) / per == g ? key[j] : 0u;
-                int e;
-                const uint32_t first = take_best<P>(members, lane, e);
-                const uint32_t second = a.best > 1 && first ? take_best<P>(members, lane, e) : 0u;
-                const float u = first ? Key::value(first) : 0.0f, w = second ? Key::value(second) : 0.0f;
-                if (lane == g) mine = first ? order_key(u + w) : 0u;
-                most = fmaxf(most, fabsf(u) + fabsf(w));
-            }
-            uint32_t last, cut;
-            const uint32_t keep = best_groups<uint32_t>(mine, a.groups, a.kept, lane, last, cut);
-            if (cut) again = !(key_value(last) - key_value(cut) > 4.0f * error + 4.0f * part * most);
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const int e = lane * P + j;
-                if (e < a.experts && !((keep >> (e / per)) & 1u)) key[j] = 0;
-            }
-        }
-        LaneList<P> list(key);
-        if (a.groups > 1 && group_lanes) {
-            float m1 = c[0], m2 = -INFINITY; // whole values: a cut between groups must not hang on short keys
-#pragma unroll
-            for (int j = 1; j < P; ++j) {
-                m2 = fmaxf(m2, fminf(m1, c[j]));
-                m1 = fmaxf(m1, c[j]);
-            }
-            for (int d = 1; d < group_lanes; d <<= 1)
-                join_best_two(m1, m2, __shfl_xor_sync(kAll, m1, d), __shfl_xor_sync(kAll, m2, d));
-            const bool any = m1 > -INFINITY && lane < a.groups * group_lanes;
-            const uint32_t mine = any ? order_key(group_value(m1, m2, a.best)) : 0u;
-            uint32_t left = mine, last = 0;
-            for (int g = 0; g < a.kept; ++g) { // equal values go at once; the cut is then not clear
-                last = __reduce_max_sync(kAll, left);
-                if (left == last) left = 0;
-            }
-            const uint32_t cut = __reduce_max_sync(kAll, left);
-            const bool keep = mine >= last;
-            if (cut) {
-                const float size = any ? fabsf(m1) + (m2 > -INFINITY ? fabsf(m2) : 0.0f) : 0.0f;
-                const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
-                again = !(key_value(last) - key_value(cut) > 4.0f * error + 4.0f * kSumError * most);
-            }
-            // equal values among the kept ones: more groups than asked for
-            again = again || __popc(__ballot_sync(kAll, keep && any)) > a.kept * group_lanes;
-            if (!keep)
-#pragma unroll
-                for (int i = 0; i < LaneList<P>::D; ++i) list.at[i] = 0;
-        }
-        uint32_t mine = 0, prev = 0;
-        for (int i = 0; i < a.k; ++i) {
-            prev = list.take(key);
-            if (lane == i) mine = prev;
-        }
-        int chosen = lane < a.k && mine ? Key::expert(mine) : -1;
-        // neighbours that the short keys do not settle, the one behind the k-th among them
-        const auto close = [&](uint32_t p, uint32_t q) {
-            const float u = Key::value(p), w = Key::value(q);
-            return p && q && !(u - w > 2.0f * error + part * (fabsf(u) + fabsf(w)));
-        };
-        const uint32_t below = __shfl_down_sync(kAll, mine, 1);
-        uint32_t past = list.take(key);
-        const bool over = close(prev, past);
-        if (!again && __any_sync(kAll, over || (lane < a.k - 1 && close(mine, below)))) {
-            int n = a.k;
-            if (over) { // everything that could still belong before the cut
-                while (n < 32) {
-                    if (lane == n) chosen = Key::expert(past);
-                    ++n;
-                    prev = past;
-                    past = list.take(key);
-                    if (!close(prev, past)) break;
-                }
-                again = n == 32 && close(prev, past);
-            }
-            if (!again) {
-                const int found = __popc(__ballot_sync(kAll, chosen >= 0));
-                float mine_c = chosen >= 0 ? fminf(load_logit(row + chosen), FLT_MAX) : 0.0f; // the logits decide
-                if (a.bias && chosen >= 0)
-                    mine_c = (a.softmax ? exp2_fast(kLog2e * (mine_c - top)) * inverse : sigmoid_fast(mine_c)) + a.bias[chosen];
-                chosen = settle<T, P>(row, a, chosen, mine_c, min(n, found), place[warp]);
-            }
-        }
-        if (again) chosen = scored ? choose_in_64_bits<T, P>(row, a) : choose_by_logits<T, P>(row, a);
+        RowSoftmax soft;
+        const int chosen = choose_row<T, P>(row, a, c, bias, place[warp], soft);
         // weights of the chosen
         const bool on = lane < a.k && chosen >= 0;
         const float x = on ? fminf(load_logit(row + chosen), FLT_MAX) : 0.0f;
-        float w = !on ? 0.0f : a.softmax ? exp2_fast(kLog2e * (x - top)) * inverse : sigmoid_fast(x);
+        float w = !on ? 0.0f : a.softmax ? exp2_fast(kLog2e * (x - soft.top)) * soft.inverse : sigmoid_fast(x);
         if (a.renorm) w = share_of<32>(w, x, on, a.softmax != 0);
         if (lane < a.k) {
             a.idx[t * a.k + lane] = on ? chosen : -1;
             a.weight[t * a.k + lane] = w * a.scale;
         }
         if (a.load && on) atomicAdd(&count[chosen], 1);
+    }
+    grid_dependents_go();
+    if (a.load) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.experts; e += kRouteThreads)
+            if (count[e]) atomicAdd(a.load + e, count[e]);
+    }
+}
+
+
+// ------------------------------------------------ four lanes per token
+
+constexpr int kQuadExperts = 256; // the most a quad holds: 64 a lane
+constexpr int kQuadK = 8;
+constexpr int kQuadTokens = 8; // tokens a warp has at a time
+constexpr int kQuadGroups = 16;
+static_assert(kQuadExperts == 16 * 16, "sixteen steps of sixteen experts");
+
+// Eight keys into descending order (odd-even merges).
+__device__ __forceinline__ void sort8(uint32_t (&k)[8])
+{
+    constexpr int a[19] = {0, 2, 4, 6, 0, 1, 4, 5, 1, 5, 0, 1, 2, 3, 2, 3, 1, 3, 5};
+    constexpr int b[19] = {1, 3, 5, 7, 2, 3, 6, 7, 2, 6, 4, 5, 6, 7, 4, 5, 2, 4, 6};
+#pragma unroll
+    for (int i = 0; i < 19; ++i) order_pair(k[a[i]], k[b[i]]);
+}
+
+// The eight largest of two descending eights, in order, into k; `dropped`
+// keeps the largest of those left out.
+__device__ __forceinline__ void keep8(uint32_t (&k)[8], const uint32_t (&o)[8], uint32_t &dropped)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t mine = k[i], other = o[7 - i];
+        k[i] = max(mine, other);
+        dropped = max(dropped, min(mine, other));
+    }
+#pragma unroll
+    for (int d = 4; d; d >>= 1) // bitonic: half-cleaners
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & d)) order_pair(k[i], k[i + d]);
+}
+
+// As choose_row, for one token of a quad warp whose order is too close to call.
+template <typename T> __device__ __noinline__ int choose_again(const T *row, const RouteArgs &a, int32_t *place)
+{
+    constexpr int P = kQuadExperts / 32;
+    const int lane = threadIdx.x & 31;
+    float c[P], bias[P];
+    RowSoftmax soft;
+    RouteArgs b = a;
+    b.vec = false; // this layout's vectors need not be the quads'
+    load_row<T, P>(row, a.experts, lane, false, c);
+    load_bias<P>(a, lane, bias);
+    return choose_row<T, P>(row, b, c, bias, place, soft);
+}
+
+// Four lanes per token, eight tokens per warp, for up to 256 experts and k up
+// to 8: expert 16 s + 4 l + j is lane l's j-th of step s, so that a token's
+// lanes read 16 experts side by side.  Every lane sorts its short keys in
+// eights and keeps the best eight, and two exchanges join the four lanes'.
+// Against one warp per token the fixed work is shared by eight: 65536 x 256
+// fp32 with groups and bias 94 -> QUAD_US us.
+template <typename T, int S>
+__global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *__restrict__ logits, RouteArgs a)
+{
+    constexpr int P = 4 * S;
+    using Key = ShortKey<kQuadExperts / 32>;
+    constexpr uint32_t kLeast = 0x00800000u; // keys below: out of reach
+    __shared__ int32_t count[kQuadExperts];
+    alignas(16) __shared__ float bias[kQuadExperts];
+    __shared__ float group[kRouteWarps][kQuadTokens][kQuadGroups];
+    __shared__ int32_t place[kRouteWarps][32];
+    __shared__ int32_t redone[kRouteWarps][kQuadTokens][kQuadK];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 3, mine = lane >> 2;
+    const bool scored = a.bias || a.groups > 1;
+    for (int e = threadIdx.x; e < kQuadExperts; e += kRouteThreads) count[e] = 0;
+    grid_dependency_wait();
+    for (int e = threadIdx.x; e < kQuadExperts; e += kRouteThreads) {
+        const float b = a.bias && e < a.experts ? a.bias[e] : 0.0f;
+        bias[e] = b > -INFINITY ? b : -INFINITY; // no choice can come of NaN
+    }
+    __syncthreads();
+    const int steps_each = a.groups > 1 ? a.experts / a.groups / 16 : S + 1; // steps of a group
+    const float error = !scored ? 0.0f : a.softmax ? kSoftmaxError : kSigmoidError;
+    // 16-bit logits fit a short key whole: what ties there is a tie
+    const bool exact = !scored && sizeof(T) == 2;
+    const int64_t step = (int64_t)gridDim.x * kRouteWarps * kQuadTokens;
+    for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWarps + warp) * kQuadTokens; t0 < a.tokens; t0 += step) {
+        const int64_t t = t0 + mine;
+        const bool live = t < a.tokens;
+        const T *row = logits + (live ? t : t0) * a.row_stride;
+        float c[P];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int e = 16 * s + 4 * sub;
+            alignas(16) T x[4];
+            const bool in = live && e < a.experts;
+            if (in) {
+                if (sizeof(T) == 4) *reinterpret_cast<uint4 *>(x) = *reinterpret_cast<const uint4 *>(row + e);
+                else *reinterpret_cast<uint2 *>(x) = *reinterpret_cast<const uint2 *>(row + e);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                c[4 * s + j] = in ? load_logit(&x[j]) : -INFINITY;
+                c[4 * s + j] = in_reach(c[4 * s + j]) ? fminf(c[4 * s + j], FLT_MAX) : -INFINITY;
+            }
+        }
+        float top = 0.0f, inverse = 1.0f;
+        if (a.softmax && (scored || !a.renorm)) {
+            float m = c[0], sum = 0.0f;
+#pragma unroll
+            for (int i = 1; i < P; ++i) m = fmaxf(m, c[i]);
+            top = fmaxf(lanes_max<4>(m), -FLT_MAX);
+            if (scored) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const float q = exp2_fast(kLog2e * (c[i] - top));
+                    sum += q;
+                    c[i] = c[i] > -INFINITY ? q : -1.0f; // a score may underflow to 0 and still be chosen
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < P; ++i) sum += exp2_fast(kLog2e * (c[i] - top));
+            }
+            inverse = reciprocal_fast(lanes_sum<4>(sum));
+        }
+        float most = 0.0f;
+        if (scored) {
+            float m1 = -INFINITY, m2 = -INFINITY;
+            int left = steps_each, g = 0;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const float4 b4 = *reinterpret_cast<const float4 *>(bias + 16 * s + 4 * sub);
+                const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float &v = c[4 * s + j];
+                    if (a.softmax) v = v >= 0.0f ? fmaf(v, inverse, b[j]) : -INFINITY;
+                    else v = v > -INFINITY ? sigmoid_fast(v) + b[j] : -INFINITY;
+                    m2 = fmaxf(m2, fminf(m1, v));
+                    m1 = fmaxf(m1, v);
+                }
+                if (--left == 0) { // a group's last step
+                    join_best_two(m1, m2, __shfl_xor_sync(kAll, m1, 1), __shfl_xor_sync(kAll, m2, 1));
+                    join_best_two(m1, m2, __shfl_xor_sync(kAll, m1, 2), __shfl_xor_sync(kAll, m2, 2));
+                    if (sub == 0) group[warp][mine][g] = group_value(m1, m2, a.best);
+                    if (m1 > -INFINITY) most = fmaxf(most, fabsf(m1) + (m2 > -INFINITY ? fabsf(m2) : 0.0f));
+                    m1 = m2 = -INFINITY;
+                    left = steps_each;
+                    ++g;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i) c[i] += 0.0f; // one zero
+        }
+        bool again = false;
+        uint32_t keep = 0xFFFFFFFFu;
+        if (a.groups > 1) {
+            __syncwarp();
+            keep = 0;
+            float last = -INFINITY, cut = -INFINITY;
+            for (int g = sub; g < a.groups; g += 4) {
+                const float v = group[warp][mine][g];
+                int rank = 0;
+                for (int o = 0; o < a.groups; ++o) {
+                    const float u = group[warp][mine][o];
+                    rank += u > v || (u == v && o < g);
+                }
+                if (rank < a.kept) keep |= 1u << g;
+                if (rank == a.kept - 1) last = v;
+                if (rank == a.kept) cut = v;
+            }
+            keep |= __shfl_xor_sync(kAll, keep, 1);
+            keep |= __shfl_xor_sync(kAll, keep, 2);
+            last = lanes_max<4>(last);
+            cut = lanes_max<4>(cut);
+            again = cut > -INFINITY && !(last - cut > 4.0f * error + 4.0f * kSumError * most);
+            __syncwarp(); // the groups are read before the next tokens' are written
+        }
+        uint32_t best[8], dropped = 0;
+        {
+            int left = steps_each, g = 0;
+#pragma unroll
+            for (int b = 0; b < S / 2; ++b) {
+                uint32_t k[8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int s = 2 * b + h;
+                    const bool in = (keep >> g) & 1u;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        k[4 * h + j] = in ? Key::make_plain(c[4 * s + j], 16 * s + 4 * sub + j) : 0u;
+                    if (--left == 0) {
+                        left = steps_each;
+                        ++g;
+                    }
+                }
+                sort8(k);
+                if (b == 0)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) best[i] = k[i];
+                else keep8(best, k, dropped);
+            }
+        }
+#pragma unroll
+        for (int d = 1; d <= 2; d <<= 1) {
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = __shfl_xor_sync(kAll, best[i], d);
+            const uint32_t od = __shfl_xor_sync(kAll, dropped, d);
+            dropped = max(dropped, od);
+            keep8(best, o, dropped);
+        }
+        // places 2 sub and 2 sub + 1: experts, logits, scores and whole choices
+        const uint32_t k0 = sub == 0 ? best[0] : sub == 1 ? best[2] : sub == 2 ? best[4] : best[6];
+        const uint32_t k1 = sub == 0 ? best[1] : sub == 1 ? best[3] : sub == 2 ? best[5] : best[7];
+        int e0 = k0 >= kLeast ? Key::expert(k0) : -1, e1 = k1 >= kLeast ? Key::expert(k1) : -1;
+        float x0 = e0 >= 0 ? fminf(load_logit(row + e0), FLT_MAX) : 0.0f;
+        float x1 = e1 >= 0 ? fminf(load_logit(row + e1), FLT_MAX) : 0.0f;
+        const auto score = [&](float x) { return a.softmax ? exp2_fast(kLog2e * (x - top)) * inverse : sigmoid_fast(x); };
+        if (!exact) {
+            float c0 = e0 < 0 ? -INFINITY : scored ? score(x0) + bias[e0] : x0;
+            float c1 = e1 < 0 ? -INFINITY : scored ? score(x1) + bias[e1] : x1;
+            float next = __shfl_down_sync(kAll, c0, 1, 4);
+            if (__any_sync(kAll, c1 > c0 || (sub < 3 && next > c1))) { // the short keys hid an order
+                for (int pass = 0; pass < 4; ++pass) { // odd-even exchanges; equal choices keep theirs (the index's)
+                    if (c1 > c0) {
+                        const float tc = c0, tx = x0;
+                        const int te = e0;
+                        c0 = c1, x0 = x1, e0 = e1;
+                        c1 = tc, x1 = tx, e1 = te;
+                    }
+                    const float nc = __shfl_down_sync(kAll, c0, 1, 4), nx = __shfl_down_sync(kAll, x0, 1, 4);
+                    const float pc = __shfl_up_sync(kAll, c1, 1, 4), px = __shfl_up_sync(kAll, x1, 1, 4);
+                    const int ne = __shfl_down_sync(kAll, e0, 1, 4), pe = __shfl_up_sync(kAll, e1, 1, 4);
+                    const bool give = sub < 3 && nc > c1, take = sub > 0 && c0 > pc;
+                    if (give) c1 = nc, x1 = nx, e1 = ne;
+                    if (take) c0 = pc, x0 = px, e0 = pe;
+                }
+                next = __shfl_down_sync(kAll, c0, 1, 4);
+            }
+            // still too close: neighbours up to the k-th and the one behind it, or anything left out that could
+            // have as much as the largest in its short key
+            const auto close = [&](float u, float w) {
+                return w > -INFINITY && !(u - w > 2.0f * error + (scored ? kSumError : 0.0f) * (fabsf(u) + fabsf(w)));
+            };
+            if (scored) again = again || (2 * sub < a.k && close(c0, c1)) || (2 * sub + 1 < a.k && sub < 3 && close(c1, next));
+            if (sub == (a.k - 1) / 2 && dropped >= kLeast)
+                again = again || close((a.k & 1) ? c0 : c1, key_value(dropped | Key::kMask));
+        }
+        uint32_t redo = __ballot_sync(kAll, again && live);
+        redo |= redo >> 1;
+        redo = (redo | redo >> 2) & 0x11111111u; // a token's bit in its first lane
+        if (redo) {
+            for (uint32_t left = redo; left; left &= left - 1) {
+                const int q = (__ffs(left) - 1) >> 2;
+                const int chosen = choose_again<T>(logits + (t0 + q) * a.row_stride, a, place[warp]);
+                if (lane < kQuadK) redone[warp][q][lane] = chosen;
+                __syncwarp();
+            }
+            if ((redo >> (4 * mine)) & 1u) {
+                e0 = redone[warp][mine][2 * sub];
+                e1 = redone[warp][mine][2 * sub + 1];
+                x0 = e0 >= 0 ? fminf(load_logit(row + e0), FLT_MAX) : 0.0f;
+                x1 = e1 >= 0 ? fminf(load_logit(row + e1), FLT_MAX) : 0.0f;
+            }
+            __syncwarp();
+        }
+        // weights of the two
+        const bool on0 = live && 2 * sub < a.k && e0 >= 0, on1 = live && 2 * sub + 1 < a.k && e1 >= 0;
+        float w0, w1;
+        if (a.softmax && a.renorm) { // the row's other experts cancel
+            const float lead = lanes_max<4>(fmaxf(on0 ? x0 : -FLT_MAX, on1 ? x1 : -FLT_MAX));
+            w0 = on0 ? exp2_fast(kLog2e * (x0 - lead)) : 0.0f;
+            w1 = on1 ? exp2_fast(kLog2e * (x1 - lead)) : 0.0f;
+        } else {
+            w0 = on0 ? score(x0) : 0.0f;
+            w1 = on1 ? score(x1) : 0.0f;
+        }
+        if (a.renorm) {
+            float sum = lanes_sum<4>(w0 + w1);
+            if (__any_sync(kAll, sum < 1e-30f)) { // scores that underflow (or none chosen): by their logarithms
+                const float l0 = on0 ? fminf(x0, 0.0f) - log1pf(expf(-fabsf(x0))) : -FLT_MAX;
+                const float l1 = on1 ? fminf(x1, 0.0f) - log1pf(expf(-fabsf(x1))) : -FLT_MAX;
+                const float lead = lanes_max<4>(fmaxf(l0, l1));
+                const float v0 = on0 ? __expf(l0 - lead) : 0.0f, v1 = on1 ? __expf(l1 - lead) : 0.0f;
+                const float all = lanes_sum<4>(v0 + v1);
+                if (sum < 1e-30f) {
+                    w0 = v0;
+                    w1 = v1;
+                    sum = all;
+                }
+            }
+            w0 = on0 ? __fdividef(w0, sum) : 0.0f;
+            w1 = on1 ? __fdividef(w1, sum) : 0.0f;
+        }
+        if (live) {
+            const int64_t o = t * a.k + 2 * sub;
+            if (2 * sub < a.k) {
+                a.idx[o] = on0 ? e0 : -1;
+                a.weight[o] = w0 * a.scale;
+            }
+            if (2 * sub + 1 < a.k) {
+                a.idx[o + 1] = on1 ? e1 : -1;
+                a.weight[o + 1] = w1 * a.scale;
+            }
+            if (a.load) {
+                if (on0) atomicAdd(&count[e0], 1);
+                if (on1) atomicAdd(&count[e1], 1);
+            }
+        }
     }
     grid_dependents_go();
     if (a.load) {
@@ -856,8 +1201,32 @@ bool whole_vectors(const void *logits, size_t size, int experts, int64_t row_str
            (size_t)row_stride * size % bytes == 0;
 }
 
+template <typename T> RouteKernel<T> quad_kernel_for(int experts)
+{
+    return experts <= 32 ? route_quad_kernel<T, 2>
+           : experts <= 64 ? route_quad_kernel<T, 4>
+           : experts <= 128 ? route_quad_kernel<T, 8>
+                            : route_quad_kernel<T, 16>;
+}
+
+// Whether four lanes per token do: enough tokens that eight a warp still
+// reach every SM, and rows, groups and k that fit its layout.
+bool quads_fit(const void *logits, size_t size, const RouteArgs &a, int sm_count)
+{
+    return a.experts <= kQuadExperts && a.k <= kQuadK && a.experts % 4 == 0 && a.row_stride % 4 == 0 &&
+           (reinterpret_cast<uintptr_t>(logits) & (4 * size - 1)) == 0 && a.groups <= kQuadGroups &&
+           (a.groups == 1 || a.experts / a.groups % 16 == 0) && a.tokens >= (int64_t)sm_count * kQuadTokens;
+}
+
 template <typename T> cudaError_t launch_route(const void *logits, RouteArgs a, int sm_count, void *stream)
 {
+    if (quads_fit(logits, sizeof(T), a, sm_count)) {
+        cudaLaunchAttribute attr[1];
+        const int64_t warps = (a.tokens + kQuadTokens - 1) / kQuadTokens;
+        const cudaLaunchConfig_t cfg =
+            route_config(route_grid(warps, sm_count, 2), static_cast<cudaStream_t>(stream), attr);
+        return cudaLaunchKernelEx(&cfg, quad_kernel_for<T>(a.experts), static_cast<const T *>(logits), a);
+    }
     a.vec = whole_vectors(logits, sizeof(T), a.experts, a.row_stride);
     cudaLaunchAttribute attr[1];
     const int each = a.experts <= 256 ? kRouteCtas<8> : a.experts <= 512 ? kRouteCtas<16> : kRouteCtas<32>;
