@@ -728,7 +728,132 @@ __device__ __forceinline__ void keep8(uint32_t (&k)[8], const uint32_t (&o)[8], 
             if (!(i & d)) order_pair(k[i], k[i + d]);
 }
 
-// As choose_row, for one token of a quad warp whose order is too close to call.
+// The slow parts below run for a token in some thousands, whose warp the
+// kernel then waits for: their loops stay rolled, because fetching code that
+// no other warp has run takes longer than running it (the whole of choose_row
+// and choose_in_64_bits in their place: 31 us of a 74 us kernel).
+
+// Sum of exp(x - top) over a row in 64 bits, in every lane.
+template <typename T> __device__ __noinline__ double sum_in_64_bits(const T *row, int experts, float top)
+{
+    double sum = 0;
+#pragma unroll 1
+    for (int e = threadIdx.x & 31; e < experts; e += 32) {
+        const float x = load_logit(row + e);
+        if (in_reach(x)) sum += exp((double)fminf(x, FLT_MAX) - (double)top);
+    }
+#pragma unroll 1
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+    return sum;
+}
+
+// An expert's choice in 64 bits (`top` and `sum` of its row's softmax); -inf
+// where it has none.
+template <typename T>
+__device__ __noinline__ double choice_in_64_bits(const T *row, const RouteArgs &a, int expert, float top, double sum)
+{
+    const float x = load_logit(row + expert);
+    if (!in_reach(x)) return -INFINITY;
+    const double e = exp(a.softmax ? (double)fminf(x, FLT_MAX) - (double)top : -(double)fminf(x, FLT_MAX));
+    double c = a.softmax ? e / sum : 1.0 / (1.0 + e);
+    if (a.bias) c += (double)a.bias[expert];
+    return c > -INFINITY ? c : -INFINITY;
+}
+
+// The groups kept, where the values around the cut are too close to call
+// (`last` the last kept, `cut` the first left out, `margin` their error): the
+// groups in between are valued again in 64 bits.  `value`: the groups' values.
+template <typename T>
+__device__ __noinline__ uint32_t decide_groups(const T *row, const RouteArgs &a, const float *value, float last, float cut,
+                                               float margin, float top)
+{
+    const int lane = threadIdx.x & 31, per = a.experts / a.groups;
+    const float v = lane < a.groups ? value[lane] : -INFINITY;
+    const bool open = lane < a.groups && !(v < cut - margin) && !(v > last + margin) && v > -INFINITY;
+    const uint32_t unsure = __ballot_sync(kAll, open);
+    const uint32_t in = __ballot_sync(kAll, lane < a.groups && !open && v > last);
+    const double sum = a.softmax ? sum_in_64_bits(row, a.experts, top) : 1.0;
+    double mine = 0;
+#pragma unroll 1
+    for (uint32_t left = unsure; left; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        double m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll 1
+        for (int i = lane; i < per; i += 32) {
+            const double c = choice_in_64_bits(row, a, g * per + i, top, sum);
+            m2 = fmax(m2, fmin(m1, c));
+            m1 = fmax(m1, c);
+        }
+#pragma unroll 1
+        for (int d = 16; d; d >>= 1) {
+            const double o1 = __shfl_xor_sync(kAll, m1, d), o2 = __shfl_xor_sync(kAll, m2, d);
+            m2 = fmax(fmin(m1, o1), fmax(m2, o2));
+            m1 = fmax(m1, o1);
+        }
+        if (lane == g) mine = a.best > 1 && m2 > -INFINITY ? m1 + m2 : m1;
+    }
+    int rank = __popc(in);
+#pragma unroll 1
+    for (uint32_t left = unsure; left; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        const double o = __shfl_sync(kAll, mine, g);
+        rank += o > mine || (o == mine && g < lane);
+    }
+    return in | __ballot_sync(kAll, open && rank < a.kept);
+}
+
+// The choice of a row whose order short keys and 32 bits left open, given the
+// groups kept and a bound that no chosen expert's choice lies below: the few
+// experts from there on, in order by the logits, or with a bias in 64 bits.
+// Lane i < k gets the i-th or -1; `lost` where there are too many of them.
+template <typename T>
+__device__ __noinline__ int choose_from(const T *row, const RouteArgs &a, uint32_t keep, float least, RowSoftmax soft,
+                                        int32_t *place, bool &lost)
+{
+    const int lane = threadIdx.x & 31, per = a.experts / a.groups;
+    const bool scored = a.bias || a.groups > 1;
+    int n = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < a.experts; e0 += 32) {
+        const int e = e0 + lane;
+        float c = -INFINITY;
+        if (e < a.experts && in_reach(load_logit(row + e)) && (a.groups == 1 || ((keep >> (e / per)) & 1u))) {
+            c = fminf(load_logit(row + e), FLT_MAX);
+            if (scored)
+                c = (a.softmax ? exp2_fast(kLog2e * (c - soft.top)) * soft.inverse : sigmoid_fast(c)) +
+                    (a.bias ? a.bias[e] : 0.0f);
+        }
+        const bool in = c > -INFINITY && c >= least;
+        const uint32_t mask = __ballot_sync(kAll, in);
+        const int at = n + __popc(mask & ((1u << lane) - 1u));
+        if (in && at < 32) place[at] = e;
+        n += __popc(mask);
+    }
+    __syncwarp();
+    lost = n > 32;
+    if (lost) return -1;
+    const int expert = lane < n ? place[lane] : -1;
+    double c = expert < 0 ? -INFINITY : (double)fminf(load_logit(row + expert), FLT_MAX);
+    if (a.bias) { // without one the logits decide
+        const double sum = a.softmax ? sum_in_64_bits(row, a.experts, soft.top) : 1.0;
+        c = expert < 0 ? -INFINITY : choice_in_64_bits(row, a, expert, soft.top, sum);
+    }
+    int rank = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const double o = __shfl_sync(kAll, c, i);
+        const int oe = __shfl_sync(kAll, expert, i);
+        rank += o > c || (o == c && oe < expert);
+    }
+    __syncwarp();
+    if (expert >= 0) place[rank] = expert;
+    __syncwarp();
+    const int chosen = lane < n && lane < a.k ? place[lane] : -1;
+    __syncwarp();
+    return chosen;
+}
+
+// As choose_row, for one token of a quad warp (heavy ties).
 template <typename T> __device__ __noinline__ int choose_again(const T *row, const RouteArgs &a, int32_t *place)
 {
     constexpr int P = kQuadExperts / 32;
@@ -842,7 +967,6 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
 #pragma unroll
             for (int i = 0; i < P; ++i) c[i] += 0.0f; // one zero
         }
-        bool again = false;
         uint32_t keep = 0xFFFFFFFFu;
         if (a.groups > 1) {
             __syncwarp();
@@ -863,7 +987,15 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
             keep |= __shfl_xor_sync(kAll, keep, 2);
             last = lanes_max<4>(last);
             cut = lanes_max<4>(cut);
-            again = cut > -INFINITY && !(last - cut > 4.0f * error + 4.0f * kSumError * most);
+            const float margin = 4.0f * error + 4.0f * kSumError * most;
+            const bool unsure = live && cut > -INFINITY && !(last - cut > margin);
+            for (uint32_t left = __ballot_sync(kAll, unsure) & 0x11111111u; left; left &= left - 1) {
+                const int first = __ffs(left) - 1, q = first >> 2;
+                const uint32_t kept = decide_groups(
+                    logits + (t0 + q) * a.row_stride, a, group[warp][q], __shfl_sync(kAll, last, first),
+                    __shfl_sync(kAll, cut, first), __shfl_sync(kAll, margin, first), __shfl_sync(kAll, top, first));
+                if (mine == q) keep = kept;
+            }
             __syncwarp(); // the groups are read before the next tokens' are written
         }
         uint32_t best[8], dropped = 0;
@@ -906,6 +1038,8 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
         int e0 = k0 >= kLeast ? Key::expert(k0) : -1, e1 = k1 >= kLeast ? Key::expert(k1) : -1;
         float x0 = e0 >= 0 ? fminf(load_logit(row + e0), FLT_MAX) : 0.0f;
         float x1 = e1 >= 0 ? fminf(load_logit(row + e1), FLT_MAX) : 0.0f;
+        bool again = false;
+        float least = -FLT_MAX; // nothing below it is chosen (in the lane of the k-th)
         const auto score = [&](float x) { return a.softmax ? exp2_fast(kLog2e * (x - top)) * inverse : sigmoid_fast(x); };
         if (!exact) {
             float c0 = e0 < 0 ? -INFINITY : scored ? score(x0) + bias[e0] : x0;
@@ -934,16 +1068,25 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
                 return w > -INFINITY && !(u - w > 2.0f * error + (scored ? kSumError : 0.0f) * (fabsf(u) + fabsf(w)));
             };
             if (scored) again = again || (2 * sub < a.k && close(c0, c1)) || (2 * sub + 1 < a.k && sub < 3 && close(c1, next));
-            if (sub == (a.k - 1) / 2 && dropped >= kLeast)
-                again = again || close((a.k & 1) ? c0 : c1, key_value(dropped | Key::kMask));
+            if (sub == (a.k - 1) / 2) {
+                const float kth = (a.k & 1) ? c0 : c1;
+                if (dropped >= kLeast) again = again || close(kth, key_value(dropped | Key::kMask));
+                if (kth > -INFINITY)
+                    least = scored && kth < INFINITY ? kth - 3.0f * error - 3.0f * kSumError * fabsf(kth) : kth;
+            }
         }
         uint32_t redo = __ballot_sync(kAll, again && live);
         redo |= redo >> 1;
         redo = (redo | redo >> 2) & 0x11111111u; // a token's bit in its first lane
         if (redo) {
             for (uint32_t left = redo; left; left &= left - 1) {
-                const int q = (__ffs(left) - 1) >> 2;
-                const int chosen = choose_again<T>(logits + (t0 + q) * a.row_stride, a, place[warp]);
+                const int first = __ffs(left) - 1, q = first >> 2;
+                const T *other = logits + (t0 + q) * a.row_stride;
+                const RowSoftmax soft = {__shfl_sync(kAll, top, first), __shfl_sync(kAll, inverse, first)};
+                bool lost;
+                int chosen = choose_from(other, a, __shfl_sync(kAll, keep, first),
+                                         __shfl_sync(kAll, least, first + (a.k - 1) / 2), soft, place[warp], lost);
+                if (lost) chosen = choose_again<T>(other, a, place[warp]);
                 if (lane < kQuadK) redone[warp][q][lane] = chosen;
                 __syncwarp();
             }
