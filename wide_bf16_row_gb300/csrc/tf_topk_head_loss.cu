@@ -705,11 +705,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     send_bf16(&map_out, out, col, row - lane, true);
                 }
             } else if (!shape.of_weight(u)) {
-                for (int c = 0; c < chunks; ++c) {
+                for (int c = 0; c < chunks && t.n * kTileCols + c0 + c * kChunk < a.dim; ++c) {
                     float x[kChunk];
                     tmem_load(lanes + c0 + c * kChunk, x);
                     const int col = t.n * kTileCols + c0 + c * kChunk;
-                    const bool any = row - lane < count && col < a.dim; // rows past the count get sums nothing reads
+                    const bool any = row - lane < count; // rows past the count get sums nothing reads
                     if (elect_one()) box_read_wait<0>();
                     __syncwarp();
                     put_row_f32(box, lane, x);
@@ -725,14 +725,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
             } else {
                 const float scale = a.header->grad_scale;
-                for (int c = 0; c < chunks; ++c) {
+                for (int c = 0; c < chunks && t.n * kTileCols + c0 + c * kChunk < a.dim; ++c) {
                     float x[kChunk];
                     tmem_load(lanes + c0 + c * kChunk, x);
                     const int col = t.n * kTileCols + c0 + c * kChunk;
                     uint32_t out[kChunk / 2];
 #pragma unroll
                     for (int i = 0; i < kChunk / 2; ++i) out[i] = pack_bf16(x[2 * i] * scale, x[2 * i + 1] * scale);
-                    send_bf16(&map_wout, out, col, a.begin + row - lane, col < a.dim && row - lane < a.cols);
+                    send_bf16(&map_wout, out, col, a.begin + row - lane, row - lane < a.cols);
                 }
             }
             tc_fence_before();
@@ -826,14 +826,14 @@ __global__ void __launch_bounds__(kPrepareThreads)
 // tile (the products sum over whole K steps of rows).
 __global__ void __launch_bounds__(256)
     head_loss_gather_kernel(const __nv_bfloat16 *hidden, int64_t stride, int dim, const RowHeader *header,
-                            const int32_t *order, __nv_bfloat16 *packed)
+                            const int32_t *order, int pitch, __nv_bfloat16 *packed)
 {
     grid_dependency_wait();
     const int count = header->count;
     const int end = max(1, ceil_div(count, kTileRows)) * kTileRows;
     const int vecs = dim / 8;
     for (int j = blockIdx.x; j < end; j += gridDim.x) {
-        uint4 *dst = reinterpret_cast<uint4 *>(packed + (size_t)j * dim);
+        uint4 *dst = reinterpret_cast<uint4 *>(packed + (size_t)j * pitch);
         if (j < count) {
             const uint4 *src = reinterpret_cast<const uint4 *>(hidden + (size_t)order[j] * stride);
             for (int i = threadIdx.x; i < vecs; i += blockDim.x) dst[i] = src[i];
@@ -1109,6 +1109,9 @@ cudaError_t launch_product(const PairMaps &m, PairArgs &a, int64_t most_units, i
     return cudaLaunchKernelEx(&cfg, pair_product_kernel<kMode, false>, m.a, m.b, m.wa, m.wb, m.out, m.wout, a);
 }
 
+// Row pitch of the packed hidden states: whole 128-byte lines, whatever dim.
+int64_t packed_pitch(int64_t dim) { return (dim + kStepK - 1) / kStepK * kStepK; }
+
 int64_t pad_rows_of(int64_t rows) { return (rows + kTileRows - 1) / kTileRows * kTileRows; }
 
 // Carves a workspace into 256-byte aligned parts.
@@ -1125,17 +1128,20 @@ struct Carver {
 
 // Columns of a tile for the forward product: the widest tile moves the
 // fewest bytes through shared memory, a narrower one may fill the last round
-// of the pairs better.  A round costs about its width plus 32 columns.
+// of the pairs better.  A round costs about its width plus 32 columns.  Of
+// packed rows the host does not know how many count: all of them and half are
+// weighed alike.
 int tile_width(int64_t rows, int64_t vocab, int pairs)
 {
     const int64_t m = pad_rows_of(rows) / kTileRows;
     int best = kTileCols;
-    int64_t cost = INT64_MAX;
+    int64_t least = INT64_MAX;
     for (int w = kTileCols; w >= 64; w -= 64) {
-        const int64_t units = m * ((vocab + w - 1) / w);
-        const int64_t c = (units + pairs - 1) / pairs * (w + 32);
-        if (c < cost) {
-            cost = c;
+        const int64_t tiles = (vocab + w - 1) / w;
+        const int64_t rounds = (m * tiles + pairs - 1) / pairs + ((m + 1) / 2 * tiles + pairs - 1) / pairs;
+        const int64_t cost = rounds * (w + 32);
+        if (cost < least) {
+            least = cost;
             best = w;
         }
     }
@@ -1160,7 +1166,7 @@ LossSpace loss_space(const void *p, int64_t rows, int64_t dim, int64_t parts)
         s.header = c.take<RowHeader>(1);
         s.order = c.take<int32_t>(rows);
         s.place = c.take<int32_t>(rows);
-        s.packed = c.take<__nv_bfloat16>(pad_rows_of(rows) * dim);
+        s.packed = c.take<__nv_bfloat16>(pad_rows_of(rows) * packed_pitch(dim));
     }
     s.partial = c.take<float2>(parts * pad_rows_of(rows));
     s.bytes = (size_t)(c.at - (reinterpret_cast<uintptr_t>(p))) + 256;
@@ -1198,7 +1204,7 @@ GradSpace grad_space(const void *p, int64_t rows, int64_t dim, int64_t vocab, in
     s.header = c.take<RowHeader>(1);
     s.order = c.take<int32_t>(rows);
     s.place = c.take<int32_t>(rows);
-    s.packed = c.take<__nv_bfloat16>(pad * dim);
+    s.packed = c.take<__nv_bfloat16>(pad * packed_pitch(dim));
     if (hidden) s.sums = c.take<float>((int64_t)s.splits * pad * dim);
     s.prob = c.take<__nv_bfloat16>(pad * piece);
     s.bytes = (size_t)(c.at - (reinterpret_cast<uintptr_t>(p))) + 256;
@@ -1268,8 +1274,8 @@ int run_loss(const void *hidden, int64_t hidden_stride, const void *weight, int6
     PairMaps m = {};
     const bool packed = s.packed != nullptr;
     const int box = rows <= kHalf ? (int)((rows + 7) / 8 * 8) : kHalf; // rows of A a CTA loads (set_ring)
-    if (!encode_map(&m.a, packed ? s.packed : hidden, dim, packed ? pad_rows_of(rows) : rows, packed ? dim : hidden_stride,
-                    box) ||
+    if (!encode_map(&m.a, packed ? s.packed : hidden, dim, packed ? pad_rows_of(rows) : rows,
+                    packed ? packed_pitch(dim) : hidden_stride, box) ||
         !encode_map(&m.b, weight, dim, vocab, weight_stride, width / 2))
         return tf_topk_internal_fail_cuda((int)cudaErrorInvalidValue);
     cudaLaunchAttribute attr[1];
@@ -1283,7 +1289,7 @@ int run_loss(const void *hidden, int64_t hidden_stride, const void *weight, int6
         if (e == cudaSuccess)
             e = cudaLaunchKernelEx(&cfg, head_loss_gather_kernel, static_cast<const __nv_bfloat16 *>(hidden),
                                    hidden_stride, (int)dim, (const RowHeader *)s.header, (const int32_t *)s.order,
-                                   s.packed);
+                                   (int)packed_pitch(dim), s.packed);
     }
     PairArgs a = {};
     a.header = s.header;
@@ -1351,13 +1357,13 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
     const cudaStream_t strm = static_cast<cudaStream_t>(stream);
     const int box = rows <= kHalf ? (int)((rows + 7) / 8 * 8) : kHalf; // rows of A a CTA loads (set_ring)
     PairMaps prob = {}, grads = {};
-    if (!encode_map(&prob.a, s.packed, dim, pad, dim, box) || !encode_map(&prob.b, weight, dim, vocab, weight_stride, kHalf) ||
+    if (!encode_map(&prob.a, s.packed, dim, pad, packed_pitch(dim), box) || !encode_map(&prob.b, weight, dim, vocab, weight_stride, kHalf) ||
         !encode_out(&prob.out, s.prob, false, piece, pad) ||
         (d_hidden && (!encode_map(&grads.a, s.prob, piece, pad, piece, box) ||
                       !encode_map(&grads.b, weight, dim, vocab, weight_stride, kStepK) ||
                       !encode_out(&grads.out, s.sums, true, dim, pad * s.splits))) ||
         (d_weight && (!encode_map(&grads.wa, s.prob, piece, pad, piece, kStepK) ||
-                      !encode_map(&grads.wb, s.packed, dim, pad, dim, kStepK) ||
+                      !encode_map(&grads.wb, s.packed, dim, pad, packed_pitch(dim), kStepK) ||
                       !encode_out(&grads.wout, d_weight, false, dim, vocab))))
         return tf_topk_internal_fail_cuda((int)cudaErrorInvalidValue);
     // every share of the sums starts in the first piece, the widest
@@ -1371,7 +1377,8 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
     cfg = config((int)(pad < 4 * sms ? pad : 4 * sms), 256, 0, strm, attr);
     if (e == cudaSuccess)
         e = cudaLaunchKernelEx(&cfg, head_loss_gather_kernel, static_cast<const __nv_bfloat16 *>(hidden), hidden_stride,
-                               (int)dim, (const RowHeader *)s.header, (const int32_t *)s.order, s.packed);
+                               (int)dim, (const RowHeader *)s.header, (const int32_t *)s.order, (int)packed_pitch(dim),
+                               s.packed);
     PairArgs a = {};
     a.header = s.header;
     a.order = s.order;
