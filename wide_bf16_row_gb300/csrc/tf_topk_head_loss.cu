@@ -101,10 +101,18 @@ struct RowHeader {
     int32_t splits;   // shares of K that the hidden states' gradient is summed in
 };
 
+// What the epilogue needs of a packed row.
+struct __align__(16) RowFacts {
+    int32_t target;
+    float lse2; // lse in powers of two
+    float grad;
+    float unused;
+};
+
 struct PairArgs {
     const RowHeader *header;  // null: every row counts, in its own place
-    const int32_t *order;     // [count] the row at each place (null: the same)
-    const void *target;       // int64 or int32 [rows]
+    const RowFacts *facts;    // [count] of packed rows
+    const void *target;       // int64 or int32 [rows], where rows are not packed
     int32_t target64;
     int32_t rows;             // all rows
     int32_t dim;
@@ -116,8 +124,6 @@ struct PairArgs {
     int32_t pad_rows;         // row pitch of `partial`
     int32_t first;            // kHidden: the sums start here
     float2 *partial;          // kLse: [2 * column tiles][pad_rows]: reference exponent, sum
-    const float *lse;         // kProb [rows]
-    const float *grad;        // kProb [rows]
 };
 
 // ---------------------------------------------------------------- PTX helpers
@@ -405,12 +411,15 @@ template <int kMode> struct Shape {
     __device__ int64_t units() const { return h_units + (kMode == kHidden ? 0 : (int64_t)m_tiles * n_tiles); }
     // Whether a unit is a tile of d_weight.
     __device__ bool of_weight(int64_t u) const { return kMode == kWeight || (kMode == kGrads && u >= h_units); }
-    __device__ Unit at(int64_t u) const
+    __device__ Unit at(int64_t u) const { return units() <= INT32_MAX ? at_index((int32_t)u) : at_index(u); }
+
+  private:
+    template <typename I> __device__ Unit at_index(I u) const
     {
         Unit t;
-        if (kMode == kHidden || (kMode == kGrads && u < h_units)) {
+        if (kMode == kHidden || (kMode == kGrads && u < (I)h_units)) {
             t.m = (int)(u % h_tiles);
-            const int64_t r = u / h_tiles;
+            const I r = u / h_tiles;
             t.n = (int)(r % n_tiles);
             t.split = (int)(r / n_tiles);
             t.k0 = (int)((int64_t)h_steps * t.split / splits);
@@ -419,13 +428,17 @@ template <int kMode> struct Shape {
         }
         // groups of kGroupRows row tiles; in a group the row tile moves
         // first, so that the pairs at work share the tiles of B
-        u -= h_units;
-        const int64_t per_group = (int64_t)kGroupRows * n_tiles;
-        const int g = (int)(u / per_group);
-        const int64_t r = u - g * per_group;
-        const int in_group = min(kGroupRows, m_tiles - g * kGroupRows);
-        t.m = g * kGroupRows + (int)(r % in_group);
-        t.n = (int)(r / in_group);
+        u -= (I)h_units;
+        int g = 0, in_group = m_tiles;
+        I r = u;
+        if (m_tiles > kGroupRows) {
+            const I per_group = (I)kGroupRows * n_tiles;
+            g = (int)(u / per_group);
+            r = u - g * per_group;
+            in_group = min(kGroupRows, m_tiles - g * kGroupRows);
+        }
+        t.m = g * kGroupRows + (in_group > 1 ? (int)(r % in_group) : 0);
+        t.n = in_group > 1 ? (int)(r / in_group) : (int)r;
         t.split = 0;
         t.k0 = 0;
         t.k1 = k_steps;
@@ -633,25 +646,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         float ref = 0.0f, top = -INFINITY, sum = 0.0f;
         // few rows: the warps that have none (but for kProb's zeros) skip the tile
         const bool no_rows = kFew && kMode != kProb && (int)rank * kHalf + 32 * q >= count;
-        for (int64_t u = pair; u < units; u += pairs, ++tile) {
-            const Unit t = shape.at(u);
-            const uint32_t buf = tile & 1, use = tile >> 1;
-            const int row = t.m * kTileRows + (int)rank * kHalf + 32 * q + lane; // M index of this thread
-            // what the thread needs of its row, fetched while the products run
-            int at = -1; // the target's column of the piece
-            float lse2 = 0.0f, g = 0.0f;
+        // a row's facts are fetched a tile ahead
+        const auto row_of = [&](int m) { return m * kTileRows + (int)rank * kHalf + 32 * q + lane; };
+        const auto facts_of = [&](int row) {
+            RowFacts f = {-1, 0.0f, 0.0f, 0.0f};
             if ((kMode == kLse || kMode == kProb) && row < count) {
-                const int r = a.order ? a.order[row] : row;
-                const int64_t target = target_of(a.target, a.target64, r);
-                if (target >= a.begin && target < (int64_t)a.begin + a.cols) at = (int)(target - a.begin);
-                if (kMode == kProb) {
-                    lse2 = a.lse[r] * kLog2e;
-                    g = a.grad[r] / a.header->grad_scale;
+                if (a.facts) {
+                    f = a.facts[row];
+                } else {
+                    const int64_t target = target_of(a.target, a.target64, row);
+                    f.target = target >= 0 && target < a.vocab ? (int32_t)target : -1;
                 }
+            }
+            return f;
+        };
+        Unit t = {}, ahead = {};
+        RowFacts facts = {}, facts_ahead = {};
+        if (pair < units) {
+            ahead = shape.at(pair);
+            facts_ahead = facts_of(row_of(ahead.m));
+        }
+        for (int64_t u = pair; u < units; u += pairs, ++tile) {
+            t = ahead;
+            facts = facts_ahead;
+            const uint32_t buf = tile & 1, use = tile >> 1;
+            const int row = row_of(t.m); // M index of this thread
+            if (u + pairs < units) {
+                ahead = shape.at(u + pairs);
+                if (ahead.m != t.m) facts_ahead = facts_of(row_of(ahead.m));
             }
             const bool ready = mbar_wait(&sm.acc_full[buf], use & 1, abort);
             if (!__all_sync(0xFFFFFFFFu, ready)) break;
             tc_fence_after();
+            // the target's column of the piece
+            const int at = facts.target >= a.begin && facts.target < a.begin + a.cols ? facts.target - a.begin : -1;
+            const float lse2 = facts.lse2, g = kMode == kProb ? facts.grad / a.header->grad_scale : 0.0f;
             const uint32_t lanes = tmem + buf * kTileCols + ((uint32_t)(32 * q) << 16);
             // columns of the tile that this thread takes
             const int c0 = h * half_cols, chunks = no_rows ? 0 : half_cols / kChunk;
@@ -675,9 +704,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                         for (int i = 0; i < kChunk; ++i)
                             if (i == hit) x[i] = -INFINITY;
-                    float m = x[0];
+                    // four chains each: one of 32 steps is longer than the rest of the chunk
+                    float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                    for (int i = 1; i < kChunk; ++i) m = fmaxf(m, x[i]);
+                    for (int i = 4; i < kChunk; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
+                    const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     if (m > top) {
                         // an infinite maximum keeps reference 0: inf and NaN then show in the sum
                         const float next = fabsf(m) < INFINITY ? m * kLog2e : 0.0f;
@@ -685,8 +716,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         ref = next;
                         top = m;
                     }
+                    float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) sum += exp2_fast(fmaf(x[i], kLog2e, -ref));
+                    for (int i = 0; i < kChunk; ++i) s4[i & 3] += exp2_fast(fmaf(x[i], kLog2e, -ref));
+                    sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
                 }
                 if (row < count && !kFew)
                     a.partial[(size_t)(2 * t.n + h) * a.pad_rows + row] =
@@ -767,13 +800,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
 constexpr int kPrepareThreads = 1024;
 
-// One CTA: the rows that count, in their order (order[j] the row at place j,
-// place[r] its place or -1), and the largest finite |g|, by which every g is
+// One CTA: the rows that count, in their order (order[j] the row at place j and
+// its facts, place[r] the row's place or -1), and the largest finite |g|, by which every g is
 // divided before G is rounded to bf16: with one g for all rows (a mean) the
 // target's entry of G is then exactly p - 1, and no g leaves bf16's range.
 __global__ void __launch_bounds__(kPrepareThreads)
-    head_loss_prepare_kernel(const void *target, int target64, int64_t ignore, const float *grad, int rows, int vocab,
-                             int dim, int pairs, int most_splits, RowHeader *header, int32_t *order, int32_t *place)
+    head_loss_prepare_kernel(const void *target, int target64, int64_t ignore, const float *lse, const float *grad,
+                             int rows, int vocab, int dim, int pairs, int most_splits, RowHeader *header,
+                             int32_t *order, int32_t *place, RowFacts *facts)
 {
     __shared__ int warp_sum[32];
     __shared__ float warp_max[32];
@@ -784,12 +818,17 @@ __global__ void __launch_bounds__(kPrepareThreads)
     for (int r0 = 0; r0 < rows; r0 += kPrepareThreads) {
         const int r = r0 + tid;
         bool counts = false;
+        RowFacts fact = {-1, 0.0f, 0.0f, 0.0f};
         if (r < rows) {
             const int64_t t = target_of(target, target64, r);
+            if (grad) {
+                fact.lse2 = lse[r] * kLog2e;
+                fact.grad = grad[r];
+            }
             counts = t != ignore && t >= 0 && t < vocab;
-            if (counts && grad) {
-                const float g = fabsf(grad[r]);
-                if (g < INFINITY) top = fmaxf(top, g);
+            if (counts) {
+                fact.target = (int32_t)t;
+                if (fabsf(fact.grad) < INFINITY) top = fmaxf(top, fabsf(fact.grad));
             }
         }
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, counts);
@@ -804,7 +843,10 @@ __global__ void __launch_bounds__(kPrepareThreads)
         const int at = before + __popc(mask & ((1u << lane) - 1u));
         if (r < rows) {
             place[r] = counts ? at : -1;
-            if (counts) order[at] = r;
+            if (counts) {
+                order[at] = r;
+                facts[at] = fact;
+            }
         }
         base += total;
         __syncthreads();
@@ -1156,6 +1198,7 @@ int tile_width(int64_t rows, int64_t vocab, int pairs)
 struct LossSpace {
     RowHeader *header;
     int32_t *order, *place;
+    RowFacts *facts;
     __nv_bfloat16 *packed;
     float2 *partial;
     size_t bytes;
@@ -1171,6 +1214,7 @@ LossSpace loss_space(const void *p, int64_t rows, int64_t dim, int64_t parts)
         s.header = c.take<RowHeader>(1);
         s.order = c.take<int32_t>(rows);
         s.place = c.take<int32_t>(rows);
+        s.facts = c.take<RowFacts>(rows);
         s.packed = c.take<__nv_bfloat16>(pad_rows_of(rows) * packed_pitch(dim));
     }
     s.partial = c.take<float2>(parts * pad_rows_of(rows));
@@ -1181,6 +1225,7 @@ LossSpace loss_space(const void *p, int64_t rows, int64_t dim, int64_t parts)
 struct GradSpace {
     RowHeader *header;
     int32_t *order, *place;
+    RowFacts *facts;
     __nv_bfloat16 *packed;
     float *sums;
     __nv_bfloat16 *prob;
@@ -1209,6 +1254,7 @@ GradSpace grad_space(const void *p, int64_t rows, int64_t dim, int64_t vocab, in
     s.header = c.take<RowHeader>(1);
     s.order = c.take<int32_t>(rows);
     s.place = c.take<int32_t>(rows);
+    s.facts = c.take<RowFacts>(rows);
     s.packed = c.take<__nv_bfloat16>(pad * packed_pitch(dim));
     if (hidden) s.sums = c.take<float>((int64_t)s.splits * pad * dim);
     s.prob = c.take<__nv_bfloat16>(pad * piece);
@@ -1288,8 +1334,8 @@ int run_loss(const void *hidden, int64_t hidden_stride, const void *weight, int6
     if (packed) {
         cudaLaunchConfig_t cfg = config(1, kPrepareThreads, 0, strm, attr);
         e = cudaLaunchKernelEx(&cfg, head_loss_prepare_kernel, target, (int)(target_bytes == 8), ignore,
-                               (const float *)nullptr, (int)rows, (int)vocab, (int)dim, pairs, 1, s.header, s.order,
-                               s.place);
+                               (const float *)nullptr, (const float *)nullptr, (int)rows, (int)vocab, (int)dim, pairs, 1,
+                               s.header, s.order, s.place, s.facts);
         cfg = config((int)(rows < 4 * sms ? rows : 4 * sms), 256, 0, strm, attr);
         if (e == cudaSuccess)
             e = cudaLaunchKernelEx(&cfg, head_loss_gather_kernel, static_cast<const __nv_bfloat16 *>(hidden),
@@ -1298,7 +1344,7 @@ int run_loss(const void *hidden, int64_t hidden_stride, const void *weight, int6
     }
     PairArgs a = {};
     a.header = s.header;
-    a.order = s.order;
+    a.facts = s.facts;
     a.target = target;
     a.target64 = target_bytes == 8;
     a.rows = (int32_t)rows;
@@ -1377,8 +1423,8 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = config(1, kPrepareThreads, 0, strm, attr);
     cudaError_t e = cudaLaunchKernelEx(&cfg, head_loss_prepare_kernel, target, (int)(target_bytes == 8), ignore,
-                                       grad_loss, (int)rows, (int)vocab, (int)dim, pairs, splits, s.header, s.order,
-                                       s.place);
+                                       lse, grad_loss, (int)rows, (int)vocab, (int)dim, pairs, splits, s.header,
+                                       s.order, s.place, s.facts);
     cfg = config((int)(pad < 4 * sms ? pad : 4 * sms), 256, 0, strm, attr);
     if (e == cudaSuccess)
         e = cudaLaunchKernelEx(&cfg, head_loss_gather_kernel, static_cast<const __nv_bfloat16 *>(hidden), hidden_stride,
@@ -1386,7 +1432,7 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
                                s.packed);
     PairArgs a = {};
     a.header = s.header;
-    a.order = s.order;
+    a.facts = s.facts;
     a.target = target;
     a.target64 = target_bytes == 8;
     a.rows = (int32_t)rows;
@@ -1394,8 +1440,6 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
     a.vocab = (int32_t)vocab;
     a.width = kTileCols;
     a.pad_rows = (int32_t)pad;
-    a.lse = lse;
-    a.grad = grad_loss;
     const int64_t row_tiles = pad / kTileRows, dim_tiles = (dim + kTileCols - 1) / kTileCols;
     for (int64_t begin = 0; begin < vocab && e == cudaSuccess; begin += piece) {
         a.begin = (int32_t)begin;
