@@ -170,11 +170,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
                      : "r"(saddr(bar)), "r"(parity)
                      : "memory");
         if (ok) return true;
-        if (*abort) return false;
+        if (abort && *abort) return false;
     }
     atomicCAS(&g_head_loss_fault, 0u, kFaultWait);
-    *abort = 1;
+    if (abort) *abort = 1;
     return false;
+}
+
+// Bounded wait of the wind-down: goes on whether or not the CTA gave up.
+__device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity)
+{
+    mbar_wait(bar, parity, nullptr);
 }
 
 // As mbar_wait, by a whole warp: the same answer in every lane.
@@ -261,22 +267,32 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// This warp's 32 accumulator lanes (lane = thread), kChunk columns from `taddr`.
-__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[kChunk])
+// This warp's 32 accumulator lanes (lane = thread), kChunk columns from
+// `taddr`, on their way into `r` until tmem_wait.
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[kChunk])
 {
-    uint32_t r[kChunk];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
                  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
                  "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+                   "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+                   "=r"(r[30]), "=r"(r[31])
                  : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[kChunk])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
 }
 
 __device__ __forceinline__ void cluster_sync()
@@ -489,7 +505,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // Rows of A that are not loaded leave whatever the ring holds in their
     // lanes of the accumulator, which nothing reads; the MMA reads on from a
     // short share of A into what follows it in the ring.
-    const int half_cols = kMode == kLse || kMode == kProb ? a.width / 2 : kHalf; // one CTA's share of B
+    const int half_cols = kMode == kLse ? a.width / 2 : kHalf; // one CTA's share of B
     // (Whole shares have the ring's shape at compile time: the issuing thread
     // keeps up better, 615 against 631 us on 800 x 2048 x 248320.)
     const uint32_t share_a = kFew ? (uint32_t)a.row_box * kStepK * 2 : kShare;
@@ -583,7 +599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (rank == 0)
                 for (uint32_t j = 0; j < stages; ++j) {
                     const uint32_t filled = j < s ? turn + 1 : turn; // times stage j was filled
-                    if (filled) mbar_wait(&sm.full[j], (filled - 1) & 1, abort);
+                    if (filled) mbar_drain(&sm.full[j], (filled - 1) & 1);
                 }
         }
     } else if (warp == 1) {
@@ -618,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                  saddr(&sm.drain))
                              : "memory");
             __syncwarp();
-            mbar_wait(&sm.drain, 0, abort);
+            mbar_drain(&sm.drain, 0);
         }
     } else {
         // ---- epilogue
@@ -660,6 +676,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
             return f;
         };
+        // body(c, x) for the chunks of an accumulator (loading the next one
+        // meanwhile costs more registers than it hides: 12 % slower tiles)
+        const auto walk = [&](uint32_t taddr, int chunks, auto body) {
+            for (int c = 0; c < chunks; ++c) {
+                uint32_t r[kChunk];
+                tmem_load(taddr + c * kChunk, r);
+                tmem_wait(r);
+                float x[kChunk];
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) x[i] = __uint_as_float(r[i]);
+                body(c, x);
+            }
+        };
         Unit t = {}, ahead = {};
         RowFacts facts = {}, facts_ahead = {};
         if (pair < units) {
@@ -684,15 +713,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const uint32_t lanes = tmem + buf * kTileCols + ((uint32_t)(32 * q) << 16);
             // columns of the tile that this thread takes
             const int c0 = h * half_cols, chunks = no_rows ? 0 : half_cols / kChunk;
+            // gradients: those that hold columns of them
+            const int chunks_in_dim = min(chunks, ceil_div(max(0, a.dim - t.n * kTileCols - c0), kChunk));
             if (kMode == kGrads) { // boxes of the other kind may still be on their way out
                 if (elect_one()) box_read_wait<0>();
                 __syncwarp();
             }
             if (kMode == kLse) {
                 if (!kFew) ref = 0.0f, top = -INFINITY, sum = 0.0f;
-                for (int c = 0; c < chunks; ++c) {
-                    float x[kChunk];
-                    tmem_load(lanes + c0 + c * kChunk, x);
+                walk(lanes + c0, chunks, [&](int c, float (&x)[kChunk]) {
                     const int col = t.n * a.width + c0 + c * kChunk; // of the piece
                     const int left = a.cols - col;
                     if (left < kChunk)
@@ -720,32 +749,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) s4[i & 3] += exp2_fast(fmaf(x[i], kLog2e, -ref));
                     sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                }
+                });
                 if (row < count && !kFew)
                     a.partial[(size_t)(2 * t.n + h) * a.pad_rows + row] =
                         make_float2(top == -INFINITY ? -INFINITY : ref, sum);
             } else if (kMode == kProb) {
-                for (int c = 0; c < chunks; ++c) {
-                    float x[kChunk];
-                    tmem_load(lanes + c0 + c * kChunk, x);
-                    const int col = t.n * a.width + c0 + c * kChunk;
+                // rows past the count are zeros up to the last K step of the
+                // products over rows, and nothing reads those behind it
+                const int end = max(1, ceil_div(count, kStepK)) * kStepK;
+                walk(lanes + c0, row - lane < end ? kHalf / kChunk : 0, [&](int c, float (&x)[kChunk]) {
+                    const int col = t.n * kTileCols + c0 + c * kChunk;
                     const int left = row < count ? a.cols - col : 0;
                     const int hit = at - col;
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) x[i] = exp2_fast(fmaf(x[i], kLog2e, -lse2));
+                    if (__any_sync(0xFFFFFFFFu, (uint32_t)hit < (uint32_t)kChunk))
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i)
+                            if (i == hit) x[i] -= 1.0f;
+                    if (__any_sync(0xFFFFFFFFu, left < kChunk))
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i) x[i] = i < left ? x[i] : 0.0f;
                     uint32_t out[kChunk / 2];
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) {
-                        x[i] = exp2_fast(fmaf(x[i], kLog2e, -lse2));
-                        if (i == hit) x[i] -= 1.0f;
-                        x[i] = i < left ? x[i] * g : 0.0f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < kChunk / 2; ++i) out[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+                    for (int i = 0; i < kChunk / 2; ++i) out[i] = pack_bf16(x[2 * i] * g, x[2 * i + 1] * g);
                     send_bf16(&map_out, out, col, row - lane, true);
-                }
+                });
             } else if (!shape.of_weight(u)) {
-                for (int c = 0; c < chunks && t.n * kTileCols + c0 + c * kChunk < a.dim; ++c) {
-                    float x[kChunk];
-                    tmem_load(lanes + c0 + c * kChunk, x);
+                walk(lanes + c0, chunks_in_dim, [&](int c, float (&x)[kChunk]) {
                     const int col = t.n * kTileCols + c0 + c * kChunk;
                     const bool any = row - lane < count; // rows past the count get sums nothing reads
                     if (elect_one()) box_read_wait<0>();
@@ -760,18 +791,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         box_commit();
                     }
                     __syncwarp();
-                }
+                });
             } else {
                 const float scale = a.header->grad_scale;
-                for (int c = 0; c < chunks && t.n * kTileCols + c0 + c * kChunk < a.dim; ++c) {
-                    float x[kChunk];
-                    tmem_load(lanes + c0 + c * kChunk, x);
+                walk(lanes + c0, chunks_in_dim, [&](int c, float (&x)[kChunk]) {
                     const int col = t.n * kTileCols + c0 + c * kChunk;
                     uint32_t out[kChunk / 2];
 #pragma unroll
                     for (int i = 0; i < kChunk / 2; ++i) out[i] = pack_bf16(x[2 * i] * scale, x[2 * i + 1] * scale);
                     send_bf16(&map_wout, out, col, a.begin + row - lane, row - lane < a.cols);
-                }
+                });
             }
             tc_fence_before();
             __syncwarp();
@@ -789,6 +818,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (kMode != kLse) grid_dependents_go();
     tc_fence_before();
     __syncthreads();
+    // a pair that gave up may have copies in flight that no barrier of this
+    // CTA counts: time for them to land (tens of times a copy's own)
+    if (*abort)
+        for (int i = 0; i < 64; ++i) __nanosleep(1000);
     cluster_sync(); // neither CTA leaves while the other may still reach its shared memory
     if (warp == 1) {
         tc_fence_after();
