@@ -50,11 +50,14 @@ template <int P> constexpr int kRouteCtas = P <= 8 ? 4 : P <= 16 ? 2 : 1; // CTA
 // Errors of the 32-bit scores, rounded up (u = 2^-24).  Sigmoid: exp2 of a
 // rounded product, |x| s(1 - s) <= 0.23 bounding the share of the rounded
 // exponent and s(1 - s) <= 1/4 that of exp2's 2 ulp; a sum and a reciprocal
-// of at most 1: under 6 u.  Softmax: |x| exp(-|x|) <= 0.37, a sum of 32 lanes'
-// at most 32 terms (36 u), a reciprocal, a product: under 45 u.  Adding the
-// bias rounds by u of the sum.
+// of at most 1: under 6 u.  Softmax: the rounded exponent (2 u |x|
+// relative, with |x| exp(-|x|) <= 0.37), a sum of 32 lanes' at most 32 terms
+// (36 u), exp2, a reciprocal, a product: under 50 u; relative to the score,
+// with |x| <= 88 where it is not flushed to 0: under 230 u.  Adding the bias
+// rounds by u of the sum.
 constexpr float kSigmoidError = 5e-7f;
 constexpr float kSoftmaxError = 4e-6f;
+constexpr float kSoftmaxPart = 1.4e-5f;
 constexpr float kSumError = 1.2e-7f;
 
 static_assert(kMaxRouteK <= 32, "a lane per chosen expert");
@@ -92,31 +95,10 @@ __device__ __forceinline__ float key_value(uint32_t key)
 {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
-__device__ __forceinline__ uint64_t order_key64(double v)
-{
-    const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
-    return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
-}
-
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
-    return v;
-}
-__device__ __forceinline__ double warp_sum64(double v)
-{
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
-    return v;
-}
-__device__ __forceinline__ uint64_t warp_max64(uint64_t v)
-{
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        const uint64_t o = __shfl_xor_sync(kAll, v, d);
-        v = o > v ? o : v;
-    }
     return v;
 }
 __device__ __forceinline__ float warp_max(float v)
@@ -148,117 +130,22 @@ __device__ __forceinline__ uint32_t take_best(uint32_t (&key)[P], int lane, int 
     return best;
 }
 
-template <int P>
-__device__ __forceinline__ uint64_t take_best64(uint64_t (&key)[P], int lane, int &expert)
-{
-    uint64_t mine = 0;
-#pragma unroll
-    for (int j = 0; j < P; ++j) mine = key[j] > mine ? key[j] : mine;
-    const uint64_t best = warp_max64(mine);
-    if (best == 0) {
-        expert = -1;
-        return 0;
-    }
-    const int owner = __ffs(__ballot_sync(kAll, mine == best)) - 1;
-    int at = 0;
-#pragma unroll
-    for (int j = P - 1; j >= 0; --j) at = key[j] == best ? j : at;
-#pragma unroll
-    for (int j = 0; j < P; ++j)
-        if (lane == owner && j == at) key[j] = 0;
-    expert = __shfl_sync(kAll, lane * P + at, owner);
-    return best;
-}
-
 // The groups kept, as a mask, from the groups' values: lane g < groups holds
-// group g's key.  `cut`: the first key left out (0 when none is left out).
-template <typename K>
-__device__ __forceinline__ uint32_t best_groups(K mine, int groups, int kept, int lane, K &last, K &cut)
+// group g's key.  `last`: the last key kept, `cut`: the first left out (0 when
+// none is left out).
+__device__ __forceinline__ uint32_t best_groups(uint32_t mine, int groups, int kept, int lane, uint32_t &last, uint32_t &cut)
 {
     uint32_t rank = 0;
     for (int g = 0; g < groups; ++g) {
-        const K other = __shfl_sync(kAll, mine, g);
+        const uint32_t other = __shfl_sync(kAll, mine, g);
         rank += other > mine || (other == mine && g < lane);
     }
     const bool keep = lane < groups && rank < (uint32_t)kept;
     const uint32_t on_edge = __ballot_sync(kAll, lane < groups && rank == (uint32_t)kept - 1);
     const uint32_t past = __ballot_sync(kAll, lane < groups && rank == (uint32_t)kept);
-    last = on_edge ? __shfl_sync(kAll, mine, __ffs(on_edge) - 1) : (K)0;
-    cut = past ? __shfl_sync(kAll, mine, __ffs(past) - 1) : (K)0;
+    last = on_edge ? __shfl_sync(kAll, mine, __ffs(on_edge) - 1) : 0u;
+    cut = past ? __shfl_sync(kAll, mine, __ffs(past) - 1) : 0u;
     return __ballot_sync(kAll, keep);
-}
-
-// The choice of one row in 64 bits: lane i gets the i-th chosen expert or -1.
-template <typename T, int P>
-__device__ __noinline__ int choose_in_64_bits(const T *row, const RouteArgs &a)
-{
-    const int lane = threadIdx.x & 31;
-    double v[P];
-    double top = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-        const int e = lane * P + j;
-        const float x = e < a.experts ? load_logit(row + e) : -INFINITY;
-        v[j] = in_reach(x) ? (double)fminf(x, FLT_MAX) : (double)-INFINITY;
-        top = fmax(top, v[j]);
-    }
-    if (a.softmax) {
-#pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmax(top, __shfl_xor_sync(kAll, top, d));
-        double sum = 0;
-#pragma unroll
-        for (int j = 0; j < P; ++j) sum += v[j] > -INFINITY ? exp(v[j] - top) : 0.0;
-        sum = warp_sum64(sum);
-#pragma unroll
-        for (int j = 0; j < P; ++j)
-            if (v[j] > -INFINITY) v[j] = exp(v[j] - top) / sum;
-    } else {
-#pragma unroll
-        for (int j = 0; j < P; ++j)
-            if (v[j] > -INFINITY) v[j] = 1.0 / (1.0 + exp(-v[j]));
-    }
-    uint64_t key[P], by_group[P];
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-        const int e = lane * P + j;
-        double c = v[j];
-        if (c > -INFINITY && a.bias) c += (double)a.bias[e];
-        const bool ok = c > -INFINITY; // neither NaN nor -inf
-        by_group[j] = ok ? order_key64(c) : 0ull;
-        key[j] = by_group[j];
-        if (ok && !a.bias) key[j] = order_key64((double)fminf(load_logit(row + e), FLT_MAX));
-    }
-    if (a.groups > 1) {
-        const int per = a.experts / a.groups;
-        uint64_t mine = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            uint64_t members[P];
-#pragma unroll
-            for (int j = 0; j < P; ++j) members[j] = (lane * P + j) / per == g ? by_group[j] : 0ull;
-            int e;
-            const uint64_t first = take_best64<P>(members, lane, e);
-            const uint64_t second = a.best > 1 && first ? take_best64<P>(members, lane, e) : 0ull;
-            const auto value = [](uint64_t k) {
-                return __longlong_as_double((long long)(k & 0x8000000000000000ull ? k ^ 0x8000000000000000ull : ~k));
-            };
-            const double sum = first ? value(first) + (second ? value(second) : 0.0) : 0.0;
-            if (lane == g) mine = first ? order_key64(sum) : 0ull;
-        }
-        uint64_t last, cut;
-        const uint32_t keep = best_groups<uint64_t>(mine, a.groups, a.kept, lane, last, cut);
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-            const int e = lane * P + j;
-            if (e < a.experts && !((keep >> (e / per)) & 1u)) key[j] = 0;
-        }
-    }
-    int chosen = -1;
-    for (int i = 0; i < a.k; ++i) {
-        int e;
-        if (take_best64<P>(key, lane, e) == 0) break;
-        if (lane == i) chosen = e;
-    }
-    return chosen;
 }
 
 // Sum and maximum over the W lanes (a power of two) that hold one token.
@@ -435,21 +322,206 @@ template <int P> struct LaneList {
     }
 };
 
-// The k best experts of a row by the logits alone, from whole keys.
-template <typename T, int P>
-__device__ __noinline__ int choose_by_logits(const T *row, const RouteArgs &a)
+// What of a row's softmax the weights need.
+struct RowSoftmax {
+    float top, inverse; // exp(x - top) * inverse
+};
+
+// The slow parts below run for a token in some thousands, whose warp the
+// kernel then waits for: their loops stay rolled, because fetching code that
+// no other warp has run takes longer than running it (unrolled, they were 31
+// us of a 74 us kernel).
+
+// Sum of exp(x - top) over a row in 64 bits, in every lane.
+template <typename T> __device__ __noinline__ double sum_in_64_bits(const T *row, int experts, float top)
 {
-    const int lane = threadIdx.x & 31;
-    float x[P];
-    load_row<T, P>(row, a.experts, lane, a.vec, x);
-    uint32_t key[P];
-#pragma unroll
-    for (int j = 0; j < P; ++j) key[j] = x[j] > -INFINITY ? order_key(x[j]) : 0u;
+    double sum = 0;
+#pragma unroll 1
+    for (int e = threadIdx.x & 31; e < experts; e += 32) {
+        const float x = load_logit(row + e);
+        if (in_reach(x)) sum += exp((double)fminf(x, FLT_MAX) - (double)top);
+    }
+#pragma unroll 1
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+    return sum;
+}
+
+// A logit's score in 64 bits (`top` and `sum` of its row's softmax); -inf for
+// an expert out of reach.
+__device__ __noinline__ double score_in_64_bits(const RouteArgs &a, float x, float top, double sum)
+{
+    if (!in_reach(x)) return -INFINITY;
+    const double e = exp(a.softmax ? (double)fminf(x, FLT_MAX) - (double)top : -(double)fminf(x, FLT_MAX));
+    return a.softmax ? e / sum : 1.0 / (1.0 + e);
+}
+
+// An expert's choice in 64 bits; -inf where it has none.
+template <typename T>
+__device__ __noinline__ double choice_in_64_bits(const T *row, const RouteArgs &a, int expert, float top, double sum)
+{
+    double c = score_in_64_bits(a, load_logit(row + expert), top, sum);
+    if (a.bias) c += (double)a.bias[expert];
+    return c > -INFINITY ? c : -INFINITY;
+}
+
+// The groups kept, where the values around the cut are too close to call
+// (`last` the last kept, `cut` the first left out, `margin` their error): the
+// groups in between are valued again in 64 bits.  `value`: the groups' values,
+// or null to value them all.  Without a bias a group's best are those of the
+// largest logits, so only they are scored in 64 bits.
+template <typename T>
+__device__ __noinline__ uint32_t decide_groups(const T *row, const RouteArgs &a, const float *value, float last, float cut,
+                                               float margin, float top)
+{
+    const int lane = threadIdx.x & 31, per = a.experts / a.groups;
+    const float v = value && lane < a.groups ? value[lane] : -INFINITY;
+    const bool open = lane < a.groups && (!value || (!(v < cut - margin) && !(v > last + margin) && v > -INFINITY));
+    const uint32_t unsure = __ballot_sync(kAll, open);
+    const uint32_t in = __ballot_sync(kAll, lane < a.groups && !open && v > last);
+    const double sum = a.softmax ? sum_in_64_bits(row, a.experts, top) : 1.0;
+    double mine = 0;
+    float x1 = -INFINITY, x2 = -INFINITY; // the lane's group's best logits
+#pragma unroll 1
+    for (uint32_t left = unsure; left; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        if (!a.bias) {
+            float m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll 1
+            for (int i = lane; i < per; i += 32) {
+                const float x = load_logit(row + g * per + i);
+                const float c = in_reach(x) ? fminf(x, FLT_MAX) : -INFINITY;
+                m2 = fmaxf(m2, fminf(m1, c));
+                m1 = fmaxf(m1, c);
+            }
+#pragma unroll 1
+            for (int d = 16; d; d >>= 1) join_best_two(m1, m2, __shfl_xor_sync(kAll, m1, d), __shfl_xor_sync(kAll, m2, d));
+            if (lane == g) x1 = m1, x2 = a.best > 1 ? m2 : -INFINITY;
+        } else {
+            double m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll 1
+            for (int i = lane; i < per; i += 32) {
+                const double c = choice_in_64_bits(row, a, g * per + i, top, sum);
+                m2 = fmax(m2, fmin(m1, c));
+                m1 = fmax(m1, c);
+            }
+#pragma unroll 1
+            for (int d = 16; d; d >>= 1) {
+                const double o1 = __shfl_xor_sync(kAll, m1, d), o2 = __shfl_xor_sync(kAll, m2, d);
+                m2 = fmax(fmin(m1, o1), fmax(m2, o2));
+                m1 = fmax(m1, o1);
+            }
+            if (lane == g) mine = a.best > 1 && m2 > -INFINITY ? m1 + m2 : m1;
+        }
+    }
+    if (!a.bias) {
+        mine = score_in_64_bits(a, x1, top, sum);
+        if (x2 > -INFINITY) mine += score_in_64_bits(a, x2, top, sum);
+    }
+    int rank = __popc(in);
+#pragma unroll 1
+    for (uint32_t left = unsure; left; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        const double o = __shfl_sync(kAll, mine, g);
+        rank += o > mine || (o == mine && g < lane);
+    }
+    return in | __ballot_sync(kAll, open && rank < a.kept);
+}
+
+// The choice of a row whose order short keys and 32 bits left open, given the
+// groups kept and a bound that no chosen expert's choice lies below: the few
+// experts from there on, in order by the logits, or with a bias in 64 bits.
+// Lane i < k gets the i-th or -1; `lost` where there are too many of them.
+template <typename T>
+__device__ __noinline__ int choose_from(const T *row, const RouteArgs &a, uint32_t keep, float least, RowSoftmax soft,
+                                        int32_t *place, bool &lost)
+{
+    const int lane = threadIdx.x & 31, per = a.experts / a.groups;
+    int n = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < a.experts; e0 += 32) {
+        const int e = e0 + lane;
+        float c = -INFINITY;
+        if (e < a.experts && in_reach(load_logit(row + e)) && (a.groups == 1 || ((keep >> (e / per)) & 1u))) {
+            c = fminf(load_logit(row + e), FLT_MAX);
+            if (a.bias)
+                c = (a.softmax ? exp2_fast(kLog2e * (c - soft.top)) * soft.inverse : sigmoid_fast(c)) + a.bias[e];
+        }
+        const bool in = c > -INFINITY && c >= least;
+        const uint32_t mask = __ballot_sync(kAll, in);
+        const int at = n + __popc(mask & ((1u << lane) - 1u));
+        if (in && at < 32) place[at] = e;
+        n += __popc(mask);
+    }
+    __syncwarp();
+    lost = n > 32;
+    if (lost) return -1;
+    const int expert = lane < n ? place[lane] : -1;
+    double c = expert < 0 ? -INFINITY : (double)fminf(load_logit(row + expert), FLT_MAX);
+    if (a.bias) { // without one the logits decide
+        const double sum = a.softmax ? sum_in_64_bits(row, a.experts, soft.top) : 1.0;
+        c = expert < 0 ? -INFINITY : choice_in_64_bits(row, a, expert, soft.top, sum);
+    }
+    int rank = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const double o = __shfl_sync(kAll, c, i);
+        const int oe = __shfl_sync(kAll, expert, i);
+        rank += o > c || (o == c && oe < expert);
+    }
+    __syncwarp();
+    if (expert >= 0) place[rank] = expert;
+    __syncwarp();
+    const int chosen = lane < n && lane < a.k ? place[lane] : -1;
+    __syncwarp();
+    return chosen;
+}
+
+// The whole choice of a row in 64 bits, or without a bias by the logits (heavy
+// ties): one expert at a time.  Lane i < k gets the i-th or -1.
+template <typename T> __device__ __noinline__ int choose_slowly(const T *row, const RouteArgs &a)
+{
+    const int lane = threadIdx.x & 31, per = a.experts / a.groups;
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int e = lane; e < a.experts; e += 32) {
+        const float x = load_logit(row + e);
+        if (in_reach(x)) top = fmaxf(top, fminf(x, FLT_MAX));
+    }
+    top = warp_max(top);
+    const double sum = a.softmax && a.bias ? sum_in_64_bits(row, a.experts, top) : 1.0;
+    const uint32_t keep = a.groups > 1 ? decide_groups(row, a, nullptr, 0.0f, 0.0f, 0.0f, top) : 0xFFFFFFFFu;
+    double c[kMaxExperts / 32];
+#pragma unroll 1
+    for (int i = 0, e = lane; e < a.experts; ++i, e += 32) {
+        const float x = load_logit(row + e);
+        c[i] = -INFINITY;
+        if (in_reach(x) && ((keep >> (a.groups > 1 ? e / per : 0)) & 1u))
+            c[i] = a.bias ? choice_in_64_bits(row, a, e, top, sum) : (double)fminf(x, FLT_MAX);
+    }
     int chosen = -1;
-    for (int i = 0; i < a.k; ++i) {
-        int e;
-        if (take_best<P>(key, lane, e) == 0) break;
-        if (lane == i) chosen = e;
+#pragma unroll 1
+    for (int round = 0; round < a.k; ++round) {
+        double best = -INFINITY;
+        int at = kMaxExperts;
+#pragma unroll 1
+        for (int i = 0, e = lane; e < a.experts; ++i, e += 32)
+            if (c[i] > best) {
+                best = c[i];
+                at = e;
+            }
+        const int own = at;
+#pragma unroll 1
+        for (int d = 16; d; d >>= 1) {
+            const double o = __shfl_xor_sync(kAll, best, d);
+            const int oe = __shfl_xor_sync(kAll, at, d);
+            if (o > best || (o == best && oe < at)) {
+                best = o;
+                at = oe;
+            }
+        }
+        if (!(best > -INFINITY)) break;
+        if (own == at) c[at >> 5] = -INFINITY;
+        if (lane == round) chosen = at;
     }
     return chosen;
 }
@@ -458,7 +530,7 @@ __device__ __noinline__ int choose_by_logits(const T *row, const RouteArgs &a)
 // could not settle: by the logits, or with a bias by the choices, in 64 bits
 // where 32 leave neighbours closer than their error.  `c` is the lane's choice
 // in 32 bits.  Lane i gets the i-th.
-template <typename T, int P>
+template <typename T>
 __device__ __noinline__ int settle(const T *row, const RouteArgs &a, int expert, float c, int n, int *place)
 {
     const int lane = threadIdx.x & 31;
@@ -473,29 +545,17 @@ __device__ __noinline__ int settle(const T *row, const RouteArgs &a, int expert,
         close |= mine && oe != expert && !(fabsf(o - c) > error + kSumError * (fabsf(o) + fabsf(c)));
     }
     if (a.bias && __any_sync(kAll, close)) {
-        const float x = mine ? fminf(load_logit(row + expert), FLT_MAX) : 0.0f;
-        double d;
-        if (a.softmax) {
-            float y[P];
-            load_row<T, P>(row, a.experts, lane, a.vec, y);
-            float top = y[0];
-#pragma unroll
-            for (int j = 1; j < P; ++j) top = fmaxf(top, y[j]);
-            top = warp_max(top);
-            double sum = 0;
+        float top = -INFINITY;
 #pragma unroll 1
-            for (int j = 0; j < P; ++j) {
-                const int e = lane * P + j;
-                const float z = e < a.experts ? load_logit(row + e) : -INFINITY;
-                if (in_reach(z)) sum += exp((double)fminf(z, FLT_MAX) - top);
-            }
-            sum = warp_sum64(sum);
-            d = exp((double)x - top) / sum;
-        } else {
-            d = 1.0 / (1.0 + exp(-(double)x));
+        for (int e = lane; a.softmax && e < a.experts; e += 32) {
+            const float x = load_logit(row + e);
+            if (in_reach(x)) top = fmaxf(top, fminf(x, FLT_MAX));
         }
-        if (mine) d += (double)a.bias[expert];
+        top = warp_max(top);
+        const double sum = a.softmax ? sum_in_64_bits(row, a.experts, top) : 1.0;
+        const double d = mine ? choice_in_64_bits(row, a, expert, top, sum) : -INFINITY;
         rank = 0;
+#pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const double o = __shfl_sync(kAll, d, i);
             const int oe = __shfl_sync(kAll, expert, i);
@@ -508,11 +568,6 @@ __device__ __noinline__ int settle(const T *row, const RouteArgs &a, int expert,
     __syncwarp();
     return chosen;
 }
-
-// What of a row's softmax the weights need.
-struct RowSoftmax {
-    float top, inverse; // exp(x - top) * inverse
-};
 
 // The choice of one row by a whole warp, from its logits (load_row) in `c`
 // (overwritten): lane i < k gets the i-th expert or -1.  A lane sorts its best
@@ -570,7 +625,7 @@ __device__ __forceinline__ int choose_row(const T *row, const RouteArgs &a, floa
             most = fmaxf(most, fabsf(u) + fabsf(w));
         }
         uint32_t last, cut;
-        const uint32_t keep = best_groups<uint32_t>(mine, a.groups, a.kept, lane, last, cut);
+        const uint32_t keep = best_groups(mine, a.groups, a.kept, lane, last, cut);
         if (cut) again = !(key_value(last) - key_value(cut) > 4.0f * error + 4.0f * part * most);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
@@ -639,10 +694,10 @@ __device__ __forceinline__ int choose_row(const T *row, const RouteArgs &a, floa
             float mine_c = chosen >= 0 ? fminf(load_logit(row + chosen), FLT_MAX) : 0.0f; // the logits decide
             if (a.bias && chosen >= 0)
                 mine_c = (a.softmax ? exp2_fast(kLog2e * (mine_c - top)) * inverse : sigmoid_fast(mine_c)) + a.bias[chosen];
-            chosen = settle<T, P>(row, a, chosen, mine_c, min(n, found), place);
+            chosen = settle(row, a, chosen, mine_c, min(n, found), place);
         }
     }
-    if (again) chosen = scored ? choose_in_64_bits<T, P>(row, a) : choose_by_logits<T, P>(row, a);
+    if (again) chosen = choose_slowly(row, a);
     return chosen;
 }
 
@@ -728,143 +783,37 @@ __device__ __forceinline__ void keep8(uint32_t (&k)[8], const uint32_t (&o)[8], 
             if (!(i & d)) order_pair(k[i], k[i + d]);
 }
 
-// The slow parts below run for a token in some thousands, whose warp the
-// kernel then waits for: their loops stay rolled, because fetching code that
-// no other warp has run takes longer than running it (the whole of choose_row
-// and choose_in_64_bits in their place: 31 us of a 74 us kernel).
+// A choice's error in 32 bits, but for the sum with its bias.
+__device__ __forceinline__ float score_error(bool softmax, float s) { return softmax ? kSoftmaxPart * s : kSigmoidError; }
 
-// Sum of exp(x - top) over a row in 64 bits, in every lane.
-template <typename T> __device__ __noinline__ double sum_in_64_bits(const T *row, int experts, float top)
+// Whether an expert that was left out -- short key below `below` -- could
+// belong in front of the k-th choice `kth` (expert `ke`, logit `kx`).  Without
+// a bias the logits tell; with one, what equals the k-th in logit and bias is
+// a tie, and in order.  By the whole warp.
+template <typename T>
+__device__ __noinline__ bool left_out_matters(const T *row, const RouteArgs &a, uint32_t keep, uint32_t below, float kth,
+                                              float kx, int ke, RowSoftmax soft)
 {
-    double sum = 0;
+    using Key = ShortKey<kQuadExperts / 32>;
+    const int per = a.experts / a.groups;
+    const bool scored = a.bias || a.groups > 1, softmax = a.softmax != 0;
+    const float kb = a.bias ? a.bias[ke] : 0.0f;
+    const float ks = score_error(softmax, a.bias ? kth - kb : 0.0f);
+    bool matters = false;
 #pragma unroll 1
-    for (int e = threadIdx.x & 31; e < experts; e += 32) {
+    for (int e = threadIdx.x & 31; e < a.experts; e += 32) {
         const float x = load_logit(row + e);
-        if (in_reach(x)) sum += exp((double)fminf(x, FLT_MAX) - (double)top);
+        if (!in_reach(x) || !((keep >> (a.groups > 1 ? e / per : 0)) & 1u)) continue;
+        const float z = fminf(x, FLT_MAX);
+        const float b = a.bias ? a.bias[e] : 0.0f;
+        const float s = !scored ? 0.0f : softmax ? exp2_fast(kLog2e * (z - soft.top)) * soft.inverse : sigmoid_fast(z);
+        const float c = scored ? s + b : z + 0.0f;
+        if (!(c > -INFINITY) || Key::make_plain(c, e) >= below) continue;
+        if (!a.bias) matters = matters || z > kx;
+        else if (z != kx || b != kb)
+            matters = matters || !(kth - c > ks + score_error(softmax, s) + kSumError * (fabsf(kth) + fabsf(c)));
     }
-#pragma unroll 1
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-    return sum;
-}
-
-// An expert's choice in 64 bits (`top` and `sum` of its row's softmax); -inf
-// where it has none.
-template <typename T>
-__device__ __noinline__ double choice_in_64_bits(const T *row, const RouteArgs &a, int expert, float top, double sum)
-{
-    const float x = load_logit(row + expert);
-    if (!in_reach(x)) return -INFINITY;
-    const double e = exp(a.softmax ? (double)fminf(x, FLT_MAX) - (double)top : -(double)fminf(x, FLT_MAX));
-    double c = a.softmax ? e / sum : 1.0 / (1.0 + e);
-    if (a.bias) c += (double)a.bias[expert];
-    return c > -INFINITY ? c : -INFINITY;
-}
-
-// The groups kept, where the values around the cut are too close to call
-// (`last` the last kept, `cut` the first left out, `margin` their error): the
-// groups in between are valued again in 64 bits.  `value`: the groups' values.
-template <typename T>
-__device__ __noinline__ uint32_t decide_groups(const T *row, const RouteArgs &a, const float *value, float last, float cut,
-                                               float margin, float top)
-{
-    const int lane = threadIdx.x & 31, per = a.experts / a.groups;
-    const float v = lane < a.groups ? value[lane] : -INFINITY;
-    const bool open = lane < a.groups && !(v < cut - margin) && !(v > last + margin) && v > -INFINITY;
-    const uint32_t unsure = __ballot_sync(kAll, open);
-    const uint32_t in = __ballot_sync(kAll, lane < a.groups && !open && v > last);
-    const double sum = a.softmax ? sum_in_64_bits(row, a.experts, top) : 1.0;
-    double mine = 0;
-#pragma unroll 1
-    for (uint32_t left = unsure; left; left &= left - 1) {
-        const int g = __ffs(left) - 1;
-        double m1 = -INFINITY, m2 = -INFINITY;
-#pragma unroll 1
-        for (int i = lane; i < per; i += 32) {
-            const double c = choice_in_64_bits(row, a, g * per + i, top, sum);
-            m2 = fmax(m2, fmin(m1, c));
-            m1 = fmax(m1, c);
-        }
-#pragma unroll 1
-        for (int d = 16; d; d >>= 1) {
-            const double o1 = __shfl_xor_sync(kAll, m1, d), o2 = __shfl_xor_sync(kAll, m2, d);
-            m2 = fmax(fmin(m1, o1), fmax(m2, o2));
-            m1 = fmax(m1, o1);
-        }
-        if (lane == g) mine = a.best > 1 && m2 > -INFINITY ? m1 + m2 : m1;
-    }
-    int rank = __popc(in);
-#pragma unroll 1
-    for (uint32_t left = unsure; left; left &= left - 1) {
-        const int g = __ffs(left) - 1;
-        const double o = __shfl_sync(kAll, mine, g);
-        rank += o > mine || (o == mine && g < lane);
-    }
-    return in | __ballot_sync(kAll, open && rank < a.kept);
-}
-
-// The choice of a row whose order short keys and 32 bits left open, given the
-// groups kept and a bound that no chosen expert's choice lies below: the few
-// experts from there on, in order by the logits, or with a bias in 64 bits.
-// Lane i < k gets the i-th or -1; `lost` where there are too many of them.
-template <typename T>
-__device__ __noinline__ int choose_from(const T *row, const RouteArgs &a, uint32_t keep, float least, RowSoftmax soft,
-                                        int32_t *place, bool &lost)
-{
-    const int lane = threadIdx.x & 31, per = a.experts / a.groups;
-    const bool scored = a.bias || a.groups > 1;
-    int n = 0;
-#pragma unroll 1
-    for (int e0 = 0; e0 < a.experts; e0 += 32) {
-        const int e = e0 + lane;
-        float c = -INFINITY;
-        if (e < a.experts && in_reach(load_logit(row + e)) && (a.groups == 1 || ((keep >> (e / per)) & 1u))) {
-            c = fminf(load_logit(row + e), FLT_MAX);
-            if (scored)
-                c = (a.softmax ? exp2_fast(kLog2e * (c - soft.top)) * soft.inverse : sigmoid_fast(c)) +
-                    (a.bias ? a.bias[e] : 0.0f);
-        }
-        const bool in = c > -INFINITY && c >= least;
-        const uint32_t mask = __ballot_sync(kAll, in);
-        const int at = n + __popc(mask & ((1u << lane) - 1u));
-        if (in && at < 32) place[at] = e;
-        n += __popc(mask);
-    }
-    __syncwarp();
-    lost = n > 32;
-    if (lost) return -1;
-    const int expert = lane < n ? place[lane] : -1;
-    double c = expert < 0 ? -INFINITY : (double)fminf(load_logit(row + expert), FLT_MAX);
-    if (a.bias) { // without one the logits decide
-        const double sum = a.softmax ? sum_in_64_bits(row, a.experts, soft.top) : 1.0;
-        c = expert < 0 ? -INFINITY : choice_in_64_bits(row, a, expert, soft.top, sum);
-    }
-    int rank = 0;
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-        const double o = __shfl_sync(kAll, c, i);
-        const int oe = __shfl_sync(kAll, expert, i);
-        rank += o > c || (o == c && oe < expert);
-    }
-    __syncwarp();
-    if (expert >= 0) place[rank] = expert;
-    __syncwarp();
-    const int chosen = lane < n && lane < a.k ? place[lane] : -1;
-    __syncwarp();
-    return chosen;
-}
-
-// As choose_row, for one token of a quad warp (heavy ties).
-template <typename T> __device__ __noinline__ int choose_again(const T *row, const RouteArgs &a, int32_t *place)
-{
-    constexpr int P = kQuadExperts / 32;
-    const int lane = threadIdx.x & 31;
-    float c[P], bias[P];
-    RowSoftmax soft;
-    RouteArgs b = a;
-    b.vec = false; // this layout's vectors need not be the quads'
-    load_row<T, P>(row, a.experts, lane, false, c);
-    load_bias<P>(a, lane, bias);
-    return choose_row<T, P>(row, b, c, bias, place, soft);
+    return __any_sync(kAll, matters);
 }
 
 // Four lanes per token, eight tokens per warp, for up to 256 experts and k up
@@ -1038,12 +987,15 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
         int e0 = k0 >= kLeast ? Key::expert(k0) : -1, e1 = k1 >= kLeast ? Key::expert(k1) : -1;
         float x0 = e0 >= 0 ? fminf(load_logit(row + e0), FLT_MAX) : 0.0f;
         float x1 = e1 >= 0 ? fminf(load_logit(row + e1), FLT_MAX) : 0.0f;
-        bool again = false;
-        float least = -FLT_MAX; // nothing below it is chosen (in the lane of the k-th)
+        bool again = false, edge = false; // open: the order of the chosen, and what they leave out
+        float least = -FLT_MAX;           // nothing below it is chosen
+        float kth = -INFINITY, kx = 0.0f; // the k-th choice, its logit and expert
+        int ke = -1;
         const auto score = [&](float x) { return a.softmax ? exp2_fast(kLog2e * (x - top)) * inverse : sigmoid_fast(x); };
         if (!exact) {
-            float c0 = e0 < 0 ? -INFINITY : scored ? score(x0) + bias[e0] : x0;
-            float c1 = e1 < 0 ? -INFINITY : scored ? score(x1) + bias[e1] : x1;
+            // (without a bias the logits are the order, whatever the keys hold)
+            float c0 = e0 < 0 ? -INFINITY : a.bias ? score(x0) + bias[e0] : x0;
+            float c1 = e1 < 0 ? -INFINITY : a.bias ? score(x1) + bias[e1] : x1;
             float next = __shfl_down_sync(kAll, c0, 1, 4);
             if (__any_sync(kAll, c1 > c0 || (sub < 3 && next > c1))) { // the short keys hid an order
                 for (int pass = 0; pass < 4; ++pass) { // odd-even exchanges; equal choices keep theirs (the index's)
@@ -1062,31 +1014,55 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
                 }
                 next = __shfl_down_sync(kAll, c0, 1, 4);
             }
-            // still too close: neighbours up to the k-th and the one behind it, or anything left out that could
-            // have as much as the largest in its short key
-            const auto close = [&](float u, float w) {
-                return w > -INFINITY && !(u - w > 2.0f * error + (scored ? kSumError : 0.0f) * (fabsf(u) + fabsf(w)));
+            // Still too close: neighbours up to the k-th and the one behind
+            // it, unless they are one choice twice (same logit, same bias: a
+            // tie, and in order), or a choice left out.
+            const auto close = [&](float u, float w, float errors) {
+                return w > -INFINITY && !(u - w > errors + (scored ? kSumError : 0.0f) * (fabsf(u) + fabsf(w)));
             };
-            if (scored) again = again || (2 * sub < a.k && close(c0, c1)) || (2 * sub + 1 < a.k && sub < 3 && close(c1, next));
-            if (sub == (a.k - 1) / 2) {
-                const float kth = (a.k & 1) ? c0 : c1;
-                if (dropped >= kLeast) again = again || close(kth, key_value(dropped | Key::kMask));
-                if (kth > -INFINITY)
-                    least = scored && kth < INFINITY ? kth - 3.0f * error - 3.0f * kSumError * fabsf(kth) : kth;
+            if (a.bias) {
+                const float r0 = e0 < 0 ? 0.0f : score_error(a.softmax != 0, c0 - bias[e0]);
+                const float r1 = e1 < 0 ? 0.0f : score_error(a.softmax != 0, c1 - bias[e1]);
+                const float rn = __shfl_down_sync(kAll, r0, 1, 4);
+                const float xn = __shfl_down_sync(kAll, x0, 1, 4);
+                const int en = __shfl_down_sync(kAll, e0, 1, 4);
+                if (2 * sub < a.k && close(c0, c1, r0 + r1)) again = x0 != x1 || bias[e0] != bias[e1];
+                if (2 * sub + 1 < a.k && sub < 3 && close(c1, next, r1 + rn)) again = again || x1 != xn || bias[e1] != bias[en];
             }
+            const int last = (a.k - 1) / 2; // the k-th choice's lane
+            kth = __shfl_sync(kAll, (a.k & 1) ? c0 : c1, last, 4);
+            kx = __shfl_sync(kAll, (a.k & 1) ? x0 : x1, last, 4);
+            ke = __shfl_sync(kAll, (a.k & 1) ? e0 : e1, last, 4);
+            if (kth > -INFINITY) least = a.bias && kth < INFINITY ? kth - 3.0f * error - 3.0f * kSumError * fabsf(kth) : kth;
+            // anything left out has at most the largest value of its short key
+            edge = ke >= 0 && dropped >= kLeast &&
+                   close(a.bias || !scored ? kth : score(kx), key_value(dropped | Key::kMask), 2.0f * error);
         }
-        uint32_t redo = __ballot_sync(kAll, again && live);
-        redo |= redo >> 1;
-        redo = (redo | redo >> 2) & 0x11111111u; // a token's bit in its first lane
+        // a token's bit in its first lane
+        const auto by_token = [&](uint32_t lanes) {
+            lanes |= lanes >> 1;
+            return (lanes | lanes >> 2) & 0x11111111u;
+        };
+        uint32_t redo = by_token(__ballot_sync(kAll, (again || edge) && live));
         if (redo) {
+            const uint32_t order = by_token(__ballot_sync(kAll, again && live));
             for (uint32_t left = redo; left; left &= left - 1) {
                 const int first = __ffs(left) - 1, q = first >> 2;
                 const T *other = logits + (t0 + q) * a.row_stride;
                 const RowSoftmax soft = {__shfl_sync(kAll, top, first), __shfl_sync(kAll, inverse, first)};
+                const uint32_t kept = __shfl_sync(kAll, keep, first);
                 bool lost;
-                int chosen = choose_from(other, a, __shfl_sync(kAll, keep, first),
-                                         __shfl_sync(kAll, least, first + (a.k - 1) / 2), soft, place[warp], lost);
-                if (lost) chosen = choose_again<T>(other, a, place[warp]);
+                int chosen = choose_from(other, a, kept, __shfl_sync(kAll, least, first), soft, place[warp], lost);
+                if (lost) { // heavy ties: are they only that?
+                    const float u = __shfl_sync(kAll, kth, first), x = __shfl_sync(kAll, kx, first);
+                    const int e = __shfl_sync(kAll, ke, first);
+                    if (!left_out_matters(other, a, kept, __shfl_sync(kAll, best[7], first), u, x, e, soft) &&
+                        !((order >> first) & 1u)) {
+                        redo &= ~(1u << first);
+                        continue;
+                    }
+                    chosen = choose_slowly(other, a);
+                }
                 if (lane < kQuadK) redone[warp][q][lane] = chosen;
                 __syncwarp();
             }
