@@ -117,6 +117,25 @@ def test_sizes(rows, dim, vocab):
     run(*_inputs(rows, dim, vocab, seed=rows + dim + vocab, wide=rows % 2 == 0))
 
 
+def test_rows_beyond_one_block():
+    """More rows than the loss takes at a time, a ragged last block; the workspace it asks for is enough and one byte
+    less than it needs is refused."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    rows = 16384 + 77
+    hidden, weight, target = _inputs(rows, 64, 300, seed=4, ignored=0.1)
+    loss, lse, dh, dw = run(hidden, weight, target)
+    again = topk.head_loss_bf16(hidden[16384:], weight, target[16384:])
+    assert torch.equal(loss[16384:], again[0]) and torch.equal(lse[16384:], again[1])
+    small = torch.empty(1024, dtype=torch.uint8, device="cuda")
+    for call in (lambda: topk.head_loss_bf16(hidden, weight, target, workspace=small),
+                 lambda: topk.head_loss_grad_bf16(hidden, weight, target, lse, loss, workspace=small)):
+        with pytest.raises(topk.TopkError) as e:
+            call()
+        assert e.value.status == topk.ERR_SCRATCH
+
+
 @pytest.mark.parametrize("rows,ignored", [(40, 0.5), (300, 0.3), (600, 0.9), (1000, 0.999)])
 def test_ignored_rows(rows, ignored):
     run(*_inputs(rows, 136, 1111, seed=rows, ignored=ignored))

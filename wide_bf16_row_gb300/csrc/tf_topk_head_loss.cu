@@ -1228,6 +1228,10 @@ int tile_width(int64_t rows, int64_t vocab, int pairs)
     return best;
 }
 
+// Rows the loss takes at a time: its workspace grows with them (16 bytes per
+// row and tile), and so many fill the device hundreds of times over.
+constexpr int64_t kLossRows = 16384;
+
 struct LossSpace {
     RowHeader *header;
     int32_t *order, *place;
@@ -1255,6 +1259,19 @@ LossSpace loss_space(const void *p, int64_t rows, int64_t dim, int64_t parts)
     return s;
 }
 
+// Bytes of a workspace at `p` that serves every block of rows.
+size_t loss_bytes(const void *p, int64_t rows, int64_t dim, int64_t vocab, int pairs)
+{
+    size_t most = 0;
+    for (const int64_t n : {rows < kLossRows ? rows : kLossRows, rows % kLossRows}) {
+        if (n == 0) continue;
+        const int width = tile_width(n, vocab, pairs);
+        const size_t bytes = loss_space(p, n, dim, 2 * ((vocab + width - 1) / width)).bytes;
+        most = bytes > most ? bytes : most;
+    }
+    return most;
+}
+
 struct GradSpace {
     RowHeader *header;
     int32_t *order, *place;
@@ -1269,12 +1286,14 @@ struct GradSpace {
 
 constexpr int64_t kProbBytes = 256ll << 20; // G of a piece, where the caller has the room
 
-// Shares the workspace holds sums for: few tiles want many.
+// Shares the workspace holds sums for: few tiles want many, and from 16
+// rounds on a share more no longer saves what its sums cost.
 int most_splits(int64_t rows, int64_t dim, int pairs)
 {
     const int64_t tiles = pad_rows_of(rows) / kTileRows * ((dim + kTileCols - 1) / kTileCols);
-    const int64_t s = (2 * (int64_t)pairs + tiles - 1) / tiles;
-    return (int)(s < 4 ? 4 : s > 32 ? 32 : s);
+    const int64_t few = (2 * (int64_t)pairs + tiles - 1) / tiles, many = (16 * (int64_t)pairs + tiles - 1) / tiles;
+    const int64_t s = few > 4 ? few : many < 4 ? many : 4;
+    return (int)(s > 32 ? 32 : s);
 }
 
 GradSpace grad_space(const void *p, int64_t rows, int64_t dim, int64_t vocab, int pairs, bool hidden, int64_t piece)
@@ -1335,26 +1354,14 @@ bool bad_stride(int64_t stride, int64_t dim, int64_t n)
     return stride < dim || stride % 8 != 0 || stride >= (1ll << 39) || (n > 0 && stride > INT64_MAX / 4 / n);
 }
 
-int run_loss(const void *hidden, int64_t hidden_stride, const void *weight, int64_t weight_stride, int64_t rows,
-             int32_t dim, int64_t vocab, const void *target, int32_t target_bytes, int64_t ignore, void *workspace,
-             size_t workspace_bytes, float *loss, float *lse, void *stream)
+// One block of rows of the loss (checked arguments).
+int loss_of_rows(const void *hidden, int64_t hidden_stride, const void *weight, int64_t weight_stride, int64_t rows,
+                 int32_t dim, int64_t vocab, const void *target, int32_t target_bytes, int64_t ignore, void *workspace,
+                 float *loss, float *lse, int pairs, int sms, cudaStream_t strm)
 {
-    if (bad_shape(rows, dim, vocab) || bad_stride(hidden_stride, dim, rows) || bad_stride(weight_stride, dim, vocab))
-        return TF_TOPK_ERR_SHAPE;
-    if (rows == 0) return TF_TOPK_OK;
-    if (target_bytes != 4 && target_bytes != 8) return TF_TOPK_ERR_ARG;
-    if (!hidden || !weight || !target || !workspace || !loss || !lse) return TF_TOPK_ERR_NULL;
-    if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(target, (size_t)target_bytes) || !aligned(loss, 4) ||
-        !aligned(lse, 4))
-        return TF_TOPK_ERR_ALIGN;
-    int pairs = 0, sms = 0;
-    const int st = loss_setup(&pairs, &sms);
-    if (st != TF_TOPK_OK) return st;
     const int width = tile_width(rows, vocab, pairs);
     const int64_t tiles = (vocab + width - 1) / width;
     const LossSpace s = loss_space(workspace, rows, dim, 2 * tiles);
-    if (s.bytes > workspace_bytes) return TF_TOPK_ERR_SCRATCH;
-    const cudaStream_t strm = static_cast<cudaStream_t>(stream);
     PairMaps m = {};
     const bool packed = s.packed != nullptr;
     const int box = rows <= kHalf ? (int)((rows + 7) / 8 * 8) : kHalf; // rows of A a CTA loads (set_ring)
@@ -1401,6 +1408,33 @@ int run_loss(const void *hidden, int64_t hidden_stride, const void *weight, int6
                                (int)(target_bytes == 8), ignore, (int)rows, loss, lse);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? TF_TOPK_OK : tf_topk_internal_fail_cuda((int)e);
+}
+
+int run_loss(const void *hidden, int64_t hidden_stride, const void *weight, int64_t weight_stride, int64_t rows,
+             int32_t dim, int64_t vocab, const void *target, int32_t target_bytes, int64_t ignore, void *workspace,
+             size_t workspace_bytes, float *loss, float *lse, void *stream)
+{
+    if (bad_shape(rows, dim, vocab) || bad_stride(hidden_stride, dim, rows) || bad_stride(weight_stride, dim, vocab))
+        return TF_TOPK_ERR_SHAPE;
+    if (rows == 0) return TF_TOPK_OK;
+    if (target_bytes != 4 && target_bytes != 8) return TF_TOPK_ERR_ARG;
+    if (!hidden || !weight || !target || !workspace || !loss || !lse) return TF_TOPK_ERR_NULL;
+    if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(target, (size_t)target_bytes) || !aligned(loss, 4) ||
+        !aligned(lse, 4))
+        return TF_TOPK_ERR_ALIGN;
+    int pairs = 0, sms = 0;
+    const int st = loss_setup(&pairs, &sms);
+    if (st != TF_TOPK_OK) return st;
+    if (loss_bytes(workspace, rows, dim, vocab, pairs) > workspace_bytes) return TF_TOPK_ERR_SCRATCH;
+    for (int64_t r = 0; r < rows; r += kLossRows) {
+        const int64_t n = rows - r < kLossRows ? rows - r : kLossRows;
+        const int s = loss_of_rows(static_cast<const char *>(hidden) + (size_t)r * hidden_stride * 2, hidden_stride, weight,
+                                   weight_stride, n, dim, vocab,
+                                   static_cast<const char *>(target) + (size_t)r * target_bytes, target_bytes, ignore,
+                                   workspace, loss + r, lse + r, pairs, sms, static_cast<cudaStream_t>(stream));
+        if (s != TF_TOPK_OK) return s;
+    }
+    return TF_TOPK_OK;
 }
 
 int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int64_t weight_stride, int64_t rows,
@@ -1529,8 +1563,7 @@ size_t tf_topk_head_loss_bf16_workspace(int64_t rows, int32_t dim, int64_t vocab
 {
     int pairs = 0, sms = 0;
     if (rows < 1 || bad_shape(rows, dim, vocab) || loss_setup(&pairs, &sms) != TF_TOPK_OK) return 0;
-    const int width = tile_width(rows, vocab, pairs);
-    return loss_space(nullptr, rows, dim, 2 * ((vocab + width - 1) / width)).bytes + 256;
+    return loss_bytes(nullptr, rows, dim, vocab, pairs) + 256;
 }
 
 int tf_topk_head_loss_grad_bf16(const void *hidden, int64_t hidden_stride, const void *weight, int64_t weight_stride,
