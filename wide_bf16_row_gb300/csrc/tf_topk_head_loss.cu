@@ -554,54 +554,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
     if (warp == 0) {
         // ---- TMA producer
-        {
-            // both CTAs' bytes; of few rows only the leading CTA has any
-            const uint32_t bytes = (kFew ? share_a : 2 * share_a) + 2 * (uint32_t)half_cols * kStepK * 2;
-            const bool has_a = !kFew || rank == 0;
-            const uint32_t full0 = peer_addr(&sm.full[0], 0); // the leading CTA's barriers
-            uint32_t s = 0, turn = 0;                         // ring stage, times round the ring
-            bool ok = true;
-            for (int64_t u = pair; u < units && ok; u += pairs) {
-                const Unit t = shape.at(u);
-                const bool weight = shape.of_weight(u);
-                const int row = t.m * kTileRows + (int)rank * kHalf;
-                const int col = t.n * kTileCols + (int)rank * kHalf;
-                const int voc = a.begin + t.n * a.width + (int)rank * half_cols;
-                for (int k = t.k0; k < t.k1; ++k) {
-                    ok = *abort == 0 && (turn == 0 || mbar_wait(&sm.empty[s], (turn - 1) & 1, abort));
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok) break;
-                    if (elect_one()) {
-                        if (rank == 0) mbar_expect_tx(&sm.full[s], bytes);
-                        const uint32_t bar = full0 + s * (uint32_t)sizeof(uint64_t);
-                        uint8_t *da = ring_a + s * share_a, *db = ring_b + s * share_b;
-                        const int kx = k * kStepK;
-                        if (kMode == kLse || kMode == kProb) {
-                            if (has_a) tma_load(da, &map_a, kx, row, bar);
-                            tma_load(db, &map_b, kx, voc, bar);
-                        } else if (!weight) {
-                            if (has_a) tma_load(da, &map_a, kx, row, bar);
-                            tma_load(db, &map_b, col, a.begin + kx, bar);
-                            tma_load(db + kShare / 2, &map_b, col + 64, a.begin + kx, bar);
-                        } else {
-                            tma_load(da, &map_wa, row, kx, bar);
-                            tma_load(da + kShare / 2, &map_wa, row + 64, kx, bar);
-                            tma_load(db, &map_wb, col, kx, bar);
-                            tma_load(db + kShare / 2, &map_wb, col + 64, kx, bar);
-                        }
+        // both CTAs' bytes; of few rows only the leading CTA has any
+        const uint32_t bytes = (kFew ? share_a : 2 * share_a) + 2 * (uint32_t)half_cols * kStepK * 2;
+        const bool has_a = !kFew || rank == 0;
+        const uint32_t full0 = peer_addr(&sm.full[0], 0); // the leading CTA's barriers
+        uint32_t s = 0, turn = 0;                         // ring stage, times round the ring
+        bool ok = true;
+        for (int64_t u = pair; u < units && ok; u += pairs) {
+            const Unit t = shape.at(u);
+            const bool weight = shape.of_weight(u);
+            const int row = t.m * kTileRows + (int)rank * kHalf;
+            const int col = t.n * kTileCols + (int)rank * kHalf;
+            const int voc = a.begin + t.n * a.width + (int)rank * half_cols;
+            for (int k = t.k0; k < t.k1; ++k) {
+                ok = *abort == 0 && (turn == 0 || mbar_wait(&sm.empty[s], (turn - 1) & 1, abort));
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                if (elect_one()) {
+                    if (rank == 0) mbar_expect_tx(&sm.full[s], bytes);
+                    const uint32_t bar = full0 + s * (uint32_t)sizeof(uint64_t);
+                    uint8_t *da = ring_a + s * share_a, *db = ring_b + s * share_b;
+                    const int kx = k * kStepK;
+                    if (kMode == kLse || kMode == kProb) {
+                        if (has_a) tma_load(da, &map_a, kx, row, bar);
+                        tma_load(db, &map_b, kx, voc, bar);
+                    } else if (!weight) {
+                        if (has_a) tma_load(da, &map_a, kx, row, bar);
+                        tma_load(db, &map_b, col, a.begin + kx, bar);
+                        tma_load(db + kShare / 2, &map_b, col + 64, a.begin + kx, bar);
+                    } else {
+                        tma_load(da, &map_wa, row, kx, bar);
+                        tma_load(da + kShare / 2, &map_wa, row + 64, kx, bar);
+                        tma_load(db, &map_wb, col, kx, bar);
+                        tma_load(db + kShare / 2, &map_wb, col + 64, kx, bar);
                     }
-                    __syncwarp();
-                    if (++s == stages) s = 0, ++turn;
                 }
+                __syncwarp();
+                if (++s == stages) s = 0, ++turn;
             }
-            // both CTAs' copies land before the pair leaves: the last fill of
-            // each stage (the leader's barrier counts both CTAs' bytes)
-            if (rank == 0)
-                for (uint32_t j = 0; j < stages; ++j) {
-                    const uint32_t filled = j < s ? turn + 1 : turn; // times stage j was filled
-                    if (filled) mbar_drain(&sm.full[j], (filled - 1) & 1);
-                }
         }
+        // both CTAs' copies land before the pair leaves: the last fill of
+        // each stage (the leader's barrier counts both CTAs' bytes)
+        if (rank == 0)
+            for (uint32_t j = 0; j < stages; ++j) {
+                const uint32_t filled = j < s ? turn + 1 : turn; // times stage j was filled
+                if (filled) mbar_drain(&sm.full[j], (filled - 1) & 1);
+            }
     } else if (warp == 1) {
         // ---- MMA issuer (the leading CTA's)
         if (rank == 0) {
@@ -832,16 +830,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // ---------------------------------------------------------------- rows before and after
 
 constexpr int kPrepareThreads = 1024;
+constexpr int kPackRows = 4096; // rows whose order a CTA can hold
 
-// One CTA: the rows that count, in their order (order[j] the row at place j and
-// its facts, place[r] the row's place or -1), and the largest finite |g|, by which every g is
-// divided before G is rounded to bf16: with one g for all rows (a mean) the
-// target's entry of G is then exactly p - 1, and no g leaves bf16's range.
+// A packed row: a copy of a hidden row, or zeros.
+__device__ __forceinline__ void pack_row(__nv_bfloat16 *to, const __nv_bfloat16 *from, int dim, int thread, int threads)
+{
+    uint4 *dst = reinterpret_cast<uint4 *>(to);
+    const uint4 *src = reinterpret_cast<const uint4 *>(from);
+    for (int i = thread; i < dim / 8; i += threads) dst[i] = src ? src[i] : make_uint4(0, 0, 0, 0);
+}
+
+// The rows that count, in their order (order[j] the row at place j and its
+// facts, place[r] the row's place or -1), and the largest finite |g|, by
+// which every g is divided before G is rounded to bf16: with one g for all
+// rows (a mean) the target's entry of G is then exactly p - 1, and no g leaves
+// bf16's range.  kCopy, up to kPackRows rows: every CTA finds the order for
+// itself and copies its share of the rows, a launch less (2 us of 96 at
+// 333x1032x32771; with more rows the scans would outweigh it and
+// head_loss_gather_kernel copies); the first CTA writes the rest.
+template <bool kCopy>
 __global__ void __launch_bounds__(kPrepareThreads)
     head_loss_prepare_kernel(const void *target, int target64, int64_t ignore, const float *lse, const float *grad,
                              int rows, int vocab, int dim, int pairs, int most_splits, RowHeader *header,
-                             int32_t *order, int32_t *place, RowFacts *facts)
+                             int32_t *order, int32_t *place, RowFacts *facts, const __nv_bfloat16 *hidden,
+                             int64_t stride, int pitch, __nv_bfloat16 *packed)
 {
+    __shared__ int32_t own_order[kCopy ? kPackRows : 1];
     __shared__ int warp_sum[32];
     __shared__ float warp_max[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -874,10 +888,11 @@ __global__ void __launch_bounds__(kPrepareThreads)
             total += n;
         }
         const int at = before + __popc(mask & ((1u << lane) - 1u));
-        if (r < rows) {
+        if (kCopy && counts) own_order[at] = r;
+        if (r < rows && blockIdx.x == 0) {
             place[r] = counts ? at : -1;
             if (counts) {
-                order[at] = r;
+                if (!kCopy) order[at] = r;
                 facts[at] = fact;
             }
         }
@@ -888,7 +903,7 @@ __global__ void __launch_bounds__(kPrepareThreads)
     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
     if (lane == 0) warp_max[warp] = top;
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 0 && blockIdx.x == 0) {
         top = warp_max[lane];
 #pragma unroll
         for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
@@ -898,6 +913,12 @@ __global__ void __launch_bounds__(kPrepareThreads)
             header->grad_scale = top > 0.0f ? top : 1.0f;
             header->splits = splits;
         }
+    }
+    if (kCopy) { // 256 threads a row
+        const int end = max(1, ceil_div(base, kTileRows)) * kTileRows, at_once = kPrepareThreads / 256;
+        for (int j = blockIdx.x * at_once + tid / 256; j < end; j += gridDim.x * at_once)
+            pack_row(packed + (size_t)j * pitch, j < base ? hidden + (size_t)own_order[j] * stride : nullptr, dim, tid & 255,
+                     256);
     }
     grid_dependents_go();
 }
@@ -911,16 +932,9 @@ __global__ void __launch_bounds__(256)
     grid_dependency_wait();
     const int count = header->count;
     const int end = max(1, ceil_div(count, kTileRows)) * kTileRows;
-    const int vecs = dim / 8;
-    for (int j = blockIdx.x; j < end; j += gridDim.x) {
-        uint4 *dst = reinterpret_cast<uint4 *>(packed + (size_t)j * pitch);
-        if (j < count) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(hidden + (size_t)order[j] * stride);
-            for (int i = threadIdx.x; i < vecs; i += blockDim.x) dst[i] = src[i];
-        } else {
-            for (int i = threadIdx.x; i < vecs; i += blockDim.x) dst[i] = make_uint4(0, 0, 0, 0);
-        }
-    }
+    for (int j = blockIdx.x; j < end; j += gridDim.x)
+        pack_row(packed + (size_t)j * pitch, j < count ? hidden + (size_t)order[j] * stride : nullptr, dim, threadIdx.x,
+                 blockDim.x);
     grid_dependents_go();
 }
 
@@ -939,8 +953,9 @@ __device__ __forceinline__ float2 join(float2 p, float2 q)
 // products still run), the partial sums of a row joined, and both into loss
 // and lse.
 __global__ void __launch_bounds__(kRowsThreads)
-    head_loss_rows_kernel(const float2 *__restrict__ partial, int parts, int pad_rows, const int32_t *place, const __nv_bfloat16 *__restrict__ hidden,
-                          int64_t hidden_stride, const __nv_bfloat16 *__restrict__ weight, int64_t weight_stride,
+    head_loss_rows_kernel(const float2 *__restrict__ partial, int parts, int pad_rows, const int32_t *place,
+                          const __nv_bfloat16 *__restrict__ hidden, int64_t hidden_stride,
+                          const __nv_bfloat16 *__restrict__ weight, int64_t weight_stride,
                           int dim, int vocab, const void *target, int target64, int64_t ignore, int rows, float *loss,
                           float *lse)
 {
@@ -1354,6 +1369,32 @@ bool bad_stride(int64_t stride, int64_t dim, int64_t n)
     return stride < dim || stride % 8 != 0 || stride >= (1ll << 39) || (n > 0 && stride > INT64_MAX / 4 / n);
 }
 
+// Finds and packs the rows that count (`lse`, `grad` null for the loss alone).
+template <typename Space>
+cudaError_t pack_rows(const Space &s, const void *hidden, int64_t stride, int64_t rows, int32_t dim, int64_t vocab,
+                      const void *target, int32_t target_bytes, int64_t ignore, const float *lse, const float *grad,
+                      int pairs, int splits, int sms, cudaStream_t stream)
+{
+    const auto *from = static_cast<const __nv_bfloat16 *>(hidden);
+    const int pitch = (int)packed_pitch(dim), wide = target_bytes == 8;
+    cudaLaunchAttribute attr[1];
+    if (rows <= kPackRows) {
+        const int64_t ctas = (pad_rows_of(rows) + 3) / 4;
+        const cudaLaunchConfig_t cfg = config((int)(ctas < sms ? ctas : sms), kPrepareThreads, 0, stream, attr);
+        return cudaLaunchKernelEx(&cfg, head_loss_prepare_kernel<true>, target, wide, ignore, lse, grad, (int)rows,
+                                  (int)vocab, (int)dim, pairs, splits, s.header, s.order, s.place, s.facts, from, stride,
+                                  pitch, s.packed);
+    }
+    cudaLaunchConfig_t cfg = config(1, kPrepareThreads, 0, stream, attr);
+    const cudaError_t e =
+        cudaLaunchKernelEx(&cfg, head_loss_prepare_kernel<false>, target, wide, ignore, lse, grad, (int)rows, (int)vocab,
+                           (int)dim, pairs, splits, s.header, s.order, s.place, s.facts, from, stride, pitch, s.packed);
+    if (e != cudaSuccess) return e;
+    cfg = config((int)(rows < 4 * sms ? rows : 4 * sms), 256, 0, stream, attr);
+    return cudaLaunchKernelEx(&cfg, head_loss_gather_kernel, from, stride, (int)dim, (const RowHeader *)s.header,
+                              (const int32_t *)s.order, pitch, s.packed);
+}
+
 // One block of rows of the loss (checked arguments).
 int loss_of_rows(const void *hidden, int64_t hidden_stride, const void *weight, int64_t weight_stride, int64_t rows,
                  int32_t dim, int64_t vocab, const void *target, int32_t target_bytes, int64_t ignore, void *workspace,
@@ -1371,17 +1412,9 @@ int loss_of_rows(const void *hidden, int64_t hidden_stride, const void *weight, 
         return tf_topk_internal_fail_cuda((int)cudaErrorInvalidValue);
     cudaLaunchAttribute attr[1];
     cudaError_t e = cudaSuccess;
-    if (packed) {
-        cudaLaunchConfig_t cfg = config(1, kPrepareThreads, 0, strm, attr);
-        e = cudaLaunchKernelEx(&cfg, head_loss_prepare_kernel, target, (int)(target_bytes == 8), ignore,
-                               (const float *)nullptr, (const float *)nullptr, (int)rows, (int)vocab, (int)dim, pairs, 1,
-                               s.header, s.order, s.place, s.facts);
-        cfg = config((int)(rows < 4 * sms ? rows : 4 * sms), 256, 0, strm, attr);
-        if (e == cudaSuccess)
-            e = cudaLaunchKernelEx(&cfg, head_loss_gather_kernel, static_cast<const __nv_bfloat16 *>(hidden),
-                                   hidden_stride, (int)dim, (const RowHeader *)s.header, (const int32_t *)s.order,
-                                   (int)packed_pitch(dim), s.packed);
-    }
+    if (packed)
+        e = pack_rows(s, hidden, hidden_stride, rows, dim, vocab, target, target_bytes, ignore, nullptr, nullptr, pairs, 1,
+                      sms, strm);
     PairArgs a = {};
     a.header = s.header;
     a.facts = s.facts;
@@ -1488,15 +1521,8 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
     const int64_t steps = ((vocab < piece ? vocab : piece) + kStepK - 1) / kStepK;
     const int splits = (int)(s.splits < steps ? s.splits : steps);
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = config(1, kPrepareThreads, 0, strm, attr);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, head_loss_prepare_kernel, target, (int)(target_bytes == 8), ignore,
-                                       lse, grad_loss, (int)rows, (int)vocab, (int)dim, pairs, splits, s.header,
-                                       s.order, s.place, s.facts);
-    cfg = config((int)(pad < 4 * sms ? pad : 4 * sms), 256, 0, strm, attr);
-    if (e == cudaSuccess)
-        e = cudaLaunchKernelEx(&cfg, head_loss_gather_kernel, static_cast<const __nv_bfloat16 *>(hidden), hidden_stride,
-                               (int)dim, (const RowHeader *)s.header, (const int32_t *)s.order, (int)packed_pitch(dim),
-                               s.packed);
+    cudaError_t e = pack_rows(s, hidden, hidden_stride, rows, dim, vocab, target, target_bytes, ignore, lse, grad_loss,
+                              pairs, splits, sms, strm);
     PairArgs a = {};
     a.header = s.header;
     a.facts = s.facts;
@@ -1525,7 +1551,7 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
             e = launch_product<kWeight>(grads, a, weight_units, pairs, strm);
     }
     if (e == cudaSuccess && d_hidden) {
-        cfg = config((int)(rows < 8 * sms ? rows : 8 * sms), 256, 0, strm, attr);
+        const cudaLaunchConfig_t cfg = config((int)(rows < 8 * sms ? rows : 8 * sms), 256, 0, strm, attr);
         e = cudaLaunchKernelEx(&cfg, head_loss_hidden_kernel, (const float *)s.sums, a.pad_rows, (int)dim,
                                (const RowHeader *)s.header, (const int32_t *)s.place, (int)rows,
                                static_cast<__nv_bfloat16 *>(d_hidden));
