@@ -339,3 +339,42 @@ def test_no_rows():
     assert loss.shape == lse.shape == (0,)
     dh, dw = topk.head_loss_grad_bf16(hidden, weight, target, lse, loss)
     assert dh.shape == (0, 64) and not torch.any(dw != 0)
+
+
+@pytest.mark.parametrize("rows", [4096, 4097])
+def test_many_rows_packed(rows):
+    """Up to 4096 rows are found and packed in one launch, more in two."""
+    run(*_inputs(rows, 72, 300, seed=rows, ignored=0.3, hidden_pad=8))
+
+
+def _inside(shape, dtype, before=8, after=512):
+    """A tensor in the middle of bytes of 0xA5, and a check that those still stand."""
+    import torch
+    size = int(np.prod(shape)) * dtype.itemsize
+    block = torch.full((before * 16 + size + after,), 0xA5, dtype=torch.uint8, device="cuda")
+    part = block[before * 16:before * 16 + size].view(dtype).view(shape)
+    return part, lambda: bool((block[:before * 16] == 0xA5).all()) and bool((block[before * 16 + size:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("rows,dim,vocab", [(1, 8, 1), (5, 72, 130), (130, 64, 257), (300, 136, 515), (4097, 72, 300)])
+@pytest.mark.parametrize("least", [False, True])
+def test_nothing_beside_the_outputs_is_written(rows, dim, vocab, least):
+    """Outputs and workspaces of exactly their sizes inside larger buffers; bf16 bits as int16; int32 targets."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    hidden, weight, target = _inputs(rows, dim, vocab, seed=11, ignored=0.2, wide=False)
+    bits = hidden.contiguous().view(torch.int16), weight.contiguous().view(torch.int16)
+    g = torch.rand(rows, device="cuda")
+    loss, lse = topk.head_loss_bf16(hidden, weight, target)
+    need = topk.tf_topk_head_loss_bf16_workspace(rows, dim, vocab)
+    grad_need = topk.tf_topk_head_loss_grad_bf16_workspace(rows, dim, vocab, least)
+    parts = [_inside((rows,), torch.float32), _inside((rows,), torch.float32), _inside((need,), torch.uint8, 1),
+             _inside((rows, dim), torch.bfloat16), _inside((vocab, dim), torch.bfloat16), _inside((grad_need,), torch.uint8, 1)]
+    outs = [p for p, _ in parts]
+    topk.head_loss_bf16(*bits, target, out=outs[:2], workspace=outs[2])
+    topk.head_loss_grad_bf16(*bits, target, outs[1], g, out=outs[3:5], workspace=outs[5])
+    assert all(ok() for _, ok in parts)
+    assert torch.equal(outs[0], loss) and torch.equal(outs[1], lse)
+    check_grad(hidden, weight, target, g, *outs[3:5])
+    assert topk.device_fault() == 0

@@ -290,3 +290,30 @@ def test_no_tokens():
     idx, weight = topk.route_experts(x, 2)
     assert idx.shape == (0, 2) and weight.shape == (0, 2)
     assert topk.route_experts_grad(x, idx, weight).shape == (0, 16)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens,experts,k,renorm", [(1, 7, 3, True), (33, 60, 4, False), (1301, 256, 8, True), (1301, 64, 6, False)])
+def test_nothing_beside_the_outputs_is_written(dtype, tokens, experts, k, renorm):
+    """Outputs of exactly their sizes inside larger buffers."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    x = _logits(tokens, experts, dtype, 3)
+    g = torch.randn(tokens, k, device="cuda")
+
+    def inside(shape, kind):
+        size = int(np.prod(shape)) * kind.itemsize
+        block = torch.full((256 + size + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+        return block, block[256:256 + size].view(kind).view(shape)
+    blocks, parts = zip(inside((tokens, k), torch.int32), inside((tokens, k), torch.float32),
+                        inside((experts,), torch.int32), inside((tokens, experts), x.dtype))
+    parts[2].zero_()
+    topk.route_experts(x, k, renormalize=renorm, load=parts[2], out=parts[:2])
+    topk.route_experts_grad(x, parts[0], g, renormalize=renorm, out=parts[3])
+    for block in blocks:
+        assert bool((block[:256] == 0xA5).all()) and bool((block[-256:] == 0xA5).all())
+    idx, weight = topk.route_experts(x, k, renormalize=renorm)
+    assert torch.equal(parts[0], idx) and torch.equal(parts[1], weight)
+    assert torch.equal(parts[2], torch.bincount(idx.view(-1).long(), minlength=experts).int())
+    assert torch.equal(parts[3], topk.route_experts_grad(x, idx, g, renormalize=renorm))
