@@ -106,48 +106,6 @@ __device__ __forceinline__ float warp_max(float v)
     return key_value(__reduce_max_sync(kAll, order_key(v)));
 }
 
-// Takes the largest remaining key of the warp out of `key`: its value and
-// its expert (the lowest on ties); 0 and -1 when none is left.
-template <int P>
-__device__ __forceinline__ uint32_t take_best(uint32_t (&key)[P], int lane, int &expert)
-{
-    uint32_t mine = 0;
-#pragma unroll
-    for (int j = 0; j < P; ++j) mine = max(mine, key[j]);
-    const uint32_t best = __reduce_max_sync(kAll, mine);
-    if (best == 0) {
-        expert = -1;
-        return 0;
-    }
-    const int owner = __ffs(__ballot_sync(kAll, mine == best)) - 1;
-    int at = 0;
-#pragma unroll
-    for (int j = P - 1; j >= 0; --j) at = key[j] == best ? j : at;
-#pragma unroll
-    for (int j = 0; j < P; ++j)
-        if (lane == owner && j == at) key[j] = 0;
-    expert = __shfl_sync(kAll, lane * P + at, owner);
-    return best;
-}
-
-// The groups kept, as a mask, from the groups' values: lane g < groups holds
-// group g's key.  `last`: the last key kept, `cut`: the first left out (0 when
-// none is left out).
-__device__ __forceinline__ uint32_t best_groups(uint32_t mine, int groups, int kept, int lane, uint32_t &last, uint32_t &cut)
-{
-    uint32_t rank = 0;
-    for (int g = 0; g < groups; ++g) {
-        const uint32_t other = __shfl_sync(kAll, mine, g);
-        rank += other > mine || (other == mine && g < lane);
-    }
-    const bool keep = lane < groups && rank < (uint32_t)kept;
-    const uint32_t on_edge = __ballot_sync(kAll, lane < groups && rank == (uint32_t)kept - 1);
-    const uint32_t past = __ballot_sync(kAll, lane < groups && rank == (uint32_t)kept);
-    last = on_edge ? __shfl_sync(kAll, mine, __ffs(on_edge) - 1) : 0u;
-    cut = past ? __shfl_sync(kAll, mine, __ffs(past) - 1) : 0u;
-    return __ballot_sync(kAll, keep);
-}
-
 // Sum and maximum over the W lanes (a power of two) that hold one token.
 template <int W> __device__ __forceinline__ float lanes_sum(float v)
 {
@@ -575,13 +533,15 @@ __device__ __noinline__ int settle(const T *row, const RouteArgs &a, int expert,
 // choices in order.
 template <typename T, int P>
 __device__ __forceinline__ int choose_row(const T *row, const RouteArgs &a, float (&c)[P], const float (&bias)[P],
-                                          int32_t *place, RowSoftmax &soft)
+                                          int32_t *place, float *swap, RowSoftmax &soft)
 {
     using Key = ShortKey<P>;
     const int lane = threadIdx.x & 31;
     const int per = a.experts / a.groups;
-    // lanes that hold one group, when whole lanes do and their count is a power of two
-    const int group_lanes = per % P == 0 && ((per / P) & (per / P - 1)) == 0 ? per / P : 0;
+    // Lanes that value one group, a power of two: those that hold it, when whole
+    // lanes do; else its members go through `swap` (33 * P floats).
+    const bool own_lanes = per % P == 0 && ((per / P) & (per / P - 1)) == 0;
+    const int group_lanes = own_lanes ? per / P : 1 << (31 - __clz(32 / a.groups));
     const bool scored = a.bias || a.groups > 1; // else the logits alone decide
     // errors of a choice: of the score, and relative to the sum with the bias
     const float error = !scored ? 0.0f : a.softmax ? kSoftmaxError : kSigmoidError;
@@ -610,36 +570,26 @@ __device__ __forceinline__ int choose_row(const T *row, const RouteArgs &a, floa
 #pragma unroll
     for (int j = 0; j < P; ++j) key[j] = c[j] > -INFINITY ? Key::make(c[j], lane * P + j) : 0u;
     bool again = false; // too close to call in 32 bits
-    if (a.groups > 1 && !group_lanes) {
-        uint32_t mine = 0;
-        float most = 0.0f;
-        for (int g = 0; g < a.groups; ++g) {
-            uint32_t members[P];
+    if (a.groups > 1) {
+        float m1 = -INFINITY, m2 = -INFINITY; // whole values: a cut between groups must not hang on short keys
+        if (own_lanes) {
 #pragma unroll
-            for (int j = 0; j < P; ++j) members[j] = (lane * P + j) / per == g ? key[j] : 0u;
-            int e;
-            const uint32_t first = take_best<P>(members, lane, e);
-            const uint32_t second = a.best > 1 && first ? take_best<P>(members, lane, e) : 0u;
-            const float u = first ? Key::value(first) : 0.0f, w = second ? Key::value(second) : 0.0f;
-            if (lane == g) mine = first ? order_key(u + w) : 0u;
-            most = fmaxf(most, fabsf(u) + fabsf(w));
-        }
-        uint32_t last, cut;
-        const uint32_t keep = best_groups(mine, a.groups, a.kept, lane, last, cut);
-        if (cut) again = !(key_value(last) - key_value(cut) > 4.0f * error + 4.0f * part * most);
+            for (int j = 0; j < P; ++j) {
+                m2 = fmaxf(m2, fminf(m1, c[j]));
+                m1 = fmaxf(m1, c[j]);
+            }
+        } else { // the groups' members change hands
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            const int e = lane * P + j;
-            if (e < a.experts && !((keep >> (e / per)) & 1u)) key[j] = 0;
-        }
-    }
-    LaneList<P> list(key);
-    if (a.groups > 1 && group_lanes) {
-        float m1 = c[0], m2 = -INFINITY; // whole values: a cut between groups must not hang on short keys
-#pragma unroll
-        for (int j = 1; j < P; ++j) {
-            m2 = fmaxf(m2, fminf(m1, c[j]));
-            m1 = fmaxf(m1, c[j]);
+            for (int j = 0; j < P; ++j) swap[lane * P + j + lane * P / 32] = c[j];
+            __syncwarp();
+            const int g = lane / group_lanes;
+            if (g < a.groups)
+                for (int e = g * per + lane % group_lanes; e < (g + 1) * per; e += group_lanes) {
+                    const float v = swap[e + e / 32];
+                    m2 = fmaxf(m2, fminf(m1, v));
+                    m1 = fmaxf(m1, v);
+                }
+            __syncwarp();
         }
         for (int d = 1; d < group_lanes; d <<= 1)
             join_best_two(m1, m2, __shfl_xor_sync(kAll, m1, d), __shfl_xor_sync(kAll, m2, d));
@@ -658,11 +608,25 @@ __device__ __forceinline__ int choose_row(const T *row, const RouteArgs &a, floa
             again = !(key_value(last) - key_value(cut) > 4.0f * error + 4.0f * kSumError * most);
         }
         // equal values among the kept ones: more groups than asked for
-        again = again || __popc(__ballot_sync(kAll, keep && any)) > a.kept * group_lanes;
-        if (!keep)
+        const uint32_t kept = __ballot_sync(kAll, keep && any);
+        again = again || __popc(kept) > a.kept * group_lanes;
+        if (own_lanes) {
 #pragma unroll
-            for (int i = 0; i < LaneList<P>::D; ++i) list.at[i] = 0;
+            for (int j = 0; j < P; ++j) key[j] = keep ? key[j] : 0u;
+        } else {
+            int g = lane * P / per, left = (g + 1) * per - lane * P; // experts to the end of the group
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                if (left == 0) {
+                    ++g;
+                    left = per;
+                }
+                --left;
+                if (g >= a.groups || !((kept >> (g * group_lanes)) & 1u)) key[j] = 0;
+            }
+        }
     }
+    LaneList<P> list(key);
     uint32_t mine = 0, prev = 0;
     for (int i = 0; i < a.k; ++i) {
         prev = list.take(key);
@@ -709,6 +673,7 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<P>) route_kernel(con
 {
     __shared__ int32_t count[kMaxExperts];
     __shared__ int32_t place[kRouteWarps][32];
+    __shared__ float swap[kRouteWarps][33 * P];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (a.load) {
         for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) count[e] = 0;
@@ -728,7 +693,7 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<P>) route_kernel(con
         for (int j = 0; j < P; ++j) c[j] = next[j];
         if (t + step < a.tokens) load_row<T, P>(logits + (t + step) * a.row_stride, a.experts, lane, a.vec, next);
         RowSoftmax soft;
-        const int chosen = choose_row<T, P>(row, a, c, bias, place[warp], soft);
+        const int chosen = choose_row<T, P>(row, a, c, bias, place[warp], swap[warp], soft);
         // weights of the chosen
         const bool on = lane < a.k && chosen >= 0;
         const float x = on ? fminf(load_logit(row + chosen), FLT_MAX) : 0.0f;
