@@ -385,6 +385,33 @@ __device__ __noinline__ uint32_t decide_groups(const T *row, const RouteArgs &a,
     return in | __ballot_sync(kAll, open && rank < a.kept);
 }
 
+// As decide_groups, from the values of the groups as the lanes have them:
+// group g's `value`, if there is `any`, in several lanes or none.
+template <typename T>
+__device__ __noinline__ uint32_t settle_groups(const T *row, const RouteArgs &a, bool any, int g, float value, float margin,
+                                               float top, float *place)
+{
+    const int lane = threadIdx.x & 31;
+    place[lane] = -INFINITY;
+    __syncwarp();
+    if (any) place[g] = value;
+    __syncwarp();
+    const float mine = place[lane];
+    int rank = 0;
+#pragma unroll 1
+    for (int o = 0; o < a.groups; ++o) {
+        const float v = place[o];
+        rank += v > mine || (v == mine && o < lane);
+    }
+    const bool in = lane < a.groups;
+    const int last = __ffs(__ballot_sync(kAll, in && rank == a.kept - 1)) - 1;
+    const int cut = __ffs(__ballot_sync(kAll, in && rank == a.kept)) - 1;
+    const uint32_t kept =
+        decide_groups(row, a, place, __shfl_sync(kAll, mine, last), __shfl_sync(kAll, mine, cut), margin, top);
+    __syncwarp();
+    return kept;
+}
+
 // The choice of a row whose order short keys and 32 bits left open, given the
 // groups kept and a bound that no chosen expert's choice lies below: the few
 // experts from there on, in order by the logits, or with a bias in 64 bits.
@@ -601,15 +628,18 @@ __device__ __forceinline__ int choose_row(const T *row, const RouteArgs &a, floa
             if (left == last) left = 0;
         }
         const uint32_t cut = __reduce_max_sync(kAll, left);
-        const bool keep = mine >= last;
-        if (cut) {
-            const float size = any ? fabsf(m1) + (m2 > -INFINITY ? fabsf(m2) : 0.0f) : 0.0f;
-            const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
-            again = !(key_value(last) - key_value(cut) > 4.0f * error + 4.0f * kSumError * most);
+        const float size = any ? fabsf(m1) + (m2 > -INFINITY ? fabsf(m2) : 0.0f) : 0.0f;
+        const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
+        const float margin = 4.0f * error + 4.0f * kSumError * most;
+        bool keep = any && mine >= last;
+        uint32_t kept = __ballot_sync(kAll, keep);
+        // too close to call, or of equal values more kept than asked for
+        if ((cut && !(key_value(last) - key_value(cut) > margin)) || __popc(kept) > a.kept * group_lanes) {
+            const int g = lane / group_lanes;
+            kept = settle_groups(row, a, any, g, group_value(m1, m2, a.best), margin, top, swap);
+            keep = any && ((kept >> g) & 1u);
+            kept = __ballot_sync(kAll, keep);
         }
-        // equal values among the kept ones: more groups than asked for
-        const uint32_t kept = __ballot_sync(kAll, keep && any);
-        again = again || __popc(kept) > a.kept * group_lanes;
         if (own_lanes) {
 #pragma unroll
             for (int j = 0; j < P; ++j) key[j] = keep ? key[j] : 0u;
