@@ -554,21 +554,42 @@ __device__ __noinline__ int settle(const T *row, const RouteArgs &a, int expert,
     return chosen;
 }
 
+// The lanes that value one group, a power of two of them: those that hold it,
+// when whole lanes do (`own`); else its members change hands through shared
+// memory.
+struct GroupLanes {
+    bool own;
+    int per, lanes;             // experts of a group, lanes that value it
+    int group, begin, end;      // the lane's group; the members it looks at, `lanes` apart
+    int first_lane, first_left; // of the lane's first expert's group: its first lane, its experts from there on
+};
+
+template <int P> __device__ __forceinline__ GroupLanes group_lanes(const RouteArgs &a, int lane)
+{
+    GroupLanes of;
+    of.per = a.experts / a.groups;
+    const int whole = of.per / P;
+    of.own = of.per % P == 0 && (whole & (whole - 1)) == 0;
+    of.lanes = of.own ? whole : 1 << (31 - __clz(32 / a.groups));
+    of.group = lane / of.lanes;
+    of.begin = of.group * of.per + lane % of.lanes;
+    of.end = of.group < a.groups ? (of.group + 1) * of.per : 0;
+    const int first = lane * P / of.per;
+    of.first_lane = first * of.lanes; // past the last group too, where no key is
+    of.first_left = (first + 1) * of.per - lane * P;
+    return of;
+}
+
 // The choice of one row by a whole warp, from its logits (load_row) in `c`
 // (overwritten): lane i < k gets the i-th expert or -1.  A lane sorts its best
 // few experts' short keys; k warp maxima over the lanes' best then name the
 // choices in order.
 template <typename T, int P>
 __device__ __forceinline__ int choose_row(const T *row, const RouteArgs &a, float (&c)[P], const float (&bias)[P],
-                                          int32_t *place, float *swap, RowSoftmax &soft)
+                                          const GroupLanes &of, int32_t *place, float *swap, RowSoftmax &soft)
 {
     using Key = ShortKey<P>;
     const int lane = threadIdx.x & 31;
-    const int per = a.experts / a.groups;
-    // Lanes that value one group, a power of two: those that hold it, when whole
-    // lanes do; else its members go through `swap` (33 * P floats).
-    const bool own_lanes = per % P == 0 && ((per / P) & (per / P - 1)) == 0;
-    const int group_lanes = own_lanes ? per / P : 1 << (31 - __clz(32 / a.groups));
     const bool scored = a.bias || a.groups > 1; // else the logits alone decide
     // errors of a choice: of the score, and relative to the sum with the bias
     const float error = !scored ? 0.0f : a.softmax ? kSoftmaxError : kSigmoidError;
@@ -599,7 +620,7 @@ __device__ __forceinline__ int choose_row(const T *row, const RouteArgs &a, floa
     bool again = false; // too close to call in 32 bits
     if (a.groups > 1) {
         float m1 = -INFINITY, m2 = -INFINITY; // whole values: a cut between groups must not hang on short keys
-        if (own_lanes) {
+        if (of.own) {
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 m2 = fmaxf(m2, fminf(m1, c[j]));
@@ -607,20 +628,18 @@ __device__ __forceinline__ int choose_row(const T *row, const RouteArgs &a, floa
             }
         } else { // the groups' members change hands
 #pragma unroll
-            for (int j = 0; j < P; ++j) swap[lane * P + j + lane * P / 32] = c[j];
+            for (int j = 0; j < P; ++j) swap[lane * P + j + (lane * P >> 5)] = c[j];
             __syncwarp();
-            const int g = lane / group_lanes;
-            if (g < a.groups)
-                for (int e = g * per + lane % group_lanes; e < (g + 1) * per; e += group_lanes) {
-                    const float v = swap[e + e / 32];
-                    m2 = fmaxf(m2, fminf(m1, v));
-                    m1 = fmaxf(m1, v);
-                }
+            for (int e = of.begin; e < of.end; e += of.lanes) {
+                const float v = swap[e + (e >> 5)];
+                m2 = fmaxf(m2, fminf(m1, v));
+                m1 = fmaxf(m1, v);
+            }
             __syncwarp();
         }
-        for (int d = 1; d < group_lanes; d <<= 1)
+        for (int d = 1; d < of.lanes; d <<= 1)
             join_best_two(m1, m2, __shfl_xor_sync(kAll, m1, d), __shfl_xor_sync(kAll, m2, d));
-        const bool any = m1 > -INFINITY && lane < a.groups * group_lanes;
+        const bool any = m1 > -INFINITY && of.group < a.groups;
         const uint32_t mine = any ? order_key(group_value(m1, m2, a.best)) : 0u;
         uint32_t left = mine, last = 0;
         for (int g = 0; g < a.kept; ++g) { // equal values go at once; the cut is then not clear
@@ -634,25 +653,24 @@ __device__ __forceinline__ int choose_row(const T *row, const RouteArgs &a, floa
         bool keep = any && mine >= last;
         uint32_t kept = __ballot_sync(kAll, keep);
         // too close to call, or of equal values more kept than asked for
-        if ((cut && !(key_value(last) - key_value(cut) > margin)) || __popc(kept) > a.kept * group_lanes) {
-            const int g = lane / group_lanes;
-            kept = settle_groups(row, a, any, g, group_value(m1, m2, a.best), margin, top, swap);
-            keep = any && ((kept >> g) & 1u);
+        if ((cut && !(key_value(last) - key_value(cut) > margin)) || __popc(kept) > a.kept * of.lanes) {
+            kept = settle_groups(row, a, any, of.group, group_value(m1, m2, a.best), margin, top, swap);
+            keep = any && ((kept >> of.group) & 1u);
             kept = __ballot_sync(kAll, keep);
         }
-        if (own_lanes) {
+        if (of.own) {
 #pragma unroll
             for (int j = 0; j < P; ++j) key[j] = keep ? key[j] : 0u;
         } else {
-            int g = lane * P / per, left = (g + 1) * per - lane * P; // experts to the end of the group
+            int at = of.first_lane, left = of.first_left;
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 if (left == 0) {
-                    ++g;
-                    left = per;
+                    at += of.lanes;
+                    left = of.per;
                 }
                 --left;
-                if (g >= a.groups || !((kept >> (g * group_lanes)) & 1u)) key[j] = 0;
+                if (!((kept >> (at & 31)) & 1u)) key[j] = 0;
             }
         }
     }
@@ -712,6 +730,7 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<P>) route_kernel(con
     grid_dependency_wait();
     float bias[P];
     load_bias<P>(a, lane, bias);
+    const GroupLanes of = group_lanes<P>(a, lane);
     const int64_t step = (int64_t)gridDim.x * kRouteWarps;
     int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
     float next[P];
@@ -723,7 +742,7 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<P>) route_kernel(con
         for (int j = 0; j < P; ++j) c[j] = next[j];
         if (t + step < a.tokens) load_row<T, P>(logits + (t + step) * a.row_stride, a.experts, lane, a.vec, next);
         RowSoftmax soft;
-        const int chosen = choose_row<T, P>(row, a, c, bias, place[warp], swap[warp], soft);
+        const int chosen = choose_row<T, P>(row, a, c, bias, of, place[warp], swap[warp], soft);
         // weights of the chosen
         const bool on = lane < a.k && chosen >= 0;
         const float x = on ? fminf(load_logit(row + chosen), FLT_MAX) : 0.0f;
