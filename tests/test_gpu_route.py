@@ -317,3 +317,36 @@ def test_nothing_beside_the_outputs_is_written(dtype, tokens, experts, k, renorm
     assert torch.equal(parts[0], idx) and torch.equal(parts[1], weight)
     assert torch.equal(parts[2], torch.bincount(idx.view(-1).long(), minlength=experts).int())
     assert torch.equal(parts[3], topk.route_experts_grad(x, idx, g, renormalize=renorm))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,k,with_bias", [(1, 1, True), (3, 8, False), (22, 8, False), (61, 5, True), (101, 8, True),
+                                                 (130, 1, True), (253, 7, False), (255, 8, True)])
+def test_odd_expert_counts_with_four_lanes_each(dtype, score, experts, k, with_bias):
+    """Rows that are no whole vectors; the last element of the last row ends the buffer."""
+    bias = _bias(experts, 3) if with_bias else None
+    check(_logits(1301, experts, dtype, seed=experts, masked=0.1), k, bias, score, renorm=k != 8 or with_bias, scale=1.5)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("stride,start,step", [(67, 0, 1), (72, 1, 1), (68, 2, 2)])
+def test_rows_off_the_vectors_with_four_lanes_each(dtype, stride, start, step):
+    check(_logits(1301 * step, stride, dtype, seed=stride)[::step, start:start + 64], 6, _bias(64, 1), "sigmoid", 4, 2, 2)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups,kept,k,best", [(22, 2, 1, 8, 2), (31, 31, 9, 7, 2), (62, 31, 4, 5, 2), (100, 4, 3, 1, 1),
+                                                        (216, 8, 5, 3, 2), (216, 27, 5, 6, 1), (510, 3, 2, 7, 2),
+                                                        (992, 31, 9, 20, 2)])
+def test_groups_across_lanes(dtype, score, experts, groups, kept, k, best):
+    """Groups whose ends lie inside a lane's experts; masked experts, groups without any, near and whole ties."""
+    import torch
+    x = _logits(1301 if experts < 500 else 150, experts, dtype, seed=experts, masked=0.1)
+    x[3::7, :experts // groups] = -float("inf")
+    x[5::7] = (x[5::7] * 2).round() / 2
+    x[6::7] = 0.5
+    check(x, k, None, score, groups, kept, best)
+    check(x, k, _bias(experts, 3), score, groups, kept, best)
+    check(x, k, torch.zeros(experts, device="cuda"), score, groups, kept, best, renorm=False)

@@ -835,8 +835,9 @@ __device__ __noinline__ bool left_out_matters(const T *row, const RouteArgs &a, 
 // lanes read 16 experts side by side.  Every lane sorts its short keys in
 // eights and keeps the best eight, and two exchanges join the four lanes'.
 // Against one warp per token the fixed work is shared by eight: 65536 x 256
-// fp32 with groups and bias takes 53 us here and took 94 there.
-template <typename T, int S>
+// fp32 with groups and bias takes 53 us here and took 94 there.  kVec: rows of
+// whole, aligned vectors of four; else element by element.
+template <typename T, int S, bool kVec>
 __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *__restrict__ logits, RouteArgs a)
 {
     constexpr int P = 4 * S;
@@ -871,13 +872,14 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
             const int e = 16 * s + 4 * sub;
             alignas(16) T x[4];
             const bool in = live && e < a.experts;
-            if (in) {
+            if (kVec && in) {
                 if (sizeof(T) == 4) *reinterpret_cast<uint4 *>(x) = *reinterpret_cast<const uint4 *>(row + e);
                 else *reinterpret_cast<uint2 *>(x) = *reinterpret_cast<const uint2 *>(row + e);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                c[4 * s + j] = in ? load_logit(&x[j]) : -INFINITY;
+                if (kVec) c[4 * s + j] = in ? load_logit(&x[j]) : -INFINITY;
+                else c[4 * s + j] = live && e + j < a.experts ? load_logit(row + e + j) : -INFINITY;
                 c[4 * s + j] = in_reach(c[4 * s + j]) ? fminf(c[4 * s + j], FLT_MAX) : -INFINITY;
             }
         }
@@ -1334,31 +1336,33 @@ bool whole_vectors(const void *logits, size_t size, int experts, int64_t row_str
            (size_t)row_stride * size % bytes == 0;
 }
 
-template <typename T> RouteKernel<T> quad_kernel_for(int experts)
+template <typename T, bool kVec> RouteKernel<T> quad_kernel_for(int experts)
 {
-    return experts <= 32 ? route_quad_kernel<T, 2>
-           : experts <= 64 ? route_quad_kernel<T, 4>
-           : experts <= 128 ? route_quad_kernel<T, 8>
-                            : route_quad_kernel<T, 16>;
+    return experts <= 32 ? route_quad_kernel<T, 2, kVec>
+           : experts <= 64 ? route_quad_kernel<T, 4, kVec>
+           : experts <= 128 ? route_quad_kernel<T, 8, kVec>
+                            : route_quad_kernel<T, 16, kVec>;
 }
 
 // Whether four lanes per token do: enough tokens that eight a warp still
-// reach every SM, and rows, groups and k that fit its layout.
-bool quads_fit(const void *logits, size_t size, const RouteArgs &a, int sm_count)
+// reach every SM, and experts, groups and k that fit its layout.
+bool quads_fit(const RouteArgs &a, int sm_count)
 {
-    return a.experts <= kQuadExperts && a.k <= kQuadK && a.experts % 4 == 0 && a.row_stride % 4 == 0 &&
-           (reinterpret_cast<uintptr_t>(logits) & (4 * size - 1)) == 0 && a.groups <= kQuadGroups &&
+    return a.experts <= kQuadExperts && a.k <= kQuadK && a.groups <= kQuadGroups &&
            (a.groups == 1 || a.experts / a.groups % 16 == 0) && a.tokens >= (int64_t)sm_count * kQuadTokens;
 }
 
 template <typename T> cudaError_t launch_route(const void *logits, RouteArgs a, int sm_count, void *stream)
 {
-    if (quads_fit(logits, sizeof(T), a, sm_count)) {
+    if (quads_fit(a, sm_count)) {
         cudaLaunchAttribute attr[1];
         const int64_t warps = (a.tokens + kQuadTokens - 1) / kQuadTokens;
         const cudaLaunchConfig_t cfg =
             route_config(route_grid(warps, sm_count, 2), static_cast<cudaStream_t>(stream), attr);
-        return cudaLaunchKernelEx(&cfg, quad_kernel_for<T>(a.experts), static_cast<const T *>(logits), a);
+        const bool vec = a.experts % 4 == 0 && a.row_stride % 4 == 0 &&
+                         (reinterpret_cast<uintptr_t>(logits) & (4 * sizeof(T) - 1)) == 0;
+        return cudaLaunchKernelEx(&cfg, vec ? quad_kernel_for<T, true>(a.experts) : quad_kernel_for<T, false>(a.experts),
+                                  static_cast<const T *>(logits), a);
     }
     a.vec = whole_vectors(logits, sizeof(T), a.experts, a.row_stride);
     cudaLaunchAttribute attr[1];
