@@ -350,3 +350,18 @@ def test_groups_across_lanes(dtype, score, experts, groups, kept, k, best):
     check(x, k, None, score, groups, kept, best)
     check(x, k, _bias(experts, 3), score, groups, kept, best)
     check(x, k, torch.zeros(experts, device="cuda"), score, groups, kept, best, renorm=False)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups,kept,k,best", [(15, 15, 7, 8, 2), (4, 2, 1, 8, 2), (60, 5, 2, 5, 1), (91, 7, 6, 6, 2),
+                                                        (128, 16, 3, 8, 2), (127, 1, 1, 3, 2), (126, 2, 1, 8, 2)])
+def test_groups_of_any_size_with_four_lanes_each(dtype, score, experts, groups, kept, k, best):
+    import torch
+    x = _logits(1301, experts, dtype, seed=experts, masked=0.1)
+    x[3::7, :experts // groups] = -float("inf")
+    x[5::7] = (x[5::7] * 2).round() / 2
+    x[6::7] = 0.5
+    check(x, k, None, score, groups, kept, best)
+    check(x, k, _bias(experts, 3), score, groups, kept, best)
+    check(x, k, torch.zeros(experts, device="cuda"), score, groups, kept, best, renorm=False)

@@ -190,6 +190,17 @@ __device__ __forceinline__ float group_value(float m1, float m2, int best)
     return best > 1 && m2 > -INFINITY ? m1 + m2 : m1;
 }
 
+// What two groups' values have to differ by to be told apart in 32 bits:
+// four scores' errors and four roundings of sums; `most` bounds the sum of a
+// group's best two (which without a bias are scores, whose errors are relative
+// too).
+__device__ __forceinline__ float groups_margin(const RouteArgs &a, float most)
+{
+    float errors = 4.0f * (a.softmax ? kSoftmaxError : kSigmoidError);
+    if (a.softmax && !a.bias) errors = fminf(errors, 3.0f * kSoftmaxPart * most + 1e-37f);
+    return errors + 4.0f * kSumError * most;
+}
+
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
@@ -649,7 +660,7 @@ __device__ __forceinline__ int choose_row(const T *row, const RouteArgs &a, floa
         const uint32_t cut = __reduce_max_sync(kAll, left);
         const float size = any ? fabsf(m1) + (m2 > -INFINITY ? fabsf(m2) : 0.0f) : 0.0f;
         const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
-        const float margin = 4.0f * error + 4.0f * kSumError * most;
+        const float margin = groups_margin(a, most);
         bool keep = any && mine >= last;
         uint32_t kept = __ballot_sync(kAll, keep);
         // too close to call, or of equal values more kept than asked for
@@ -769,6 +780,7 @@ constexpr int kQuadExperts = 256; // the most a quad holds: 64 a lane
 constexpr int kQuadK = 8;
 constexpr int kQuadTokens = 8; // tokens a warp has at a time
 constexpr int kQuadGroups = 16;
+enum QuadMode { kQuadVec, kQuadElement, kQuadGroup };
 static_assert(kQuadExperts == 16 * 16, "sixteen steps of sixteen experts");
 
 // Eight keys into descending order (odd-even merges).
@@ -835,12 +847,16 @@ __device__ __noinline__ bool left_out_matters(const T *row, const RouteArgs &a, 
 // lanes read 16 experts side by side.  Every lane sorts its short keys in
 // eights and keeps the best eight, and two exchanges join the four lanes'.
 // Against one warp per token the fixed work is shared by eight: 65536 x 256
-// fp32 with groups and bias takes 53 us here and took 94 there.  kVec: rows of
-// whole, aligned vectors of four; else element by element.
-template <typename T, int S, bool kVec>
+// fp32 with groups and bias takes 53 us here and took 94 there.  Rows are read
+// by aligned vectors of four (kQuadVec) or by elements.  Groups are whole
+// steps, valued on the way; or of any size (kQuadGroup, up to 128 experts),
+// valued from a copy of the choices in shared memory.
+template <typename T, int S, QuadMode kMode>
 __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *__restrict__ logits, RouteArgs a)
 {
     constexpr int P = 4 * S;
+    constexpr bool kVec = kMode == kQuadVec, kAny = kMode == kQuadGroup;
+    static_assert(!kAny || P <= 32, "a lane's experts have a bit each");
     using Key = ShortKey<kQuadExperts / 32>;
     constexpr uint32_t kLeast = 0x00800000u; // keys below: out of reach
     __shared__ int32_t count[kQuadExperts];
@@ -848,6 +864,10 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
     __shared__ float group[kRouteWarps][kQuadTokens][kQuadGroups];
     __shared__ int32_t place[kRouteWarps][32];
     __shared__ int32_t redone[kRouteWarps][kQuadTokens][kQuadK];
+    // kAny: choices (tokens four banks apart), and a lane's experts by group
+    alignas(16) __shared__ float value[kAny ? kRouteWarps : 1][kQuadTokens][kAny ? 16 * S + 4 : 4];
+    __shared__ uint32_t members[kQuadGroups][4];
+    const int per = a.experts / a.groups;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 3, mine = lane >> 2;
     const bool scored = a.bias || a.groups > 1;
     for (int e = threadIdx.x; e < kQuadExperts; e += kRouteThreads) count[e] = 0;
@@ -856,8 +876,17 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
         const float b = a.bias && e < a.experts ? a.bias[e] : 0.0f;
         bias[e] = b > -INFINITY ? b : -INFINITY; // no choice can come of NaN
     }
+    if (kAny)
+        for (int m = threadIdx.x; m < 4 * a.groups; m += kRouteThreads) {
+            uint32_t bits = 0;
+            for (int i = 0; i < P; ++i) {
+                const int e = 16 * (i / 4) + 4 * (m & 3) + i % 4;
+                bits |= (uint32_t)(e / per == m / 4) << i;
+            }
+            members[m / 4][m & 3] = bits;
+        }
     __syncthreads();
-    const int steps_each = a.groups > 1 ? a.experts / a.groups / 16 : S + 1; // steps of a group
+    const int steps_each = a.groups > 1 && !kAny ? per / 16 : S + 1; // steps of a group
     const float error = !scored ? 0.0f : a.softmax ? kSoftmaxError : kSigmoidError;
     // 16-bit logits fit a short key whole: what ties there is a tie
     const bool exact = !scored && sizeof(T) == 2;
@@ -915,10 +944,15 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
                     float &v = c[4 * s + j];
                     if (a.softmax) v = v >= 0.0f ? fmaf(v, inverse, b[j]) : -INFINITY;
                     else v = v > -INFINITY ? sigmoid_fast(v) + b[j] : -INFINITY;
-                    m2 = fmaxf(m2, fminf(m1, v));
-                    m1 = fmaxf(m1, v);
+                    if (!kAny) {
+                        m2 = fmaxf(m2, fminf(m1, v));
+                        m1 = fmaxf(m1, v);
+                    }
                 }
-                if (--left == 0) { // a group's last step
+                if (kAny)
+                    *reinterpret_cast<float4 *>(&value[warp][mine][16 * s + 4 * sub]) =
+                        make_float4(c[4 * s], c[4 * s + 1], c[4 * s + 2], c[4 * s + 3]);
+                else if (--left == 0) { // a group's last step
                     join_best_two(m1, m2, __shfl_xor_sync(kAll, m1, 1), __shfl_xor_sync(kAll, m2, 1));
                     join_best_two(m1, m2, __shfl_xor_sync(kAll, m1, 2), __shfl_xor_sync(kAll, m2, 2));
                     if (sub == 0) group[warp][mine][g] = group_value(m1, m2, a.best);
@@ -933,6 +967,21 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
             for (int i = 0; i < P; ++i) c[i] += 0.0f; // one zero
         }
         uint32_t keep = 0xFFFFFFFFu;
+        if (kAny) {
+            __syncwarp();
+            for (int g = 0; g < a.groups; ++g) {
+                float m1 = -INFINITY, m2 = -INFINITY;
+                for (int i = sub; i < per; i += 4) {
+                    const float v = value[warp][mine][g * per + i];
+                    m2 = fmaxf(m2, fminf(m1, v));
+                    m1 = fmaxf(m1, v);
+                }
+                join_best_two(m1, m2, __shfl_xor_sync(kAll, m1, 1), __shfl_xor_sync(kAll, m2, 1));
+                join_best_two(m1, m2, __shfl_xor_sync(kAll, m1, 2), __shfl_xor_sync(kAll, m2, 2));
+                if (sub == 0) group[warp][mine][g] = group_value(m1, m2, a.best);
+                if (m1 > -INFINITY) most = fmaxf(most, fabsf(m1) + (m2 > -INFINITY ? fabsf(m2) : 0.0f));
+            }
+        }
         if (a.groups > 1) {
             __syncwarp();
             keep = 0;
@@ -952,7 +1001,7 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
             keep |= __shfl_xor_sync(kAll, keep, 2);
             last = lanes_max<4>(last);
             cut = lanes_max<4>(cut);
-            const float margin = 4.0f * error + 4.0f * kSumError * most;
+            const float margin = groups_margin(a, most);
             const bool unsure = live && cut > -INFINITY && !(last - cut > margin);
             for (uint32_t left = __ballot_sync(kAll, unsure) & 0x11111111u; left; left &= left - 1) {
                 const int first = __ffs(left) - 1, q = first >> 2;
@@ -963,6 +1012,9 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
             }
             __syncwarp(); // the groups are read before the next tokens' are written
         }
+        uint32_t within = 0; // kAny: the lane's experts in the groups kept
+        if (kAny)
+            for (int g = 0; g < a.groups; ++g) within |= (keep >> g) & 1u ? members[g][sub] : 0u;
         uint32_t best[8], dropped = 0;
         {
             int left = steps_each, g = 0;
@@ -972,10 +1024,9 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int s = 2 * b + h;
-                    const bool in = (keep >> g) & 1u;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        k[4 * h + j] = in ? Key::make_plain(c[4 * s + j], 16 * s + 4 * sub + j) : 0u;
+                        k[4 * h + j] = (kAny ? within >> (kAny ? 4 * s + j : 0) : keep >> g) & 1u ? Key::make_plain(c[4 * s + j], 16 * s + 4 * sub + j) : 0u;
                     if (--left == 0) {
                         left = steps_each;
                         ++g;
@@ -1336,12 +1387,13 @@ bool whole_vectors(const void *logits, size_t size, int experts, int64_t row_str
            (size_t)row_stride * size % bytes == 0;
 }
 
-template <typename T, bool kVec> RouteKernel<T> quad_kernel_for(int experts)
+template <typename T, QuadMode kMode> RouteKernel<T> quad_kernel_for(int experts)
 {
-    return experts <= 32 ? route_quad_kernel<T, 2, kVec>
-           : experts <= 64 ? route_quad_kernel<T, 4, kVec>
-           : experts <= 128 ? route_quad_kernel<T, 8, kVec>
-                            : route_quad_kernel<T, 16, kVec>;
+    if (experts <= 32) return route_quad_kernel<T, 2, kMode>;
+    if (experts <= 64) return route_quad_kernel<T, 4, kMode>;
+    if (experts <= 128) return route_quad_kernel<T, 8, kMode>;
+    if constexpr (kMode != kQuadGroup) return route_quad_kernel<T, 16, kMode>;
+    return nullptr;
 }
 
 // Whether four lanes per token do: enough tokens that eight a warp still
@@ -1349,7 +1401,7 @@ template <typename T, bool kVec> RouteKernel<T> quad_kernel_for(int experts)
 bool quads_fit(const RouteArgs &a, int sm_count)
 {
     return a.experts <= kQuadExperts && a.k <= kQuadK && a.groups <= kQuadGroups &&
-           (a.groups == 1 || a.experts / a.groups % 16 == 0) && a.tokens >= (int64_t)sm_count * kQuadTokens;
+           (a.groups == 1 || a.experts / a.groups % 16 == 0 || a.experts <= 128) && a.tokens >= (int64_t)sm_count * kQuadTokens;
 }
 
 template <typename T> cudaError_t launch_route(const void *logits, RouteArgs a, int sm_count, void *stream)
@@ -1361,8 +1413,10 @@ template <typename T> cudaError_t launch_route(const void *logits, RouteArgs a, 
             route_config(route_grid(warps, sm_count, 2), static_cast<cudaStream_t>(stream), attr);
         const bool vec = a.experts % 4 == 0 && a.row_stride % 4 == 0 &&
                          (reinterpret_cast<uintptr_t>(logits) & (4 * sizeof(T) - 1)) == 0;
-        return cudaLaunchKernelEx(&cfg, vec ? quad_kernel_for<T, true>(a.experts) : quad_kernel_for<T, false>(a.experts),
-                                  static_cast<const T *>(logits), a);
+        const auto kernel = a.groups > 1 && a.experts / a.groups % 16 ? quad_kernel_for<T, kQuadGroup>(a.experts)
+                            : vec                                     ? quad_kernel_for<T, kQuadVec>(a.experts)
+                                                                      : quad_kernel_for<T, kQuadElement>(a.experts);
+        return cudaLaunchKernelEx(&cfg, kernel, static_cast<const T *>(logits), a);
     }
     a.vec = whole_vectors(logits, sizeof(T), a.experts, a.row_stride);
     cudaLaunchAttribute attr[1];
