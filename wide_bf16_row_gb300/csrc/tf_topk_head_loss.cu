@@ -120,10 +120,11 @@ struct PairArgs {
     int32_t begin, cols;      // the piece of the vocabulary [begin, begin + cols)
     int32_t width;            // columns of a tile
     int32_t stages;           // of the ring
-    int32_t row_box;          // few rows: rows of A that the leading CTA loads (the peer none), a multiple of 8
+    int32_t row_box;          // few rows: rows of A that both CTAs load, a multiple of 8
+    int32_t slots;            // few rows: K steps of A, where all of it stays in shared memory, or 0
     int32_t pad_rows;         // row pitch of `partial`
     int32_t first;            // kHidden: the sums start here
-    float2 *partial;          // kLse: [2 * column tiles][pad_rows]: reference exponent, sum
+    float2 *partial;          // kLse: [2 * column tiles][pad_rows]: reference exponent, sum; few rows: [2 or 4 * pairs]
 };
 
 // ---------------------------------------------------------------- PTX helpers
@@ -466,7 +467,7 @@ template <int kMode> struct Shape {
 // `d`.  False when a wait gave up.
 template <bool kAMN, bool kBMN>
 __device__ __forceinline__ bool issue_tile(PairSmem &sm, uint32_t d, uint32_t idesc, int steps, uint32_t &s,
-                                           uint32_t &parity, uint32_t stages, const uint8_t *ring_a, uint32_t share_a,
+                                           uint32_t &parity, uint32_t stages, const uint8_t *ring_a, uint32_t share_a, bool a_stays,
                                            const uint8_t *ring_b, uint32_t share_b, volatile uint32_t *abort)
 {
     // 16 K steps: 32 bytes along a K-major row, 16 whole rows of an MN-major box
@@ -479,7 +480,7 @@ __device__ __forceinline__ bool issue_tile(PairSmem &sm, uint32_t d, uint32_t id
         if (++s == stages) s = 0, parity ^= 1;
         const bool next = mbar_test(&sm.full[s], parity); // answered while the products are issued
         tc_fence_after();
-        const uint64_t ad = desc_at(ring_a + here * share_a, kAMN ? kDescMN : kDescK);
+        const uint64_t ad = desc_at(ring_a + (a_stays ? k : here) * share_a, kAMN ? kDescMN : kDescK);
         const uint64_t bd = desc_at(ring_b + here * share_b, kBMN ? kDescMN : kDescK);
         if (elect_one()) {
 #pragma unroll
@@ -493,7 +494,11 @@ __device__ __forceinline__ bool issue_tile(PairSmem &sm, uint32_t d, uint32_t id
     return true;
 }
 
-template <int kMode, bool kFew>
+// Rows of a product: any number, up to kHalf, and those where all their K
+// steps stay in shared memory.
+enum PairRows { kManyRows, kFewRows, kRowsStay };
+
+template <int kMode, PairRows kRows>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                         const __grid_constant__ CUtensorMap map_wa, const __grid_constant__ CUtensorMap map_wb,
@@ -508,10 +513,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int half_cols = kMode == kLse ? a.width / 2 : kHalf; // one CTA's share of B
     // (Whole shares have the ring's shape at compile time: the issuing thread
     // keeps up better, 615 against 631 us on 800 x 2048 x 248320.)
+    constexpr bool kFew = kRows != kManyRows;
     const uint32_t share_a = kFew ? (uint32_t)a.row_box * kStepK * 2 : kShare;
     const uint32_t share_b = kFew ? (uint32_t)half_cols * kStepK * 2 : kShare;
     const uint32_t stages = kFew ? (uint32_t)a.stages : kRingBytes / (2 * kShare);
-    uint8_t *ring_a = ring, *ring_b = ring + stages * share_a;
+    constexpr bool stays = kRows == kRowsStay; // A is loaded with a pair's first tile only
+    // Few rows: both CTAs load them, so that each has all columns of the tile
+    // for them and the epilogue is shared; or the leading one alone, where the
+    // stream of B is what counts (the loss of 15 x 2048 x 98592 takes 2.5 %
+    // longer with two).
+    constexpr bool both = kFew && (kMode != kLse || stays);
+    uint8_t *ring_a = ring, *ring_b = ring + (stays ? (uint32_t)a.slots : stages) * share_a;
     uint8_t *staging = ring + kRingBytes; // 1024-byte aligned
     PairSmem &sm = *reinterpret_cast<PairSmem *>(staging + (kMode == kLse ? 0 : kStagingBytes));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -554,16 +566,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
     if (warp == 0) {
         // ---- TMA producer
-        // both CTAs' bytes; of few rows only the leading CTA has any
-        const uint32_t bytes = (kFew ? share_a : 2 * share_a) + 2 * (uint32_t)half_cols * kStepK * 2;
-        const bool has_a = !kFew || rank == 0;
+        const uint32_t bytes_a = (!kFew || both ? 2 : 1) * share_a, bytes_b = 2 * (uint32_t)half_cols * kStepK * 2;
         const uint32_t full0 = peer_addr(&sm.full[0], 0); // the leading CTA's barriers
         uint32_t s = 0, turn = 0;                         // ring stage, times round the ring
         bool ok = true;
         for (int64_t u = pair; u < units && ok; u += pairs) {
             const Unit t = shape.at(u);
             const bool weight = shape.of_weight(u);
-            const int row = t.m * kTileRows + (int)rank * kHalf;
+            const int row = t.m * kTileRows + (kFew ? 0 : (int)rank * kHalf);
             const int col = t.n * kTileCols + (int)rank * kHalf;
             const int voc = a.begin + t.n * a.width + (int)rank * half_cols;
             for (int k = t.k0; k < t.k1; ++k) {
@@ -571,9 +581,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 if (elect_one()) {
-                    if (rank == 0) mbar_expect_tx(&sm.full[s], bytes);
+                    const bool new_a = !stays || u == pair, has_a = new_a && (!kFew || both || rank == 0);
+                    if (rank == 0) mbar_expect_tx(&sm.full[s], new_a ? bytes_a + bytes_b : bytes_b);
                     const uint32_t bar = full0 + s * (uint32_t)sizeof(uint64_t);
-                    uint8_t *da = ring_a + s * share_a, *db = ring_b + s * share_b;
+                    uint8_t *da = ring_a + (stays ? k : s) * share_a, *db = ring_b + s * share_b;
                     const int kx = k * kStepK;
                     if (kMode == kLse || kMode == kProb) {
                         if (has_a) tma_load(da, &map_a, kx, row, bar);
@@ -615,13 +626,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 bool ok;
                 if (kMode == kLse || kMode == kProb)
                     ok = issue_tile<false, false>(sm, d, instruction_desc(false, false, cols), steps, s, parity, stages,
-                                                  ring_a, share_a, ring_b, share_b, abort);
+                                                  ring_a, share_a, stays, ring_b, share_b, abort);
                 else if (!shape.of_weight(u))
                     ok = issue_tile<false, true>(sm, d, instruction_desc(false, true, cols), steps, s, parity, stages,
-                                                 ring_a, share_a, ring_b, share_b, abort);
+                                                 ring_a, share_a, false, ring_b, share_b, abort);
                 else
                     ok = issue_tile<true, true>(sm, d, instruction_desc(true, true, cols), steps, s, parity, stages,
-                                                ring_a, share_a, ring_b, share_b, abort);
+                                                ring_a, share_a, false, ring_b, share_b, abort);
                 if (!ok) break;
                 if (elect_one()) mma_commit_pair(&sm.acc_full[buf]);
                 __syncwarp();
@@ -659,9 +670,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // rows over all of the pair's tiles
         float ref = 0.0f, top = -INFINITY, sum = 0.0f;
         // few rows: the warps that have none (but for kProb's zeros) skip the tile
-        const bool no_rows = kFew && kMode != kProb && (int)rank * kHalf + 32 * q >= count;
+        const int first_row = (both ? 0 : (int)rank * kHalf) + 32 * q;
+        const bool no_rows = kFew && kMode != kProb && first_row >= count;
         // a row's facts are fetched a tile ahead
-        const auto row_of = [&](int m) { return m * kTileRows + (int)rank * kHalf + 32 * q + lane; };
+        const auto row_of = [&](int m) { return m * kTileRows + first_row + lane; };
+        // the share of a tile's columns that this warp takes, in whole chunks: a
+        // half, or where both CTAs have the rows a quarter
+        constexpr int parts = both ? 4 : 2;
+        const int part = both ? 2 * h + (int)rank : h, all_chunks = half_cols / (kChunk / 2);
+        const int first_chunk = all_chunks * part / parts, last_chunk = all_chunks * (part + 1) / parts;
         const auto facts_of = [&](int row) {
             RowFacts f = {-1, 0.0f, 0.0f, 0.0f};
             if ((kMode == kLse || kMode == kProb) && row < count) {
@@ -710,7 +727,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const float lse2 = facts.lse2, g = kMode == kProb ? facts.grad / a.header->grad_scale : 0.0f;
             const uint32_t lanes = tmem + buf * kTileCols + ((uint32_t)(32 * q) << 16);
             // columns of the tile that this thread takes
-            const int c0 = h * half_cols, chunks = no_rows ? 0 : half_cols / kChunk;
+            const int c0 = first_chunk * kChunk, chunks = no_rows ? 0 : last_chunk - first_chunk;
             // gradients: those that hold columns of them
             const int chunks_in_dim = min(chunks, ceil_div(max(0, a.dim - t.n * kTileCols - c0), kChunk));
             if (kMode == kGrads) { // boxes of the other kind may still be on their way out
@@ -755,7 +772,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 // rows past the count are zeros up to the last K step of the
                 // products over rows, and nothing reads those behind it
                 const int end = max(1, ceil_div(count, kStepK)) * kStepK;
-                walk(lanes + c0, row - lane < end ? kHalf / kChunk : 0, [&](int c, float (&x)[kChunk]) {
+                walk(lanes + c0, row - lane < end ? chunks : 0, [&](int c, float (&x)[kChunk]) {
                     const int col = t.n * kTileCols + c0 + c * kChunk;
                     const int left = row < count ? a.cols - col : 0;
                     const int hit = at - col;
@@ -806,9 +823,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         if (kMode != kLse) box_wait(); // what this lane sent is written
         if (kMode == kLse && kFew) {
-            const int row = (int)rank * kHalf + 32 * q + lane;
+            const int row = first_row + lane;
             if (row < count)
-                a.partial[(size_t)(2 * pair + h) * a.pad_rows + row] =
+                a.partial[(size_t)(parts * pair + part) * a.pad_rows + row] =
                     make_float2(top == -INFINITY ? -INFINITY : ref, sum);
         }
     }
@@ -1073,15 +1090,21 @@ std::mutex g_loss_mutex;
 PFN_cuTensorMapEncodeTiled_v12000 g_loss_encode = nullptr;
 
 template <int kMode> constexpr bool kHasFew = kMode != kWeight && kMode != kGrads;
+template <int kMode> constexpr bool kHasStay = kMode == kLse || kMode == kProb;
+
+template <int kMode, PairRows kRows> cudaError_t allow_smem_of()
+{
+    return cudaFuncSetAttribute(pair_product_kernel<kMode, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)kPairSmemBytes);
+}
 
 template <int kMode> cudaError_t allow_smem()
 {
-    cudaError_t e = cudaFuncSetAttribute(pair_product_kernel<kMode, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kPairSmemBytes);
+    cudaError_t e = allow_smem_of<kMode, kManyRows>();
     if constexpr (kHasFew<kMode>)
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(pair_product_kernel<kMode, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kPairSmemBytes);
+        if (e == cudaSuccess) e = allow_smem_of<kMode, kFewRows>();
+    if constexpr (kHasStay<kMode>)
+        if (e == cudaSuccess) e = allow_smem_of<kMode, kRowsStay>();
     return e;
 }
 
@@ -1115,7 +1138,7 @@ int loss_setup(int *pairs, int *sm_count)
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             int n = 0;
-            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, pair_product_kernel<kLse, false>, &cfg);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, pair_product_kernel<kLse, kManyRows>, &cfg);
             if (e != cudaSuccess) return tf_topk_internal_fail_cuda((int)e);
             d.pairs = n < 1 ? 1 : n;
             if (!g_loss_encode) {
@@ -1179,15 +1202,20 @@ struct PairMaps {
     CUtensorMap a, b, wa, wb, out, wout;
 };
 
-// The ring of a product with up to kHalf rows: only the leading CTA loads
-// rows of A, as many as there are (in eights), and the stages take what is
-// left (15 x 2048 x 98592: 74 us, with whole shares of A 128).
+// The ring of a product with up to kHalf rows: as many rows of A as there are
+// (in eights), and the stages take what is left (15 x 2048 x 98592: 74 us, with
+// whole shares of A 128).  Rows of few K steps stay beside the ring instead of
+// coming again with every tile.
 bool set_ring(PairArgs &a, int mode, int64_t rows)
 {
     if (mode == kWeight || mode == kGrads || rows > kHalf) return false;
     a.row_box = (int32_t)((rows + 7) / 8 * 8);
     const int cols = mode == kHidden ? kHalf : a.width / 2;
-    const int fit = (int)(kRingBytes / ((uint32_t)(a.row_box + cols) * kStepK * 2));
+    const uint32_t row = kStepK * 2;
+    const int64_t steps = ((int64_t)a.dim + kStepK - 1) / kStepK, all = steps * a.row_box * row;
+    const bool stays = mode != kHidden && all <= kRingBytes / 8;
+    a.slots = stays ? (int32_t)steps : 0;
+    const int fit = (int)(stays ? (kRingBytes - all) / (cols * row) : kRingBytes / ((a.row_box + cols) * row));
     a.stages = fit < kMaxStages ? fit : kMaxStages;
     return true;
 }
@@ -1199,9 +1227,12 @@ cudaError_t launch_product(const PairMaps &m, PairArgs &a, int64_t most_units, i
     cudaLaunchAttribute attr[1];
     const int64_t n = most_units < pairs ? most_units : pairs;
     const cudaLaunchConfig_t cfg = config((int)(2 * n), kPairThreads, kMode == kLse ? kLseSmemBytes : kPairSmemBytes, stream, attr);
+    auto kernel = pair_product_kernel<kMode, kManyRows>;
     if constexpr (kHasFew<kMode>)
-        if (few) return cudaLaunchKernelEx(&cfg, pair_product_kernel<kMode, true>, m.a, m.b, m.wa, m.wb, m.out, m.wout, a);
-    return cudaLaunchKernelEx(&cfg, pair_product_kernel<kMode, false>, m.a, m.b, m.wa, m.wb, m.out, m.wout, a);
+        if (few) kernel = pair_product_kernel<kMode, kFewRows>;
+    if constexpr (kHasStay<kMode>)
+        if (few && a.slots) kernel = pair_product_kernel<kMode, kRowsStay>;
+    return cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.wa, m.wb, m.out, m.wout, a);
 }
 
 // Row pitch of the packed hidden states: whole 128-byte lines, whatever dim.
@@ -1274,6 +1305,13 @@ LossSpace loss_space(const void *p, int64_t rows, int64_t dim, int64_t parts)
     return s;
 }
 
+// Parts of a row's sum: two halves per tile, or at most four quarters per pair
+// with few rows.
+int64_t sum_parts(int64_t rows, int64_t tiles, int pairs)
+{
+    return rows > kHalf ? 2 * tiles : 4 * (tiles < pairs ? tiles : pairs);
+}
+
 // Bytes of a workspace at `p` that serves every block of rows.
 size_t loss_bytes(const void *p, int64_t rows, int64_t dim, int64_t vocab, int pairs)
 {
@@ -1281,7 +1319,7 @@ size_t loss_bytes(const void *p, int64_t rows, int64_t dim, int64_t vocab, int p
     for (const int64_t n : {rows < kLossRows ? rows : kLossRows, rows % kLossRows}) {
         if (n == 0) continue;
         const int width = tile_width(n, vocab, pairs);
-        const size_t bytes = loss_space(p, n, dim, 2 * ((vocab + width - 1) / width)).bytes;
+        const size_t bytes = loss_space(p, n, dim, sum_parts(n, (vocab + width - 1) / width, pairs)).bytes;
         most = bytes > most ? bytes : most;
     }
     return most;
@@ -1402,7 +1440,8 @@ int loss_of_rows(const void *hidden, int64_t hidden_stride, const void *weight, 
 {
     const int width = tile_width(rows, vocab, pairs);
     const int64_t tiles = (vocab + width - 1) / width;
-    const LossSpace s = loss_space(workspace, rows, dim, 2 * tiles);
+    const int64_t most_parts = sum_parts(rows, tiles, pairs);
+    const LossSpace s = loss_space(workspace, rows, dim, most_parts);
     PairMaps m = {};
     const bool packed = s.packed != nullptr;
     const int box = rows <= kHalf ? (int)((rows + 7) / 8 * 8) : kHalf; // rows of A a CTA loads (set_ring)
@@ -1430,14 +1469,14 @@ int loss_of_rows(const void *hidden, int64_t hidden_stride, const void *weight, 
     a.partial = s.partial;
     const int64_t units = tiles * (pad_rows_of(rows) / kTileRows);
     if (e == cudaSuccess) e = launch_product<kLse>(m, a, units, pairs, strm);
-    // parts of a row's sum: two halves per tile, or per pair with few rows
-    const int parts = (int)(2 * (rows > kHalf ? tiles : units < pairs ? units : pairs));
+    const int parts = (int)(rows > kHalf || a.slots ? most_parts : most_parts / 2);
     const cudaLaunchConfig_t cfg =
         config((int)((rows + kRowsPerCta - 1) / kRowsPerCta), kRowsThreads, 0, strm, attr);
     if (e == cudaSuccess)
         e = cudaLaunchKernelEx(&cfg, head_loss_rows_kernel, (const float2 *)s.partial,
-                               parts, a.pad_rows, (const int32_t *)s.place, static_cast<const __nv_bfloat16 *>(hidden), hidden_stride,
-                               static_cast<const __nv_bfloat16 *>(weight), weight_stride, (int)dim, (int)vocab, target,
+                               parts, a.pad_rows, (const int32_t *)s.place, static_cast<const __nv_bfloat16 *>(hidden),
+                               hidden_stride, static_cast<const __nv_bfloat16 *>(weight), weight_stride, (int)dim,
+                               (int)vocab, target,
                                (int)(target_bytes == 8), ignore, (int)rows, loss, lse);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? TF_TOPK_OK : tf_topk_internal_fail_cuda((int)e);
