@@ -377,11 +377,16 @@ __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b -
 // lane per candidate.
 __device__ __forceinline__ int best_splits(int row_tiles, int dim, int pairs, int most)
 {
-    const int s = (threadIdx.x & 31) + 1;
-    const int64_t tiles = (int64_t)row_tiles * ceil_div(dim, kTileCols);
-    const float rounds = (float)((tiles * s + pairs - 1) / pairs) / (float)s;
-    float cost = s <= most ? rounds * (1.0f + 0.02f * (float)s) : 3e38f;
-    int best = s;
+    const float per_share = __fdividef((float)row_tiles * (float)ceil_div(dim, kTileCols), (float)pairs); // of a round
+    float cost = 3e38f;
+    int best = most;
+    for (int s = (threadIdx.x & 31) + 1; s <= most; s += 32) {
+        const float c = __fdividef(ceilf(per_share * (float)s - 1e-3f), (float)s) * (1.0f + 0.02f * (float)s);
+        if (c < cost) {
+            cost = c;
+            best = s;
+        }
+    }
 #pragma unroll
     for (int d = 16; d; d >>= 1) {
         const float o = __shfl_xor_sync(0xFFFFFFFFu, cost, d);
@@ -1045,30 +1050,60 @@ __global__ void __launch_bounds__(kRowsThreads)
 }
 
 // d_hidden: the shares' sums of a row added up, scaled back and rounded;
-// zeros for the rows that do not count.
+// zeros for the rows that do not count.  kGroups, up to 1024 columns: few
+// columns have many shares, and several threads add up each column's.
+template <bool kGroups>
 __global__ void __launch_bounds__(256)
     head_loss_hidden_kernel(const float *__restrict__ sums, int pad_rows, int dim, const RowHeader *header,
                             const int32_t *place, int rows, __nv_bfloat16 *d_hidden)
 {
+    __shared__ float4 part[2][kGroups ? 256 : 1];
     grid_dependency_wait();
     const float scale = header->grad_scale;
     const int splits = header->splits;
-    const int vecs = dim / 8;
-    for (int r = blockIdx.x; r < rows; r += gridDim.x) {
-        const int j = place[r];
-        uint4 *dst = reinterpret_cast<uint4 *>(d_hidden + (size_t)r * dim);
-        for (int i = threadIdx.x; i < vecs; i += blockDim.x) {
-            float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (j >= 0)
+    const int vecs = dim / 8, tid = threadIdx.x;
+    // every by-th share of eight columns of a packed row
+    const auto sum = [&](int j, int i, int from, int by, float (&v)[8]) {
 #pragma unroll 4
-                for (int s = 0; s < splits; ++s) {
-                    const float4 *src = reinterpret_cast<const float4 *>(sums + ((size_t)s * pad_rows + j) * dim) + 2 * i;
-                    const float4 p = src[0], q = src[1];
+        for (int s = from; s < splits; s += by) {
+            const float4 *src = reinterpret_cast<const float4 *>(sums + ((size_t)s * pad_rows + j) * dim) + 2 * i;
+            const float4 p = src[0], q = src[1];
+            v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+            v[4] += q.x, v[5] += q.y, v[6] += q.z, v[7] += q.w;
+        }
+    };
+    const auto put = [&](int r, int i, const float (&v)[8]) {
+        reinterpret_cast<uint4 *>(d_hidden + (size_t)r * dim)[i] =
+            make_uint4(pack_bf16(v[0] * scale, v[1] * scale), pack_bf16(v[2] * scale, v[3] * scale),
+                       pack_bf16(v[4] * scale, v[5] * scale), pack_bf16(v[6] * scale, v[7] * scale));
+    };
+    if constexpr (!kGroups) {
+        for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+            const int j = place[r];
+            for (int i = tid; i < vecs; i += 256) {
+                float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (j >= 0) sum(j, i, 0, 1, v);
+                put(r, i, v);
+            }
+        }
+    } else {
+        const int groups = 256 / vecs, group = tid / vecs, i = tid - group * vecs;
+        for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+            const int j = place[r];
+            float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (j >= 0 && group < groups) sum(j, i, group, groups, v);
+            part[0][tid] = make_float4(v[0], v[1], v[2], v[3]);
+            part[1][tid] = make_float4(v[4], v[5], v[6], v[7]);
+            __syncthreads();
+            if (group == 0) {
+                for (int g = 1; g < min(groups, splits); ++g) {
+                    const float4 p = part[0][g * vecs + i], q = part[1][g * vecs + i];
                     v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
                     v[4] += q.x, v[5] += q.y, v[6] += q.z, v[7] += q.w;
                 }
-            dst[i] = make_uint4(pack_bf16(v[0] * scale, v[1] * scale), pack_bf16(v[2] * scale, v[3] * scale),
-                                pack_bf16(v[4] * scale, v[5] * scale), pack_bf16(v[6] * scale, v[7] * scale));
+                put(r, i, v);
+            }
+            __syncthreads();
         }
     }
     grid_dependents_go();
@@ -1591,9 +1626,9 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
     }
     if (e == cudaSuccess && d_hidden) {
         const cudaLaunchConfig_t cfg = config((int)(rows < 8 * sms ? rows : 8 * sms), 256, 0, strm, attr);
-        e = cudaLaunchKernelEx(&cfg, head_loss_hidden_kernel, (const float *)s.sums, a.pad_rows, (int)dim,
-                               (const RowHeader *)s.header, (const int32_t *)s.place, (int)rows,
-                               static_cast<__nv_bfloat16 *>(d_hidden));
+        e = cudaLaunchKernelEx(&cfg, dim <= 1024 ? head_loss_hidden_kernel<true> : head_loss_hidden_kernel<false>,
+                               (const float *)s.sums, a.pad_rows, (int)dim, (const RowHeader *)s.header,
+                               (const int32_t *)s.place, (int)rows, static_cast<__nv_bfloat16 *>(d_hidden));
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? TF_TOPK_OK : tf_topk_internal_fail_cuda((int)e);
