@@ -365,3 +365,19 @@ def test_groups_of_any_size_with_four_lanes_each(dtype, score, experts, groups, 
     check(x, k, None, score, groups, kept, best)
     check(x, k, _bias(experts, 3), score, groups, kept, best)
     check(x, k, torch.zeros(experts, device="cuda"), score, groups, kept, best, renorm=False)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_an_only_choice_has_weight_scale_and_no_gradient(dtype, score):
+    """Renormalised, one expert's weight is the scale whatever its logit: no rounding may leave a gradient."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    x = _logits(1301, 33, dtype, 8)
+    x[::3, 1:] = -float("inf")
+    for k, rows in ((1, slice(None)), (4, slice(None, None, 3)), (12, slice(None, None, 3))):
+        idx, weight = topk.route_experts(x, k, score=score, scale=2.5)
+        d = topk.route_experts_grad(x, idx, torch.randn(1301, k, device="cuda"), score=score, scale=2.5)
+        assert not torch.any(d[rows] != 0)
+        torch.testing.assert_close(weight[rows, 0], torch.full_like(weight[rows, 0], 2.5), rtol=2 * RTOL, atol=0)
