@@ -124,6 +124,7 @@ struct PairArgs {
     int32_t slots;            // few rows: K steps of A, where all of it stays in shared memory, or 0
     int32_t pad_rows;         // row pitch of `partial`
     int32_t first;            // kHidden: the sums start here
+    float log2e;              // for logits as the tensor cores sum them (logit_scale)
     float2 *partial;          // kLse: [2 * column tiles][pad_rows]: reference exponent, sum; few rows: [2 or 4 * pairs]
 };
 
@@ -760,14 +761,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     if (m > top) {
                         // an infinite maximum keeps reference 0: inf and NaN then show in the sum
-                        const float next = fabsf(m) < INFINITY ? m * kLog2e : 0.0f;
+                        const float next = fabsf(m) < INFINITY ? m * a.log2e : 0.0f;
                         sum *= top > -INFINITY ? exp2_fast(ref - next) : 1.0f;
                         ref = next;
                         top = m;
                     }
                     float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) s4[i & 3] += exp2_fast(fmaf(x[i], kLog2e, -ref));
+                    for (int i = 0; i < kChunk; ++i) s4[i & 3] += exp2_fast(fmaf(x[i], a.log2e, -ref));
                     sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
                 });
                 if (row < count && !kFew)
@@ -782,7 +783,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const int left = row < count ? a.cols - col : 0;
                     const int hit = at - col;
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) x[i] = exp2_fast(fmaf(x[i], kLog2e, -lse2));
+                    for (int i = 0; i < kChunk; ++i) x[i] = exp2_fast(fmaf(x[i], a.log2e, -lse2));
                     if (__any_sync(0xFFFFFFFFu, (uint32_t)hit < (uint32_t)kChunk))
 #pragma unroll
                         for (int i = 0; i < kChunk; ++i)
@@ -1442,6 +1443,12 @@ bool bad_stride(int64_t stride, int64_t dim, int64_t n)
     return stride < dim || stride % 8 != 0 || stride >= (1ll << 39) || (n > 0 && stride > INT64_MAX / 4 / n);
 }
 
+// log2(e) for a logit of the tensor cores.  They truncate their running sums,
+// one addition per 16 products, and the logit comes out too small: measured by
+// 1.0e-9 of itself per product (0.7e-6, 2.0e-6 and 4.1e-6 in the log-sum at dim
+// 512, 2048 and 4096, where the spread between rows is 0.6e-6).
+float logit_scale(int32_t dim) { return (float)(1.4426950408889634 * (1.0 + 1.0e-9 * dim)); }
+
 // Finds and packs the rows that count (`lse`, `grad` null for the loss alone).
 template <typename Space>
 cudaError_t pack_rows(const Space &s, const void *hidden, int64_t stride, int64_t rows, int32_t dim, int64_t vocab,
@@ -1490,6 +1497,7 @@ int loss_of_rows(const void *hidden, int64_t hidden_stride, const void *weight, 
         e = pack_rows(s, hidden, hidden_stride, rows, dim, vocab, target, target_bytes, ignore, nullptr, nullptr, pairs, 1,
                       sms, strm);
     PairArgs a = {};
+    a.log2e = logit_scale(dim);
     a.header = s.header;
     a.facts = s.facts;
     a.target = target;
@@ -1598,6 +1606,7 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
     cudaError_t e = pack_rows(s, hidden, hidden_stride, rows, dim, vocab, target, target_bytes, ignore, lse, grad_loss,
                               pairs, splits, sms, strm);
     PairArgs a = {};
+    a.log2e = logit_scale(dim);
     a.header = s.header;
     a.facts = s.facts;
     a.target = target;
