@@ -374,7 +374,10 @@ size_t tf_topk_head_bf16_workspace(int32_t rows, int32_t k);
  *   loss[r] = lse[r] - x[r][target[r]]
  * A row whose target is ignore_index has loss 0 and lse 0; any other target
  * outside [0, vocab) gives NaN in both (and no gradient).  The losses are per
- * row: their mean or sum is the caller's.
+ * row: their mean or sum is the caller's.  The tensor cores truncate where they
+ * add: they sum up to 512 dims (4096 with more than 128 rows), and such sums are
+ * added rounding to nearest, so that the error of an x does not grow with dim
+ * beyond; sums that fp32 holds are exact, and the target's x is summed by FMA.
  *
  *   hidden, weight  device, bf16; row r at hidden + r * hidden_stride, column
  *                   v of the vocabulary at weight + v * weight_stride

@@ -1,0 +1,79 @@
+"""GPU: the digits of the head's loss and of its gradient, where sums are exact
+or known well enough to hold the kernels to a few units in the last place."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from oracle import head_loss as oracle_loss
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from wide_bf16_row_gb300 import build
+    build.build()
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+@pytest.mark.parametrize("rows", [5, 200, 300])
+@pytest.mark.parametrize("tied", [2, 7])
+def test_exact_sums_of_large_logits(rows, tied):
+    """One-hot hidden states at 4096 dims, `tied` columns with a logit of 32 and the target among them: nothing is
+    rounded in a sum, so lse = 32 + log(tied) and loss = log(tied), but for the exponents: 32 log2 e = 46 is rounded
+    when taken as a reference and when log2 of the sum is added to it, and their product with ln 2 once more
+    (2^-19 ln 2, twice, and 2^-20); the constants are 2 u off, relatively, and the rest some u of numbers up to 3."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    dim, vocab = 4096, 700
+    hidden = torch.zeros(rows, dim, dtype=torch.bfloat16, device="cuda")
+    at = (torch.arange(rows) * 37 % dim).cuda()
+    hidden[torch.arange(rows), at] = 1
+    weight = torch.zeros(vocab, dim, dtype=torch.bfloat16, device="cuda")
+    weight[100:100 + 90 * tied:90] = 32
+    target = torch.full((rows,), 100 + 90 * (tied - 1), device="cuda")
+    loss, lse = topk.head_loss_bf16(hidden, weight, target)
+    allow = 2 * 2.0 ** -19 * 0.7 + 2.0 ** -20 + 2 * U * 32 + 16 * U
+    rest = (vocab - tied) * np.exp(-32.0)
+    assert np.abs(_np(lse) - 32 - np.log(tied + rest)).max() <= allow
+    assert np.abs(_np(loss) - np.log(tied + rest)).max() <= allow
+
+
+@pytest.mark.parametrize("rows", [3, 140, 300])
+@pytest.mark.parametrize("dim", [512, 2048, 4096, 16384])
+@pytest.mark.parametrize("lead", [0, 300])
+def test_a_leading_dim(rows, dim, lead):
+    """Logits of about 32 of which one dim holds all but a few parts in a hundred, as hidden states with a massive
+    activation have them: beyond the dims of a part the error does not grow.  The tensor cores add 16 products and the
+    sum so far at a time, each aligned to the largest of them and cut off below 2^-23 of it at the latest: 17 units
+    lost at most.  They sum 512 dims at most, 32 additions, with more than 128 rows 4096; the parts are then added
+    rounding to nearest (u of the sum each).  The exponents' roundings are those of the test above.  (Over all of 16384
+    dims in one sum such a logit lost 9.7e-3.)"""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    g = torch.Generator().manual_seed(dim + rows)
+    vocab = 300
+    hidden = (0.01 * torch.rand(rows, dim, generator=g)).bfloat16()
+    weight = torch.rand(vocab, dim, generator=g).bfloat16()
+    hidden[:, lead] = 8
+    weight[:, lead] = 4
+    target = torch.randint(0, vocab, (rows,), generator=g)
+    loss, lse = topk.head_loss_bf16(hidden.cuda(), weight.cuda(), target.cuda())
+    h, w = _np(hidden), _np(weight)
+    ref_loss, ref_lse = oracle_loss.loss(h, w, target.numpy())
+    most = 512 if rows <= 128 else 4096
+    parts = [(np.abs(h[:, i:i + most]) @ np.abs(w[:, i:i + most]).T).max(1) for i in range(0, dim, most)]
+    size = sum(parts)
+    allow = most / 16 * 17 * 2.0 ** -23 * size + (len(parts) + 1) * U * size + 4 * 2.0 ** -19 * 0.7 + 2.0 ** -19 + 1e-6
+    assert (np.abs(_np(lse) - ref_lse) <= allow).all(), (np.abs(_np(lse) - ref_lse).max(), allow.min())
+    # the target's logit: 32 lanes' sums by FMA and their butterfly
+    allow += (dim / 32 + 5) * U * size
+    assert (np.abs(_np(loss) - ref_loss) <= allow).all(), (np.abs(_np(loss) - ref_loss).max(), allow.min())

@@ -36,9 +36,9 @@
 //
 // The tensor cores truncate their running fp32 sums, which biases a logit of
 // 12 by about -2.6e-5 at 2048 dims (measured against 64 bits; the fp32 FMA
-// sum is unbiased).  In lse that is spread over many small logits, but in
-// loss it would be the target's alone, so the target's logit is summed by
-// FMA in head_loss_rows_kernel and
+// sum is unbiased).  In lse that is spread over many small logits, whose sums
+// kLse keeps short (kPartSteps), but in loss it would be the target's alone, so
+// the target's logit is summed by FMA in head_loss_rows_kernel and
 //   loss = log(1 + exp(rest - x_t)),  rest = log sum over v != t of exp(x_v),
 // which also keeps the digits of a loss near 0.
 //
@@ -65,6 +65,7 @@ namespace {
 
 constexpr int kTileRows = 256;                       // rows (M) of a pair's tile
 constexpr int kTileCols = 256;                       // columns (N) of the widest tile
+constexpr int kFewCols = 192;                        // of the widest tile of the loss with up to kHalf rows
 constexpr int kHalf = 128;                           // one CTA's share of either
 constexpr int kStepK = 64;                           // K per ring stage: one 128-byte swizzle row of bf16
 constexpr uint32_t kShare = kHalf * kStepK * 2;      // 16 KB: one CTA's whole share of an operand per stage
@@ -124,7 +125,6 @@ struct PairArgs {
     int32_t slots;            // few rows: K steps of A, where all of it stays in shared memory, or 0
     int32_t pad_rows;         // row pitch of `partial`
     int32_t first;            // kHidden: the sums start here
-    float log2e;              // for logits as the tensor cores sum them (logit_scale)
     float2 *partial;          // kLse: [2 * column tiles][pad_rows]: reference exponent, sum; few rows: [2 or 4 * pairs]
 };
 
@@ -295,6 +295,22 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[kChunk])
                    "+r"(r[30]), "+r"(r[31])
                  :
                  : "memory");
+}
+
+// Sixteen columns added to what the thread has of them (fp32 bits).
+__device__ __forceinline__ void tmem_add16(uint32_t taddr, uint32_t *to)
+{
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) to[i] = __float_as_uint(__uint_as_float(to[i]) + __uint_as_float(r[i]));
 }
 
 __device__ __forceinline__ void cluster_sync()
@@ -469,10 +485,10 @@ template <int kMode> struct Shape {
     }
 };
 
-// The products of one tile: `steps` ring stages from `s` on into accumulator
-// `d`.  False when a wait gave up.
+// K steps [begin, end) of one tile, that many ring stages from `s` on, into
+// accumulator `d`.  False when a wait gave up.
 template <bool kAMN, bool kBMN>
-__device__ __forceinline__ bool issue_tile(PairSmem &sm, uint32_t d, uint32_t idesc, int steps, uint32_t &s,
+__device__ __forceinline__ bool issue_tile(PairSmem &sm, uint32_t d, uint32_t idesc, int begin, int end, uint32_t &s,
                                            uint32_t &parity, uint32_t stages, const uint8_t *ring_a, uint32_t share_a, bool a_stays,
                                            const uint8_t *ring_b, uint32_t share_b, volatile uint32_t *abort)
 {
@@ -480,7 +496,7 @@ __device__ __forceinline__ bool issue_tile(PairSmem &sm, uint32_t d, uint32_t id
     constexpr uint64_t step_a = kAMN ? (16 * 128) >> 4 : 32 >> 4;
     constexpr uint64_t step_b = kBMN ? (16 * 128) >> 4 : 32 >> 4;
     bool ready = false;
-    for (int k = 0; k < steps; ++k) {
+    for (int k = begin; k < end; ++k) {
         if (!ready && !mbar_wait_warp(&sm.full[s], parity, abort)) return false;
         const uint32_t here = s;
         if (++s == stages) s = 0, parity ^= 1;
@@ -491,7 +507,7 @@ __device__ __forceinline__ bool issue_tile(PairSmem &sm, uint32_t d, uint32_t id
         if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kStepK / 16; ++kk)
-                mma_pair(d, ad + kk * step_a, bd + kk * step_b, idesc, k != 0 || kk != 0);
+                mma_pair(d, ad + kk * step_a, bd + kk * step_b, idesc, k != begin || kk != 0);
             mma_commit_pair(&sm.empty[here]);
         }
         __syncwarp();
@@ -504,7 +520,26 @@ __device__ __forceinline__ bool issue_tile(PairSmem &sm, uint32_t d, uint32_t id
 // steps stay in shared memory.
 enum PairRows { kManyRows, kFewRows, kRowsStay };
 
-template <int kMode, PairRows kRows>
+// K steps of a tile that the tensor cores add up by themselves, in kLse; the
+// epilogue adds such parts up, rounding to nearest.  The tensor cores cut off
+// what an addition of 16 products leaves below the last place of its largest,
+// always toward zero, and the error grows with the additions: one row's loss is
+// off by 8.6e-7 of it at 2048 dims and by 14e-7 at 4096 in one sum, by 2.7e-7
+// and 2.5e-7 in parts of 512 dims (1.6e-7 and 1.9e-7 by FMA throughout).  With
+// few rows the parts cost little (15 x 2048 x 98592: 69.0 -> 71.0 us in a
+// graph).  With many rows, whose errors differ, 1000 losses at 4096 dims are off
+// by 6.1e-7 in one sum, no more than by FMA (6.4e-7), and the parts' 128 sums a
+// thread keep the kernels before and after this one from the SM: 333 x 2048 x
+// 32771 takes 39.0 us in parts of 1024 dims, 35.3 in one.
+template <PairRows kRows> constexpr int kPartSteps = kRows == kManyRows ? 64 : 8;
+
+// Parts that a tile's K steps are summed in, each in an accumulator of its own.
+template <PairRows kRows, bool kParts> __device__ __forceinline__ int parts_of_sum(int steps)
+{
+    return kParts ? ceil_div(steps, kPartSteps<kRows>) : 1;
+}
+
+template <int kMode, PairRows kRows, bool kParts>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                         const __grid_constant__ CUtensorMap map_wa, const __grid_constant__ CUtensorMap map_wb,
@@ -621,27 +656,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // ---- MMA issuer (the leading CTA's)
         if (rank == 0) {
             const uint32_t cols = (uint32_t)half_cols * 2;
-            uint32_t s = 0, parity = 0, tile = 0;
-            for (int64_t u = pair; u < units; u += pairs, ++tile) {
+            uint32_t s = 0, parity = 0, sum = 0;
+            bool ok = true;
+            for (int64_t u = pair; u < units && ok; u += pairs) {
                 const Unit t = shape.at(u);
-                const uint32_t buf = tile & 1, use = tile >> 1;
-                if (use > 0 && !mbar_wait_warp(&sm.acc_empty[buf], (use - 1) & 1, abort)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + buf * kTileCols;
-                const int steps = t.k1 - t.k0;
-                bool ok;
-                if (kMode == kLse || kMode == kProb)
-                    ok = issue_tile<false, false>(sm, d, instruction_desc(false, false, cols), steps, s, parity, stages,
-                                                  ring_a, share_a, stays, ring_b, share_b, abort);
-                else if (!shape.of_weight(u))
-                    ok = issue_tile<false, true>(sm, d, instruction_desc(false, true, cols), steps, s, parity, stages,
-                                                 ring_a, share_a, false, ring_b, share_b, abort);
-                else
-                    ok = issue_tile<true, true>(sm, d, instruction_desc(true, true, cols), steps, s, parity, stages,
-                                                ring_a, share_a, false, ring_b, share_b, abort);
-                if (!ok) break;
-                if (elect_one()) mma_commit_pair(&sm.acc_full[buf]);
-                __syncwarp();
+                const int steps = t.k1 - t.k0, parts = parts_of_sum<kRows, kParts>(steps);
+                for (int part = 0; part < parts && ok; ++part, ++sum) {
+                    const uint32_t buf = sum & 1, use = sum >> 1;
+                    ok = use == 0 || mbar_wait_warp(&sm.acc_empty[buf], (use - 1) & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + buf * kTileCols;
+                    const int begin = kParts ? part * kPartSteps<kRows> : 0;
+                    const int end = kParts ? min(steps, begin + kPartSteps<kRows>) : steps;
+                    if (kMode == kLse || kMode == kProb)
+                        ok = issue_tile<false, false>(sm, d, instruction_desc(false, false, cols), begin, end, s, parity,
+                                                      stages, ring_a, share_a, stays, ring_b, share_b, abort);
+                    else if (!shape.of_weight(u))
+                        ok = issue_tile<false, true>(sm, d, instruction_desc(false, true, cols), begin, end, s, parity,
+                                                     stages, ring_a, share_a, false, ring_b, share_b, abort);
+                    else
+                        ok = issue_tile<true, true>(sm, d, instruction_desc(true, true, cols), begin, end, s, parity,
+                                                    stages, ring_a, share_a, false, ring_b, share_b, abort);
+                    if (!ok) break;
+                    if (elect_one()) mma_commit_pair(&sm.acc_full[buf]);
+                    __syncwarp();
+                }
             }
             // every product is done before the TMEM is freed
             if (elect_one())
@@ -671,7 +711,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             __syncwarp();
             ++sent;
         };
-        uint32_t tile = 0;
+        uint32_t done = 0; // accumulators taken
         // kLse: reference exponent (base 2), its logit, sum of exp2; with few
         // rows over all of the pair's tiles
         float ref = 0.0f, top = -INFINITY, sum = 0.0f;
@@ -716,22 +756,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             ahead = shape.at(pair);
             facts_ahead = facts_of(row_of(ahead.m));
         }
-        for (int64_t u = pair; u < units; u += pairs, ++tile) {
+        // The next accumulator, once it is whole, and its return.
+        const auto next_sum = [&]() {
+            const bool ready = mbar_wait(&sm.acc_full[done & 1], (done >> 1) & 1, abort);
+            if (!__all_sync(0xFFFFFFFFu, ready)) return false;
+            tc_fence_after();
+            return true;
+        };
+        const auto give_back = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(done & 1 ? acc_empty1 : acc_empty0);
+            ++done;
+        };
+        for (int64_t u = pair; u < units; u += pairs) {
             t = ahead;
             facts = facts_ahead;
-            const uint32_t buf = tile & 1, use = tile >> 1;
             const int row = row_of(t.m); // M index of this thread
             if (u + pairs < units) {
                 ahead = shape.at(u + pairs);
                 if (ahead.m != t.m) facts_ahead = facts_of(row_of(ahead.m));
             }
-            const bool ready = mbar_wait(&sm.acc_full[buf], use & 1, abort);
-            if (!__all_sync(0xFFFFFFFFu, ready)) break;
-            tc_fence_after();
+            if (!next_sum()) break;
             // the target's column of the piece
             const int at = facts.target >= a.begin && facts.target < a.begin + a.cols ? facts.target - a.begin : -1;
             const float lse2 = facts.lse2, g = kMode == kProb ? facts.grad / a.header->grad_scale : 0.0f;
-            const uint32_t lanes = tmem + buf * kTileCols + ((uint32_t)(32 * q) << 16);
+            const uint32_t lanes = tmem + (done & 1) * kTileCols + ((uint32_t)(32 * q) << 16);
             // columns of the tile that this thread takes
             const int c0 = first_chunk * kChunk, chunks = no_rows ? 0 : last_chunk - first_chunk;
             // gradients: those that hold columns of them
@@ -740,9 +790,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 if (elect_one()) box_read_wait<0>();
                 __syncwarp();
             }
-            if (kMode == kLse) {
+            if constexpr (kMode == kLse) {
                 if (!kFew) ref = 0.0f, top = -INFINITY, sum = 0.0f;
-                walk(lanes + c0, chunks, [&](int c, float (&x)[kChunk]) {
+                const auto take = [&](int c, float (&x)[kChunk]) {
                     const int col = t.n * a.width + c0 + c * kChunk; // of the piece
                     const int left = a.cols - col;
                     if (left < kChunk)
@@ -761,16 +811,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     if (m > top) {
                         // an infinite maximum keeps reference 0: inf and NaN then show in the sum
-                        const float next = fabsf(m) < INFINITY ? m * a.log2e : 0.0f;
+                        const float next = fabsf(m) < INFINITY ? m * kLog2e : 0.0f;
                         sum *= top > -INFINITY ? exp2_fast(ref - next) : 1.0f;
                         ref = next;
                         top = m;
                     }
                     float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) s4[i & 3] += exp2_fast(fmaf(x[i], a.log2e, -ref));
+                    for (int i = 0; i < kChunk; ++i) s4[i & 3] += exp2_fast(fmaf(x[i], kLog2e, -ref));
                     sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                });
+                };
+                if constexpr (!kParts) {
+                    walk(lanes + c0, chunks, take);
+                    give_back();
+                } else {
+                    constexpr int most_chunks = (kFew && !both ? kFewCols : kTileCols) / kChunk / parts;
+                    uint32_t sums[most_chunks][kChunk]; // fp32 bits
+#pragma unroll
+                    for (int c = 0; c < most_chunks; ++c)
+                        if (c < chunks) tmem_load(lanes + c0 + c * kChunk, sums[c]);
+#pragma unroll
+                    for (int c = 0; c < most_chunks; ++c)
+                        if (c < chunks) tmem_wait(sums[c]);
+                    give_back();
+                    bool ok = true;
+                    for (int piece = parts_of_sum<kRows, kParts>(t.k1 - t.k0); piece > 1; --piece) {
+                        ok = next_sum();
+                        if (!ok) break;
+                        const uint32_t from = tmem + (done & 1) * kTileCols + ((uint32_t)(32 * q) << 16) + c0;
+#pragma unroll
+                        for (int c = 0; c < most_chunks; ++c)
+                            if (c < chunks) {
+                                tmem_add16(from + c * kChunk, &sums[c][0]);
+                                tmem_add16(from + c * kChunk + 16, &sums[c][16]);
+                            }
+                        give_back();
+                    }
+                    if (!ok) break;
+                    // rolled: the chunk's body four times over would be more
+                    // code to fetch than the selections are to run
+#pragma unroll 1
+                    for (int c = 0; c < chunks; ++c) {
+                        float x[kChunk];
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i) {
+                            uint32_t bits = sums[0][i];
+#pragma unroll
+                            for (int k = 1; k < most_chunks; ++k) bits = c == k ? sums[k][i] : bits;
+                            x[i] = __uint_as_float(bits);
+                        }
+                        take(c, x);
+                    }
+                }
                 if (row < count && !kFew)
                     a.partial[(size_t)(2 * t.n + h) * a.pad_rows + row] =
                         make_float2(top == -INFINITY ? -INFINITY : ref, sum);
@@ -783,7 +875,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const int left = row < count ? a.cols - col : 0;
                     const int hit = at - col;
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) x[i] = exp2_fast(fmaf(x[i], a.log2e, -lse2));
+                    for (int i = 0; i < kChunk; ++i) x[i] = exp2_fast(fmaf(x[i], kLog2e, -lse2));
                     if (__any_sync(0xFFFFFFFFu, (uint32_t)hit < (uint32_t)kChunk))
 #pragma unroll
                         for (int i = 0; i < kChunk; ++i)
@@ -823,9 +915,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     send_bf16(&map_wout, out, col, a.begin + row - lane, row - lane < a.cols);
                 });
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(buf ? acc_empty1 : acc_empty0);
+            if constexpr (kMode != kLse) give_back();
         }
         if (kMode != kLse) box_wait(); // what this lane sent is written
         if (kMode == kLse && kFew) {
@@ -1130,8 +1220,13 @@ template <int kMode> constexpr bool kHasStay = kMode == kLse || kMode == kProb;
 
 template <int kMode, PairRows kRows> cudaError_t allow_smem_of()
 {
-    return cudaFuncSetAttribute(pair_product_kernel<kMode, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)kPairSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(pair_product_kernel<kMode, kRows, false>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmemBytes);
+    if constexpr (kMode == kLse)
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(pair_product_kernel<kMode, kRows, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)kPairSmemBytes);
+    return e;
 }
 
 template <int kMode> cudaError_t allow_smem()
@@ -1174,7 +1269,7 @@ int loss_setup(int *pairs, int *sm_count)
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             int n = 0;
-            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, pair_product_kernel<kLse, kManyRows>, &cfg);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, pair_product_kernel<kLse, kManyRows, true>, &cfg);
             if (e != cudaSuccess) return tf_topk_internal_fail_cuda((int)e);
             d.pairs = n < 1 ? 1 : n;
             if (!g_loss_encode) {
@@ -1256,6 +1351,13 @@ bool set_ring(PairArgs &a, int mode, int64_t rows)
     return true;
 }
 
+template <int kMode, PairRows kRows> auto product_kernel(int dim)
+{
+    if constexpr (kMode == kLse)
+        if (dim > kPartSteps<kRows> * kStepK) return pair_product_kernel<kMode, kRows, true>;
+    return pair_product_kernel<kMode, kRows, false>;
+}
+
 template <int kMode>
 cudaError_t launch_product(const PairMaps &m, PairArgs &a, int64_t most_units, int pairs, cudaStream_t stream)
 {
@@ -1263,11 +1365,11 @@ cudaError_t launch_product(const PairMaps &m, PairArgs &a, int64_t most_units, i
     cudaLaunchAttribute attr[1];
     const int64_t n = most_units < pairs ? most_units : pairs;
     const cudaLaunchConfig_t cfg = config((int)(2 * n), kPairThreads, kMode == kLse ? kLseSmemBytes : kPairSmemBytes, stream, attr);
-    auto kernel = pair_product_kernel<kMode, kManyRows>;
+    auto kernel = product_kernel<kMode, kManyRows>(a.dim);
     if constexpr (kHasFew<kMode>)
-        if (few) kernel = pair_product_kernel<kMode, kFewRows>;
+        if (few) kernel = product_kernel<kMode, kFewRows>(a.dim);
     if constexpr (kHasStay<kMode>)
-        if (few && a.slots) kernel = pair_product_kernel<kMode, kRowsStay>;
+        if (few && a.slots) kernel = product_kernel<kMode, kRowsStay>(a.dim);
     return cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.wa, m.wb, m.out, m.wout, a);
 }
 
@@ -1292,13 +1394,15 @@ struct Carver {
 // fewest bytes through shared memory, a narrower one may fill the last round
 // of the pairs better.  A round costs about its width plus 32 columns.  Of
 // packed rows the host does not know how many count: all of them and half are
-// weighed alike.
+// weighed alike.  With few rows a thread of the epilogue then has fewer sums in
+// its registers (15 x 2048 x 98592: 76.6 us with up to 256 columns, 75.2 with
+// 192).
 int tile_width(int64_t rows, int64_t vocab, int pairs)
 {
     const int64_t m = pad_rows_of(rows) / kTileRows;
     int best = kTileCols;
     int64_t least = INT64_MAX;
-    for (int w = kTileCols; w >= 64; w -= 64) {
+    for (int w = rows <= kHalf ? kFewCols : kTileCols; w >= 64; w -= 64) {
         const int64_t tiles = (vocab + w - 1) / w;
         const int64_t rounds = (m * tiles + pairs - 1) / pairs + ((m + 1) / 2 * tiles + pairs - 1) / pairs;
         const int64_t cost = rounds * (w + 32);
@@ -1443,12 +1547,6 @@ bool bad_stride(int64_t stride, int64_t dim, int64_t n)
     return stride < dim || stride % 8 != 0 || stride >= (1ll << 39) || (n > 0 && stride > INT64_MAX / 4 / n);
 }
 
-// log2(e) for a logit of the tensor cores.  They truncate their running sums,
-// one addition per 16 products, and the logit comes out too small: measured by
-// 1.0e-9 of itself per product (0.7e-6, 2.0e-6 and 4.1e-6 in the log-sum at dim
-// 512, 2048 and 4096, where the spread between rows is 0.6e-6).
-float logit_scale(int32_t dim) { return (float)(1.4426950408889634 * (1.0 + 1.0e-9 * dim)); }
-
 // Finds and packs the rows that count (`lse`, `grad` null for the loss alone).
 template <typename Space>
 cudaError_t pack_rows(const Space &s, const void *hidden, int64_t stride, int64_t rows, int32_t dim, int64_t vocab,
@@ -1497,7 +1595,6 @@ int loss_of_rows(const void *hidden, int64_t hidden_stride, const void *weight, 
         e = pack_rows(s, hidden, hidden_stride, rows, dim, vocab, target, target_bytes, ignore, nullptr, nullptr, pairs, 1,
                       sms, strm);
     PairArgs a = {};
-    a.log2e = logit_scale(dim);
     a.header = s.header;
     a.facts = s.facts;
     a.target = target;
@@ -1606,7 +1703,6 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
     cudaError_t e = pack_rows(s, hidden, hidden_stride, rows, dim, vocab, target, target_bytes, ignore, lse, grad_loss,
                               pairs, splits, sms, strm);
     PairArgs a = {};
-    a.log2e = logit_scale(dim);
     a.header = s.header;
     a.facts = s.facts;
     a.target = target;
