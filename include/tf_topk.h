@@ -411,7 +411,9 @@ size_t tf_topk_head_loss_bf16_workspace(int64_t rows, int32_t dim, int64_t vocab
  * for the rows that count (target neither ignore_index nor out of range):
  *   grad_hidden = G weight,   grad_weight = G^T hidden   (fp32 sums, rounded to bf16).
  * The logits are computed again, in pieces of the vocabulary; G of a piece is
- * held in the workspace, rounded to bf16 relative to the largest |g|.  Rows
+ * held in the workspace, rounded to bf16 relative to the largest |g|.  The
+ * target's entry is g expm1(x - lse) with the x that lse was made with, so that a
+ * sure row keeps its gradient down to the last place of its lse.  Rows
  * that do not count get zeros in grad_hidden, and whatever their hidden
  * states hold (NaN too) reaches nothing.
  *

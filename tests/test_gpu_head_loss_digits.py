@@ -77,3 +77,37 @@ def test_a_leading_dim(rows, dim, lead):
     # the target's logit: 32 lanes' sums by FMA and their butterfly
     allow += (dim / 32 + 5) * U * size
     assert (np.abs(_np(loss) - ref_loss) <= allow).all(), (np.abs(_np(loss) - ref_loss).max(), allow.min())
+
+
+@pytest.mark.parametrize("rows", [1, 300, 5000])
+@pytest.mark.parametrize("gap", [8.0, 11.0, 14.0])
+def test_gradient_of_a_sure_row(rows, gap):
+    """The target's entry of G = g (p - 1) where p is nearly 1: 64 columns at a logit of 0 and the target's, a sum of
+    4096 positive products, at `gap`.  p - 1 = expm1(x_t - lse), with lse rounded (half of its unit, 2^-21) and from
+    the same x_t; x_t by FMA, 133 roundings at most of u of itself, moves 1 - p by as much of it; the 64 exponentials
+    and their sum by 1e-5 of it; G and the gradient are each rounded to bf16 (2^-8).  One row alone has a gradient,
+    so that d_weight[target] = G h and d_hidden = G weight[target]."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    dim, vocab = 4096, 65
+    g = torch.Generator().manual_seed(int(gap))
+    hidden = (torch.rand(rows, dim, generator=g) + 0.5).bfloat16()
+    weight = torch.zeros(vocab, dim)
+    at = rows // 2
+    shape = torch.rand(dim, generator=g) + 0.5
+    weight[7] = shape * gap / (shape @ hidden[at].float())
+    weight = weight.bfloat16()
+    target = torch.full((rows,), 7)
+    grad = torch.zeros(rows)
+    grad[at] = 0.25
+    args = hidden.cuda(), weight.cuda(), target.cuda()
+    loss, lse = topk.head_loss_bf16(*args)
+    dh, dw = topk.head_loss_grad_bf16(*args, lse, grad.cuda())
+    x = float(_np(hidden)[at] @ _np(weight)[7])
+    others = 64 * np.exp(-x)
+    entry = -0.25 * others / (1 + others)  # p - 1
+    allow = 0.25 * 2.0 ** -21 + abs(entry) * (133 * U * x + 1e-5)
+    for got, by in ((_np(dw)[7], _np(hidden)[at]), (_np(dh)[at], _np(weight)[7])):
+        off = np.abs(got - entry * by)
+        assert (off <= (allow + 2 * 2.0 ** -8 * (abs(entry) + allow)) * np.abs(by)).all(), (off / np.abs(by)).max() / abs(entry)

@@ -9,7 +9,8 @@
 // and, for a gradient g[n] of loss[n]:
 //   G[n][v]  = g[n] * (exp(x[n][v] - lse[n]) - [v == target[n]])
 //   d_hidden = G weight,   d_weight = G^T hidden.
-// Rows whose target is ignored take no part.
+// Rows whose target is ignored take no part.  The target's entry of G is
+// g expm1(x_t - lse), from the logit that lse was made with (below).
 //
 // One kernel shape serves the four products: pair_product_kernel, persistent,
 // a pair of CTAs (cluster of two, tcgen05.mma cta_group::2) per tile of 256
@@ -40,7 +41,9 @@
 // kLse keeps short (kPartSteps), but in loss it would be the target's alone, so
 // the target's logit is summed by FMA in head_loss_rows_kernel and
 //   loss = log(1 + exp(rest - x_t)),  rest = log sum over v != t of exp(x_v),
-// which also keeps the digits of a loss near 0.
+// which also keeps the digits of a loss near 0.  For the same reason p_t - 1 is
+// not taken from the product's x_t, which is some 1e-5 away from the one in lse:
+// of a row that is sure to 1e-4 nothing would be left.
 //
 // No wait is unbounded: every mbarrier wait gives up after kWaitLimit polls,
 // records a fault code, and the CTA winds down.
@@ -107,7 +110,7 @@ struct __align__(16) RowFacts {
     int32_t target;
     float lse2; // lse in powers of two
     float grad;
-    float unused;
+    float less_one; // of the target: p - 1
 };
 
 struct PairArgs {
@@ -879,7 +882,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     if (__any_sync(0xFFFFFFFFu, (uint32_t)hit < (uint32_t)kChunk))
 #pragma unroll
                         for (int i = 0; i < kChunk; ++i)
-                            if (i == hit) x[i] -= 1.0f;
+                            if (i == hit) x[i] = facts.less_one;
                     if (__any_sync(0xFFFFFFFFu, left < kChunk))
 #pragma unroll
                         for (int i = 0; i < kChunk; ++i) x[i] = i < left ? x[i] : 0.0f;
@@ -953,6 +956,45 @@ __device__ __forceinline__ void pack_row(__nv_bfloat16 *to, const __nv_bfloat16 
     for (int i = thread; i < dim / 8; i += threads) dst[i] = src ? src[i] : make_uint4(0, 0, 0, 0);
 }
 
+// A row's logit of one column by FMA: 32 lanes' sums and their butterfly, the
+// same in lse and in the target's p - 1.  By a whole warp, the answer in every
+// lane; without the two rows 0.
+__device__ __forceinline__ float column_logit(const __nv_bfloat16 *hidden, const __nv_bfloat16 *weight, int dim, int lane)
+{
+    float dot = 0.0f;
+    if (hidden) {
+        const uint4 *hv = reinterpret_cast<const uint4 *>(hidden), *wv = reinterpret_cast<const uint4 *>(weight);
+#pragma unroll 4
+        for (int i = lane; i < dim / 8; i += 32) {
+            const uint4 p = hv[i], w = wv[i];
+            const uint32_t pa[4] = {p.x, p.y, p.z, p.w}, wa[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                dot = fmaf(__uint_as_float(pa[k] << 16), __uint_as_float(wa[k] << 16), dot);
+                dot = fmaf(__uint_as_float(pa[k] & 0xFFFF0000u), __uint_as_float(wa[k] & 0xFFFF0000u), dot);
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
+    return dot;
+}
+
+// p - 1 of the packed rows' targets: a warp per row, neighbours in different
+// CTAs.
+__device__ __forceinline__ void targets_less_one(const int32_t *order, int count, const void *target, int target64,
+                                                 const float *lse, const __nv_bfloat16 *hidden, int64_t stride,
+                                                 const __nv_bfloat16 *weight, int64_t weight_stride, int dim, RowFacts *facts)
+{
+    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    for (int j = (int)(threadIdx.x / 32 * gridDim.x + blockIdx.x); j < count; j += (int)gridDim.x * warps) {
+        const int r = order[j];
+        const float x = column_logit(hidden + (size_t)r * stride,
+                                     weight + (size_t)target_of(target, target64, r) * weight_stride, dim, lane);
+        if (lane == 0) facts[j].less_one = expm1f(x - lse[r]);
+    }
+}
+
 // The rows that count, in their order (order[j] the row at place j and its
 // facts, place[r] the row's place or -1), and the largest finite |g|, by
 // which every g is divided before G is rounded to bf16: with one g for all
@@ -966,7 +1008,8 @@ __global__ void __launch_bounds__(kPrepareThreads)
     head_loss_prepare_kernel(const void *target, int target64, int64_t ignore, const float *lse, const float *grad,
                              int rows, int vocab, int dim, int pairs, int most_splits, RowHeader *header,
                              int32_t *order, int32_t *place, RowFacts *facts, const __nv_bfloat16 *hidden,
-                             int64_t stride, int pitch, __nv_bfloat16 *packed)
+                             int64_t stride, const __nv_bfloat16 *weight, int64_t weight_stride, int pitch,
+                             __nv_bfloat16 *packed)
 {
     __shared__ int32_t own_order[kCopy ? kPackRows : 1];
     __shared__ int warp_sum[32];
@@ -1006,7 +1049,9 @@ __global__ void __launch_bounds__(kPrepareThreads)
             place[r] = counts ? at : -1;
             if (counts) {
                 if (!kCopy) order[at] = r;
-                facts[at] = fact;
+                facts[at].target = fact.target; // (less_one: targets_less_one)
+                facts[at].lse2 = fact.lse2;
+                facts[at].grad = fact.grad;
             }
         }
         base += total;
@@ -1028,6 +1073,8 @@ __global__ void __launch_bounds__(kPrepareThreads)
         }
     }
     if (kCopy) { // 256 threads a row
+        if (grad)
+            targets_less_one(own_order, base, target, target64, lse, hidden, stride, weight, weight_stride, dim, facts);
         const int end = max(1, ceil_div(base, kTileRows)) * kTileRows, at_once = kPrepareThreads / 256;
         for (int j = blockIdx.x * at_once + tid / 256; j < end; j += gridDim.x * at_once)
             pack_row(packed + (size_t)j * pitch, j < base ? hidden + (size_t)own_order[j] * stride : nullptr, dim, tid & 255,
@@ -1037,13 +1084,17 @@ __global__ void __launch_bounds__(kPrepareThreads)
 }
 
 // The hidden rows that count, packed, with zero rows up to the next whole
-// tile (the products sum over whole K steps of rows).
+// tile (the products sum over whole K steps of rows), and, with `lse`, their
+// targets' p - 1.
 __global__ void __launch_bounds__(256)
     head_loss_gather_kernel(const __nv_bfloat16 *hidden, int64_t stride, int dim, const RowHeader *header,
-                            const int32_t *order, int pitch, __nv_bfloat16 *packed)
+                            const int32_t *order, const void *target, int target64, const float *lse,
+                            const __nv_bfloat16 *weight, int64_t weight_stride, RowFacts *facts, int pitch,
+                            __nv_bfloat16 *packed)
 {
     grid_dependency_wait();
     const int count = header->count;
+    if (lse) targets_less_one(order, count, target, target64, lse, hidden, stride, weight, weight_stride, dim, facts);
     const int end = max(1, ceil_div(count, kTileRows)) * kTileRows;
     for (int j = blockIdx.x; j < end; j += gridDim.x)
         pack_row(packed + (size_t)j * pitch, j < count ? hidden + (size_t)order[j] * stride : nullptr, dim, threadIdx.x,
@@ -1079,23 +1130,9 @@ __global__ void __launch_bounds__(kRowsThreads)
     // only once the kernels before it had ended, so the inputs are there.
     const int r = r0 + warp;
     const int64_t t = warp < kRowsPerCta && r < rows ? target_of(target, target64, r) : ignore;
-    float dot = 0.0f;
-    if (t != ignore && t >= 0 && t < vocab) {
-        const uint4 *hv = reinterpret_cast<const uint4 *>(hidden + (size_t)r * hidden_stride);
-        const uint4 *wv = reinterpret_cast<const uint4 *>(weight + (size_t)t * weight_stride);
-#pragma unroll 4
-        for (int i = lane; i < dim / 8; i += 32) {
-            const uint4 p = hv[i], w = wv[i];
-            const uint32_t pa[4] = {p.x, p.y, p.z, p.w}, wa[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                dot = fmaf(__uint_as_float(pa[k] << 16), __uint_as_float(wa[k] << 16), dot);
-                dot = fmaf(__uint_as_float(pa[k] & 0xFFFF0000u), __uint_as_float(wa[k] & 0xFFFF0000u), dot);
-            }
-        }
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
+    const bool counts = t != ignore && t >= 0 && t < vocab;
+    const float dot = column_logit(counts ? hidden + (size_t)r * hidden_stride : nullptr,
+                                   counts ? weight + (size_t)t * weight_stride : nullptr, dim, lane);
     grid_dependency_wait();
     {
         // thread = (row tid % 4, every 64th part)
@@ -1549,28 +1586,29 @@ bool bad_stride(int64_t stride, int64_t dim, int64_t n)
 
 // Finds and packs the rows that count (`lse`, `grad` null for the loss alone).
 template <typename Space>
-cudaError_t pack_rows(const Space &s, const void *hidden, int64_t stride, int64_t rows, int32_t dim, int64_t vocab,
-                      const void *target, int32_t target_bytes, int64_t ignore, const float *lse, const float *grad,
+cudaError_t pack_rows(const Space &s, const void *hidden, int64_t stride, const void *weight, int64_t weight_stride,
+                      int64_t rows, int32_t dim, int64_t vocab, const void *target, int32_t target_bytes, int64_t ignore, const float *lse, const float *grad,
                       int pairs, int splits, int sms, cudaStream_t stream)
 {
-    const auto *from = static_cast<const __nv_bfloat16 *>(hidden);
+    const auto *from = static_cast<const __nv_bfloat16 *>(hidden), *head = static_cast<const __nv_bfloat16 *>(weight);
     const int pitch = (int)packed_pitch(dim), wide = target_bytes == 8;
     cudaLaunchAttribute attr[1];
     if (rows <= kPackRows) {
         const int64_t ctas = (pad_rows_of(rows) + 3) / 4;
         const cudaLaunchConfig_t cfg = config((int)(ctas < sms ? ctas : sms), kPrepareThreads, 0, stream, attr);
         return cudaLaunchKernelEx(&cfg, head_loss_prepare_kernel<true>, target, wide, ignore, lse, grad, (int)rows,
-                                  (int)vocab, (int)dim, pairs, splits, s.header, s.order, s.place, s.facts, from, stride,
-                                  pitch, s.packed);
+                                  (int)vocab, (int)dim, pairs, splits, s.header, s.order, s.place, s.facts, from, stride, head,
+                                  weight_stride, pitch, s.packed);
     }
     cudaLaunchConfig_t cfg = config(1, kPrepareThreads, 0, stream, attr);
     const cudaError_t e =
         cudaLaunchKernelEx(&cfg, head_loss_prepare_kernel<false>, target, wide, ignore, lse, grad, (int)rows, (int)vocab,
-                           (int)dim, pairs, splits, s.header, s.order, s.place, s.facts, from, stride, pitch, s.packed);
+                           (int)dim, pairs, splits, s.header, s.order, s.place, s.facts, from, stride, head,
+                           weight_stride, pitch, s.packed);
     if (e != cudaSuccess) return e;
     cfg = config((int)(rows < 4 * sms ? rows : 4 * sms), 256, 0, stream, attr);
     return cudaLaunchKernelEx(&cfg, head_loss_gather_kernel, from, stride, (int)dim, (const RowHeader *)s.header,
-                              (const int32_t *)s.order, pitch, s.packed);
+                              (const int32_t *)s.order, target, wide, lse, head, weight_stride, s.facts, pitch, s.packed);
 }
 
 // One block of rows of the loss (checked arguments).
@@ -1592,8 +1630,8 @@ int loss_of_rows(const void *hidden, int64_t hidden_stride, const void *weight, 
     cudaLaunchAttribute attr[1];
     cudaError_t e = cudaSuccess;
     if (packed)
-        e = pack_rows(s, hidden, hidden_stride, rows, dim, vocab, target, target_bytes, ignore, nullptr, nullptr, pairs, 1,
-                      sms, strm);
+        e = pack_rows(s, hidden, hidden_stride, weight, weight_stride, rows, dim, vocab, target, target_bytes, ignore,
+                      nullptr, nullptr, pairs, 1, sms, strm);
     PairArgs a = {};
     a.header = s.header;
     a.facts = s.facts;
@@ -1700,8 +1738,8 @@ int run_grad(const void *hidden, int64_t hidden_stride, const void *weight, int6
     const int64_t steps = ((vocab < piece ? vocab : piece) + kStepK - 1) / kStepK;
     const int splits = (int)(s.splits < steps ? s.splits : steps);
     cudaLaunchAttribute attr[1];
-    cudaError_t e = pack_rows(s, hidden, hidden_stride, rows, dim, vocab, target, target_bytes, ignore, lse, grad_loss,
-                              pairs, splits, sms, strm);
+    cudaError_t e = pack_rows(s, hidden, hidden_stride, weight, weight_stride, rows, dim, vocab, target, target_bytes,
+                              ignore, lse, grad_loss, pairs, splits, sms, strm);
     PairArgs a = {};
     a.header = s.header;
     a.facts = s.facts;
