@@ -111,3 +111,32 @@ def test_gradient_of_a_sure_row(rows, gap):
     for got, by in ((_np(dw)[7], _np(hidden)[at]), (_np(dh)[at], _np(weight)[7])):
         off = np.abs(got - entry * by)
         assert (off <= (allow + 2 * 2.0 ** -8 * (abs(entry) + allow)) * np.abs(by)).all(), (off / np.abs(by)).max() / abs(entry)
+
+
+@pytest.mark.parametrize("rows", [4, 150, 300])
+@pytest.mark.parametrize("dim", [64, 4608])
+@pytest.mark.parametrize("level", [0.0, 100.0, -100.0])
+def test_infinite_columns(rows, dim, level):
+    """A column of -inf logits has no share and an infinite loss of its own; one of +inf has all of it, however large
+    the other logits.  Sums are exact; the exponents' roundings as above."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    inf = float("inf")
+    vocab = 600
+    hidden = torch.zeros(rows, dim, dtype=torch.bfloat16, device="cuda")
+    hidden[:, 0] = 1
+    target = torch.arange(rows, device="cuda") * 5 % vocab
+    own = target == 5
+    for column in (-inf, inf):
+        weight = torch.zeros(vocab, dim, dtype=torch.bfloat16, device="cuda")
+        weight[:, 0] = level
+        weight[5, 0] = column
+        loss, lse = topk.head_loss_bf16(hidden, weight, target)
+        assert own.any()
+        if column == inf:
+            assert (lse == inf).all() and (loss[own] == 0).all() and (loss[~own] == inf).all()
+        else:
+            allow = 4 * 2.0 ** -17 * 0.7 + 2.0 ** -17 + 16 * U
+            assert (lse - level - np.log(599)).abs().max() <= allow
+            assert (loss[own] == inf).all() and (loss[~own] - np.log(599)).abs().max() <= allow

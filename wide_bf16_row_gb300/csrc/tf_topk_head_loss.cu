@@ -813,8 +813,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     for (int i = 4; i < kChunk; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
                     const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     if (m > top) {
-                        // an infinite maximum keeps reference 0: inf and NaN then show in the sum
-                        const float next = fabsf(m) < INFINITY ? m * kLog2e : 0.0f;
+                        // the reference of an infinite maximum is finite, so that inf and NaN show in the
+                        // sum, and above all others, so that no part of the sum outdoes it
+                        const float next = fminf(m * kLog2e, FLT_MAX);
                         sum *= top > -INFINITY ? exp2_fast(ref - next) : 1.0f;
                         ref = next;
                         top = m;
