@@ -140,3 +140,19 @@ def test_infinite_columns(rows, dim, level):
             allow = 4 * 2.0 ** -17 * 0.7 + 2.0 ** -17 + 16 * U
             assert (lse - level - np.log(599)).abs().max() <= allow
             assert (loss[own] == inf).all() and (loss[~own] - np.log(599)).abs().max() <= allow
+
+
+@pytest.mark.parametrize("rows", [4, 150, 300])
+@pytest.mark.parametrize("dim", [64, 4608])
+def test_no_column_has_a_share(rows, dim):
+    """All logits -inf: lse = log 0 = -inf, and the loss -inf + inf has no value."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    inf = float("inf")
+    hidden = torch.zeros(rows, dim, dtype=torch.bfloat16, device="cuda")
+    hidden[:, 0] = 1
+    weight = torch.zeros(600, dim, dtype=torch.bfloat16, device="cuda")
+    weight[:, 0] = -inf
+    loss, lse = topk.head_loss_bf16(hidden, weight, torch.arange(rows, device="cuda"))
+    assert (lse == -inf).all() and torch.isnan(loss).all()

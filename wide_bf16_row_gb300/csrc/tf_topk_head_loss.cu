@@ -1172,7 +1172,7 @@ __global__ void __launch_bounds__(kRowsThreads)
             const float above = rest - dot;
             const float tail = log1pf(expf(-fabsf(above)));
             loss[r] = isnan(above) ? above : fmaxf(above, 0.0f) + tail;
-            lse[r] = isnan(above) ? above : fmaxf(rest, dot) + tail;
+            lse[r] = isnan(above) ? rest + dot : fmaxf(rest, dot) + tail; // (both infinite: that infinity)
         }
     }
     grid_dependents_go();
