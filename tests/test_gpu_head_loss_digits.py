@@ -156,3 +156,50 @@ def test_no_column_has_a_share(rows, dim):
     weight[:, 0] = -inf
     loss, lse = topk.head_loss_bf16(hidden, weight, torch.arange(rows, device="cuda"))
     assert (lse == -inf).all() and torch.isnan(loss).all()
+
+
+def test_the_smallest_workspace_is_taken_and_one_byte_less_refused():
+    """At each place of a workspace the least size that a call takes, found by halving, is within the queried one;
+    a byte less is refused before anything is launched, and the call at that size is right and writes nothing past it."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    g = torch.Generator().manual_seed(1)
+    rows, dim, vocab = 300, 72, 500
+    hidden, weight = torch.randn(rows, dim, generator=g).bfloat16().cuda(), torch.randn(vocab, dim, generator=g).bfloat16().cuda()
+    target = torch.randint(0, vocab, (rows,), generator=g).cuda()
+    grad = torch.ones(rows, device="cuda")
+    want = topk.head_loss_bf16(hidden, weight, target)
+    want_grad = topk.head_loss_grad_bf16(hidden, weight, target, want[1], grad)
+    for start in (0, 16, 240):
+        for loss in (True, False):
+            need = topk.tf_topk_head_loss_bf16_workspace(rows, dim, vocab) if loss else \
+                topk.tf_topk_head_loss_grad_bf16_workspace(rows, dim, vocab, True)
+            block = torch.full((start + need + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+
+            def call(size):
+                space = block[start:start + size]
+                if loss:
+                    return topk.head_loss_bf16(hidden, weight, target, workspace=space)
+                return topk.head_loss_grad_bf16(hidden, weight, target, want[1], grad, workspace=space)
+
+            lo, hi = 8, need
+            call(hi)
+            while lo + 1 < hi:
+                mid = (lo + hi) // 2
+                try:
+                    call(mid)
+                    hi = mid
+                except topk.TopkError as e:
+                    assert e.status == topk.ERR_SCRATCH
+                    lo = mid
+            with pytest.raises(topk.TopkError):
+                call(hi - 1)
+            block.fill_(0xA5)
+            got = call(hi)
+            assert bool((block[start + hi:] == 0xA5).all()) and bool((block[:start] == 0xA5).all())
+            if loss:
+                assert all(torch.equal(a, b) for a, b in zip(got, want))
+            else:
+                assert torch.equal(got[1], want_grad[1])
+                torch.testing.assert_close(got[0], want_grad[0], rtol=2.0 ** -7, atol=2.0 ** -7)
