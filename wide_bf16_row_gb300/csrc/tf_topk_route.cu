@@ -51,10 +51,10 @@ template <int P> constexpr int kRouteCtas = P <= 8 ? 4 : P <= 16 ? 2 : 1; // CTA
 // rounded product, |x| s(1 - s) <= 0.23 bounding the share of the rounded
 // exponent and s(1 - s) <= 1/4 that of exp2's 2 ulp; a sum and a reciprocal
 // of at most 1: under 6 u.  Softmax: the rounded exponent (2 u |x|
-// relative, with |x| exp(-|x|) <= 0.37), a sum of 32 lanes' at most 32 terms
-// (36 u), exp2, a reciprocal, a product: under 50 u; relative to the score,
-// with |x| <= 88 where it is not flushed to 0: under 230 u.  Adding the bias
-// rounds by u of the sum.
+// relative, with |x| exp(-|x|) <= 0.37), a sum (32 lanes of at most 32 terms:
+// 36 u; four lanes of 64 terms in four chains: 19 u), exp2, a reciprocal, a
+// product: under 50 u; relative to the score, with |x| <= 88 where it is not
+// flushed to 0: under 230 u.  Adding the bias rounds by u of the sum.
 constexpr float kSigmoidError = 5e-7f;
 constexpr float kSoftmaxError = 4e-6f;
 constexpr float kSoftmaxPart = 1.4e-5f;
@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
         }
         float top = 0.0f, inverse = 1.0f;
         if (a.softmax && (scored || !a.renorm)) {
-            float m = c[0], sum = 0.0f;
+            float m = c[0], sum[4] = {0.0f, 0.0f, 0.0f, 0.0f}; // in chains: their error is what the margins count on
 #pragma unroll
             for (int i = 1; i < P; ++i) m = fmaxf(m, c[i]);
             top = fmaxf(lanes_max<4>(m), -FLT_MAX);
@@ -924,14 +924,14 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
                     const float q = exp2_fast(kLog2e * (c[i] - top));
-                    sum += q;
+                    sum[i & 3] += q;
                     c[i] = c[i] > -INFINITY ? q : -1.0f; // a score may underflow to 0 and still be chosen
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < P; ++i) sum += exp2_fast(kLog2e * (c[i] - top));
+                for (int i = 0; i < P; ++i) sum[i & 3] += exp2_fast(kLog2e * (c[i] - top));
             }
-            inverse = reciprocal_fast(lanes_sum<4>(sum));
+            inverse = reciprocal_fast(lanes_sum<4>((sum[0] + sum[1]) + (sum[2] + sum[3])));
         }
         float most = 0.0f;
         if (scored) {
