@@ -36,3 +36,26 @@ def test_a_softmax_sum_that_rounds_one_way(tokens, with_bias, experts, step):
     assert torch.equal(idx.cpu(), lead.int().expand(tokens, 4))
     p = np.exp(x[0].double().numpy())
     assert (np.abs(weight.double().cpu().numpy() * p.sum() - 1) <= 50 * U).all()
+
+
+@pytest.mark.parametrize("k", [1, 2, 3, 4, 5, 6])
+def test_a_near_tie_behind_the_next_choice(k):
+    """The k-th choice and the one behind it are small scores with large biases and known to 2 u; the one behind that
+    is a score of nearly 1, known less well, and in truth before both: its softmax sum rounds one way (as above), so
+    that in 32 bits it comes out 13 u too low."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    x = torch.full((1301, 256), float(np.log(0.55 * 2.0 ** -23)))
+    x[:, 0] = 0
+    p = np.exp(x[0].double().numpy())
+    p /= p.sum()
+    bias = torch.full((256,), -10.0)
+    bias[10:10 * k:10] = torch.arange(k, 1, -1).float()
+    bias[10 * k] = 1.0
+    bias[100] = 1.0 - 5 * U
+    bias[0] = 1.0 + p[100] + 1e-8 - p[0]
+    idx, _ = topk.route_experts(x.cuda(), k, bias=bias.cuda())
+    expected, _, _ = oracle_route.route(x[:1].numpy(), k, bias.numpy())
+    assert expected[0, k - 1] == 0
+    assert np.array_equal(idx.cpu().numpy(), np.repeat(expected, 1301, 0))

@@ -1083,9 +1083,14 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
                 }
                 next = __shfl_down_sync(kAll, c0, 1, 4);
             }
-            // Still too close: neighbours up to the k-th and the one behind
-            // it, unless they are one choice twice (same logit, same bias: a
-            // tie, and in order), or a choice left out.
+            const int last = (a.k - 1) / 2; // the k-th choice's lane
+            kth = __shfl_sync(kAll, (a.k & 1) ? c0 : c1, last, 4);
+            kx = __shfl_sync(kAll, (a.k & 1) ? x0 : x1, last, 4);
+            ke = __shfl_sync(kAll, (a.k & 1) ? e0 : e1, last, 4);
+            // Still too close: neighbours up to the k-th, the k-th and any
+            // behind it (whose errors may be larger than its neighbour's),
+            // unless they are one choice twice (same logit, same bias: a tie,
+            // and in order), or a choice left out.
             const auto close = [&](float u, float w, float errors) {
                 return w > -INFINITY && !(u - w > errors + (scored ? kSumError : 0.0f) * (fabsf(u) + fabsf(w)));
             };
@@ -1095,13 +1100,13 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *_
                 const float rn = __shfl_down_sync(kAll, r0, 1, 4);
                 const float xn = __shfl_down_sync(kAll, x0, 1, 4);
                 const int en = __shfl_down_sync(kAll, e0, 1, 4);
-                if (2 * sub < a.k && close(c0, c1, r0 + r1)) again = x0 != x1 || bias[e0] != bias[e1];
-                if (2 * sub + 1 < a.k && sub < 3 && close(c1, next, r1 + rn)) again = again || x1 != xn || bias[e1] != bias[en];
+                const float kb = ke < 0 ? 0.0f : bias[ke], kr = score_error(a.softmax != 0, kth - kb);
+                const int at = 2 * sub;
+                if (at + 1 < a.k && close(c0, c1, r0 + r1)) again = x0 != x1 || bias[e0] != bias[e1];
+                if (at + 2 < a.k && close(c1, next, r1 + rn)) again = again || x1 != xn || bias[e1] != bias[en];
+                if (at >= a.k && close(kth, c0, kr + r0)) again = again || kx != x0 || kb != bias[e0];
+                if (at + 1 >= a.k && close(kth, c1, kr + r1)) again = again || kx != x1 || kb != bias[e1];
             }
-            const int last = (a.k - 1) / 2; // the k-th choice's lane
-            kth = __shfl_sync(kAll, (a.k & 1) ? c0 : c1, last, 4);
-            kx = __shfl_sync(kAll, (a.k & 1) ? x0 : x1, last, 4);
-            ke = __shfl_sync(kAll, (a.k & 1) ? e0 : e1, last, 4);
             if (kth > -INFINITY) least = a.bias && kth < INFINITY ? kth - 3.0f * error - 3.0f * kSumError * fabsf(kth) : kth;
             // anything left out has at most the largest value of its short key
             edge = ke >= 0 && dropped >= kLeast &&
