@@ -59,3 +59,28 @@ def test_a_near_tie_behind_the_next_choice(k):
     expected, _, _ = oracle_route.route(x[:1].numpy(), k, bias.numpy())
     assert expected[0, k - 1] == 0
     assert np.array_equal(idx.cpu().numpy(), np.repeat(expected, 1301, 0))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k", [3, 8, 12])
+def test_a_token_does_not_see_its_neighbours(score, k):
+    """Weights and gradients of a token are the same bits alone, beside tokens without experts and beside tokens whose
+    scores underflow."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    g = torch.Generator().manual_seed(k)
+    tokens, experts = 64, 40
+    x = torch.randn(tokens, experts, generator=g)
+    grad = torch.randn(tokens, k, generator=g)
+    how = {"score": score, "scale": 2.5}
+    idx, weight = topk.route_experts(x.cuda(), k, **how)
+    d = topk.route_experts_grad(x.cuda(), idx, grad.cuda(), **how)
+    for other in (-float("inf"), -120.0):
+        mixed = torch.full((4 * tokens, experts), other)
+        mixed[::4] = x
+        grads = torch.ones(4 * tokens, k)
+        grads[::4] = grad
+        idx2, weight2 = topk.route_experts(mixed.cuda(), k, **how)
+        d2 = topk.route_experts_grad(mixed.cuda(), idx2, grads.cuda(), **how)
+        assert torch.equal(idx2[::4], idx) and torch.equal(weight2[::4], weight) and torch.equal(d2[::4], d)

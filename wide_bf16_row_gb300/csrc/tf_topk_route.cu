@@ -121,22 +121,25 @@ template <int W> __device__ __forceinline__ float lanes_max(float v)
 }
 
 // The chosen scores of a token (a lane each, or `on` false) divided by their
-// sum; where the scores themselves underflow, through their logarithms.  An
-// only one's share is 1, not its product with a reciprocal: the gradient is
-// then 0.
+// sum; where a token's scores themselves underflow, through their logarithms
+// (whatever the warp's other tokens need).  An only one's share is 1, not its
+// product with a reciprocal: the gradient is then 0.
 template <int W> __device__ __forceinline__ float share_of(float s, float x, bool on, bool softmax)
 {
-    float log_s = x;
+    float log_s = x, plain = 0.0f;
+    bool enough = false;
     if (!softmax) {
         const float total = lanes_sum<W>(on ? s : 0.0f);
-        if (__all_sync(kAll, total >= 1e-30f)) return !on ? 0.0f : s == total ? 1.0f : __fdividef(s, total);
+        enough = total >= 1e-30f;
+        plain = !on ? 0.0f : s == total ? 1.0f : __fdividef(s, total);
+        if (__all_sync(kAll, enough)) return plain;
         log_s = fminf(x, 0.0f) - log1pf(expf(-fabsf(x)));
     }
     // softmax: the row's other experts cancel
     const float top = lanes_max<W>(on ? log_s : -INFINITY);
     const float q = on ? __expf(log_s - top) : 0.0f;
     const float total = lanes_sum<W>(q);
-    return !on ? 0.0f : q == total ? 1.0f : __fdividef(q, total);
+    return enough ? plain : !on ? 0.0f : q == total ? 1.0f : __fdividef(q, total);
 }
 
 // A lane's P logits of a row, its experts lane * P ..: -inf past the last
