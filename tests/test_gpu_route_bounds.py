@@ -84,3 +84,28 @@ def test_a_token_does_not_see_its_neighbours(score, k):
         idx2, weight2 = topk.route_experts(mixed.cuda(), k, **how)
         d2 = topk.route_experts_grad(mixed.cuda(), idx2, grads.cuda(), **how)
         assert torch.equal(idx2[::4], idx) and torch.equal(weight2[::4], weight) and torch.equal(d2[::4], d)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_nothing_flows_to_experts_out_of_reach(score, renorm, bad):
+    """A gradient that overflowed stays with the experts that have a part in the weights: logits of -inf and NaN get 0,
+    and the other tokens what they get without it."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(50, 40, generator=g)
+    x[:, 3::5] = -float("inf")
+    x[:, 4::7] = float("nan")
+    how = {"score": score, "renormalize": renorm}
+    idx, _ = topk.route_experts(x.cuda(), 4, **how)
+    grad = torch.randn(50, 4, generator=g).cuda()
+    want = topk.route_experts_grad(x.cuda(), idx, grad, **how)
+    grad[::3, 1] = bad
+    d = topk.route_experts_grad(x.cuda(), idx, grad, **how)
+    assert (d.cpu()[~(x > -float("inf"))] == 0).all()
+    rest = torch.arange(50) % 3 != 0
+    assert torch.equal(d[rest], want[rest])
+    assert not torch.isfinite(d[::3]).all()

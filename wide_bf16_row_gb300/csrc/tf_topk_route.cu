@@ -1341,7 +1341,7 @@ route_softmax_grad_kernel(const T *__restrict__ logits, T *__restrict__ out, Rou
         const float g = on ? a.scale * g_in : 0.0f;
         const float dot = warp_sum(g * own);
 #pragma unroll
-        for (int j = 0; j < P; ++j) s[j] = -dot * (s[j] / total);
+        for (int j = 0; j < P; ++j) s[j] = s[j] > 0.0f ? -dot * (s[j] / total) : 0.0f; // 0 times an infinite dot too
         store_row<T, P>(dst, a.experts, lane, a.vec, s);
         __syncwarp(); // the chosen experts' values replace the row's
         float d = g;
