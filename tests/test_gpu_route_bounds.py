@@ -109,3 +109,28 @@ def test_nothing_flows_to_experts_out_of_reach(score, renorm, bad):
     rest = torch.arange(50) % 3 != 0
     assert torch.equal(d[rest], want[rest])
     assert not torch.isfinite(d[::3]).all()
+
+
+def test_heavy_near_ties_left_out():
+    """More than 32 candidates, eight of them one choice eight times over, and one that in 32 bits falls just below
+    them, at the border of a short key, and in truth lies above: its score times the inverse sum, rounded or not
+    before the bias is added, gives one key or the other."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    tokens = 1301
+    for shift in range(12):
+        x = torch.full((tokens, 256), float(np.log(0.55 * 2.0 ** -23)))
+        x[:, 0] = 0
+        x[:, 1] = float(np.float32(-0.3 - 0.01 * shift)) + torch.arange(-650, 651) * 2.0 ** -25
+        x[:, 200:240] = -40
+        p = np.exp(x[650].double().numpy())
+        p /= p.sum()
+        bias = torch.full((256,), -10.0)
+        bias[200:208] = 0.75
+        bias[208:240] = 0.75 - 2e-6 - 2e-7 * torch.arange(32)
+        bias[1] = 0.75 - p[1]
+        idx, _ = topk.route_experts(x.cuda(), 8, bias=bias.cuda())
+        expected, _, _ = oracle_route.route(x.numpy(), 8, bias.numpy())
+        bad = np.flatnonzero((idx.cpu().numpy() != expected).any(1))
+        assert not len(bad), (shift, bad[:5], idx[int(bad[0])], expected[bad[0]])

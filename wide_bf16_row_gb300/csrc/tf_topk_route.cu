@@ -837,8 +837,10 @@ __device__ __noinline__ bool left_out_matters(const T *row, const RouteArgs &a, 
         if (!in_reach(x) || !((keep >> (a.groups > 1 ? e / per : 0)) & 1u)) continue;
         const float z = fminf(x, FLT_MAX);
         const float b = a.bias ? a.bias[e] : 0.0f;
-        const float s = !scored ? 0.0f : softmax ? exp2_fast(kLog2e * (z - soft.top)) * soft.inverse : sigmoid_fast(z);
-        const float c = scored ? s + b : z + 0.0f;
+        // c to the last bit as the tokens' lanes have it: its key tells whether it was left out
+        const float q = softmax ? exp2_fast(kLog2e * (z - soft.top)) : sigmoid_fast(z);
+        const float s = softmax ? q * soft.inverse : q;
+        const float c = !scored ? z + 0.0f : softmax ? fmaf(q, soft.inverse, b) : q + b;
         if (!(c > -INFINITY) || Key::make_plain(c, e) >= below) continue;
         if (!a.bias) matters = matters || z > kx;
         else if (z != kx || b != kb)
