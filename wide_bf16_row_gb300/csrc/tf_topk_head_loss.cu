@@ -81,7 +81,13 @@ constexpr int kChunk = 32;                           // accumulator columns an e
 constexpr uint32_t kStagingWarp = 32 * kChunk * 4;   // an epilogue warp's outgoing chunk of fp32 (or two of bf16)
 constexpr uint32_t kStagingBytes = kEpiWarps * kStagingWarp;
 constexpr int kGroupRows = 16;                       // row tiles that share the sweep over the columns
-constexpr uint32_t kWaitLimit = 1u << 20;
+// Polls of a wait: a second, for a poll of a barrier that does not complete
+// suspends the warp for 3.9 us (measured).
+#ifndef TF_TOPK_TEST_WAIT_TIMEOUT
+constexpr uint32_t kWaitLimit = 1u << 18;
+#else // test build (below): 16 ms
+constexpr uint32_t kWaitLimit = 1u << 12;
+#endif
 constexpr uint32_t kFaultWait = 1;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -183,10 +189,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
 }
 
 // Bounded wait of the wind-down: goes on whether or not the CTA gave up.
-__device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity)
-{
-    mbar_wait(bar, parity, nullptr);
-}
+__device__ __forceinline__ bool mbar_drain(uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, nullptr); }
 
 // As mbar_wait, by a whole warp: the same answer in every lane.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile uint32_t *abort)
@@ -649,18 +652,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
         }
         // both CTAs' copies land before the pair leaves: the last fill of
-        // each stage (the leader's barrier counts both CTAs' bytes)
-        if (rank == 0)
-            for (uint32_t j = 0; j < stages; ++j) {
-                const uint32_t filled = j < s ? turn + 1 : turn; // times stage j was filled
-                if (filled) mbar_drain(&sm.full[j], (filled - 1) & 1);
-            }
+        // each stage (the leader's barrier counts both CTAs' bytes).  Where one
+        // does not, for a second, the others would not either.
+        bool landed = rank == 0;
+        for (uint32_t j = 0; j < stages && landed; ++j) {
+            const uint32_t filled = j < s ? turn + 1 : turn; // times stage j was filled
+            if (filled) landed = mbar_drain(&sm.full[j], (filled - 1) & 1);
+        }
     } else if (warp == 1) {
         // ---- MMA issuer (the leading CTA's)
         if (rank == 0) {
             const uint32_t cols = (uint32_t)half_cols * 2;
             uint32_t s = 0, parity = 0, sum = 0;
             bool ok = true;
+#ifdef TF_TOPK_TEST_WAIT_TIMEOUT
+            ok = mbar_wait_warp(&sm.drain, 0, abort); // nothing completes it yet: the wait runs out
+#endif
             for (int64_t u = pair; u < units && ok; u += pairs) {
                 const Unit t = shape.at(u);
                 const int steps = t.k1 - t.k0, parts = parts_of_sum<kRows, kParts>(steps);
