@@ -1123,9 +1123,11 @@ __device__ __forceinline__ float2 join(float2 p, float2 q)
 
 // The rows' losses: four rows per CTA.  The target's logit by FMA (while the
 // products still run), the partial sums of a row joined, and both into loss
-// and lse.
+// and lse.  (`partial`, and `sums` of the kernel below, change while the kernel
+// may already run: no __restrict__, which would let their loads be taken for
+// loads of constants and move across the wait.)
 __global__ void __launch_bounds__(kRowsThreads)
-    head_loss_rows_kernel(const float2 *__restrict__ partial, int parts, int pad_rows, const int32_t *place,
+    head_loss_rows_kernel(const float2 *partial, int parts, int pad_rows, const int32_t *place,
                           const __nv_bfloat16 *__restrict__ hidden, int64_t hidden_stride,
                           const __nv_bfloat16 *__restrict__ weight, int64_t weight_stride,
                           int dim, int vocab, const void *target, int target64, int64_t ignore, int rows, float *loss,
@@ -1190,7 +1192,7 @@ __global__ void __launch_bounds__(kRowsThreads)
 // columns have many shares, and several threads add up each column's.
 template <bool kGroups>
 __global__ void __launch_bounds__(256)
-    head_loss_hidden_kernel(const float *__restrict__ sums, int pad_rows, int dim, const RowHeader *header,
+    head_loss_hidden_kernel(const float *sums, int pad_rows, int dim, const RowHeader *header,
                             const int32_t *place, int rows, __nv_bfloat16 *d_hidden)
 {
     __shared__ float4 part[2][kGroups ? 256 : 1];

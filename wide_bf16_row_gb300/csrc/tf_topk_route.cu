@@ -74,6 +74,9 @@ struct RouteArgs {
     int32_t *load;
 };
 
+// The kernel before this one, which may write its inputs, has ended.  (Inputs are
+// not __restrict__: their loads could be taken for loads of constants and move
+// across the wait.)
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependents_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -733,7 +736,7 @@ __device__ __forceinline__ int choose_row(const T *row, const RouteArgs &a, floa
 // special-function ones per sigmoid) and of the k rounds, not by the row's
 // bytes.  For what route_quad_kernel does not take.
 template <typename T, int P>
-__global__ void __launch_bounds__(kRouteThreads, kRouteCtas<P>) route_kernel(const T *__restrict__ logits, RouteArgs a)
+__global__ void __launch_bounds__(kRouteThreads, kRouteCtas<P>) route_kernel(const T *logits, RouteArgs a)
 {
     __shared__ int32_t count[kMaxExperts];
     __shared__ int32_t place[kRouteWarps][32];
@@ -859,7 +862,7 @@ __device__ __noinline__ bool left_out_matters(const T *row, const RouteArgs &a, 
 // steps, valued on the way; or of any size (kQuadGroup, up to 128 experts),
 // valued from a copy of the choices in shared memory.
 template <typename T, int S, QuadMode kMode>
-__global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *__restrict__ logits, RouteArgs a)
+__global__ void __launch_bounds__(kRouteThreads, 2) route_quad_kernel(const T *logits, RouteArgs a)
 {
     constexpr int P = 4 * S;
     constexpr bool kVec = kMode == kQuadVec, kAny = kMode == kQuadGroup;
@@ -1273,7 +1276,7 @@ template <int W> __device__ __forceinline__ bool add_twins(float &d, bool on, in
 // per warp; their rows are cleared, then the chosen experts' values stored.
 template <typename T, int W>
 __global__ void __launch_bounds__(kRouteThreads)
-route_grad_kernel(const T *__restrict__ logits, T *__restrict__ out, RouteGradArgs a)
+route_grad_kernel(const T *logits, T *__restrict__ out, RouteGradArgs a)
 {
     constexpr int kTokens = 32 / W;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, place = lane & (W - 1);
@@ -1316,7 +1319,7 @@ route_grad_kernel(const T *__restrict__ logits, T *__restrict__ out, RouteGradAr
 // gradient.  One warp per token, the row's exponentials in registers.
 template <typename T, int P>
 __global__ void __launch_bounds__(kRouteThreads)
-route_softmax_grad_kernel(const T *__restrict__ logits, T *__restrict__ out, RouteGradArgs a)
+route_softmax_grad_kernel(const T *logits, T *__restrict__ out, RouteGradArgs a)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
