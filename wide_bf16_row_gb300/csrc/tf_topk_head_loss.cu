@@ -397,18 +397,18 @@ __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b -
 // Shares of K that the hidden states' gradient is summed in, `most` at most,
 // so that its tiles come out in nearly whole rounds of the pairs; every share
 // more costs its sums' traffic, taken as a fiftieth of a round.  One warp, a
-// lane per candidate.
+// lane per candidate: kMostSplits at most, so that one tile (up to 256 rows and
+// dims) keeps no more pairs busy.
+constexpr int kMostSplits = 32;
 __device__ __forceinline__ int best_splits(int row_tiles, int dim, int pairs, int most)
 {
     const float per_share = __fdividef((float)row_tiles * (float)ceil_div(dim, kTileCols), (float)pairs); // of a round
     float cost = 3e38f;
     int best = most;
-    for (int s = (threadIdx.x & 31) + 1; s <= most; s += 32) {
-        const float c = __fdividef(ceilf(per_share * (float)s - 1e-3f), (float)s) * (1.0f + 0.02f * (float)s);
-        if (c < cost) {
-            cost = c;
-            best = s;
-        }
+    const int s = (threadIdx.x & 31) + 1;
+    if (s <= most) {
+        cost = __fdividef(ceilf(per_share * (float)s - 1e-3f), (float)s) * (1.0f + 0.02f * (float)s);
+        best = s;
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) {
@@ -1189,7 +1189,8 @@ __global__ void __launch_bounds__(kRowsThreads)
 
 // d_hidden: the shares' sums of a row added up, scaled back and rounded;
 // zeros for the rows that do not count.  kGroups, up to 1024 columns: few
-// columns have many shares, and several threads add up each column's.
+// columns have many shares, and several threads add up each column's
+// (46 x 144 x 164754: 77 -> 74 us).
 template <bool kGroups>
 __global__ void __launch_bounds__(256)
     head_loss_hidden_kernel(const float *sums, int pad_rows, int dim, const RowHeader *header,
@@ -1533,7 +1534,7 @@ int most_splits(int64_t rows, int64_t dim, int pairs)
     const int64_t tiles = pad_rows_of(rows) / kTileRows * ((dim + kTileCols - 1) / kTileCols);
     const int64_t few = (2 * (int64_t)pairs + tiles - 1) / tiles, many = (16 * (int64_t)pairs + tiles - 1) / tiles;
     const int64_t s = few > 4 ? few : many < 4 ? many : 4;
-    return (int)(s > 32 ? 32 : s);
+    return (int)(s > kMostSplits ? kMostSplits : s);
 }
 
 GradSpace grad_space(const void *p, int64_t rows, int64_t dim, int64_t vocab, int pairs, bool hidden, int64_t piece)
