@@ -160,10 +160,12 @@ __device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank)
 }
 
 // Tells a barrier of the cluster that this warp has read its accumulator.
-// Relaxed: what it orders are tensor memory loads, which have completed
-// (tcgen05.wait::ld) and are fenced off (tcgen05.fence).  A release at cluster
-// scope would wait for the warp's stores to global memory as well: 2.5 us per
-// tile (330 x 168 x 105859: 45 us with it, 38 without).
+// Relaxed: what has to come before it are tensor memory loads, and their values
+// are in registers by then (tcgen05.wait::ld), so that no later product can
+// change them.  It rests on that, not on the memory model, in which the
+// tcgen05.fence pair would want a release here.  A release at cluster scope
+// would wait for the warp's stores to global memory as well: 2.5 us per tile
+// (330 x 168 x 105859: 45 us with it, 38 without).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
