@@ -10,6 +10,8 @@ from oracle import route as oracle_route
 pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
+# four lanes per token take over at 40 tokens per SM at the latest
+MANY = 6505
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -18,7 +20,7 @@ def _lib():
     build.build()
 
 
-@pytest.mark.parametrize("tokens", [70, 1301])
+@pytest.mark.parametrize("tokens", [70, 1301, MANY])
 @pytest.mark.parametrize("with_bias", [True, False])
 @pytest.mark.parametrize("experts,step", [(256, 4), (256, 8), (128, 4), (96, 3), (1024, 32)])
 def test_a_softmax_sum_that_rounds_one_way(tokens, with_bias, experts, step):
@@ -46,7 +48,7 @@ def test_a_near_tie_behind_the_next_choice(k):
     import torch
 
     from wide_bf16_row_gb300 import topk
-    x = torch.full((1301, 256), float(np.log(0.55 * 2.0 ** -23)))
+    x = torch.full((MANY, 256), float(np.log(0.55 * 2.0 ** -23)))
     x[:, 0] = 0
     p = np.exp(x[0].double().numpy())
     p /= p.sum()
@@ -58,7 +60,7 @@ def test_a_near_tie_behind_the_next_choice(k):
     idx, _ = topk.route_experts(x.cuda(), k, bias=bias.cuda())
     expected, _, _ = oracle_route.route(x[:1].numpy(), k, bias.numpy())
     assert expected[0, k - 1] == 0
-    assert np.array_equal(idx.cpu().numpy(), np.repeat(expected, 1301, 0))
+    assert np.array_equal(idx.cpu().numpy(), np.repeat(expected, MANY, 0))
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
@@ -118,9 +120,8 @@ def test_heavy_near_ties_left_out():
     import torch
 
     from wide_bf16_row_gb300 import topk
-    tokens = 1301
     for shift in range(12):
-        x = torch.full((tokens, 256), float(np.log(0.55 * 2.0 ** -23)))
+        x = torch.full((1301, 256), float(np.log(0.55 * 2.0 ** -23)))
         x[:, 0] = 0
         x[:, 1] = float(np.float32(-0.3 - 0.01 * shift)) + torch.arange(-650, 651) * 2.0 ** -25
         x[:, 200:240] = -40
@@ -130,7 +131,41 @@ def test_heavy_near_ties_left_out():
         bias[200:208] = 0.75
         bias[208:240] = 0.75 - 2e-6 - 2e-7 * torch.arange(32)
         bias[1] = 0.75 - p[1]
-        idx, _ = topk.route_experts(x.cuda(), 8, bias=bias.cuda())
-        expected, _, _ = oracle_route.route(x.numpy(), 8, bias.numpy())
+        idx, _ = topk.route_experts(x.repeat(5, 1).cuda(), 8, bias=bias.cuda())
+        expected = np.tile(oracle_route.route(x.numpy(), 8, bias.numpy())[0], (5, 1))
         bad = np.flatnonzero((idx.cpu().numpy() != expected).any(1))
         assert not len(bad), (shift, bad[:5], idx[int(bad[0])], expected[bad[0]])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups,kept,k,best,with_bias", [
+    (256, 8, 4, 8, 2, True), (256, 16, 15, 8, 1, False), (240, 5, 2, 1, 2, True), (255, 1, 1, 8, 2, True),
+    (256, 1, 1, 7, 2, False), (128, 8, 3, 7, 2, False), (126, 2, 1, 8, 2, True), (100, 4, 3, 1, 1, True),
+    (91, 7, 6, 6, 2, False), (64, 4, 2, 6, 2, True), (61, 1, 1, 5, 2, True), (32, 2, 1, 3, 1, True),
+    (22, 2, 1, 8, 2, True), (15, 15, 7, 8, 2, False), (4, 2, 1, 8, 2, True), (1, 1, 1, 1, 2, True)])
+def test_many_tokens_in_every_layout(dtype, score, experts, groups, kept, k, best, with_bias):
+    """Enough tokens that four lanes take each, with a bias and groups too: 271 rows -- masked experts, empty rows,
+    coarse ones with ties, equal ones -- 24 times over and one row more, against the 64-bit oracle."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    g = torch.Generator().manual_seed(experts + k)
+    x = 1.5 * torch.randn(271, experts, generator=g)
+    x[torch.rand(271, experts, generator=g) < 0.1] = -float("inf")
+    x[torch.rand(271, experts, generator=g) < 0.02] = float("nan")
+    x[::11] = -float("inf")
+    x[5::7] = (x[5::7] * 2).round() / 2
+    x[6::7] = 0.5
+    x = x.to({"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}[dtype])
+    bias = 0.1 * torch.randn(experts, generator=g) if with_bias else None
+    many = torch.cat([x.repeat(24, 1), x[:1]])
+    load = torch.zeros(experts, dtype=torch.int32, device="cuda")
+    idx, weight = topk.route_experts(many.cuda(), k, bias=None if bias is None else bias.cuda(), score=score, groups=groups,
+                                     groups_kept=kept, group_best=best, scale=1.5, load=load)
+    ref_idx, ref_weight, _ = oracle_route.route(x.float().numpy(), k, None if bias is None else bias.numpy(), score, groups,
+                                                kept, best, True, 1.5)
+    ref_idx, ref_weight = (np.concatenate([np.tile(r, (24, 1)), r[:1]]) for r in (ref_idx, ref_weight))
+    assert np.array_equal(idx.cpu().numpy(), ref_idx)
+    np.testing.assert_allclose(weight.cpu().numpy(), ref_weight, rtol=1e-5, atol=1e-37)
+    assert np.array_equal(load.cpu().numpy(), np.bincount(ref_idx[ref_idx >= 0], minlength=experts))

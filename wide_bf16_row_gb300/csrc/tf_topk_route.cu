@@ -1411,12 +1411,23 @@ template <typename T, QuadMode kMode> RouteKernel<T> quad_kernel_for(int experts
     return nullptr;
 }
 
-// Whether four lanes per token do: enough tokens that eight a warp still
-// reach every SM, and experts, groups and k that fit its layout.
+// Whether four lanes per token do: experts, groups and k that fit their layout,
+// and so many tokens per SM that they beat a warp per token.  Eight warps of
+// eight tokens are a CTA, so that up to 64 tokens per SM some SMs have none; a
+// quad's time hardly grows until then, a warp's does from the first.  Both (us,
+// four lanes / a warp per token, on 152 SMs, in a graph; with a bias a few of the
+// rows are settled in 64 bits, which 3 to 6 us depend on):
+//   tokens                       1216      2432      3648      6080      9728
+//   60 fp16, k 4                 2.9/3.2   2.9/3.8   2.9/4.6   3.0/6.0   3.0/7.4
+//   128 bf16, k 8                4.1/3.9   4.2/5.0   4.2/6.5   4.3/8.0   4.3/10
+//   256 bf16, k 8                6.7/4.8   6.7/6.3   6.8/7.9   6.9/10    7.0/13
+//   128 fp32, bias, k 8          8.7/4.4   8.5/5.4   8.7/6.5   9.1/9.8   9.3/12
+//   256 fp32, bias, 8 groups     8.8/6.1    14/8.2    15/11     15/14     15/17
 bool quads_fit(const RouteArgs &a, int sm_count)
 {
+    const int64_t each = a.bias || a.groups > 1 ? 40 : a.experts > 128 ? 16 : 8;
     return a.experts <= kQuadExperts && a.k <= kQuadK && a.groups <= kQuadGroups &&
-           (a.groups == 1 || a.experts / a.groups % 16 == 0 || a.experts <= 128) && a.tokens >= (int64_t)sm_count * kQuadTokens;
+           (a.groups == 1 || a.experts / a.groups % 16 == 0 || a.experts <= 128) && a.tokens >= sm_count * each;
 }
 
 template <typename T> cudaError_t launch_route(const void *logits, RouteArgs a, int sm_count, void *stream)
