@@ -203,3 +203,30 @@ def test_the_smallest_workspace_is_taken_and_one_byte_less_refused():
             else:
                 assert torch.equal(got[1], want_grad[1])
                 torch.testing.assert_close(got[0], want_grad[0], rtol=2.0 ** -7, atol=2.0 ** -7)
+
+
+@pytest.mark.parametrize("rows", [3, 300])
+@pytest.mark.parametrize("level", [9.5, 13.0, 17.25, 25.0, 40.5, 61.0, -33.0])
+@pytest.mark.parametrize("tied", [2, 3, 90])
+def test_a_loss_has_the_digits_of_its_own_size(rows, level, tied):
+    """All columns at one logit or `tied` at it and the others far below: loss = log of their number, whatever the
+    logit.  An exponent is a multiple of log2 e less its rounded reference, which a fused product takes exactly; the
+    reference's logarithm less the target's logit cancels to a few u of 1; log2 of the sum, its product with ln 2, the
+    exponential and log1p are 2 u each of numbers up to log 700 = 6.6, their sums u."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    vocab = 700
+    hidden = torch.zeros(rows, 64, dtype=torch.bfloat16, device="cuda")
+    hidden[:, 5] = 1
+    weight = torch.zeros(vocab, 64, dtype=torch.bfloat16, device="cuda")
+    weight[:, 5] = level - 64
+    weight[50:50 + tied, 5] = level
+    target = torch.full((rows,), 51, device="cuda")
+    for columns, others in ((tied, np.exp(-64.0) * (vocab - tied)), (vocab, 0.0)):
+        if columns == vocab:
+            weight[:, 5] = level
+        loss, lse = topk.head_loss_bf16(hidden, weight, target)
+        ref = np.log(columns + others)
+        assert np.abs(_np(loss) - ref).max() <= (8 * ref + 8) * U, (np.abs(_np(loss) - ref).max() / U, ref)
+        assert np.abs(_np(lse) - level - ref).max() <= (8 * ref + 8 + 2 * abs(level + ref)) * U

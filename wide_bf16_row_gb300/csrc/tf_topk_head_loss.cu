@@ -91,6 +91,7 @@ constexpr uint32_t kWaitLimit = 1u << 12;
 constexpr uint32_t kFaultWait = 1;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLn2Rest = 7.3e-9f; // 1 / kLog2e (the float) = kLn2 (the float) + this
 
 enum Mode { kLse, kProb, kHidden, kWeight, kGrads };
 
@@ -1178,9 +1179,12 @@ __global__ void __launch_bounds__(kRowsThreads)
         } else {
             float2 all = part[0][warp];
             for (int w = 1; w < kRowsThreads / 32; ++w) all = join(all, part[w][warp]);
-            // a vocabulary of one column leaves no other: rest = -inf
-            const float rest = all.x == -INFINITY && all.y == 0.0f ? -INFINITY : (all.x + log2f(all.y)) * kLn2;
-            const float above = rest - dot;
+            // rest, and rest - dot with what is large cancelled before the logarithm of the sum is added, so
+            // that a loss has the digits of its own size
+            const float more = log2f(all.y) * kLn2;
+            float rest = fmaf(all.x, kLn2, more), above = fmaf(all.x, kLn2Rest, fmaf(all.x, kLn2, -dot)) + more;
+            // a vocabulary of one column leaves no other
+            if (all.x == -INFINITY && all.y == 0.0f) rest = -INFINITY, above = -INFINITY - dot;
             const float tail = log1pf(expf(-fabsf(above)));
             loss[r] = isnan(above) ? above : fmaxf(above, 0.0f) + tail;
             lse[r] = isnan(above) ? rest + dot : fmaxf(rest, dot) + tail; // (both infinite: that infinity)
