@@ -230,3 +230,21 @@ def test_a_loss_has_the_digits_of_its_own_size(rows, level, tied):
         ref = np.log(columns + others)
         assert np.abs(_np(loss) - ref).max() <= (8 * ref + 8) * U, (np.abs(_np(loss) - ref).max() / U, ref)
         assert np.abs(_np(lse) - level - ref).max() <= (8 * ref + 8 + 2 * abs(level + ref)) * U
+
+
+@pytest.mark.parametrize("rows", [3, 300])
+def test_the_target_s_logit_keeps_its_last_digits(rows):
+    """The target's products are 32 and thirty-one quarters of a unit of it, one to a lane of its sum; the two other
+    columns' logits are 32.  Added up in fp32 three of the quarters would be lost, 2.9e-6 of the logit and two thirds
+    of that of the loss; the allowance is that of the test above."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    hidden = torch.zeros(rows, 256, dtype=torch.bfloat16, device="cuda")
+    hidden[:, ::8] = 1
+    weight = torch.zeros(3, 256, dtype=torch.bfloat16, device="cuda")
+    weight[:, 0] = 32
+    weight[1, 8::8] = 2.0 ** -20
+    loss, _ = topk.head_loss_bf16(hidden, weight, torch.ones(rows, dtype=torch.int64, device="cuda"))
+    ref = np.log(1 + 2 * np.exp(-31 * 2.0 ** -20))
+    assert np.abs(_np(loss) - ref).max() <= (8 * ref + 8) * U, np.abs(_np(loss) - ref).max() / U

@@ -91,7 +91,6 @@ constexpr uint32_t kWaitLimit = 1u << 12;
 constexpr uint32_t kFaultWait = 1;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLn2Rest = 7.3e-9f; // 1 / kLog2e (the float) = kLn2 (the float) + this
 
 enum Mode { kLse, kProb, kHidden, kWeight, kGrads };
 
@@ -967,10 +966,10 @@ __device__ __forceinline__ void pack_row(__nv_bfloat16 *to, const __nv_bfloat16 
     for (int i = thread; i < dim / 8; i += threads) dst[i] = src ? src[i] : make_uint4(0, 0, 0, 0);
 }
 
-// A row's logit of one column by FMA: 32 lanes' sums and their butterfly, the
+// A row's logit of one column by FMA, 32 lanes' sums added up in 64 bits, the
 // same in lse and in the target's p - 1.  By a whole warp, the answer in every
 // lane; without the two rows 0.
-__device__ __forceinline__ float column_logit(const __nv_bfloat16 *hidden, const __nv_bfloat16 *weight, int dim, int lane)
+__device__ __forceinline__ double column_logit(const __nv_bfloat16 *hidden, const __nv_bfloat16 *weight, int dim, int lane)
 {
     float dot = 0.0f;
     if (hidden) {
@@ -986,9 +985,10 @@ __device__ __forceinline__ float column_logit(const __nv_bfloat16 *hidden, const
             }
         }
     }
+    double all = dot;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
-    return dot;
+    for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
+    return all;
 }
 
 // p - 1 of the packed rows' targets: a warp per row, neighbours in different
@@ -1000,8 +1000,9 @@ __device__ __forceinline__ void targets_less_one(const int32_t *order, int count
     const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
     for (int j = (int)(threadIdx.x / 32 * gridDim.x + blockIdx.x); j < count; j += (int)gridDim.x * warps) {
         const int r = order[j];
-        const float x = column_logit(hidden + (size_t)r * stride,
-                                     weight + (size_t)target_of(target, target64, r) * weight_stride, dim, lane);
+        const float x =
+            (float)column_logit(hidden + (size_t)r * stride,
+                                weight + (size_t)target_of(target, target64, r) * weight_stride, dim, lane);
         if (lane == 0) facts[j].less_one = expm1f(x - lse[r]);
     }
 }
@@ -1144,8 +1145,8 @@ __global__ void __launch_bounds__(kRowsThreads)
     const int r = r0 + warp;
     const int64_t t = warp < kRowsPerCta && r < rows ? target_of(target, target64, r) : ignore;
     const bool counts = t != ignore && t >= 0 && t < vocab;
-    const float dot = column_logit(counts ? hidden + (size_t)r * hidden_stride : nullptr,
-                                   counts ? weight + (size_t)t * weight_stride : nullptr, dim, lane);
+    const double target_logit = column_logit(counts ? hidden + (size_t)r * hidden_stride : nullptr,
+                                             counts ? weight + (size_t)t * weight_stride : nullptr, dim, lane);
     grid_dependency_wait();
     {
         // thread = (row tid % 4, every 64th part)
@@ -1179,10 +1180,10 @@ __global__ void __launch_bounds__(kRowsThreads)
         } else {
             float2 all = part[0][warp];
             for (int w = 1; w < kRowsThreads / 32; ++w) all = join(all, part[w][warp]);
-            // rest, and rest - dot with what is large cancelled before the logarithm of the sum is added, so
-            // that a loss has the digits of its own size
-            const float more = log2f(all.y) * kLn2;
-            float rest = fmaf(all.x, kLn2, more), above = fmaf(all.x, kLn2Rest, fmaf(all.x, kLn2, -dot)) + more;
+            // rest, and rest - dot with what is large cancelled, in 64 bits, before the logarithm of the sum is
+            // added, so that a loss has the digits of its own size
+            const float dot = (float)target_logit, more = log2f(all.y) * kLn2;
+            float rest = fmaf(all.x, kLn2, more), above = (float)(all.x * (1.0 / (double)kLog2e) - target_logit) + more;
             // a vocabulary of one column leaves no other
             if (all.x == -INFINITY && all.y == 0.0f) rest = -INFINITY, above = -INFINITY - dot;
             const float tail = log1pf(expf(-fabsf(above)));
