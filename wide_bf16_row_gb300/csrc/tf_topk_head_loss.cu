@@ -91,6 +91,7 @@ constexpr uint32_t kWaitLimit = 1u << 12;
 constexpr uint32_t kFaultWait = 1;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLn2Rest = 7.35e-9f; // 1 / kLog2e (the float) less kLn2 (the float)
 
 enum Mode { kLse, kProb, kHidden, kWeight, kGrads };
 
@@ -892,7 +893,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     if (__any_sync(0xFFFFFFFFu, (uint32_t)hit < (uint32_t)kChunk))
 #pragma unroll
                         for (int i = 0; i < kChunk; ++i)
-                            if (i == hit) x[i] = facts.less_one;
+                            x[i] = i == hit ? facts.less_one : x[i]; // (a conditional store costs 24 registers)
                     if (__any_sync(0xFFFFFFFFu, left < kChunk))
 #pragma unroll
                         for (int i = 0; i < kChunk; ++i) x[i] = i < left ? x[i] : 0.0f;
@@ -966,10 +967,11 @@ __device__ __forceinline__ void pack_row(__nv_bfloat16 *to, const __nv_bfloat16 
     for (int i = thread; i < dim / 8; i += threads) dst[i] = src ? src[i] : make_uint4(0, 0, 0, 0);
 }
 
-// A row's logit of one column by FMA, 32 lanes' sums added up in 64 bits, the
-// same in lse and in the target's p - 1.  By a whole warp, the answer in every
-// lane; without the two rows 0.
-__device__ __forceinline__ double column_logit(const __nv_bfloat16 *hidden, const __nv_bfloat16 *weight, int dim, int lane)
+// A row's logit of one column by FMA, the same in lse and in the target's p - 1:
+// 32 lanes' sums, added up with what each addition rounds away (x the sum, y the
+// rest; in 64 bits a loss takes 1.6 us longer).  By a whole warp, the answer in
+// every lane; without the two rows 0.
+__device__ __forceinline__ float2 column_logit(const __nv_bfloat16 *hidden, const __nv_bfloat16 *weight, int dim, int lane)
 {
     float dot = 0.0f;
     if (hidden) {
@@ -985,25 +987,31 @@ __device__ __forceinline__ double column_logit(const __nv_bfloat16 *hidden, cons
             }
         }
     }
-    double all = dot;
+    float rest = 0.0f;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
-    return all;
+    for (int d = 16; d; d >>= 1) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, dot, d), more = __shfl_xor_sync(0xFFFFFFFFu, rest, d);
+        const float sum = dot + other, part = sum - dot;
+        rest += more + ((dot - (sum - part)) + (other - part)); // exact, of a finite sum
+        dot = sum;
+    }
+    return make_float2(dot, fabsf(dot) < INFINITY ? rest : 0.0f);
 }
 
 // p - 1 of the packed rows' targets: a warp per row, neighbours in different
-// CTAs.
+// CTAs, and few rows in those that copy none.
 __device__ __forceinline__ void targets_less_one(const int32_t *order, int count, const void *target, int target64,
                                                  const float *lse, const __nv_bfloat16 *hidden, int64_t stride,
                                                  const __nv_bfloat16 *weight, int64_t weight_stride, int dim, RowFacts *facts)
 {
     const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
-    for (int j = (int)(threadIdx.x / 32 * gridDim.x + blockIdx.x); j < count; j += (int)gridDim.x * warps) {
+    for (int j = (int)(threadIdx.x / 32 * gridDim.x + (gridDim.x - 1 - blockIdx.x)); j < count; j += (int)gridDim.x * warps) {
         const int r = order[j];
-        const float x =
-            (float)column_logit(hidden + (size_t)r * stride,
-                                weight + (size_t)target_of(target, target64, r) * weight_stride, dim, lane);
-        if (lane == 0) facts[j].less_one = expm1f(x - lse[r]);
+        const float l = lse[r];
+        const float x = column_logit(hidden + (size_t)r * stride,
+                                     weight + (size_t)target_of(target, target64, r) * weight_stride, dim, lane)
+                            .x;
+        if (lane == 0) facts[j].less_one = expm1f(x - l);
     }
 }
 
@@ -1014,8 +1022,9 @@ __device__ __forceinline__ void targets_less_one(const int32_t *order, int count
 // bf16's range.  kCopy, up to kPackRows rows: every CTA finds the order for
 // itself and copies its share of the rows, a launch less (2 us of 96 at
 // 333x1032x32771; with more rows the scans would outweigh it and
-// head_loss_gather_kernel copies); the first CTA writes the rest.
-template <bool kCopy>
+// head_loss_gather_kernel copies); the first CTA writes the rest.  kGrad: the
+// gradient's (the loss's has registers few enough to run beside the product).
+template <bool kCopy, bool kGrad>
 __global__ void __launch_bounds__(kPrepareThreads)
     head_loss_prepare_kernel(const void *target, int target64, int64_t ignore, const float *lse, const float *grad,
                              int rows, int vocab, int dim, int pairs, int most_splits, RowHeader *header,
@@ -1036,7 +1045,7 @@ __global__ void __launch_bounds__(kPrepareThreads)
         RowFacts fact = {-1, 0.0f, 0.0f, 0.0f};
         if (r < rows) {
             const int64_t t = target_of(target, target64, r);
-            if (grad) {
+            if (kGrad) {
                 fact.lse2 = lse[r] * kLog2e;
                 fact.grad = grad[r];
             }
@@ -1085,7 +1094,7 @@ __global__ void __launch_bounds__(kPrepareThreads)
         }
     }
     if (kCopy) { // 256 threads a row
-        if (grad)
+        if (kGrad)
             targets_less_one(own_order, base, target, target64, lse, hidden, stride, weight, weight_stride, dim, facts);
         const int end = max(1, ceil_div(base, kTileRows)) * kTileRows, at_once = kPrepareThreads / 256;
         for (int j = blockIdx.x * at_once + tid / 256; j < end; j += gridDim.x * at_once)
@@ -1145,8 +1154,8 @@ __global__ void __launch_bounds__(kRowsThreads)
     const int r = r0 + warp;
     const int64_t t = warp < kRowsPerCta && r < rows ? target_of(target, target64, r) : ignore;
     const bool counts = t != ignore && t >= 0 && t < vocab;
-    const double target_logit = column_logit(counts ? hidden + (size_t)r * hidden_stride : nullptr,
-                                             counts ? weight + (size_t)t * weight_stride : nullptr, dim, lane);
+    const float2 dot = column_logit(counts ? hidden + (size_t)r * hidden_stride : nullptr,
+                                    counts ? weight + (size_t)t * weight_stride : nullptr, dim, lane);
     grid_dependency_wait();
     {
         // thread = (row tid % 4, every 64th part)
@@ -1180,15 +1189,16 @@ __global__ void __launch_bounds__(kRowsThreads)
         } else {
             float2 all = part[0][warp];
             for (int w = 1; w < kRowsThreads / 32; ++w) all = join(all, part[w][warp]);
-            // rest, and rest - dot with what is large cancelled, in 64 bits, before the logarithm of the sum is
-            // added, so that a loss has the digits of its own size
-            const float dot = (float)target_logit, more = log2f(all.y) * kLn2;
-            float rest = fmaf(all.x, kLn2, more), above = (float)(all.x * (1.0 / (double)kLog2e) - target_logit) + more;
+            // rest, and rest - dot with what is large cancelled before the logarithm of the sum is added, so
+            // that a loss has the digits of its own size
+            const float more = log2f(all.y) * kLn2;
+            float rest = fmaf(all.x, kLn2, more);
+            float above = fmaf(all.x, kLn2, -dot.x) + fmaf(all.x, kLn2Rest, -dot.y) + more;
             // a vocabulary of one column leaves no other
-            if (all.x == -INFINITY && all.y == 0.0f) rest = -INFINITY, above = -INFINITY - dot;
+            if (all.x == -INFINITY && all.y == 0.0f) rest = -INFINITY, above = -INFINITY - dot.x;
             const float tail = log1pf(expf(-fabsf(above)));
             loss[r] = isnan(above) ? above : fmaxf(above, 0.0f) + tail;
-            lse[r] = isnan(above) ? rest + dot : fmaxf(rest, dot) + tail; // (both infinite: that infinity)
+            lse[r] = isnan(above) ? rest + dot.x : fmaxf(rest, dot.x) + tail; // (both infinite: that infinity)
         }
     }
     grid_dependents_go();
@@ -1611,20 +1621,18 @@ cudaError_t pack_rows(const Space &s, const void *hidden, int64_t stride, const 
     const auto *from = static_cast<const __nv_bfloat16 *>(hidden), *head = static_cast<const __nv_bfloat16 *>(weight);
     const int pitch = (int)packed_pitch(dim), wide = target_bytes == 8;
     cudaLaunchAttribute attr[1];
-    if (rows <= kPackRows) {
-        const int64_t ctas = (pad_rows_of(rows) + 3) / 4;
+    const auto prepare = [&](auto kernel, int64_t ctas) {
         const cudaLaunchConfig_t cfg = config((int)(ctas < sms ? ctas : sms), kPrepareThreads, 0, stream, attr);
-        return cudaLaunchKernelEx(&cfg, head_loss_prepare_kernel<true>, target, wide, ignore, lse, grad, (int)rows,
-                                  (int)vocab, (int)dim, pairs, splits, s.header, s.order, s.place, s.facts, from, stride, head,
-                                  weight_stride, pitch, s.packed);
-    }
-    cudaLaunchConfig_t cfg = config(1, kPrepareThreads, 0, stream, attr);
+        return cudaLaunchKernelEx(&cfg, kernel, target, wide, ignore, lse, grad, (int)rows, (int)vocab, (int)dim, pairs, splits,
+                                  s.header, s.order, s.place, s.facts, from, stride, head, weight_stride, pitch, s.packed);
+    };
+    if (rows <= kPackRows)
+        return prepare(grad ? head_loss_prepare_kernel<true, true> : head_loss_prepare_kernel<true, false>,
+                       (pad_rows_of(rows) + 3) / 4);
     const cudaError_t e =
-        cudaLaunchKernelEx(&cfg, head_loss_prepare_kernel<false>, target, wide, ignore, lse, grad, (int)rows, (int)vocab,
-                           (int)dim, pairs, splits, s.header, s.order, s.place, s.facts, from, stride, head,
-                           weight_stride, pitch, s.packed);
+        prepare(grad ? head_loss_prepare_kernel<false, true> : head_loss_prepare_kernel<false, false>, 1);
     if (e != cudaSuccess) return e;
-    cfg = config((int)(rows < 4 * sms ? rows : 4 * sms), 256, 0, stream, attr);
+    const cudaLaunchConfig_t cfg = config((int)(rows < 4 * sms ? rows : 4 * sms), 256, 0, stream, attr);
     return cudaLaunchKernelEx(&cfg, head_loss_gather_kernel, from, stride, (int)dim, (const RowHeader *)s.header,
                               (const int32_t *)s.order, target, wide, lse, head, weight_stride, s.facts, pitch, s.packed);
 }
