@@ -169,3 +169,20 @@ def test_many_tokens_in_every_layout(dtype, score, experts, groups, kept, k, bes
     assert np.array_equal(idx.cpu().numpy(), ref_idx)
     np.testing.assert_allclose(weight.cpu().numpy(), ref_weight, rtol=1e-5, atol=1e-37)
     assert np.array_equal(load.cpu().numpy(), np.bincount(ref_idx[ref_idx >= 0], minlength=experts))
+
+
+@pytest.mark.parametrize("tokens", [70, MANY])
+@pytest.mark.parametrize("with_bias", [True, False])
+def test_small_softmax_scores_are_within_their_bound(tokens, with_bias):
+    """Scores down to exp(-86), whose exponents' roundings count: 253 u of the score, which the choice allows for."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    g = torch.Generator().manual_seed(7)
+    x = -86 * torch.rand(tokens, 8, generator=g)
+    x[:, 0] = 0
+    bias = torch.zeros(8, device="cuda") if with_bias else None
+    idx, weight = topk.route_experts(x.cuda(), 8, bias=bias, renormalize=False)
+    p = torch.softmax(x.double(), 1).gather(1, idx.cpu().long())
+    assert ((weight.cpu().double() / p - 1).abs() <= 253 * U).all()
+    assert torch.equal(idx.cpu(), x.sort(dim=1, descending=True, stable=True).indices.int())

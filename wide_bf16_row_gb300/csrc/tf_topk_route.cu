@@ -50,14 +50,15 @@ template <int P> constexpr int kRouteCtas = P <= 8 ? 4 : P <= 16 ? 2 : 1; // CTA
 // Errors of the 32-bit scores, rounded up (u = 2^-24).  Sigmoid: exp2 of a
 // rounded product, |x| s(1 - s) <= 0.23 bounding the share of the rounded
 // exponent and s(1 - s) <= 1/4 that of exp2's 2 ulp; a sum and a reciprocal
-// of at most 1: under 6 u.  Softmax: the rounded exponent (2 u |x|
-// relative, with |x| exp(-|x|) <= 0.37), a sum (32 lanes of at most 32 terms:
-// 36 u; four lanes of 64 terms in four chains: 19 u), exp2, a reciprocal, a
-// product: under 50 u; relative to the score, with |x| <= 88 where it is not
-// flushed to 0: under 230 u.  Adding the bias rounds by u of the sum.
+// of at most 1: under 6 u.  Softmax: the exponent's roundings and that of
+// log2 e (2.3 u |x| relative, with |x| exp(-|x|) <= 0.37), a sum (32 lanes of at
+// most 32 terms: 36 u; four lanes of 64 terms in four chains: 19 u), exp2 in the
+// sum and in the score (4 u each), a reciprocal, a product: under 50 u; relative
+// to the score, with |x| <= 88 where it is not flushed to 0: under 253 u.  Adding
+// the bias rounds by u of the sum.
 constexpr float kSigmoidError = 5e-7f;
 constexpr float kSoftmaxError = 4e-6f;
-constexpr float kSoftmaxPart = 1.4e-5f;
+constexpr float kSoftmaxPart = 1.6e-5f;
 constexpr float kSumError = 1.2e-7f;
 
 static_assert(kMaxRouteK <= 32, "a lane per chosen expert");
