@@ -279,33 +279,23 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // This warp's 32 accumulator lanes (lane = thread), kChunk columns from
-// `taddr`, on their way into `r` until tmem_wait.
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[kChunk])
+// `taddr`.  The wait stands in the same statement: until it is over nothing may
+// touch the registers, not even to move or spill them.
+__device__ __forceinline__ void tmem_take(uint32_t taddr, uint32_t (&r)[kChunk])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
                  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
                    "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
                    "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
                    "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
                    "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
                    "=r"(r[30]), "=r"(r[31])
-                 : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[kChunk])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                   "+r"(r[30]), "+r"(r[31])
-                 :
+                 : "r"(taddr)
                  : "memory");
 }
-
 // Sixteen columns added to what the thread has of them (fp32 bits).
 __device__ __forceinline__ void tmem_add16(uint32_t taddr, uint32_t *to)
 {
@@ -533,8 +523,8 @@ enum PairRows { kManyRows, kFewRows, kRowsStay };
 // epilogue adds such parts up, rounding to nearest.  The tensor cores cut off
 // what an addition of 16 products leaves below the last place of its largest,
 // always toward zero, and the error grows with the additions: one row's loss is
-// off by 8.6e-7 of it at 2048 dims and by 14e-7 at 4096 in one sum, by 2.7e-7
-// and 2.5e-7 in parts of 512 dims (1.6e-7 and 1.9e-7 by FMA throughout).  With
+// off by 8.6e-7 of it at 2048 dims and by 14e-7 at 4096 in one sum, by 2.4e-7
+// and 2.2e-7 in parts of 512 dims (1.6e-7 and 1.9e-7 by FMA throughout).  With
 // few rows the parts cost little (15 x 2048 x 98592: 69.0 -> 71.0 us in a
 // graph).  With many rows, whose errors differ, 1000 losses at 4096 dims are off
 // by 6.1e-7 in one sum, no more than by FMA (6.4e-7), and the parts' 128 sums a
@@ -755,8 +745,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const auto walk = [&](uint32_t taddr, int chunks, auto body) {
             for (int c = 0; c < chunks; ++c) {
                 uint32_t r[kChunk];
-                tmem_load(taddr + c * kChunk, r);
-                tmem_wait(r);
+                tmem_take(taddr + c * kChunk, r);
                 float x[kChunk];
 #pragma unroll
                 for (int i = 0; i < kChunk; ++i) x[i] = __uint_as_float(r[i]);
@@ -843,10 +832,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     uint32_t sums[most_chunks][kChunk]; // fp32 bits
 #pragma unroll
                     for (int c = 0; c < most_chunks; ++c)
-                        if (c < chunks) tmem_load(lanes + c0 + c * kChunk, sums[c]);
-#pragma unroll
-                    for (int c = 0; c < most_chunks; ++c)
-                        if (c < chunks) tmem_wait(sums[c]);
+                        if (c < chunks) tmem_take(lanes + c0 + c * kChunk, sums[c]);
                     give_back();
                     bool ok = true;
                     for (int piece = parts_of_sum<kRows, kParts>(t.k1 - t.k0); piece > 1; --piece) {
@@ -1615,7 +1601,8 @@ bool bad_stride(int64_t stride, int64_t dim, int64_t n)
 // Finds and packs the rows that count (`lse`, `grad` null for the loss alone).
 template <typename Space>
 cudaError_t pack_rows(const Space &s, const void *hidden, int64_t stride, const void *weight, int64_t weight_stride,
-                      int64_t rows, int32_t dim, int64_t vocab, const void *target, int32_t target_bytes, int64_t ignore, const float *lse, const float *grad,
+                      int64_t rows, int32_t dim, int64_t vocab, const void *target, int32_t target_bytes,
+                      int64_t ignore, const float *lse, const float *grad,
                       int pairs, int splits, int sms, cudaStream_t stream)
 {
     const auto *from = static_cast<const __nv_bfloat16 *>(hidden), *head = static_cast<const __nv_bfloat16 *>(weight);
