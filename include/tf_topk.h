@@ -500,6 +500,158 @@ int tf_topk_route_grad(const void *logits, int32_t dtype, int64_t tokens, int32_
                        int32_t k, const int32_t *idx, const float *grad_weight, int32_t score, int32_t renormalize,
                        float scale, void *out_grad_logits, void *stream);
 
+/*
+ * Tokens sorted by expert and back: from tf_topk_route's choices to the
+ * experts' rows, and from the experts' results to the tokens.  With f = t * k +
+ * j for choice j of token t, the choices inside [0, experts) are sorted by
+ * expert, and by f within an expert:
+ *   slot[t][j]  the place of the choice, or -1 if it takes no part;
+ *   source[s]   the f at place s, or -1 behind the last one;
+ *   offsets[e]  the first place of expert e; offsets[experts] is how many take part.
+ * A token may have the same expert twice.
+ *
+ *   idx          device int32 [tokens][k], as tf_topk_route wrote it.
+ *   tokens, k    tokens * k < 2^31; k 1..TF_TOPK_ROUTE_MAX_K.
+ *   experts      1..TF_TOPK_ROUTE_MAX_EXPERTS.
+ *   workspace    device, at least tf_topk_sort_experts_workspace(..) bytes, 4-byte
+ *                aligned (NULL where that is 0); its contents do not matter.
+ *                Calls that overlap on the GPU must not share it.
+ *   out_slot     device int32 [tokens][k]; out_source int32 [tokens * k];
+ *   out_offsets  device int32 [experts + 1] (written with tokens 0 too).
+ * Asynchronous on `stream`; allocates nothing.  Returns a TF_TOPK_* status:
+ * ERR_K, ERR_SHAPE, ERR_NULL, ERR_ALIGN, ERR_SCRATCH, ERR_DEVICE or ERR_CUDA.
+ */
+int tf_topk_sort_experts(const int32_t *idx, int64_t tokens, int32_t k, int32_t experts, void *workspace,
+                         size_t workspace_bytes, int32_t *out_slot, int32_t *out_source, int32_t *out_offsets,
+                         void *stream);
+
+/* Workspace bytes tf_topk_sort_experts needs on the current device; 0 where it
+ * needs none, and for invalid arguments. */
+size_t tf_topk_sort_experts_workspace(int64_t tokens, int32_t k, int32_t experts);
+
+/*
+ * The tokens' rows in the order of tf_topk_sort_experts:
+ *   rows[s] = x[source[s] / k], zeros where source[s] is -1.
+ *   x            device, [tokens] rows of `dim` elements of `dtype`
+ *                (TF_TOPK_DTYPE_*), row_stride elements apart.
+ *   slot, source device, as tf_topk_sort_experts wrote them (places outside
+ *                [0, tokens * k) are passed over).
+ *   out_rows     device, [tokens * k][dim] of `dtype`, packed; must not overlap x.
+ * Pointers aligned to the element size (16-byte rows are the fast ones).  The gradient
+ * for x is tf_topk_combine_tokens of the rows' gradient without weights.
+ * Asynchronous on `stream`; allocates nothing.  Returns a TF_TOPK_* status:
+ * ERR_DTYPE, ERR_K, ERR_SHAPE, ERR_NULL, ERR_ALIGN, ERR_DEVICE or ERR_CUDA.
+ */
+int tf_topk_gather_tokens(const void *x, int32_t dtype, int64_t tokens, int32_t dim, int64_t row_stride, int32_t k,
+                          const int32_t *slot, const int32_t *source, void *out_rows, void *stream);
+
+/*
+ * The tokens' rows in 8 bits, in the order of tf_topk_sort_experts or, with slot
+ * and source NULL and k 1, in their own.  For each block b of TF_TOPK_FP8_BLOCK
+ * elements of a row (the last may be shorter):
+ *   scale[b] = max(largest |x|, 2^-100) * (1 / 448)    (1 / 448 and the product rounded to 32 bits)
+ *   q        = e4m3( x / scale[b] )                    (rounded to 32 bits, then half to even)
+ * so that q * scale stands for x within 2^-4 of its value or 2^-10 scale.  A block
+ * with a NaN or an infinity has a scale of NaN or infinity: its products are NaN.
+ *   dim          a multiple of 16.
+ *   out_q        device, [tokens * k][dim] bytes, 16-byte aligned.
+ *   out_scale    device float [tokens * k][ceil(dim / TF_TOPK_FP8_BLOCK)].
+ * Places behind the last one hold zeros, their scales too.  The rest as tf_topk_gather_tokens.
+ */
+#define TF_TOPK_FP8_BLOCK 128
+int tf_topk_quantize_tokens(const void *x, int32_t dtype, int64_t tokens, int32_t dim, int64_t row_stride, int32_t k,
+                            const int32_t *slot, const int32_t *source, void *out_q, float *out_scale, void *stream);
+
+/*
+ * The experts' rows back to their tokens:
+ *   out[t] = sum over j of weight[t][j] * rows[slot[t][j]]
+ * in the order of j, in 32 bits, rounded once; choices without a place are
+ * left out, whatever their weight.
+ *   rows         device, [tokens * k] rows of `dim` elements of `dtype`, row_stride apart.
+ *   weight       device float [tokens][k], or NULL: all 1.
+ *   out          device, [tokens][dim] of `dtype`, packed; must not overlap rows.
+ * The rest as tf_topk_gather_tokens.
+ */
+int tf_topk_combine_tokens(const void *rows, int32_t dtype, int64_t tokens, int32_t dim, int64_t row_stride, int32_t k,
+                           const int32_t *slot, const float *weight, void *out, void *stream);
+
+/*
+ * Gradient of tf_topk_combine_tokens, with grad_out [tokens][dim] (grad_stride
+ * elements apart) the gradient of its result:
+ *   out_grad_rows[s]      = weight[t][j] * grad_out[t]   (zeros where source[s] is -1)
+ *   out_grad_weight[t][j] = sum over dims of grad_out[t] * rows[slot[t][j]]   (fp32; 0 without a place)
+ * out_grad_rows: device, [tokens * k][dim] of `dtype`, packed; must not overlap the
+ * inputs.  A token's results do not depend on the other tokens.  The rest as
+ * tf_topk_gather_tokens.
+ */
+int tf_topk_combine_tokens_grad(const void *grad_out, int32_t dtype, int64_t tokens, int32_t dim, int64_t grad_stride,
+                                const void *rows, int64_t row_stride, int32_t k, const int32_t *slot,
+                                const int32_t *source, const float *weight, void *out_grad_rows,
+                                float *out_grad_weight, void *stream);
+
+/*
+ * Product of rows in 8 bits with weights in 8 bits (e4m3 both), of one matrix or
+ * of the experts' matrices over their sorted rows.  For row r of group g, column
+ * n and blocks b of TF_TOPK_FP8_BLOCK dims:
+ *   out[r][n] = sum over b of scale[r][b] * weight_scale[g][n / 128][b]
+ *               * sum over the dims d of b of q[r][d] * weight[g][n][d]
+ * A block's sum is the tensor cores' (fp32, truncating), the sum over the blocks is
+ * fp32 FMA.  Rows behind the last group become zeros.
+ *
+ *   q            device, [rows][dim] e4m3, packed, 16-byte aligned (as
+ *                tf_topk_quantize_tokens writes it); scale float [rows][ceil(dim / 128)].
+ *   dim          >= 16, a multiple of 16.
+ *   weight       device, [groups][cols][dim] e4m3, packed, 16-byte aligned;
+ *                weight_scale float [groups][ceil(cols / 128)][ceil(dim / 128)].
+ *   groups       1..TF_TOPK_ROUTE_MAX_EXPERTS; groups * cols < 2^31 - 1024.
+ *   offsets      device int32 [groups + 1], ascending from 0, at most rows: group g has the rows
+ *                [offsets[g], offsets[g + 1]); as tf_topk_sort_experts wrote it.  NULL:
+ *                one group of all rows.
+ *   dtype        TF_TOPK_DTYPE_* of out: device, [rows][cols], packed, aligned to its
+ *                element; must not overlap the inputs.
+ * Asynchronous on `stream`; allocates nothing; the same inputs give the same
+ * bits, and a row's do not depend on the other rows.  Returns a TF_TOPK_* status:
+ * ERR_DTYPE, ERR_SHAPE, ERR_NULL, ERR_ALIGN, ERR_DEVICE or ERR_CUDA.
+ */
+int tf_topk_product_fp8(const void *q, const float *scale, int64_t rows, int32_t dim, const void *weight,
+                        const float *weight_scale, int64_t cols, int32_t groups, const int32_t *offsets,
+                        int32_t dtype, void *out, void *stream);
+
+/*
+ * Logits made ready for tf_topk_select: penalties for a request's tokens so far,
+ * biases, a grammar's mask.  For row r and column c, n being how often c stands
+ * in the answer so far, each step in 32 bits and the result rounded once:
+ *   x = x > 0 ? x / repetition[r] : x * repetition[r]     if c stands in the prompt or the answer
+ *   x = x - frequency[r] * n - presence[r]                if n > 0
+ *   x = x + bias                                          if c has one
+ *   x = -inf                                              if c is not allowed
+ * A column that nothing names keeps its bits.  NaN stays NaN unless it is not allowed.
+ *
+ *   logits       device, [rows] rows of `cols` elements of `dtype` (TF_TOPK_DTYPE_*),
+ *                row_stride elements apart, aligned to the element size.
+ *   tokens       device int32, [rows] rows of `width` tokens, token_stride apart: the
+ *                first prompts[r] (NULL: 0) are row r's prompt, those up to lengths[r]
+ *                (NULL: width) its answer.  Tokens outside [0, cols) are passed over.
+ *                width 0: none.
+ *   repetition, presence, frequency  device float [rows], or NULL: 1, 0, 0.
+ *   bias_token   device int32, [rows] rows of `biases` (0..TF_TOPK_PENALTY_MAX_BIASES)
+ *                columns, bias_stride apart, and bias_value, float, alike; a column
+ *                outside [0, cols) is passed over, and of a column's entries the last counts.
+ *   allowed      device, [rows] rows of ceil(cols / 32) words, allowed_stride apart, bit c
+ *                % 32 of word c / 32 for column c; or NULL: all.
+ *   out          device, rows of `dtype`, out_stride apart; may be logits itself (with
+ *                the same stride), and must not overlap it otherwise.
+ * Asynchronous on `stream`; allocates nothing; the same inputs give the same
+ * bits.  Returns a TF_TOPK_* status: ERR_DTYPE, ERR_SHAPE, ERR_NULL, ERR_ALIGN,
+ * ERR_DEVICE or ERR_CUDA.
+ */
+#define TF_TOPK_PENALTY_MAX_BIASES 65535
+int tf_topk_penalize(const void *logits, int32_t dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                     const int32_t *tokens, int64_t token_stride, int32_t width, const int32_t *lengths,
+                     const int32_t *prompts, const float *repetition, const float *presence, const float *frequency,
+                     const int32_t *bias_token, const float *bias_value, int64_t bias_stride, int32_t biases,
+                     const uint32_t *allowed, int64_t allowed_stride, void *out, int64_t out_stride, void *stream);
+
 /* Human-readable text for a TF_TOPK_* status (static storage). */
 const char *tf_topk_strerror(int status);
 

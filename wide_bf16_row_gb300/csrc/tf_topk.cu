@@ -3137,6 +3137,7 @@ int run_select(const void *logits, int32_t dtype, int64_t rows, int64_t cols, in
 int tf_topk_internal_fail_cuda(int cuda_error) { return fail_cuda(static_cast<cudaError_t>(cuda_error)); }
 uint32_t tf_topk_internal_head_fault_take();
 uint32_t tf_topk_internal_head_loss_fault_take();
+uint32_t tf_topk_internal_product_fault_take();
 
 // The current device's SM count, or the status that bars it (the other
 // translation units' launches).
@@ -3227,6 +3228,8 @@ int tf_topk_device_fault(void)
     if (f == 0) f = fh;
     const uint32_t fl = tf_topk_internal_head_loss_fault_take();
     if (f == 0) f = fl;
+    const uint32_t fp = tf_topk_internal_product_fault_take();
+    if (f == 0) f = fp;
     if (f != 0) {
         const uint32_t zero = 0;
         e = cudaMemcpyToSymbol(g_fault, &zero, sizeof zero);

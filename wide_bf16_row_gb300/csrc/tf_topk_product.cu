@@ -1,0 +1,708 @@
+// Products in 8 bits for GB300 (sm_103a): rows of e4m3 values with a scale for
+// each 128 of a row, times weights of e4m3 values with a scale for each block
+// of 128 x 128; one matrix, or the experts' matrices over their sorted rows.
+//
+// What is computed, for a row r of group g, a column n and blocks b of 128 dims:
+//   y[r][n] = sum_b scale[r][b] * weight_scale[g][n / 128][b]
+//                   * sum_{d in b} q[r][d] * weight[g][n][d]
+// A block's sum is the tensor cores' (fp32, 4 products of 32 steps); the sum
+// over the blocks, with their scales, is fp32 FMA in registers, so that each
+// block's scale is applied exactly where it belongs and the tensor cores'
+// truncating additions reach over 128 dims only.
+//
+// A pair of CTAs (cluster of two, tcgen05.mma cta_group::2, kind::f8f6f4) per
+// tile of 256 rows of one group x 256 or 128 columns; each CTA holds 128 of the
+// rows and loads half of the columns.  Persistent: the tiles of all groups in a
+// row, found in a prefix sum over the groups that each CTA makes from the
+// offsets.  Warp roles, per CTA:
+//   warp 0     TMA producer: per ring stage a block of 128 dims of the CTA's
+//              rows and columns, 128-byte swizzle;
+//   warp 1     TMEM allocation; in the leading CTA the MMA issuer, a block into
+//              one of two accumulators;
+//   warps 2-9  a thread per row and half of the tile's columns: takes each
+//              block's sums from tensor memory, scales and adds them.
+// Bounds: with up to some 250 rows per group the weight's bytes, beyond them the
+// tensor cores, beside which the warps that scale have to keep up: 128 x 256
+// sums per CTA and block, 256 cycles of tensor memory reads and as many of FMA,
+// while the block's products take 512.
+//
+// No wait is unbounded: every mbarrier wait gives up after kWaitLimit polls,
+// records a fault code, and the CTA winds down.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <stdint.h>
+
+#include <atomic>
+#include <mutex>
+
+#include "tf_topk.h"
+
+int tf_topk_internal_fail_cuda(int cuda_error);
+int tf_topk_internal_device(int *sm_count);
+
+namespace {
+
+constexpr int kTileRows = 256;           // rows (M) of a pair's tile
+constexpr int kHalf = 128;               // one CTA's
+constexpr int kBlock = TF_TOPK_FP8_BLOCK; // dims of a scale, and of a ring stage: one 128-byte swizzle row
+constexpr int kMaxWidth = 256;
+constexpr uint32_t kShare = kHalf * kBlock; // 16 KB: one CTA's share of an operand per stage
+constexpr int kStages = 6;
+constexpr uint32_t kRingBytes = kStages * 2 * kShare;
+constexpr int kFewRows = 16; // up to so many rows of a tile are loaded as a box of their own
+constexpr int kMaxGroups = TF_TOPK_ROUTE_MAX_EXPERTS;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kTmemCols = 2 * kMaxWidth;
+constexpr int kChunk = 16;      // accumulator columns a thread takes at a time
+constexpr int kStagingCols = 16; // columns a warp turns round at a time, where its stores need it
+constexpr int kStagingPitch = kStagingCols + 1;
+constexpr int kGroupRows = 16;  // row tiles that share the sweep over the columns
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+// Polls of a wait: a second, for a poll of a barrier that does not complete
+// suspends the warp for 3.9 us.
+#ifndef TF_TOPK_TEST_WAIT_TIMEOUT
+constexpr uint32_t kWaitLimit = 1u << 18;
+#else // test build: 16 ms
+constexpr uint32_t kWaitLimit = 1u << 12;
+#endif
+constexpr uint32_t kFaultWait = 1;
+
+__device__ uint32_t g_product_fault;
+
+struct __align__(16) ProductSmem {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    uint32_t abort;
+    int32_t warp_sum[kThreads / 32];
+    int32_t begin[kMaxGroups + 1]; // a group's first row; [groups] is the end of the last
+    int32_t tiles[kMaxGroups + 1]; // tiles of the groups before
+    float staging[kEpiWarps][32 * kStagingPitch];
+};
+
+struct ProductArgs {
+    const float *scale;        // [rows][blocks]
+    const float *weight_scale; // [groups][column blocks][blocks]
+    const int32_t *offsets;    // null: one group of all rows
+    void *out;
+    int32_t rows, cols, groups, blocks, col_blocks, col_tiles;
+    int32_t wide_stores; // a thread's columns go out in 32-byte stores
+};
+
+// ---------------------------------------------------------------- PTX helpers
+
+__device__ __forceinline__ uint32_t saddr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(bar)), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(bar)), "r"(bytes) : "memory");
+}
+
+// Address of the same shared-memory object in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr(p)), "r"(rank));
+    return r;
+}
+
+// Tells a barrier of the cluster that this warp has read its accumulator.
+// Relaxed: what has to come before it are tensor memory loads, and their values
+// are in registers by then (tcgen05.wait::ld), so that no later product can
+// change them; nothing else is handed over.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// Bounded wait for the phase with this parity; gives up after kWaitLimit
+// polls (recording the fault) or once another warp of this CTA has.
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort)
+{
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(saddr(bar)), "r"(parity)
+                     : "memory");
+        if (ok) return true;
+        if (abort && *abort) return false;
+    }
+    atomicCAS(&g_product_fault, 0u, kFaultWait);
+    if (abort) *abort = 1;
+    return false;
+}
+
+// As mbar_wait, by a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile uint32_t *abort)
+{
+    const bool ok = mbar_wait(bar, parity, abort);
+    return __all_sync(kAll, ok);
+}
+
+// One lane of a converged warp, always the same: the operands of the TMA and
+// MMA instructions it issues come from uniform registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// One box of a tensor map into this CTA's shared memory; its bytes count on
+// the leading CTA's barrier.
+__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int32_t x, int32_t y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(saddr(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+// Shared-memory matrix descriptor of a K-major tile written by TMA with the
+// 128-byte swizzle: start address >> 4, eight rows of 128 bytes 1024 bytes
+// apart (stride byte offset at bit 32), version 1 at bit 46, swizzle mode 2 at
+// bit 61.
+constexpr uint64_t kDescK = (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+
+__device__ __forceinline__ uint64_t desc_at(const void *p) { return kDescK | ((saddr(p) & 0x3FFFFu) >> 4); }
+
+// Instruction descriptor of tcgen05.mma kind::f8f6f4: fp32 accumulator (bit
+// 4), e4m3 A and B (0 at bits 7 and 10), both K-major, N / 8 at bit 17, M / 16
+// at bit 24.
+template <uint32_t n> constexpr uint32_t kInstruction =
+    (1u << 4) | ((n >> 3) << 17) | ((uint32_t)(kTileRows >> 4) << 24);
+
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+                 : "memory");
+}
+
+// Arrive on this barrier in both CTAs of the pair once every tcgen05
+// operation this thread issued before has completed.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     saddr(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// This warp's 32 accumulator lanes (lane = thread), kChunk columns from
+// `taddr`.  The wait stands in the same statement: until it is over nothing may
+// touch the registers, not even to move or spill them.
+__device__ __forceinline__ void tmem_take(uint32_t taddr, uint32_t (&r)[kChunk])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependents_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __half)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ void put(float *to, float x) { *to = x; }
+__device__ __forceinline__ void put(__half *to, float x) { *to = __float2half_rn(x); }
+__device__ __forceinline__ void put(__nv_bfloat16 *to, float x) { *to = __float2bfloat16_rn(x); }
+
+__device__ __forceinline__ void store32(void *to, const uint32_t (&v)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// ---------------------------------------------------------------- the tiles
+
+__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+struct Tile {
+    int group, row, end, col; // first row and the group's end, first column
+};
+
+// The tile with this number, by a whole warp.  The group is the last with no
+// more tiles before it: 32 boundaries at a time, in two steps.
+__device__ __forceinline__ Tile tile_at(const ProductSmem &sm, const ProductArgs &a, int u, int width)
+{
+    const int lane = threadIdx.x & 31;
+    int g = (lane + 1) * 32;
+    const int block = __popc(__ballot_sync(kAll, g <= a.groups && sm.tiles[min(g, a.groups)] <= u));
+    g = block * 32 + lane + 1;
+    const int group = block * 32 + __popc(__ballot_sync(kAll, g <= a.groups && sm.tiles[min(g, a.groups)] <= u));
+    Tile t;
+    t.group = group;
+    t.end = sm.begin[group + 1];
+    const int begin = sm.begin[group], all = ceil_div(t.end - begin, kTileRows);
+    // sweeps of kGroupRows row tiles; in a sweep the row tile moves first, so
+    // that the pairs at work share the weight's tiles
+    int r = u - sm.tiles[group], sweep = 0, m_tiles = all;
+    if (all > kGroupRows) {
+        sweep = r / (kGroupRows * a.col_tiles);
+        r -= sweep * kGroupRows * a.col_tiles;
+        m_tiles = min(kGroupRows, all - sweep * kGroupRows);
+    }
+    const int n = m_tiles > 1 ? r / m_tiles : r;
+    t.row = begin + (sweep * kGroupRows + r - n * m_tiles) * kTileRows;
+    t.col = n * width;
+    return t;
+}
+
+// A thread's row of finished sums.  32-byte stores where rows and columns
+// allow them; otherwise the warp turns 16 columns at a time round in shared
+// memory, so that lanes next to each other write columns next to each other.
+template <typename Out, int kCols>
+__device__ __forceinline__ void put_sums(const ProductArgs &a, const float (&sum)[kCols], float *staging, int row0, int end,
+                                         int col0)
+{
+    const int lane = threadIdx.x & 31;
+    Out *out = static_cast<Out *>(a.out);
+    if (a.wide_stores) {
+        if (row0 + lane >= end) return;
+        Out *to = out + (int64_t)(row0 + lane) * a.cols + col0;
+        constexpr int kEach = 32 / sizeof(Out);
+#pragma unroll
+        for (int c = 0; c < kCols; c += kEach) {
+            if (col0 + c >= a.cols) break; // cols is a multiple of kEach
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if constexpr (sizeof(Out) == 4)
+                    v[i] = __float_as_uint(sum[c + i]);
+                else
+                    v[i] = pack2(sum[c + 2 * i], sum[c + 2 * i + 1], Out());
+            }
+            store32(to + c, v);
+        }
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < kCols; c += kStagingCols) {
+#pragma unroll
+        for (int i = 0; i < kStagingCols; ++i) staging[lane * kStagingPitch + i] = sum[c + i];
+        __syncwarp();
+        const int col = col0 + c + (lane & 15);
+#pragma unroll 4
+        for (int r = lane >> 4; r < 32; r += 2)
+            if (row0 + r < end && col < a.cols)
+                put(out + (int64_t)(row0 + r) * a.cols + col, staging[r * kStagingPitch + (lane & 15)]);
+        __syncwarp();
+    }
+}
+
+template <typename Out, int kWidth>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    product_fp8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_few,
+                       const __grid_constant__ CUtensorMap map_w, const ProductArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    ProductSmem &sm = *reinterpret_cast<ProductSmem *>(ring + kRingBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = blockIdx.x & 1; // in the pair; rank 0 leads
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    constexpr int kShareCols = kWidth / 2; // a CTA loads
+    constexpr uint32_t kStage = 2 * kShare;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sm.acc_full[b], 1);
+            mbar_init(&sm.acc_empty[b], 2 * kEpiWarps);
+        }
+        mbar_init(&sm.drain, 1);
+        sm.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_q) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sm.tmem_base)),
+                     "n"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    grid_dependency_wait(); // the inputs may come from the kernel before on the stream
+    // the groups' first rows and the tiles before each, four groups a thread;
+    // offsets that are out of range or run backwards give empty groups
+    {
+        int first = tid * 4, n[4], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int g = first + i;
+            n[i] = 0;
+            if (g < a.groups) {
+                const int lo = g == 0 ? 0 : min(max(a.offsets[g], 0), a.rows);
+                const int hi = a.offsets ? min(max(a.offsets[g + 1], 0), a.rows) : a.rows;
+                n[i] = hi > lo ? ceil_div(hi - lo, kTileRows) * a.col_tiles : 0;
+                sm.begin[g] = lo;
+                if (g == a.groups - 1) sm.begin[a.groups] = hi;
+            }
+            sum += n[i];
+        }
+        int upto = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(kAll, upto, d);
+            if (lane >= d) upto += o;
+        }
+        if (lane == 31) sm.warp_sum[warp] = upto;
+        tc_fence_before();
+        __syncthreads();
+        int before = upto - sum;
+        for (int w = 0; w < warp; ++w) before += sm.warp_sum[w];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (first + i <= a.groups) sm.tiles[first + i] = before;
+            before += n[i];
+        }
+    }
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    const int units = sm.tiles[a.groups];
+    volatile uint32_t *abort = &sm.abort;
+
+    if (warp == 0) {
+        // ---- TMA producer
+        const uint32_t full0 = peer_addr(&sm.full[0], 0); // the leading CTA's barriers
+        uint32_t s = 0, turn = 0;                         // ring stage, times round the ring
+        bool ok = true;
+        for (int u = pair; u < units && ok; u += pairs) {
+            const Tile t = tile_at(sm, a, u, kWidth);
+            const int left = t.end - t.row;
+            const bool few = left <= kFewRows, both = left > kHalf, has_rows = rank == 0 || both;
+            const uint32_t bytes = (few ? kFewRows * kBlock : both ? 2 * kShare : kShare) + kWidth * kBlock;
+            const int wrow = t.group * a.cols + t.col + (int)rank * kShareCols;
+            for (int b = 0; b < a.blocks; ++b) {
+                ok = *abort == 0 && (turn == 0 || mbar_wait(&sm.empty[s], (turn - 1) & 1, abort));
+                ok = __all_sync(kAll, ok);
+                if (!ok) break;
+                if (elect_one()) {
+                    if (rank == 0) mbar_expect_tx(&sm.full[s], bytes);
+                    const uint32_t bar = full0 + s * (uint32_t)sizeof(uint64_t);
+                    uint8_t *at = ring + s * kStage;
+                    if (has_rows) tma_load(at, few ? &map_few : &map_q, b * kBlock, t.row + (int)rank * kHalf, bar);
+                    tma_load(at + kShare, &map_w, b * kBlock, wrow, bar);
+                }
+                __syncwarp();
+                if (++s == kStages) s = 0, ++turn;
+            }
+        }
+        // both CTAs' copies land before the pair leaves: the last fill of
+        // each stage (the leader's barrier counts both CTAs' bytes)
+        bool landed = rank == 0;
+        for (uint32_t j = 0; j < kStages && landed; ++j) {
+            const uint32_t filled = j < s ? turn + 1 : turn; // times stage j was filled
+            if (filled) landed = mbar_wait(&sm.full[j], (filled - 1) & 1, nullptr);
+        }
+    } else if (warp == 1) {
+        // ---- MMA issuer (the leading CTA's)
+        if (rank == 0) {
+            constexpr uint32_t idesc = kInstruction<kWidth>;
+            uint32_t s = 0, parity = 0, sum = 0;
+            bool ok = true;
+#ifdef TF_TOPK_TEST_WAIT_TIMEOUT
+            ok = mbar_wait_warp(&sm.drain, 0, abort); // nothing completes it yet: the wait runs out
+#endif
+            for (int u = pair; u < units && ok; u += pairs) {
+                for (int b = 0; b < a.blocks; ++b, ++sum) {
+                    const uint32_t buf = sum & 1, use = sum >> 1;
+                    ok = (use == 0 || mbar_wait_warp(&sm.acc_empty[buf], (use - 1) & 1, abort)) &&
+                         mbar_wait_warp(&sm.full[s], parity, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t ad = desc_at(ring + s * kStage), bd = desc_at(ring + s * kStage + kShare);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < kBlock / 32; ++k) // 32 steps: 32 bytes along a row
+                            mma_pair(tmem + buf * kMaxWidth, ad + k * 2, bd + k * 2, idesc, k != 0);
+                        mma_commit_pair(&sm.empty[s]);
+                        mma_commit_pair(&sm.acc_full[buf]);
+                    }
+                    __syncwarp();
+                    if (++s == kStages) s = 0, parity ^= 1;
+                }
+            }
+            // every product is done before the TMEM is freed
+            if (elect_one())
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                 saddr(&sm.drain))
+                             : "memory");
+            __syncwarp();
+            mbar_wait(&sm.drain, 0, nullptr);
+        }
+    } else {
+        // ---- scaling and sums
+        constexpr int kCols = kWidth / 2; // of a thread
+        const int q = warp & 3, h = (warp - 2) >> 2;
+        const uint32_t empty0 = peer_addr(&sm.acc_empty[0], 0), empty1 = peer_addr(&sm.acc_empty[1], 0);
+        const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + h * kCols;
+        uint32_t done = 0; // accumulators taken
+        bool ok = true;
+        for (int u = pair; u < units && ok; u += pairs) {
+            const Tile t = tile_at(sm, a, u, kWidth);
+            const int row0 = t.row + (int)rank * kHalf + 32 * q, col0 = t.col + h * kCols;
+            const bool has_rows = row0 < t.end;
+            // a row's scales and the columns' are fetched two blocks ahead
+            const float *rs = a.scale + (int64_t)min(row0 + lane, a.rows - 1) * a.blocks;
+            const float *ws = a.weight_scale +
+                              ((int64_t)t.group * a.col_blocks + min(col0 / kBlock, a.col_blocks - 1)) * a.blocks;
+            float r0 = rs[0], w0 = ws[0], r1 = 0.0f, w1 = 0.0f;
+            if (a.blocks > 1) r1 = rs[1], w1 = ws[1];
+            float sum[kCols];
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
+            for (int b = 0; b < a.blocks; ++b, ++done) {
+                const uint32_t buf = done & 1;
+                const float f = r0 * w0;
+                r0 = r1, w0 = w1;
+                if (b + 2 < a.blocks) r1 = rs[b + 2], w1 = ws[b + 2];
+                ok = mbar_wait_warp(&sm.acc_full[buf], (done >> 1) & 1, abort);
+                if (!ok) break;
+                tc_fence_after();
+                if (has_rows) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c += kChunk) {
+                        uint32_t x[kChunk];
+                        tmem_take(lanes + buf * kMaxWidth + c, x);
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i) sum[c + i] = fmaf(f, __uint_as_float(x[i]), sum[c + i]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(buf ? empty1 : empty0);
+            }
+            if (ok && has_rows) put_sums<Out, kCols>(a, sum, sm.staging[warp - 2], row0, t.end, col0);
+        }
+        // rows behind the last group
+        Out *out = static_cast<Out *>(a.out);
+        const int used = sm.begin[a.groups];
+        const int64_t from = (int64_t)used * a.cols, to = (int64_t)a.rows * a.cols;
+        constexpr int kEach = 16 / sizeof(Out);
+        const int64_t whole = min(to, from + (int64_t)((16 - (reinterpret_cast<uintptr_t>(out + from) & 15)) & 15) / (int64_t)sizeof(Out));
+        const int64_t vecs = (to - whole) / kEach;
+        const int64_t me = (int64_t)blockIdx.x * (32 * kEpiWarps) + tid - 64, all = (int64_t)gridDim.x * (32 * kEpiWarps);
+        for (int64_t i = me; i < vecs; i += all) reinterpret_cast<uint4 *>(out + whole)[i] = make_uint4(0, 0, 0, 0);
+        if (me < kEach) {
+            if (from + me < whole) put(out + from + me, 0.0f);
+            if (whole + vecs * kEach + me < to) put(out + whole + vecs * kEach + me, 0.0f);
+        }
+    }
+    __syncwarp();
+    grid_dependents_go();
+    tc_fence_before();
+    __syncthreads();
+    // a pair that gave up may have copies in flight that no barrier of this
+    // CTA counts: time for them to land (tens of times a copy's own)
+    if (*abort)
+        for (int i = 0; i < 64; ++i) __nanosleep(1000);
+    cluster_sync(); // neither CTA leaves while the other may still reach its shared memory
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+constexpr size_t kSmemBytes = 1024 + (size_t)kRingBytes + sizeof(ProductSmem);
+static_assert(kSmemBytes <= 227 * 1024, "the kernel's shared memory fits one CTA");
+
+constexpr int kMaxDevices = 64;
+struct ProductDevice {
+    std::atomic<bool> ready{false};
+    int pairs = 0; // CTA pairs that fit the device at a time
+};
+ProductDevice g_product_dev[kMaxDevices];
+std::mutex g_product_mutex;
+PFN_cuTensorMapEncodeTiled_v12000 g_product_encode = nullptr;
+
+using ProductKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, ProductArgs);
+
+ProductKernel product_kernel(int32_t dtype, int width)
+{
+    if (dtype == TF_TOPK_DTYPE_F32) return width == 256 ? product_fp8_kernel<float, 256> : product_fp8_kernel<float, 128>;
+    if (dtype == TF_TOPK_DTYPE_F16) return width == 256 ? product_fp8_kernel<__half, 256> : product_fp8_kernel<__half, 128>;
+    return width == 256 ? product_fp8_kernel<__nv_bfloat16, 256> : product_fp8_kernel<__nv_bfloat16, 128>;
+}
+
+// Per device, once: the kernels' shared memory limits, the pairs the device
+// holds, and the driver's tensor-map encoder.
+int product_setup(int *pairs)
+{
+    int sm_count = 0, dev = 0;
+    const int st = tf_topk_internal_device(&sm_count);
+    if (st != TF_TOPK_OK) return st;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return tf_topk_internal_fail_cuda((int)e);
+    if (dev >= kMaxDevices) return TF_TOPK_ERR_DEVICE;
+    ProductDevice &d = g_product_dev[dev];
+    if (!d.ready.load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lock(g_product_mutex);
+        if (!d.ready.load(std::memory_order_relaxed)) {
+            for (int32_t dtype : {TF_TOPK_DTYPE_BF16, TF_TOPK_DTYPE_F16, TF_TOPK_DTYPE_F32})
+                for (int width : {128, 256})
+                    if (e == cudaSuccess)
+                        e = cudaFuncSetAttribute(product_kernel(dtype, width),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)(sm_count / 2 * 2), 1, 1);
+            cfg.blockDim = dim3(kThreads, 1, 1);
+            cfg.dynamicSmemBytes = kSmemBytes;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (e == cudaSuccess)
+                e = cudaOccupancyMaxActiveClusters(&n, product_kernel(TF_TOPK_DTYPE_BF16, 256), &cfg);
+            if (e != cudaSuccess) return tf_topk_internal_fail_cuda((int)e);
+            d.pairs = n < 1 ? 1 : n;
+            if (!g_product_encode) {
+                void *fn = nullptr;
+                cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+                e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+                if (e != cudaSuccess) return tf_topk_internal_fail_cuda((int)e);
+                if (q != cudaDriverEntryPointSuccess || !fn) return TF_TOPK_ERR_DEVICE;
+                g_product_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+            }
+            d.ready.store(true, std::memory_order_release);
+        }
+    }
+    *pairs = d.pairs;
+    return TF_TOPK_OK;
+}
+
+// A map of packed rows of bytes, boxes of 128 x box_rows with the 128-byte
+// swizzle; coordinates past either extent read as zero.
+bool encode_map(CUtensorMap *map, const void *p, int64_t inner, int64_t outer, int box_rows)
+{
+    cuuint64_t gdim[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+    cuuint64_t gstride[1] = {(cuuint64_t)inner};
+    cuuint32_t box[2] = {(cuuint32_t)kBlock, (cuuint32_t)box_rows};
+    cuuint32_t estride[2] = {1, 1};
+    return g_product_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), gdim, gstride, box, estride,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// Tiles there can be: a group's last one may be short, and groups without rows have none.
+int64_t most_units(int64_t rows, int64_t groups, int64_t cols, int width)
+{
+    return (rows / kTileRows + (rows < groups ? rows : groups)) * ((cols + width - 1) / width);
+}
+
+} // namespace
+
+// This file's fault word, read and cleared (tf_topk_device_fault reports it).
+uint32_t tf_topk_internal_product_fault_take()
+{
+    uint32_t f = 0;
+    if (cudaMemcpyFromSymbol(&f, g_product_fault, sizeof f) != cudaSuccess) return 0;
+    if (f) {
+        const uint32_t zero = 0;
+        cudaMemcpyToSymbol(g_product_fault, &zero, sizeof zero);
+    }
+    return f;
+}
+
+extern "C" int tf_topk_product_fp8(const void *q, const float *scale, int64_t rows, int32_t dim, const void *weight,
+                                   const float *weight_scale, int64_t cols, int32_t groups, const int32_t *offsets,
+                                   int32_t dtype, void *out, void *stream)
+{
+    if (dtype != TF_TOPK_DTYPE_BF16 && dtype != TF_TOPK_DTYPE_F16 && dtype != TF_TOPK_DTYPE_F32)
+        return TF_TOPK_ERR_DTYPE;
+    if (rows < 0 || rows > INT32_MAX - kTileRows || dim < 16 || dim % 16 != 0 || cols < 1 || groups < 1 ||
+        groups > kMaxGroups || (!offsets && groups != 1) || cols > (INT32_MAX - 1024) / groups ||
+        most_units(rows, groups, cols, kHalf) > INT32_MAX / 2)
+        return TF_TOPK_ERR_SHAPE;
+    if (rows == 0) return TF_TOPK_OK;
+    if (!q || !scale || !weight || !weight_scale || !out) return TF_TOPK_ERR_NULL;
+    const size_t size = dtype == TF_TOPK_DTYPE_F32 ? 4 : 2;
+    if (!aligned(q, 16) || !aligned(weight, 16) || !aligned(scale, 4) || !aligned(weight_scale, 4) ||
+        !aligned(offsets, 4) || !aligned(out, size))
+        return TF_TOPK_ERR_ALIGN;
+    int pairs = 0;
+    const int st = product_setup(&pairs);
+    if (st != TF_TOPK_OK) return st;
+    const int width = cols <= kHalf ? 128 : 256;
+    CUtensorMap map_q, map_few, map_w;
+    if (!encode_map(&map_q, q, dim, rows, kHalf) || !encode_map(&map_few, q, dim, rows, kFewRows) ||
+        !encode_map(&map_w, weight, dim, (int64_t)groups * cols, width / 2))
+        return tf_topk_internal_fail_cuda((int)cudaErrorInvalidValue);
+    ProductArgs a;
+    a.scale = scale;
+    a.weight_scale = weight_scale;
+    a.offsets = offsets;
+    a.out = out;
+    a.rows = (int32_t)rows;
+    a.cols = (int32_t)cols;
+    a.groups = groups;
+    a.blocks = (dim + kBlock - 1) / kBlock;
+    a.col_blocks = (int32_t)((cols + kBlock - 1) / kBlock);
+    a.col_tiles = (int32_t)((cols + width - 1) / width);
+    a.wide_stores = aligned(out, 32) && (size_t)cols * size % 32 == 0;
+    const int64_t units = most_units(rows, groups, cols, width);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * (units < pairs ? units : pairs)), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, product_kernel(dtype, width), map_q, map_few, map_w, a);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? TF_TOPK_OK : tf_topk_internal_fail_cuda((int)e);
+}

@@ -11,12 +11,16 @@ probabilities over the lists), ``head_topk_bf16`` (the draft head's
 product and the top-k in one kernel), ``head_loss_bf16`` and
 ``head_loss_grad_bf16`` (the head's cross entropy and its gradient without the
 logits), ``route_experts`` and ``route_experts_grad`` (each token's experts and
-their weights).  The raw C entry points are exposed under their C names.
+their weights), ``sort_by_expert``, ``gather_tokens``, ``combine_tokens`` and
+their gradients (tokens sorted by expert and back), ``quantize_tokens_fp8`` and
+``product_fp8`` (rows in 8 bits and their products with weights in 8 bits),
+``penalize_logits`` (penalties, biases and masks before the top-k).  The raw C entry points are exposed under their C names.
 """
 from __future__ import annotations
 
 import ctypes
 from pathlib import Path
+from typing import Any, NamedTuple
 
 PKG = Path(__file__).resolve().parent
 LIBRARY = PKG / "libtf_topk.so"
@@ -103,6 +107,24 @@ def library() -> ctypes.CDLL:
         lib.tf_topk_route_grad.restype = ctypes.c_int
         lib.tf_topk_route_grad.argtypes = [c_p, c_i32, c_i64, c_i32, c_i64, c_i32, c_p, c_p, c_i32, c_i32,
                                            ctypes.c_float, c_p, c_p]
+        lib.tf_topk_sort_experts.restype = ctypes.c_int
+        lib.tf_topk_sort_experts.argtypes = [c_p, c_i64, c_i32, c_i32, c_p, c_size, c_p, c_p, c_p, c_p]
+        lib.tf_topk_sort_experts_workspace.restype = c_size
+        lib.tf_topk_sort_experts_workspace.argtypes = [c_i64, c_i32, c_i32]
+        lib.tf_topk_gather_tokens.restype = ctypes.c_int
+        lib.tf_topk_gather_tokens.argtypes = [c_p, c_i32, c_i64, c_i32, c_i64, c_i32, c_p, c_p, c_p, c_p]
+        lib.tf_topk_quantize_tokens.restype = ctypes.c_int
+        lib.tf_topk_quantize_tokens.argtypes = [c_p, c_i32, c_i64, c_i32, c_i64, c_i32, c_p, c_p, c_p, c_p, c_p]
+        lib.tf_topk_combine_tokens.restype = ctypes.c_int
+        lib.tf_topk_combine_tokens.argtypes = [c_p, c_i32, c_i64, c_i32, c_i64, c_i32, c_p, c_p, c_p, c_p]
+        lib.tf_topk_combine_tokens_grad.restype = ctypes.c_int
+        lib.tf_topk_combine_tokens_grad.argtypes = [c_p, c_i32, c_i64, c_i32, c_i64, c_p, c_i64, c_i32, c_p, c_p, c_p,
+                                                    c_p, c_p, c_p]
+        lib.tf_topk_product_fp8.restype = ctypes.c_int
+        lib.tf_topk_product_fp8.argtypes = [c_p, c_p, c_i64, c_i32, c_p, c_p, c_i64, c_i32, c_p, c_i32, c_p, c_p]
+        lib.tf_topk_penalize.restype = ctypes.c_int
+        lib.tf_topk_penalize.argtypes = [c_p, c_i32, c_i64, c_i64, c_i64, c_p, c_i64, c_i32, c_p, c_p, c_p, c_p, c_p,
+                                         c_p, c_p, c_i64, c_i32, c_p, c_i64, c_p, c_i64, c_p]
         lib.tf_topk_strerror.restype = ctypes.c_char_p
         lib.tf_topk_strerror.argtypes = [ctypes.c_int]
         lib.tf_topk_last_cuda_error.restype = ctypes.c_int
@@ -663,6 +685,383 @@ def route_experts_grad(logits, idx, grad_weight, *, score: str = "softmax", reno
     _check((_lib or library()).tf_topk_route_grad(
         logits.data_ptr(), code, tokens, experts, stride, k, idx.data_ptr(), grad_weight.data_ptr(), how,
         bool(renormalize), scale, out.data_ptr(), _stream_handle(stream, dev)))
+    return out
+
+
+class ExpertOrder(NamedTuple):
+    """The order of routing's choices by expert, as ``sort_by_expert`` gives it."""
+
+    slot: Any  # int32 [tokens, k]: the place of each choice, -1 for one that takes no part
+    source: Any  # int32 [tokens * k]: the choice (t * k + j) at each place, -1 behind the last
+    offsets: Any  # int32 [experts + 1]: the first place of each expert, and the end of the last
+
+
+def tf_topk_sort_experts(idx: int, tokens: int, k: int, experts: int, workspace: int | None, workspace_bytes: int,
+                         out_slot: int, out_source: int, out_offsets: int, stream: int | None) -> int:
+    """The C entry point of the sort by expert with raw pointers; returns the status code."""
+    return library().tf_topk_sort_experts(idx, tokens, k, experts, workspace, workspace_bytes, out_slot, out_source,
+                                          out_offsets, stream)
+
+
+def tf_topk_sort_experts_workspace(tokens: int, k: int, experts: int) -> int:
+    """Workspace bytes tf_topk_sort_experts needs on the current device (0 where it needs none)."""
+    return library().tf_topk_sort_experts_workspace(tokens, k, experts)
+
+
+def sort_by_expert(idx, experts: int, *, out=None, workspace=None, stream=None) -> ExpertOrder:
+    """Order of ``route_experts``'s choices by expert, and by token and place
+    within an expert (a stable sort).
+
+    ``idx``: CUDA int32 [tokens, k], contiguous; choices outside
+    [0, ``experts``) take no part.  Returns an ``ExpertOrder``.  ``out`` may
+    supply its three tensors, ``workspace`` a CUDA tensor of at least
+    ``tf_topk_sort_experts_workspace(tokens, k, experts)`` bytes.
+    """
+    torch = _torch or _need_torch()
+    if idx.dtype is not torch.int32:
+        raise TypeError(f"idx must be int32, got {idx.dtype}")
+    if not idx.is_cuda or idx.dim() != 2 or not idx.is_contiguous():
+        raise ValueError("idx must be a contiguous 2-D CUDA tensor")
+    dev = idx.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return sort_by_expert(idx, experts, out=out, workspace=workspace, stream=stream)
+    tokens, k = idx.shape
+    n = tokens * k
+    if out is None:
+        # a bad count of experts is the library's to refuse
+        order = ExpertOrder(_empty((tokens, k), torch.int32, dev, stream), _empty((n,), torch.int32, dev, stream),
+                            _empty((max(experts, 0) + 1,), torch.int32, dev, stream))
+    else:
+        order = ExpertOrder(*out)
+        _check_out(order.slot, (tokens, k), torch.int32, dev, "slot")
+        _check_out(order.source, (n,), torch.int32, dev, "source")
+        _check_out(order.offsets, (experts + 1,), torch.int32, dev, "offsets")
+    lib = _lib or library()
+    space, room = None, 0
+    if workspace is not None:
+        space = _workspace(workspace, None, (), dev, stream)
+    elif lib.tf_topk_sort_experts_workspace(tokens, k, experts):
+        space = _workspace(None, lib.tf_topk_sort_experts_workspace, (tokens, k, experts), dev, stream)
+    if space is not None:
+        room, space_ptr = space.nbytes, space.data_ptr()
+    else:
+        space_ptr = None
+    _check(lib.tf_topk_sort_experts(idx.data_ptr(), tokens, k, experts, space_ptr, room, order.slot.data_ptr(),
+                                    order.source.data_ptr(), order.offsets.data_ptr(), _stream_handle(stream, dev)))
+    return order
+
+
+def _rows_code(x, name):
+    """(dtype code, rows, dim, row stride) of a matrix of rows, checked."""
+    global _logit_codes
+    if _logit_codes is None:
+        torch = _need_torch()
+        _logit_codes = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
+    code = _logit_codes.get(x.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
+    if not x.is_cuda or x.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    rows, dim = x.shape
+    stride = x.stride()
+    if dim > 1 and stride[1] != 1:
+        raise ValueError(f"{name} must have contiguous columns")
+    return code, rows, dim, stride[0] if rows > 1 else dim
+
+
+def _order_of(order, tokens, dev):
+    """(slot, source, k) of an order for so many tokens, checked."""
+    slot, source = order[0], order[1]
+    if slot.dim() != 2 or slot.shape[0] != tokens:
+        raise ValueError("the order is not of this many tokens")
+    k = slot.shape[1]
+    _check_out(slot, (tokens, k), _torch.int32, dev, "slot")
+    _check_out(source, (tokens * k,), _torch.int32, dev, "source")
+    return slot, source, k
+
+
+def tf_topk_gather_tokens(x: int, dtype: int, tokens: int, dim: int, row_stride: int, k: int, slot: int, source: int,
+                          out_rows: int, stream: int | None) -> int:
+    """The C entry point of the gather by expert with raw pointers; returns the status code."""
+    return library().tf_topk_gather_tokens(x, dtype, tokens, dim, row_stride, k, slot, source, out_rows, stream)
+
+
+def gather_tokens(x, order: ExpertOrder, *, out=None, stream=None):
+    """The tokens' rows in the order of ``sort_by_expert``: a row for each
+    choice, zeros behind the last.  ``x``: CUDA bf16 / fp16 / fp32
+    [tokens, dim], contiguous columns.  Returns [tokens * k, dim] of its dtype."""
+    code, tokens, dim, stride = _rows_code(x, "x")
+    torch, dev = _torch, x.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return gather_tokens(x, order, out=out, stream=stream)
+    slot, source, k = _order_of(order, tokens, dev)
+    if out is None:
+        out = _empty((tokens * k, dim), x.dtype, dev, stream)
+    else:
+        _check_out(out, (tokens * k, dim), x.dtype, dev, "out")
+    _check((_lib or library()).tf_topk_gather_tokens(x.data_ptr(), code, tokens, dim, stride, k, slot.data_ptr(),
+                                                     source.data_ptr(), out.data_ptr(), _stream_handle(stream, dev)))
+    return out
+
+
+def tf_topk_combine_tokens(rows: int, dtype: int, tokens: int, dim: int, row_stride: int, k: int, slot: int,
+                           weight: int | None, out: int, stream: int | None) -> int:
+    """The C entry point of the experts' rows combined by token; returns the status code."""
+    return library().tf_topk_combine_tokens(rows, dtype, tokens, dim, row_stride, k, slot, weight, out, stream)
+
+
+def combine_tokens(rows, order: ExpertOrder, weight=None, *, out=None, stream=None):
+    """The experts' rows back to their tokens: out[t] = sum over j of
+    weight[t, j] * rows[slot[t, j]], in 32 bits, rounded once.
+
+    ``rows``: CUDA bf16 / fp16 / fp32 [tokens * k, dim], contiguous columns;
+    ``weight``: float32 [tokens, k] as ``route_experts`` returns it, or None
+    for plain sums.  Choices without a place are left out, whatever their
+    weight.  Returns [tokens, dim] of the rows' dtype.
+    """
+    code, n, dim, stride = _rows_code(rows, "rows")
+    torch, dev = _torch, rows.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return combine_tokens(rows, order, weight, out=out, stream=stream)
+    tokens = order[0].shape[0]
+    slot, _, k = _order_of(order, tokens, dev)
+    if n != tokens * k:
+        raise ValueError("rows must have one row for each choice")
+    if weight is not None:
+        _check_out(weight, (tokens, k), torch.float32, dev, "weight")
+    if out is None:
+        out = _empty((tokens, dim), rows.dtype, dev, stream)
+    else:
+        _check_out(out, (tokens, dim), rows.dtype, dev, "out")
+    _check((_lib or library()).tf_topk_combine_tokens(
+        rows.data_ptr(), code, tokens, dim, stride, k, slot.data_ptr(), None if weight is None else weight.data_ptr(),
+        out.data_ptr(), _stream_handle(stream, dev)))
+    return out
+
+
+def gather_tokens_grad(grad_rows, order: ExpertOrder, *, out=None, stream=None):
+    """Gradient of ``gather_tokens`` for x: each token's sum over its rows of
+    ``grad_rows`` [tokens * k, dim], in 32 bits, rounded once."""
+    return combine_tokens(grad_rows, order, None, out=out, stream=stream)
+
+
+def tf_topk_combine_tokens_grad(grad_out: int, dtype: int, tokens: int, dim: int, grad_stride: int, rows: int,
+                                row_stride: int, k: int, slot: int, source: int, weight: int, out_grad_rows: int,
+                                out_grad_weight: int, stream: int | None) -> int:
+    """The C entry point of the gradient of tf_topk_combine_tokens; returns the status code."""
+    return library().tf_topk_combine_tokens_grad(grad_out, dtype, tokens, dim, grad_stride, rows, row_stride, k, slot,
+                                                 source, weight, out_grad_rows, out_grad_weight, stream)
+
+
+def combine_tokens_grad(grad_out, rows, order: ExpertOrder, weight, *, out=None, stream=None):
+    """Gradient of ``combine_tokens``: with ``grad_out`` [tokens, dim] (the
+    rows' dtype) gives ``(grad_rows [tokens * k, dim], grad_weight float32
+    [tokens, k])``; rows behind the last place and choices without one get 0."""
+    code, tokens, dim, grad_stride = _rows_code(grad_out, "grad_out")
+    torch, dev = _torch, grad_out.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return combine_tokens_grad(grad_out, rows, order, weight, out=out, stream=stream)
+    slot, source, k = _order_of(order, tokens, dev)
+    _, n, width, row_stride = _rows_code(rows, "rows")
+    if n != tokens * k or width != dim or rows.dtype is not grad_out.dtype or rows.device != dev:
+        raise ValueError("rows must have one row for each choice, of grad_out's dim, dtype and device")
+    _check_out(weight, (tokens, k), torch.float32, dev, "weight")
+    if out is None:
+        grad_rows = _empty((n, dim), rows.dtype, dev, stream)
+        grad_weight = _empty((tokens, k), torch.float32, dev, stream)
+    else:
+        grad_rows, grad_weight = out
+        _check_out(grad_rows, (n, dim), rows.dtype, dev, "grad_rows")
+        _check_out(grad_weight, (tokens, k), torch.float32, dev, "grad_weight")
+    _check((_lib or library()).tf_topk_combine_tokens_grad(
+        grad_out.data_ptr(), code, tokens, dim, grad_stride, rows.data_ptr(), row_stride, k, slot.data_ptr(),
+        source.data_ptr(), weight.data_ptr(), grad_rows.data_ptr(), grad_weight.data_ptr(),
+        _stream_handle(stream, dev)))
+    return grad_rows, grad_weight
+
+
+FP8_BLOCK = 128
+
+
+def tf_topk_quantize_tokens(x: int, dtype: int, tokens: int, dim: int, row_stride: int, k: int, slot: int | None,
+                            source: int | None, out_q: int, out_scale: int, stream: int | None) -> int:
+    """The C entry point of rows in 8 bits with raw pointers; returns the status code."""
+    return library().tf_topk_quantize_tokens(x, dtype, tokens, dim, row_stride, k, slot, source, out_q, out_scale,
+                                             stream)
+
+
+def quantize_tokens_fp8(x, order: ExpertOrder | None = None, *, out=None, stream=None):
+    """Rows in 8 bits: e4m3 values with a scale for each 128 of a row, the
+    scale being the largest magnitude over 448.
+
+    ``x``: CUDA bf16 / fp16 / fp32 [tokens, dim], contiguous columns, dim a
+    multiple of 16.  With ``order`` the rows come in the order of
+    ``sort_by_expert`` (zeros behind the last place).  Returns ``(q
+    float8_e4m3fn [rows, dim], scale float32 [rows, ceil(dim / 128)])`` for
+    ``product_fp8``.
+    """
+    code, tokens, dim, stride = _rows_code(x, "x")
+    torch, dev = _torch, x.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return quantize_tokens_fp8(x, order, out=out, stream=stream)
+    slot, source, k = (None, None, 1) if order is None else _order_of(order, tokens, dev)
+    rows, blocks = tokens * k, -(-dim // FP8_BLOCK)
+    if out is None:
+        q = _empty((rows, dim), torch.float8_e4m3fn, dev, stream)
+        scale = _empty((rows, blocks), torch.float32, dev, stream)
+    else:
+        q, scale = out
+        _check_out(q, (rows, dim), torch.float8_e4m3fn, dev, "q")
+        _check_out(scale, (rows, blocks), torch.float32, dev, "scale")
+    _check((_lib or library()).tf_topk_quantize_tokens(
+        x.data_ptr(), code, tokens, dim, stride, k, None if slot is None else slot.data_ptr(),
+        None if source is None else source.data_ptr(), q.data_ptr(), scale.data_ptr(), _stream_handle(stream, dev)))
+    return q, scale
+
+
+def tf_topk_product_fp8(q: int, scale: int, rows: int, dim: int, weight: int, weight_scale: int, cols: int,
+                        groups: int, offsets: int | None, dtype: int, out: int, stream: int | None) -> int:
+    """The C entry point of the product in 8 bits with raw pointers; returns the status code."""
+    return library().tf_topk_product_fp8(q, scale, rows, dim, weight, weight_scale, cols, groups, offsets, dtype, out,
+                                         stream)
+
+
+def product_fp8(q, scale, weight, weight_scale, *, offsets=None, dtype=None, out=None, stream=None):
+    """Product of rows in 8 bits with weights in 8 bits, of one matrix or of
+    the experts' matrices over their sorted rows; 32-bit sums, each block of
+    128 dims scaled as it is added.
+
+    ``q`` float8_e4m3fn [rows, dim] and ``scale`` float32 [rows,
+    ceil(dim / 128)] as ``quantize_tokens_fp8`` returns them; ``weight``
+    float8_e4m3fn [cols, dim] with ``weight_scale`` float32 [ceil(cols / 128),
+    ceil(dim / 128)], or with ``offsets`` (int32 [experts + 1], ascending from
+    0, as in an ``ExpertOrder``) [experts, cols, dim] and [experts, ...].  All
+    contiguous, dim a multiple of 16.  Returns [rows, cols] of ``dtype``
+    (bfloat16, float16 or float32; bfloat16 if None); rows behind the last
+    expert's become zeros.
+    """
+    torch = _torch or _need_torch()
+    f8 = torch.float8_e4m3fn
+    if q.dtype is not f8 or weight.dtype is not f8:
+        raise TypeError(f"q and weight must be float8_e4m3fn, got {q.dtype} and {weight.dtype}")
+    if not q.is_cuda or q.dim() != 2 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous 2-D CUDA tensor")
+    dev = q.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return product_fp8(q, scale, weight, weight_scale, offsets=offsets, dtype=dtype, out=out, stream=stream)
+    rows, dim = q.shape
+    shape = weight.shape
+    if offsets is None:
+        shape = (1, *shape)
+    if len(shape) != 3 or shape[2] != dim:
+        raise ValueError("weight must be [cols, dim], or with offsets [experts, cols, dim]")
+    groups, cols = shape[0], shape[1]
+    blocks, col_blocks = -(-dim // FP8_BLOCK), -(-cols // FP8_BLOCK)
+    _check_out(weight, tuple(weight.shape), f8, dev, "weight")
+    _check_out(scale, (rows, blocks), torch.float32, dev, "scale")
+    _check_out(weight_scale, (col_blocks, blocks) if offsets is None else (groups, col_blocks, blocks), torch.float32,
+               dev, "weight_scale")
+    if offsets is not None:
+        _check_out(offsets, (groups + 1,), torch.int32, dev, "offsets")
+    if out is None:
+        out = _empty((rows, cols), dtype or torch.bfloat16, dev, stream)
+    else:
+        _check_out(out, (rows, cols), dtype or out.dtype, dev, "out")
+    code = _rows_code(out, "out")[0]
+    _check((_lib or library()).tf_topk_product_fp8(
+        q.data_ptr(), scale.data_ptr(), rows, dim, weight.data_ptr(), weight_scale.data_ptr(), cols, groups,
+        None if offsets is None else offsets.data_ptr(), code, out.data_ptr(), _stream_handle(stream, dev)))
+    return out
+
+
+PENALTY_MAX_BIASES = 65535
+
+
+def tf_topk_penalize(logits: int, dtype: int, rows: int, cols: int, row_stride: int, tokens: int | None,
+                     token_stride: int, width: int, lengths: int | None, prompts: int | None, repetition: int | None,
+                     presence: int | None, frequency: int | None, bias_token: int | None, bias_value: int | None,
+                     bias_stride: int, biases: int, allowed: int | None, allowed_stride: int, out: int,
+                     out_stride: int, stream: int | None) -> int:
+    """The C entry point of penalties, biases and masks with raw pointers; returns the status code."""
+    return library().tf_topk_penalize(logits, dtype, rows, cols, row_stride, tokens, token_stride, width, lengths,
+                                      prompts, repetition, presence, frequency, bias_token, bias_value, bias_stride,
+                                      biases, allowed, allowed_stride, out, out_stride, stream)
+
+
+def _per_row(t, rows, dtype, dev, name):
+    """Address of an optional [rows] tensor, checked."""
+    if t is None:
+        return None
+    _check_out(t, (rows,), dtype, dev, name)
+    return t.data_ptr()
+
+
+def _table(t, rows, dtype, dev, name):
+    """(address, width, row stride) of an optional [rows, width] tensor with contiguous columns, checked."""
+    if t is None:
+        return None, 0, 0
+    if t.dtype is not dtype or t.device != dev or t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} must be a 2-D {dtype} tensor with the logits' rows, on their device")
+    width, stride = t.shape[1], t.stride()
+    if width > 1 and stride[1] != 1:
+        raise ValueError(f"{name} must have contiguous columns")
+    return t.data_ptr(), width, stride[0] if rows > 1 else width
+
+
+def penalize_logits(logits, *, tokens=None, lengths=None, prompts=None, repetition=None, presence=None, frequency=None,
+                    bias_tokens=None, bias_values=None, allowed=None, out=None, stream=None):
+    """Logits made ready for ``select_topk``: penalties for each request's
+    tokens so far, biases and a grammar's mask, in one pass.
+
+    ``logits``: CUDA bf16 / fp16 / fp32 [rows, cols], contiguous columns.
+    ``tokens``: int32 [rows, width]; row r's first ``prompts[r]`` (int32; none
+    if None) are its prompt, those up to ``lengths[r]`` (int32; all if None)
+    its answer so far.  ``repetition`` (over prompt and answer: a positive
+    logit is divided by it, any other multiplied), ``presence`` and
+    ``frequency`` (over the answer: subtracted once, and once for each time):
+    float32 [rows].  ``bias_tokens`` int32 and ``bias_values`` float32 [rows,
+    biases]: added to those columns (of several entries for one column the
+    last counts; columns out of range are passed over).  ``allowed``: int32
+    [rows, ceil(cols / 32)], bit c % 32 of word c // 32 set where column c
+    stays; the others become -inf.
+    Returns [rows, cols] of the logits' dtype; ``out`` may be ``logits`` itself.
+    """
+    code, rows, cols, stride = _rows_code(logits, "logits")
+    torch, dev = _torch, logits.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return penalize_logits(logits, tokens=tokens, lengths=lengths, prompts=prompts, repetition=repetition,
+                                   presence=presence, frequency=frequency, bias_tokens=bias_tokens,
+                                   bias_values=bias_values, allowed=allowed, out=out, stream=stream)
+    said, width, said_stride = _table(tokens, rows, torch.int32, dev, "tokens")
+    names, biases, bias_stride = _table(bias_tokens, rows, torch.int32, dev, "bias_tokens")
+    values, count, value_stride = _table(bias_values, rows, torch.float32, dev, "bias_values")
+    if count != biases or value_stride != bias_stride:
+        raise ValueError("bias_tokens and bias_values must have one shape and one row stride")
+    mask, words, mask_stride = _table(allowed, rows, torch.int32, dev, "allowed")
+    if allowed is not None and words != -(-cols // 32):
+        raise ValueError("allowed must have a bit for each column, in words of 32")
+    if out is None:
+        out, out_stride = _empty((rows, cols), logits.dtype, dev, stream), cols
+    elif out is logits:
+        out_stride = stride
+    else:
+        if out.dtype is not logits.dtype or out.device != dev or tuple(out.shape) != (rows, cols):
+            raise ValueError("out must have the logits' shape, dtype and device")
+        out_stride = _rows_code(out, "out")[3]
+    _check((_lib or library()).tf_topk_penalize(
+        logits.data_ptr(), code, rows, cols, stride, said, said_stride, width,
+        _per_row(lengths, rows, torch.int32, dev, "lengths"), _per_row(prompts, rows, torch.int32, dev, "prompts"),
+        _per_row(repetition, rows, torch.float32, dev, "repetition"),
+        _per_row(presence, rows, torch.float32, dev, "presence"),
+        _per_row(frequency, rows, torch.float32, dev, "frequency"), names, values, bias_stride, biases, mask,
+        mask_stride, out.data_ptr(), out_stride, _stream_handle(stream, dev)))
     return out
 
 
