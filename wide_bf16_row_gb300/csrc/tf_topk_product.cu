@@ -10,22 +10,21 @@
 // block's scale is applied exactly where it belongs and the tensor cores'
 // truncating additions reach over 128 dims only.
 //
-// A pair of CTAs (cluster of two, tcgen05.mma cta_group::2, kind::f8f6f4) per
-// tile of 256 rows of one group x 256 or 128 columns; each CTA holds 128 of the
-// rows and loads half of the columns.  Persistent: the tiles of all groups in a
-// row, found in a prefix sum over the groups that each CTA makes from the
-// offsets.  Warp roles, per CTA:
-//   warp 0     TMA producer: per ring stage a block of 128 dims of the CTA's
-//              rows and columns, 128-byte swizzle;
-//   warp 1     TMEM allocation; in the leading CTA the MMA issuer, a block into
-//              one of two accumulators;
-//   warps 2-9  a thread per row and half of the tile's columns: takes each
-//              block's sums from tensor memory, scales and adds them.
-// Bounds: with up to some 250 rows per group the weight's bytes, beyond them the
-// tensor cores, beside which the warps that scale have to keep up: 128 x 256
-// sums per CTA and block, 256 cycles of tensor memory reads and as many of FMA,
-// while the block's products take 512.
-//
+// Two kernels, both persistent over the tiles of all groups, found in a prefix
+// sum over the groups that each CTA makes from the offsets:
+//   product_wide_kernel  many rows per group, bound by the tensor cores: a pair
+//       of CTAs (cluster of two, tcgen05.mma cta_group::2, kind::f8f6f4) per tile
+//       of 256 rows x 256 or 128 columns; each CTA holds 128 of the rows and
+//       loads half of the columns.
+//   product_thin_kernel  few rows per group, bound by the weight's bytes: a CTA
+//       per tile of up to 128 columns x up to 64 rows, with the weight as the
+//       MMA's A, so that its 128 lanes are columns and a block's sums of 16 rows
+//       are 16 accumulator columns, quickly taken.
+// Warp roles, per CTA: a TMA producer (per ring stage a block of 128 dims of rows
+// and columns, 128-byte swizzle), an MMA issuer (a block into one of several
+// accumulators in tensor memory), and warps that take each block's sums from
+// there, scale and add them.
+
 // No wait is unbounded: every mbarrier wait gives up after kWaitLimit polls,
 // records a fault code, and the CTA winds down.
 
@@ -46,22 +45,31 @@ int tf_topk_internal_device(int *sm_count);
 
 namespace {
 
-constexpr int kTileRows = 256;           // rows (M) of a pair's tile
-constexpr int kHalf = 128;               // one CTA's
+constexpr int kTileRows = 256;            // wide: rows (M) of a pair's tile
+constexpr int kHalf = 128;                // wide: one CTA's; thin: columns (M) of a tile at most
 constexpr int kBlock = TF_TOPK_FP8_BLOCK; // dims of a scale, and of a ring stage: one 128-byte swizzle row
 constexpr int kMaxWidth = 256;
-constexpr uint32_t kShare = kHalf * kBlock; // 16 KB: one CTA's share of an operand per stage
-constexpr int kStages = 6;
-constexpr uint32_t kRingBytes = kStages * 2 * kShare;
-constexpr int kFewRows = 16; // up to so many rows of a tile are loaded as a box of their own
+constexpr uint32_t kShare = kHalf * kBlock; // 16 KB: 128 rows or columns of a block
+constexpr int kStages = 6;                // wide: of the ring
+constexpr uint32_t kWideStage = 2 * kShare;
+constexpr int kRowBox = 16;               // rows of a small box
+constexpr int kThinRows = 64;             // thin: rows of a tile at most
+constexpr int kThinMostStages = 10;
+constexpr uint32_t kWideRing = kStages * kWideStage, kThinRing = 92 * 1024;
+constexpr int kThinCtas = 2; // of an SM: while one waits for its loads the other's products run
 constexpr int kMaxGroups = TF_TOPK_ROUTE_MAX_EXPERTS;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
-constexpr int kTmemCols = 2 * kMaxWidth;
-constexpr int kChunk = 16;      // accumulator columns a thread takes at a time
+constexpr int kWideThreads = 32 * (2 + kEpiWarps);
+constexpr int kWideTmem = 2 * kMaxWidth;
+constexpr int kChunk = 16;       // accumulator columns a thread takes at a time
 constexpr int kStagingCols = 16; // columns a warp turns round at a time, where its stores need it
 constexpr int kStagingPitch = kStagingCols + 1;
-constexpr int kGroupRows = 16;  // row tiles that share the sweep over the columns
+constexpr int kGroupRows = 16;   // row tiles that share the sweep over the columns
+constexpr int kThinEpiWarps = 8; // two for each 32 columns, which share the rows
+constexpr int kThinThreads = 32 * (2 + kThinEpiWarps);
+constexpr int kThinAccs = 4;     // accumulators
+constexpr int kThinTmem = kThinAccs * kThinRows;
+constexpr int kScaleBlocks = 16; // thin: blocks whose scales are fetched at a time
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 // Polls of a wait: a second, for a poll of a barrier that does not complete
 // suspends the warp for 3.9 us.
@@ -74,16 +82,34 @@ constexpr uint32_t kFaultWait = 1;
 
 __device__ uint32_t g_product_fault;
 
-struct __align__(16) ProductSmem {
+using Pair = unsigned long long; // of fp32
+
+// The groups' tiles, as every CTA makes them for itself.
+struct Groups {
+    int32_t warp_sum[32];
+    int32_t begin[kMaxGroups + 1]; // a group's first row; [groups] is the end of the last
+    int32_t tiles[kMaxGroups + 1]; // tiles of the groups before
+};
+
+struct __align__(16) WideSmem {
     uint64_t full[kStages], empty[kStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
     uint32_t tmem_base;
     uint32_t abort;
-    int32_t warp_sum[kThreads / 32];
-    int32_t begin[kMaxGroups + 1]; // a group's first row; [groups] is the end of the last
-    int32_t tiles[kMaxGroups + 1]; // tiles of the groups before
+    Groups groups;
     float staging[kEpiWarps][32 * kStagingPitch];
+};
+
+struct __align__(16) ThinSmem {
+    float scale[2][kScaleBlocks][kThinRows];
+    float weight_scale[2][kScaleBlocks][2];
+    uint64_t full[kThinMostStages], empty[kThinMostStages];
+    uint64_t acc_full[kThinAccs], acc_empty[kThinAccs];
+    uint64_t drain;
+    uint32_t tmem_base;
+    uint32_t abort;
+    Groups groups;
 };
 
 struct ProductArgs {
@@ -92,6 +118,9 @@ struct ProductArgs {
     const int32_t *offsets;    // null: one group of all rows
     void *out;
     int32_t rows, cols, groups, blocks, col_blocks, col_tiles;
+    int32_t width; // columns of a tile
+    int32_t tile_rows; // thin: rows of a tile
+    int32_t stages; // thin: of the ring
     int32_t wide_stores; // a thread's columns go out in 32-byte stores
 };
 
@@ -126,13 +155,19 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr)
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// As mbar_arrive_cluster, to a barrier of this CTA.
+__device__ __forceinline__ void mbar_arrive_own(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(saddr(bar)) : "memory");
+}
+
 // Bounded wait for the phase with this parity; gives up after kWaitLimit
 // polls (recording the fault) or once another warp of this CTA has.
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort)
 {
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
         uint32_t ok;
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
                      "selp.u32 %0, 1, 0, p;\n\t}"
                      : "=r"(ok)
                      : "r"(saddr(bar)), "r"(parity)
@@ -182,8 +217,10 @@ __device__ __forceinline__ uint64_t desc_at(const void *p) { return kDescK | ((s
 // Instruction descriptor of tcgen05.mma kind::f8f6f4: fp32 accumulator (bit
 // 4), e4m3 A and B (0 at bits 7 and 10), both K-major, N / 8 at bit 17, M / 16
 // at bit 24.
-template <uint32_t n> constexpr uint32_t kInstruction =
-    (1u << 4) | ((n >> 3) << 17) | ((uint32_t)(kTileRows >> 4) << 24);
+__device__ __forceinline__ uint32_t instruction_desc(uint32_t m, uint32_t n)
+{
+    return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
 
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
 {
@@ -201,6 +238,26 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
                      saddr(bar)),
                  "h"((uint16_t)3)
                  : "memory");
+}
+
+// The same within one CTA.
+__device__ __forceinline__ void tma_load_own(void *dst, const CUtensorMap *map, int32_t x, int32_t y, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(saddr(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(saddr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void mma_own(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_commit_own(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)) : "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -244,6 +301,34 @@ __device__ __forceinline__ void put(float *to, float x) { *to = x; }
 __device__ __forceinline__ void put(__half *to, float x) { *to = __float2half_rn(x); }
 __device__ __forceinline__ void put(__nv_bfloat16 *to, float x) { *to = __float2bfloat16_rn(x); }
 
+__device__ __forceinline__ void tmem_take8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// Two fp32 sums in a register pair: one instruction for two FMAs.
+__device__ __forceinline__ Pair pair_of(uint32_t lo, uint32_t hi)
+{
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(lo), "r"(hi));
+    return p;
+}
+__device__ __forceinline__ Pair pair_of(float x) { return pair_of(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ float pair_at(Pair p, int i) { return __uint_as_float((uint32_t)(p >> (32 * i))); }
+__device__ __forceinline__ void fma_pair(Pair &sum, Pair a, Pair b)
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ Pair mul_pair(Pair a, Pair b)
+{
+    Pair p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+    return p;
+}
 __device__ __forceinline__ void store32(void *to, const uint32_t (&v)[8])
 {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -259,38 +344,93 @@ struct Tile {
     int group, row, end, col; // first row and the group's end, first column
 };
 
+// The groups' first rows and the tiles before each, by the whole CTA, four
+// groups a thread (256 threads and more) or more of them; offsets that are out
+// of range or run backwards give empty groups.
+template <int kThreads> __device__ __forceinline__ void find_groups(Groups &s, const ProductArgs &a, int tile_rows)
+{
+    constexpr int kEach = (kMaxGroups + 1 + kThreads - 1) / kThreads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int first = tid * kEach;
+    int n[kEach], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int g = first + i;
+        n[i] = 0;
+        if (g < a.groups) {
+            const int lo = g == 0 ? 0 : min(max(a.offsets[g], 0), a.rows);
+            const int hi = a.offsets ? min(max(a.offsets[g + 1], 0), a.rows) : a.rows;
+            n[i] = hi > lo ? ceil_div(hi - lo, tile_rows) * a.col_tiles : 0;
+            s.begin[g] = lo;
+            if (g == a.groups - 1) s.begin[a.groups] = hi;
+        }
+        sum += n[i];
+    }
+    int upto = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kAll, upto, d);
+        if (lane >= d) upto += o;
+    }
+    if (lane == 31) s.warp_sum[warp] = upto;
+    __syncthreads();
+    int before = upto - sum;
+    for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        if (first + i <= a.groups) s.tiles[first + i] = before;
+        before += n[i];
+    }
+}
+
 // The tile with this number, by a whole warp.  The group is the last with no
 // more tiles before it: 32 boundaries at a time, in two steps.
-__device__ __forceinline__ Tile tile_at(const ProductSmem &sm, const ProductArgs &a, int u, int width)
+__device__ __forceinline__ Tile tile_at(const Groups &s, const ProductArgs &a, int u, int tile_rows, int width)
 {
     const int lane = threadIdx.x & 31;
     int g = (lane + 1) * 32;
-    const int block = __popc(__ballot_sync(kAll, g <= a.groups && sm.tiles[min(g, a.groups)] <= u));
+    const int block = __popc(__ballot_sync(kAll, g <= a.groups && s.tiles[min(g, a.groups)] <= u));
     g = block * 32 + lane + 1;
-    const int group = block * 32 + __popc(__ballot_sync(kAll, g <= a.groups && sm.tiles[min(g, a.groups)] <= u));
+    const int group = block * 32 + __popc(__ballot_sync(kAll, g <= a.groups && s.tiles[min(g, a.groups)] <= u));
     Tile t;
     t.group = group;
-    t.end = sm.begin[group + 1];
-    const int begin = sm.begin[group], all = ceil_div(t.end - begin, kTileRows);
+    t.end = s.begin[group + 1];
+    const int begin = s.begin[group], all = ceil_div(t.end - begin, tile_rows);
     // sweeps of kGroupRows row tiles; in a sweep the row tile moves first, so
-    // that the pairs at work share the weight's tiles
-    int r = u - sm.tiles[group], sweep = 0, m_tiles = all;
+    // that the CTAs at work share the weight's tiles
+    int r = u - s.tiles[group], sweep = 0, m_tiles = all;
     if (all > kGroupRows) {
         sweep = r / (kGroupRows * a.col_tiles);
         r -= sweep * kGroupRows * a.col_tiles;
         m_tiles = min(kGroupRows, all - sweep * kGroupRows);
     }
     const int n = m_tiles > 1 ? r / m_tiles : r;
-    t.row = begin + (sweep * kGroupRows + r - n * m_tiles) * kTileRows;
+    t.row = begin + (sweep * kGroupRows + r - n * m_tiles) * tile_rows;
     t.col = n * width;
     return t;
+}
+
+// Rows behind the last group become zeros; thread `me` of `all`.
+template <typename Out>
+__device__ __forceinline__ void zero_unused(const ProductArgs &a, int used, int64_t me, int64_t all)
+{
+    Out *out = static_cast<Out *>(a.out);
+    const int64_t from = (int64_t)used * a.cols, to = (int64_t)a.rows * a.cols;
+    constexpr int kEach = 16 / sizeof(Out);
+    const int64_t lead = ((16 - (reinterpret_cast<uintptr_t>(out + from) & 15)) & 15) / sizeof(Out);
+    const int64_t whole = min(to, from + lead), vecs = (to - whole) / kEach;
+    for (int64_t i = me; i < vecs; i += all) reinterpret_cast<uint4 *>(out + whole)[i] = make_uint4(0, 0, 0, 0);
+    if (me < kEach) {
+        if (from + me < whole) put(out + from + me, 0.0f);
+        if (whole + vecs * kEach + me < to) put(out + whole + vecs * kEach + me, 0.0f);
+    }
 }
 
 // A thread's row of finished sums.  32-byte stores where rows and columns
 // allow them; otherwise the warp turns 16 columns at a time round in shared
 // memory, so that lanes next to each other write columns next to each other.
 template <typename Out, int kCols>
-__device__ __forceinline__ void put_sums(const ProductArgs &a, const float (&sum)[kCols], float *staging, int row0, int end,
+__device__ __forceinline__ void put_sums(const ProductArgs &a, const Pair (&sum)[kCols / 2], float *staging, int row0, int end,
                                          int col0)
 {
     const int lane = threadIdx.x & 31;
@@ -306,9 +446,9 @@ __device__ __forceinline__ void put_sums(const ProductArgs &a, const float (&sum
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if constexpr (sizeof(Out) == 4)
-                    v[i] = __float_as_uint(sum[c + i]);
+                    v[i] = __float_as_uint(pair_at(sum[(c + i) / 2], i & 1));
                 else
-                    v[i] = pack2(sum[c + 2 * i], sum[c + 2 * i + 1], Out());
+                    v[i] = pack2(pair_at(sum[c / 2 + i], 0), pair_at(sum[c / 2 + i], 1), Out());
             }
             store32(to + c, v);
         }
@@ -317,7 +457,7 @@ __device__ __forceinline__ void put_sums(const ProductArgs &a, const float (&sum
 #pragma unroll
     for (int c = 0; c < kCols; c += kStagingCols) {
 #pragma unroll
-        for (int i = 0; i < kStagingCols; ++i) staging[lane * kStagingPitch + i] = sum[c + i];
+        for (int i = 0; i < kStagingCols; ++i) staging[lane * kStagingPitch + i] = pair_at(sum[(c + i) / 2], i & 1);
         __syncwarp();
         const int col = col0 + c + (lane & 15);
 #pragma unroll 4
@@ -329,18 +469,17 @@ __device__ __forceinline__ void put_sums(const ProductArgs &a, const float (&sum
 }
 
 template <typename Out, int kWidth>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    product_fp8_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_few,
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+    product_wide_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_few,
                        const __grid_constant__ CUtensorMap map_w, const ProductArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    ProductSmem &sm = *reinterpret_cast<ProductSmem *>(ring + kRingBytes);
+    WideSmem &sm = *reinterpret_cast<WideSmem *>(ring + kWideRing);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = blockIdx.x & 1; // in the pair; rank 0 leads
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     constexpr int kShareCols = kWidth / 2; // a CTA loads
-    constexpr uint32_t kStage = 2 * kShare;
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -359,50 +498,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sm.tmem_base)),
-                     "n"(kTmemCols)
+                     "n"(kWideTmem)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     grid_dependency_wait(); // the inputs may come from the kernel before on the stream
-    // the groups' first rows and the tiles before each, four groups a thread;
-    // offsets that are out of range or run backwards give empty groups
-    {
-        int first = tid * 4, n[4], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int g = first + i;
-            n[i] = 0;
-            if (g < a.groups) {
-                const int lo = g == 0 ? 0 : min(max(a.offsets[g], 0), a.rows);
-                const int hi = a.offsets ? min(max(a.offsets[g + 1], 0), a.rows) : a.rows;
-                n[i] = hi > lo ? ceil_div(hi - lo, kTileRows) * a.col_tiles : 0;
-                sm.begin[g] = lo;
-                if (g == a.groups - 1) sm.begin[a.groups] = hi;
-            }
-            sum += n[i];
-        }
-        int upto = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(kAll, upto, d);
-            if (lane >= d) upto += o;
-        }
-        if (lane == 31) sm.warp_sum[warp] = upto;
-        tc_fence_before();
-        __syncthreads();
-        int before = upto - sum;
-        for (int w = 0; w < warp; ++w) before += sm.warp_sum[w];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (first + i <= a.groups) sm.tiles[first + i] = before;
-            before += n[i];
-        }
-    }
+    tc_fence_before();
+    find_groups<kWideThreads>(sm.groups, a, kTileRows);
     __syncthreads();
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
-    const int units = sm.tiles[a.groups];
+    const int units = sm.groups.tiles[a.groups];
     volatile uint32_t *abort = &sm.abort;
 
     if (warp == 0) {
@@ -411,19 +518,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t s = 0, turn = 0;                         // ring stage, times round the ring
         bool ok = true;
         for (int u = pair; u < units && ok; u += pairs) {
-            const Tile t = tile_at(sm, a, u, kWidth);
+            const Tile t = tile_at(sm.groups, a, u, kTileRows, kWidth);
             const int left = t.end - t.row;
-            const bool few = left <= kFewRows, both = left > kHalf, has_rows = rank == 0 || both;
-            const uint32_t bytes = (few ? kFewRows * kBlock : both ? 2 * kShare : kShare) + kWidth * kBlock;
+            const bool few = left <= kRowBox, both = left > kHalf, has_rows = rank == 0 || both;
+            const uint32_t bytes = (few ? kRowBox * kBlock : both ? 2 * kShare : kShare) + kWidth * kBlock;
             const int wrow = t.group * a.cols + t.col + (int)rank * kShareCols;
             for (int b = 0; b < a.blocks; ++b) {
-                ok = *abort == 0 && (turn == 0 || mbar_wait(&sm.empty[s], (turn - 1) & 1, abort));
-                ok = __all_sync(kAll, ok);
+                ok = turn == 0 || mbar_wait_warp(&sm.empty[s], (turn - 1) & 1, abort);
                 if (!ok) break;
                 if (elect_one()) {
                     if (rank == 0) mbar_expect_tx(&sm.full[s], bytes);
                     const uint32_t bar = full0 + s * (uint32_t)sizeof(uint64_t);
-                    uint8_t *at = ring + s * kStage;
+                    uint8_t *at = ring + s * kWideStage;
                     if (has_rows) tma_load(at, few ? &map_few : &map_q, b * kBlock, t.row + (int)rank * kHalf, bar);
                     tma_load(at + kShare, &map_w, b * kBlock, wrow, bar);
                 }
@@ -441,7 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ---- MMA issuer (the leading CTA's)
         if (rank == 0) {
-            constexpr uint32_t idesc = kInstruction<kWidth>;
+            const uint32_t idesc = instruction_desc(kTileRows, kWidth);
             uint32_t s = 0, parity = 0, sum = 0;
             bool ok = true;
 #ifdef TF_TOPK_TEST_WAIT_TIMEOUT
@@ -454,7 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                          mbar_wait_warp(&sm.full[s], parity, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t ad = desc_at(ring + s * kStage), bd = desc_at(ring + s * kStage + kShare);
+                    const uint64_t ad = desc_at(ring + s * kWideStage), bd = desc_at(ring + s * kWideStage + kShare);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < kBlock / 32; ++k) // 32 steps: 32 bytes along a row
@@ -476,14 +582,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---- scaling and sums
-        constexpr int kCols = kWidth / 2; // of a thread
+        constexpr int kCols = kWidth / (kEpiWarps / 4); // of a thread
         const int q = warp & 3, h = (warp - 2) >> 2;
         const uint32_t empty0 = peer_addr(&sm.acc_empty[0], 0), empty1 = peer_addr(&sm.acc_empty[1], 0);
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + h * kCols;
         uint32_t done = 0; // accumulators taken
         bool ok = true;
         for (int u = pair; u < units && ok; u += pairs) {
-            const Tile t = tile_at(sm, a, u, kWidth);
+            const Tile t = tile_at(sm.groups, a, u, kTileRows, kWidth);
             const int row0 = t.row + (int)rank * kHalf + 32 * q, col0 = t.col + h * kCols;
             const bool has_rows = row0 < t.end;
             // a row's scales and the columns' are fetched two blocks ahead
@@ -492,12 +598,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                               ((int64_t)t.group * a.col_blocks + min(col0 / kBlock, a.col_blocks - 1)) * a.blocks;
             float r0 = rs[0], w0 = ws[0], r1 = 0.0f, w1 = 0.0f;
             if (a.blocks > 1) r1 = rs[1], w1 = ws[1];
-            float sum[kCols];
+            Pair sum[kCols / 2];
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
+            for (int i = 0; i < kCols / 2; ++i) sum[i] = 0;
             for (int b = 0; b < a.blocks; ++b, ++done) {
                 const uint32_t buf = done & 1;
-                const float f = r0 * w0;
+                const Pair f = pair_of(r0 * w0);
                 r0 = r1, w0 = w1;
                 if (b + 2 < a.blocks) r1 = rs[b + 2], w1 = ws[b + 2];
                 ok = mbar_wait_warp(&sm.acc_full[buf], (done >> 1) & 1, abort);
@@ -509,7 +615,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         uint32_t x[kChunk];
                         tmem_take(lanes + buf * kMaxWidth + c, x);
 #pragma unroll
-                        for (int i = 0; i < kChunk; ++i) sum[c + i] = fmaf(f, __uint_as_float(x[i]), sum[c + i]);
+                        for (int i = 0; i < kChunk; i += 2) fma_pair(sum[(c + i) / 2], f, pair_of(x[i], x[i + 1]));
                     }
                 }
                 tc_fence_before();
@@ -518,19 +624,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (ok && has_rows) put_sums<Out, kCols>(a, sum, sm.staging[warp - 2], row0, t.end, col0);
         }
-        // rows behind the last group
-        Out *out = static_cast<Out *>(a.out);
-        const int used = sm.begin[a.groups];
-        const int64_t from = (int64_t)used * a.cols, to = (int64_t)a.rows * a.cols;
-        constexpr int kEach = 16 / sizeof(Out);
-        const int64_t whole = min(to, from + (int64_t)((16 - (reinterpret_cast<uintptr_t>(out + from) & 15)) & 15) / (int64_t)sizeof(Out));
-        const int64_t vecs = (to - whole) / kEach;
-        const int64_t me = (int64_t)blockIdx.x * (32 * kEpiWarps) + tid - 64, all = (int64_t)gridDim.x * (32 * kEpiWarps);
-        for (int64_t i = me; i < vecs; i += all) reinterpret_cast<uint4 *>(out + whole)[i] = make_uint4(0, 0, 0, 0);
-        if (me < kEach) {
-            if (from + me < whole) put(out + from + me, 0.0f);
-            if (whole + vecs * kEach + me < to) put(out + whole + vecs * kEach + me, 0.0f);
-        }
+        zero_unused<Out>(a, sm.groups.begin[a.groups], (int64_t)blockIdx.x * (32 * kEpiWarps) + tid - 64,
+                         (int64_t)gridDim.x * (32 * kEpiWarps));
     }
     __syncwarp();
     grid_dependents_go();
@@ -543,14 +638,229 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync(); // neither CTA leaves while the other may still reach its shared memory
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kWideTmem) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- few rows
+
+__device__ __forceinline__ void copy4_async(float *to, const float *from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(saddr(to)), "l"(from) : "memory");
+}
+
+template <typename Out>
+__global__ void __launch_bounds__(kThinThreads, kThinCtas)
+    product_thin_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constant__ CUtensorMap map_w,
+                        const ProductArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    ThinSmem &sm = *reinterpret_cast<ThinSmem *>(ring + kThinRing);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int s = 0; s < kThinMostStages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int b = 0; b < kThinAccs; ++b) {
+            mbar_init(&sm.acc_full[b], 1);
+            mbar_init(&sm.acc_empty[b], kThinEpiWarps);
+        }
+        mbar_init(&sm.drain, 1);
+        sm.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_rows) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sm.tmem_base)),
+                     "n"(kThinTmem)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    grid_dependency_wait(); // the inputs may come from the kernel before on the stream
+    tc_fence_before();
+    find_groups<kThinThreads>(sm.groups, a, a.tile_rows);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    const int units = sm.groups.tiles[a.groups], ctas = gridDim.x;
+    volatile uint32_t *abort = &sm.abort;
+    const auto boxes_of = [&](const Tile &t) { return ceil_div(min(t.end - t.row, a.tile_rows), kRowBox); };
+    const uint32_t stages = a.stages, stage = kShare + a.tile_rows * kBlock;
+
+    if (warp == 0) {
+        // ---- TMA producer
+        uint32_t s = 0, turn = 0; // ring stage, times round the ring
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok; u += ctas) {
+            const Tile t = tile_at(sm.groups, a, u, a.tile_rows, a.width);
+            const int boxes = boxes_of(t), wrow = t.group * a.cols + t.col;
+            const uint32_t bytes = (uint32_t)(a.width + boxes * kRowBox) * kBlock;
+            for (int b = 0; b < a.blocks; ++b) {
+                ok = turn == 0 || mbar_wait_warp(&sm.empty[s], (turn - 1) & 1, abort);
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_expect_tx(&sm.full[s], bytes);
+                    uint8_t *at = ring + s * stage;
+                    tma_load_own(at, &map_w, b * kBlock, wrow, &sm.full[s]);
+                    for (int i = 0; i < boxes; ++i)
+                        tma_load_own(at + kShare + i * kRowBox * kBlock, &map_rows, b * kBlock, t.row + i * kRowBox, &sm.full[s]);
+                }
+                __syncwarp();
+                if (++s == stages) s = 0, ++turn;
+            }
+        }
+        // the copies land before the CTA leaves: the last fill of each stage
+        bool landed = true;
+        for (uint32_t j = 0; j < stages && landed; ++j) {
+            const uint32_t filled = j < s ? turn + 1 : turn; // times stage j was filled
+            if (filled) landed = mbar_wait(&sm.full[j], (filled - 1) & 1, nullptr);
+        }
+    } else if (warp == 1) {
+        // ---- MMA issuer
+        uint32_t s = 0, parity = 0, sum = 0;
+        bool ok = true;
+#ifdef TF_TOPK_TEST_WAIT_TIMEOUT
+        ok = mbar_wait_warp(&sm.drain, 0, abort); // nothing completes it yet: the wait runs out
+#endif
+        for (int u = blockIdx.x; u < units && ok; u += ctas) {
+            const uint32_t idesc = instruction_desc(kHalf, boxes_of(tile_at(sm.groups, a, u, a.tile_rows, a.width)) * kRowBox);
+            for (int b = 0; b < a.blocks; ++b, ++sum) {
+                const uint32_t buf = sum % kThinAccs, use = sum / kThinAccs;
+                ok = (use == 0 || mbar_wait_warp(&sm.acc_empty[buf], (use - 1) & 1, abort)) &&
+                     mbar_wait_warp(&sm.full[s], parity, abort);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t ad = desc_at(ring + s * stage), bd = desc_at(ring + s * stage + kShare);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < kBlock / 32; ++k) // 32 steps: 32 bytes along a row
+                        mma_own(tmem + buf * kThinRows, ad + k * 2, bd + k * 2, idesc, k != 0);
+                    mma_commit_own(&sm.empty[s]);
+                    mma_commit_own(&sm.acc_full[buf]);
+                }
+                __syncwarp();
+                if (++s == stages) s = 0, parity ^= 1;
+            }
+        }
+        // every product is done before the TMEM is freed
+        if (elect_one()) mma_commit_own(&sm.drain);
+        __syncwarp();
+        mbar_wait(&sm.drain, 0, nullptr);
+    } else {
+        // ---- scaling and sums: two threads per column, with eight of each sixteen
+        // rows.  A wait that gives up leaves out what it waited for, not the
+        // barriers of these warps.
+        constexpr int kMine = kRowBox / 2;
+        const int q = warp & 3, h = (warp - 2) >> 2, me = tid - 64;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + h * kMine;
+        Out *out = static_cast<Out *>(a.out);
+        // The scales of kScaleBlocks blocks at a time, for these threads
+        // together: fetched while the ones before are used, from one tile into the next.
+        int next_u = blockIdx.x, next_b = 0, fetched = 0;
+        Tile next = {};
+        if (next_u < units) next = tile_at(sm.groups, a, next_u, a.tile_rows, a.width);
+        const auto fetch = [&] {
+            if (next_u < units) {
+                constexpr int kShares = 32 * kThinEpiWarps / kThinRows, kEach = kScaleBlocks / kShares;
+                const int buf = fetched & 1, row = me % kThinRows, i0 = me / kThinRows * kEach;
+                if (row < min(next.end - next.row, a.tile_rows)) {
+                    const float *from = a.scale + (int64_t)(next.row + row) * a.blocks + next_b;
+#pragma unroll
+                    for (int i = i0; i < i0 + kEach; ++i)
+                        if (next_b + i < a.blocks) copy4_async(&sm.scale[buf][i][row], from + i);
+                }
+                if (me < 2 * kScaleBlocks) {
+                    const int i = me >> 1, block = min(next.col / kBlock + (me & 1), a.col_blocks - 1);
+                    if (next_b + i < a.blocks)
+                        copy4_async(&sm.weight_scale[buf][i][me & 1],
+                                    a.weight_scale + ((int64_t)next.group * a.col_blocks + block) * a.blocks + next_b + i);
+                }
+                next_b += kScaleBlocks;
+                if (next_b >= a.blocks) {
+                    next_b = 0;
+                    next_u += ctas;
+                    if (next_u < units) next = tile_at(sm.groups, a, next_u, a.tile_rows, a.width);
+                }
+            }
+            ++fetched;
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        fetch();
+        uint32_t done = 0; // accumulators taken
+        int used = 0;      // fetches used
+        bool ok = true;
+        for (int u = blockIdx.x; u < units; u += ctas) {
+            const Tile t = tile_at(sm.groups, a, u, a.tile_rows, a.width);
+            const int boxes = boxes_of(t), rows = min(t.end - t.row, a.tile_rows);
+            const int col = t.col + 32 * q + lane;
+            const int side = min(col / kBlock - t.col / kBlock, 1);
+            const bool in = 32 * q + lane < a.width && col < a.cols;
+            Pair sum[kThinRows / kRowBox][kMine / 2];
+#pragma unroll
+            for (int c = 0; c < kThinRows / kRowBox; ++c)
+#pragma unroll
+                for (int i = 0; i < kMine / 2; ++i) sum[c][i] = 0;
+            for (int b0 = 0; b0 < a.blocks; b0 += kScaleBlocks, ++used) {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * kThinEpiWarps) : "memory");
+                fetch();
+                const int blocks = min(kScaleBlocks, a.blocks - b0), from = used & 1;
+                for (int b = 0; b < blocks && ok; ++b, ++done) {
+                    const uint32_t buf = done % kThinAccs;
+                    const Pair w = pair_of(sm.weight_scale[from][b][side]);
+                    ok = mbar_wait_warp(&sm.acc_full[buf], (done / kThinAccs) & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < kThinRows / kRowBox; ++c) {
+                        if (c >= boxes) break;
+                        const ulonglong2 *f = reinterpret_cast<const ulonglong2 *>(&sm.scale[from][b][c * kRowBox + h * kMine]);
+                        const ulonglong2 f0 = f[0], f1 = f[1];
+                        uint32_t x[kMine];
+                        tmem_take8(lanes + buf * kThinRows + c * kRowBox, x);
+                        fma_pair(sum[c][0], mul_pair(w, f0.x), pair_of(x[0], x[1]));
+                        fma_pair(sum[c][1], mul_pair(w, f0.y), pair_of(x[2], x[3]));
+                        fma_pair(sum[c][2], mul_pair(w, f1.x), pair_of(x[4], x[5]));
+                        fma_pair(sum[c][3], mul_pair(w, f1.y), pair_of(x[6], x[7]));
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_own(&sm.acc_empty[buf]);
+                }
+            }
+            if (!ok || !in) continue;
+            Out *to = out + (int64_t)t.row * a.cols + col;
+#pragma unroll
+            for (int c = 0; c < kThinRows / kRowBox; ++c)
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    const int r = c * kRowBox + h * kMine + i;
+                    if (r < rows) put(to + (int64_t)r * a.cols, pair_at(sum[c][i / 2], i & 1));
+                }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        zero_unused<Out>(a, sm.groups.begin[a.groups], (int64_t)blockIdx.x * (32 * kThinEpiWarps) + me,
+                         (int64_t)gridDim.x * (32 * kThinEpiWarps));
+    }
+    __syncwarp();
+    grid_dependents_go();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kThinTmem) : "memory");
     }
 }
 
 // ---------------------------------------------------------------- host side
 
-constexpr size_t kSmemBytes = 1024 + (size_t)kRingBytes + sizeof(ProductSmem);
-static_assert(kSmemBytes <= 227 * 1024, "the kernel's shared memory fits one CTA");
+constexpr size_t kWideSmem = 1024 + kWideRing + sizeof(WideSmem);
+constexpr size_t kThinSmem = 1024 + kThinRing + sizeof(ThinSmem);
+static_assert(kWideSmem <= 227 * 1024 && kThinCtas * (kThinSmem + 1024) <= 228 * 1024, "the kernels' shared memory fits an SM");
 
 constexpr int kMaxDevices = 64;
 struct ProductDevice {
@@ -561,22 +871,30 @@ ProductDevice g_product_dev[kMaxDevices];
 std::mutex g_product_mutex;
 PFN_cuTensorMapEncodeTiled_v12000 g_product_encode = nullptr;
 
-using ProductKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, ProductArgs);
+using WideKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, ProductArgs);
+using ThinKernel = void (*)(CUtensorMap, CUtensorMap, ProductArgs);
 
-ProductKernel product_kernel(int32_t dtype, int width)
+WideKernel wide_kernel(int32_t dtype, int width)
 {
-    if (dtype == TF_TOPK_DTYPE_F32) return width == 256 ? product_fp8_kernel<float, 256> : product_fp8_kernel<float, 128>;
-    if (dtype == TF_TOPK_DTYPE_F16) return width == 256 ? product_fp8_kernel<__half, 256> : product_fp8_kernel<__half, 128>;
-    return width == 256 ? product_fp8_kernel<__nv_bfloat16, 256> : product_fp8_kernel<__nv_bfloat16, 128>;
+    if (dtype == TF_TOPK_DTYPE_F32) return width == 256 ? product_wide_kernel<float, 256> : product_wide_kernel<float, 128>;
+    if (dtype == TF_TOPK_DTYPE_F16) return width == 256 ? product_wide_kernel<__half, 256> : product_wide_kernel<__half, 128>;
+    return width == 256 ? product_wide_kernel<__nv_bfloat16, 256> : product_wide_kernel<__nv_bfloat16, 128>;
 }
 
-// Per device, once: the kernels' shared memory limits, the pairs the device
-// holds, and the driver's tensor-map encoder.
-int product_setup(int *pairs)
+ThinKernel thin_kernel(int32_t dtype)
 {
-    int sm_count = 0, dev = 0;
-    const int st = tf_topk_internal_device(&sm_count);
+    return dtype == TF_TOPK_DTYPE_F32   ? product_thin_kernel<float>
+           : dtype == TF_TOPK_DTYPE_F16 ? product_thin_kernel<__half>
+                                        : product_thin_kernel<__nv_bfloat16>;
+}
+
+// Per device, once: the kernels' shared memory limits, the CTA pairs the device
+// holds at a time, and the driver's tensor-map encoder.
+int product_setup(int *pairs, int *sm_count)
+{
+    const int st = tf_topk_internal_device(sm_count);
     if (st != TF_TOPK_OK) return st;
+    int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return tf_topk_internal_fail_cuda((int)e);
     if (dev >= kMaxDevices) return TF_TOPK_ERR_DEVICE;
@@ -584,15 +902,18 @@ int product_setup(int *pairs)
     if (!d.ready.load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> lock(g_product_mutex);
         if (!d.ready.load(std::memory_order_relaxed)) {
-            for (int32_t dtype : {TF_TOPK_DTYPE_BF16, TF_TOPK_DTYPE_F16, TF_TOPK_DTYPE_F32})
-                for (int width : {128, 256})
-                    if (e == cudaSuccess)
-                        e = cudaFuncSetAttribute(product_kernel(dtype, width),
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+            const auto allow = [&](const void *kernel, size_t bytes) {
+                if (e == cudaSuccess)
+                    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+            };
+            for (int32_t dtype : {TF_TOPK_DTYPE_BF16, TF_TOPK_DTYPE_F16, TF_TOPK_DTYPE_F32}) {
+                for (int width : {128, 256}) allow((const void *)wide_kernel(dtype, width), kWideSmem);
+                allow((const void *)thin_kernel(dtype), kThinSmem);
+            }
             cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3((unsigned)(sm_count / 2 * 2), 1, 1);
-            cfg.blockDim = dim3(kThreads, 1, 1);
-            cfg.dynamicSmemBytes = kSmemBytes;
+            cfg.gridDim = dim3((unsigned)(*sm_count / 2 * 2), 1, 1);
+            cfg.blockDim = dim3(kWideThreads, 1, 1);
+            cfg.dynamicSmemBytes = kWideSmem;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
             attr[0].val.clusterDim.x = 2;
@@ -601,8 +922,7 @@ int product_setup(int *pairs)
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             int n = 0;
-            if (e == cudaSuccess)
-                e = cudaOccupancyMaxActiveClusters(&n, product_kernel(TF_TOPK_DTYPE_BF16, 256), &cfg);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, wide_kernel(TF_TOPK_DTYPE_BF16, 256), &cfg);
             if (e != cudaSuccess) return tf_topk_internal_fail_cuda((int)e);
             d.pairs = n < 1 ? 1 : n;
             if (!g_product_encode) {
@@ -636,9 +956,44 @@ bool encode_map(CUtensorMap *map, const void *p, int64_t inner, int64_t outer, i
 bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 // Tiles there can be: a group's last one may be short, and groups without rows have none.
-int64_t most_units(int64_t rows, int64_t groups, int64_t cols, int width)
+int64_t most_units(int64_t rows, int64_t groups, int64_t tile_rows, int64_t col_tiles)
 {
-    return (rows / kTileRows + (rows < groups ? rows : groups)) * ((cols + width - 1) / width);
+    return (rows / tile_rows + (rows < groups ? rows : groups)) * col_tiles;
+}
+
+// Columns of a thin tile: as narrow as they can be without more rounds of the
+// CTAs, in sixteens, from 32 on, so that the rounds come out whole (with a row
+// in every group; the device knows the groups' rows, the host does not).
+int thin_width(int64_t groups, int64_t cols, int ctas)
+{
+    const int64_t rounds = (groups * ((cols + kHalf - 1) / kHalf) + ctas - 1) / ctas;
+    const int64_t tiles = rounds * ctas / groups; // of a group
+    const int64_t width = ((cols + tiles - 1) / tiles + 15) / 16 * 16;
+    return width < 32 ? 32 : width > kHalf ? kHalf : (int)width;
+}
+
+// Rows of a thin tile: all there can be, or for several groups what four times
+// the average needs, in sixteens: a group beyond reads its weight again, from
+// the L2, and rows that are not there take room from the ring.
+int thin_rows(int64_t rows, int64_t groups)
+{
+    const int64_t want = groups == 1 ? rows : (4 * rows + groups - 1) / groups;
+    const int64_t tile = ((want < rows ? want : rows) + kRowBox - 1) / kRowBox * kRowBox;
+    return tile < kThinRows ? (int)tile : kThinRows;
+}
+
+cudaLaunchConfig_t config(int64_t grid, int threads, size_t smem, void *stream, cudaLaunchAttribute *attr)
+{
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
 }
 
 } // namespace
@@ -663,7 +1018,7 @@ extern "C" int tf_topk_product_fp8(const void *q, const float *scale, int64_t ro
         return TF_TOPK_ERR_DTYPE;
     if (rows < 0 || rows > INT32_MAX - kTileRows || dim < 16 || dim % 16 != 0 || cols < 1 || groups < 1 ||
         groups > kMaxGroups || (!offsets && groups != 1) || cols > (INT32_MAX - 1024) / groups ||
-        most_units(rows, groups, cols, kHalf) > INT32_MAX / 2)
+        most_units(rows, groups, kRowBox, (cols + 31) / 32) > INT32_MAX / 2)
         return TF_TOPK_ERR_SHAPE;
     if (rows == 0) return TF_TOPK_OK;
     if (!q || !scale || !weight || !weight_scale || !out) return TF_TOPK_ERR_NULL;
@@ -671,14 +1026,9 @@ extern "C" int tf_topk_product_fp8(const void *q, const float *scale, int64_t ro
     if (!aligned(q, 16) || !aligned(weight, 16) || !aligned(scale, 4) || !aligned(weight_scale, 4) ||
         !aligned(offsets, 4) || !aligned(out, size))
         return TF_TOPK_ERR_ALIGN;
-    int pairs = 0;
-    const int st = product_setup(&pairs);
+    int pairs = 0, sms = 0;
+    const int st = product_setup(&pairs, &sms);
     if (st != TF_TOPK_OK) return st;
-    const int width = cols <= kHalf ? 128 : 256;
-    CUtensorMap map_q, map_few, map_w;
-    if (!encode_map(&map_q, q, dim, rows, kHalf) || !encode_map(&map_few, q, dim, rows, kFewRows) ||
-        !encode_map(&map_w, weight, dim, (int64_t)groups * cols, width / 2))
-        return tf_topk_internal_fail_cuda((int)cudaErrorInvalidValue);
     ProductArgs a;
     a.scale = scale;
     a.weight_scale = weight_scale;
@@ -689,20 +1039,29 @@ extern "C" int tf_topk_product_fp8(const void *q, const float *scale, int64_t ro
     a.groups = groups;
     a.blocks = (dim + kBlock - 1) / kBlock;
     a.col_blocks = (int32_t)((cols + kBlock - 1) / kBlock);
-    a.col_tiles = (int32_t)((cols + width - 1) / width);
     a.wide_stores = aligned(out, 32) && (size_t)cols * size % 32 == 0;
-    const int64_t units = most_units(rows, groups, cols, width);
+    const int64_t active = rows < groups ? rows : groups; // groups that may have rows
+    const bool thin = rows <= kThinRows * active;
+    a.width = thin ? thin_width(active, cols, kThinCtas * sms) : cols <= kHalf ? 128 : 256;
+    a.tile_rows = thin ? thin_rows(rows, active) : kTileRows;
+    const int fit = (int)(kThinRing / (kShare + a.tile_rows * kBlock));
+    a.stages = fit < kThinMostStages ? fit : kThinMostStages;
+    a.col_tiles = (int32_t)((cols + a.width - 1) / a.width);
+    CUtensorMap map_q, map_few, map_w;
+    if (!encode_map(&map_few, q, dim, rows, kRowBox) || (!thin && !encode_map(&map_q, q, dim, rows, kHalf)) ||
+        !encode_map(&map_w, weight, dim, (int64_t)groups * cols, thin ? a.width : a.width / 2))
+        return tf_topk_internal_fail_cuda((int)cudaErrorInvalidValue);
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * (units < pairs ? units : pairs)), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, product_kernel(dtype, width), map_q, map_few, map_w, a);
+    cudaError_t e;
+    if (thin) {
+        const int64_t units = most_units(rows, groups, a.tile_rows, a.col_tiles);
+        const cudaLaunchConfig_t cfg = config(units < kThinCtas * sms ? units : kThinCtas * sms, kThinThreads, kThinSmem, stream, attr);
+        e = cudaLaunchKernelEx(&cfg, thin_kernel(dtype), map_few, map_w, a);
+    } else {
+        const int64_t units = most_units(rows, groups, kTileRows, a.col_tiles);
+        const cudaLaunchConfig_t cfg = config(2 * (units < pairs ? units : pairs), kWideThreads, kWideSmem, stream, attr);
+        e = cudaLaunchKernelEx(&cfg, wide_kernel(dtype, a.width), map_q, map_few, map_w, a);
+    }
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? TF_TOPK_OK : tf_topk_internal_fail_cuda((int)e);
 }
