@@ -10,12 +10,18 @@
 //   x[c] = -inf                                               if c is not allowed
 // in this order, each step rounded to 32 bits, the result once to its type.
 //
-// A CTA takes a chunk of a row's columns: it counts the request's tokens that
-// fall into the chunk in shared memory (a word per column: the answer's count,
-// the top bit for the prompt), then reads, changes and writes the chunk.  What
-// bounds it is reading and writing the logits; every chunk reads the row's
-// tokens again, from the L2, which is why a chunk is as wide as shared memory
-// allows once there are CTAs enough.
+// Two kernels.  copy_kernel reads and writes the logits, with the mask: that is
+// what bounds the whole.  name_kernel counts, in a table in shared memory, which
+// columns a row's tokens and biases name, and how often, while the copy runs; when
+// the copy is done it writes those columns again.  (In one kernel, with every
+// CTA counting for its own columns, the counting took longer than the copy: 99
+// us for 256 x 248320 with 4000 tokens against 60, of which the copy is 40, 0.94
+// of the copy bandwidth.)
+//
+// The table: for up to kHashed tokens and biases a hash table of the columns, one
+// CTA per row; for more, one word per column, the columns dealt out to several
+// CTAs in turn (common tokens are neighbours), each of which reads all of the
+// row's tokens.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -33,11 +39,17 @@ int tf_topk_internal_device(int *sm_count);
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kMostChunk = 16384; // columns
-constexpr int kLeastChunk = 2048;
-constexpr int kPad = 16;          // words beside a chunk: its first vector may start off the 16-byte boundary
-constexpr uint32_t kPrompt = 1u << 31;
+constexpr int kCopyThreads = 256;
+constexpr int kStep = 4; // vectors of a thread
+constexpr int kNameThreads = 1024;
+constexpr int kBatch = 4;              // loads of a thread at once
+constexpr int kHashed = 8192;          // tokens and biases that a hash table holds, in twice the places
+constexpr int kMostPlaces = 32768;     // of a table without a hash: 192 KB with biases
+constexpr int kLeastPlaces = 256;
+constexpr int kMostShares = 16;        // of a row's columns, for the sake of the SMs
+constexpr uint32_t kNone = 0xFFFFFFFFu;
+constexpr uint32_t kPrompt = 1u << 31, kBias = 1u << 30; // of a column's word; the answer's count below
+constexpr int kMostWidth = 1 << 29;
 
 struct PenaltyArgs {
     const void *logits;
@@ -49,7 +61,11 @@ struct PenaltyArgs {
     const uint32_t *allowed;
     int64_t cols, stride, out_stride, token_stride, bias_stride, allowed_stride;
     int32_t width, biases; // of a row
-    int32_t chunk, chunks; // columns of a chunk, chunks of a row
+    int32_t chunks;        // copy: CTAs of a row
+    int32_t places;        // name: of the table, a power of two
+    int32_t shares;        // name: CTAs of a row, a power of two
+    int32_t hashed;        // name: the table is a hash table
+    int32_t copied;        // name: a copy runs before
 };
 
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -62,171 +78,212 @@ __device__ __forceinline__ void put(float &to, float x) { to = x; }
 __device__ __forceinline__ void put(__half &to, float x) { to = __float2half_rn(x); }
 __device__ __forceinline__ void put(__nv_bfloat16 &to, float x) { to = __float2bfloat16_rn(x); }
 
+// ---------------------------------------------------------------- the copy
+
+template <typename T> union Piece {
+    uint4 raw;
+    T v[16 / sizeof(T)];
+    __device__ Piece() {}
+};
+
+// A CTA copies up to kCopyThreads * kStep vectors of a row; out may be the input itself.
+template <typename T> __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const PenaltyArgs a)
+{
+    grid_dependency_wait();
+    grid_dependents_go();
+    constexpr int kN = 16 / sizeof(T), kChunk = kCopyThreads * kStep * kN;
+    const int tid = threadIdx.x;
+    const uint32_t row = blockIdx.x / (uint32_t)a.chunks;
+    const int64_t c0 = (int64_t)(blockIdx.x - row * (uint32_t)a.chunks) * kChunk;
+    const int cols = (int)min((int64_t)kChunk, a.cols - c0);
+    const T *in = static_cast<const T *>(a.logits) + row * a.stride + c0;
+    T *out = static_cast<T *>(a.out) + row * a.out_stride + c0;
+    const uint32_t *allowed = a.allowed ? a.allowed + row * a.allowed_stride + (c0 >> 5) : nullptr; // chunks start on words
+    // whole vectors from the first 16-byte boundary on, where input and output have it in the same place
+    const int off = (int)((reinterpret_cast<uintptr_t>(in) & 15) / sizeof(T));
+    const bool vec = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+    const int head = vec ? min(cols, (kN - off) % kN) : cols;
+    const int vecs = (cols - head) / kN;
+    Piece<T> x[kStep];
+    uint32_t low[kStep], high[kStep]; // the mask's words of a vector
+#pragma unroll
+    for (int s = 0; s < kStep; ++s) {
+        const int i = tid + s * kCopyThreads, c = head + i * kN;
+        low[s] = high[s] = kNone;
+        if (i >= vecs) continue;
+        x[s].raw = *reinterpret_cast<const uint4 *>(in + c);
+        if (allowed) {
+            low[s] = allowed[c >> 5];
+            if (head % kN) high[s] = allowed[(c + kN - 1) >> 5];
+        }
+    }
+    T least;
+    put(least, -INFINITY);
+#pragma unroll
+    for (int s = 0; s < kStep; ++s) {
+        const int i = tid + s * kCopyThreads, c = head + i * kN;
+        if (i >= vecs) continue;
+        if (allowed) {
+            const uint32_t bits = __funnelshift_r(low[s], high[s], (uint32_t)c & 31);
+            if ((bits & ((1u << kN) - 1)) != (1u << kN) - 1) {
+#pragma unroll
+                for (int j = 0; j < kN; ++j)
+                    if (!(bits >> j & 1)) x[s].v[j] = least;
+            }
+        }
+        *reinterpret_cast<uint4 *>(out + c) = x[s].raw;
+    }
+    const auto one = [&](int c) { out[c] = !allowed || (allowed[c >> 5] >> (c & 31) & 1) ? in[c] : least; };
+    for (int c = tid; c < head; c += kCopyThreads) one(c);
+    for (int c = head + vecs * kN + tid; c < cols; c += kCopyThreads) one(c);
+}
+
+// ---------------------------------------------------------------- the named columns
+
 // What a request asks for.
 struct Request {
     float repetition, presence, frequency;
-    const float *bias;
 };
 
-template <typename T> __device__ __forceinline__ T changed(T logit, uint32_t word, uint32_t bias, const Request &r)
+template <typename T> __device__ __forceinline__ T changed(T logit, uint32_t word, float bias, const Request &r)
 {
     float x = as_float(logit);
-    if (word) x = x > 0.0f ? __fdiv_rn(x, r.repetition) : __fmul_rn(x, r.repetition);
-    const uint32_t n = word & ~kPrompt;
+    if (word & ~kBias) x = x > 0.0f ? __fdiv_rn(x, r.repetition) : __fmul_rn(x, r.repetition);
+    const uint32_t n = word & ~(kPrompt | kBias);
     if (n) x = __fsub_rn(__fsub_rn(x, __fmul_rn(r.frequency, (float)n)), r.presence);
-    if (bias) x = __fadd_rn(x, r.bias[bias - 1]);
+    if (word & kBias) x = __fadd_rn(x, bias);
     T out;
     put(out, x);
     return out;
 }
 
-template <typename T> __global__ void __launch_bounds__(kThreads) penalize_kernel(const PenaltyArgs a)
+template <typename T, bool kHash> __global__ void __launch_bounds__(kNameThreads) name_kernel(const PenaltyArgs a)
 {
     extern __shared__ uint4 smem[];
-    grid_dependency_wait();
-    grid_dependents_go();
+    // A copy before has waited for what comes before it, so that all but the
+    // logits may be read while it runs.
+    if (!a.copied) {
+        grid_dependency_wait();
+        grid_dependents_go();
+    }
     const int tid = threadIdx.x;
-    const int64_t row = blockIdx.x / a.chunks;
-    const int64_t c0 = (int64_t)(blockIdx.x - row * a.chunks) * a.chunk;
-    const int cols = (int)min((int64_t)a.chunk, a.cols - c0); // of this chunk
-    const T *in = static_cast<const T *>(a.logits) + row * a.stride + c0;
-    T *out = static_cast<T *>(a.out) + row * a.out_stride + c0;
-    const uint32_t *allowed = a.allowed ? a.allowed + row * a.allowed_stride : nullptr;
-
-    // whole vectors from the first 16-byte boundary on, where input and output have it in the same place
-    constexpr int kN = 16 / sizeof(T);
-    const int off = (int)((reinterpret_cast<uintptr_t>(in) & 15) / sizeof(T));
-    const bool vec = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-    const int head = vec ? min(cols, (kN - off) % kN) : cols;
-    const int vecs = (cols - head) / kN;
-
-    // a column's words stand at base + column, so that a vector's words are whole 16 bytes
-    const int base = kN - head % kN; // 1..kN
-    uint32_t *words = reinterpret_cast<uint32_t *>(smem);
-    uint16_t *places = reinterpret_cast<uint16_t *>(words + a.chunk + kPad);
+    const uint32_t row = kHash ? blockIdx.x : blockIdx.x / (uint32_t)a.shares;
+    const uint32_t share = kHash ? 0 : blockIdx.x & (uint32_t)(a.shares - 1);
+    const int shift = kHash ? 0 : __ffs(a.shares) - 1, bits = __ffs(a.places) - 1;
+    const uint32_t cols = (uint32_t)a.cols;
+    uint32_t *words = reinterpret_cast<uint32_t *>(smem);                  // [places]
+    uint32_t *keys = words + a.places;                                     // hash: [places], the columns
+    uint16_t *last = reinterpret_cast<uint16_t *>(keys + (kHash ? a.places : 0)); // [places]: of a column's last bias, from 1
     Request r;
     r.repetition = a.repetition ? a.repetition[row] : 1.0f;
     r.presence = a.presence ? a.presence[row] : 0.0f;
     r.frequency = a.frequency ? a.frequency[row] : 0.0f;
-    r.bias = a.biases > 0 ? a.bias_value + row * a.bias_stride : nullptr;
     int length = a.lengths ? min(max(a.lengths[row], 0), a.width) : a.width;
-    if (r.repetition == 1.0f && r.presence == 0.0f && r.frequency == 0.0f) length = 0; // asks for none
     const int prompt = a.prompts ? a.prompts[row] : 0;
-    const bool counts = length > 0, biases = a.biases > 0;
-    if (counts) {
-        for (int i = tid; i < (a.chunk + kPad) / 4; i += kThreads) smem[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < a.places / 4; i += kNameThreads) {
+        smem[i] = make_uint4(0, 0, 0, 0);
+        if (kHash) smem[i + a.places / 4] = make_uint4(kNone, kNone, kNone, kNone);
     }
-    if (biases) {
-        uint4 *p = reinterpret_cast<uint4 *>(places);
-        for (int i = tid; i < (a.chunk + kPad) / 8; i += kThreads) p[i] = make_uint4(0, 0, 0, 0);
-    }
-    __syncthreads();
-    if (counts) {
-        const int32_t *tokens = a.tokens + row * a.token_stride;
-        const auto note = [&](int i, int32_t token) {
-            const int64_t c = token - c0;
-            if (c < 0 || c >= cols) return;
-            if (i < prompt)
-                atomicOr(&words[base + c], kPrompt);
-            else
-                atomicAdd(&words[base + c], 1u);
-        };
-        const int lead = min(length, (int)((4 - (reinterpret_cast<uintptr_t>(tokens) / 4 & 3)) & 3));
-        const int quads = (length - lead) / 4;
-        if (tid < lead) note(tid, tokens[tid]);
-#pragma unroll 4
-        for (int i = tid; i < quads; i += kThreads) {
-            const int4 t = *reinterpret_cast<const int4 *>(tokens + lead + 4 * i);
-            const int at = lead + 4 * i;
-            note(at, t.x), note(at + 1, t.y), note(at + 2, t.z), note(at + 3, t.w);
-        }
-        for (int i = lead + 4 * quads + tid; i < length; i += kThreads) note(i, tokens[i]);
-    }
-    if (biases) {
-        // the last entry of a token counts
-        for (int i = tid; i < a.biases; i += kThreads) {
-            const int64_t c = a.bias_token[row * a.bias_stride + i] - c0;
-            if (c < 0 || c >= cols) continue;
-            uint16_t *p = &places[base + c], seen = *p;
-            while (seen < (uint16_t)(i + 1)) {
-                const uint16_t was = atomicCAS(p, seen, (uint16_t)(i + 1));
-                if (was == seen) break;
-                seen = was;
-            }
-        }
-    }
+    if (a.biases > 0)
+        for (int i = tid; i < a.places / 8; i += kNameThreads) reinterpret_cast<uint4 *>(last)[i] = make_uint4(0, 0, 0, 0);
+    if (r.repetition == 1.0f && r.presence == 0.0f && r.frequency == 0.0f) length = 0; // asks for none
     __syncthreads();
 
-    T least;
-    put(least, -INFINITY);
-    const auto allow = [&](int c) { return !allowed || (allowed[(c0 + c) >> 5] >> ((c0 + c) & 31) & 1); };
-    const auto one = [&](int c) {
-        T x = in[c];
-        const uint32_t w = counts ? words[base + c] : 0, b = biases ? places[base + c] : 0;
-        if (w | b) x = changed(x, w, b, r);
-        out[c] = allow(c) ? x : least;
+    // the place of a column in the table; the table is never full
+    const auto place_of = [&](uint32_t c) {
+        if (!kHash) return c >> shift;
+        uint32_t h = (c * 2654435769u) >> (32 - bits);
+        for (int i = 0; i < a.places; ++i) {
+            const uint32_t k = keys[h];
+            if (k == c) break;
+            if (k == kNone) {
+                const uint32_t was = atomicCAS(&keys[h], kNone, c);
+                if (was == kNone || was == c) break;
+            }
+            h = (h + 1) & (uint32_t)(a.places - 1);
+        }
+        return h;
     };
-    for (int c = tid; c < head; c += kThreads) one(c);
-    for (int c = head + vecs * kN + tid; c < cols; c += kThreads) one(c);
-    constexpr int kStep = 4;
-    for (int i0 = tid; i0 < vecs; i0 += kStep * kThreads) {
-        union Piece {
-            uint4 raw;
-            T v[kN];
-            __device__ Piece() {}
-        } x[kStep];
-        uint32_t bits[kStep];
+    const auto mine = [&](int32_t token) { // a negative token is no column
+        return (uint32_t)token < cols && (kHash || ((uint32_t)token & (uint32_t)(a.shares - 1)) == share);
+    };
+    if (length > 0) {
+        const int32_t *tokens = a.tokens + row * a.token_stride;
+        const auto note = [&](int i, int32_t token) {
+            if (!mine(token)) return;
+            const uint32_t p = place_of((uint32_t)token);
+            if (i < prompt)
+                atomicOr(&words[p], kPrompt);
+            else
+                atomicAdd(&words[p], 1u);
+        };
+        const int lead = min(length, (int)((4 - (reinterpret_cast<uintptr_t>(tokens) / 4 & 3)) & 3)); // before the first 16 bytes
+        const int quads = (length - lead) / 4;
+        const int4 *vecs = reinterpret_cast<const int4 *>(tokens + lead);
+        for (int i0 = tid; i0 < quads; i0 += kBatch * kNameThreads) {
+            int4 t[kBatch];
 #pragma unroll
-        for (int s = 0; s < kStep; ++s) {
-            const int i = i0 + s * kThreads, c = head + i * kN;
-            bits[s] = 0xFFFFFFFFu;
-            if (i >= vecs) continue;
-            x[s].raw = *reinterpret_cast<const uint4 *>(in + c);
-            if (allowed) {
-                const int64_t at = c0 + c;
-                const uint32_t lo = allowed[at >> 5], hi = allowed[(at + kN - 1) >> 5];
-                bits[s] = __funnelshift_r(lo, hi, (uint32_t)(at & 31));
+            for (int s = 0; s < kBatch; ++s)
+                t[s] = i0 + s * kNameThreads < quads ? vecs[i0 + s * kNameThreads] : make_int4(-1, -1, -1, -1);
+#pragma unroll
+            for (int s = 0; s < kBatch; ++s) {
+                const int at = lead + 4 * (i0 + s * kNameThreads);
+                note(at, t[s].x), note(at + 1, t[s].y), note(at + 2, t[s].z), note(at + 3, t[s].w);
             }
         }
-#pragma unroll
-        for (int s = 0; s < kStep; ++s) {
-            const int i = i0 + s * kThreads, c = head + i * kN;
-            if (i >= vecs) continue;
-            const int at = base + c; // a multiple of kN
-            uint32_t any = 0;
-            if (counts) {
-#pragma unroll
-                for (int j = 0; j < kN; j += 4) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(words + at + j);
-                    any |= w.x | w.y | w.z | w.w;
-                }
-            }
-            if (biases) {
-                const uint2 p = *reinterpret_cast<const uint2 *>(places + at);
-                any |= p.x | p.y;
-                if (kN == 8) {
-                    const uint2 o = *reinterpret_cast<const uint2 *>(places + at + 4);
-                    any |= o.x | o.y;
-                }
-            }
-            if (any) {
-#pragma unroll
-                for (int j = 0; j < kN; ++j) {
-                    const uint32_t w = counts ? words[at + j] : 0, b = biases ? places[at + j] : 0;
-                    if (w | b) x[s].v[j] = changed(x[s].v[j], w, b, r);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-                if (!(bits[s] >> j & 1)) x[s].v[j] = least;
-            *reinterpret_cast<uint4 *>(out + c) = x[s].raw;
+        if (tid < lead) note(tid, tokens[tid]);
+        const int rest = lead + 4 * quads + tid;
+        if (rest < length) note(rest, tokens[rest]); // up to three
+    }
+    const int32_t *bias_token = a.bias_token + (a.biases > 0 ? row * a.bias_stride : 0);
+    for (int i = tid; i < a.biases; i += kNameThreads) {
+        const int32_t token = bias_token[i];
+        if (!mine(token)) continue;
+        const uint32_t p = place_of((uint32_t)token);
+        atomicOr(&words[p], kBias);
+        uint16_t seen = last[p]; // the last entry of a column counts
+        while (seen < (uint16_t)(i + 1)) {
+            const uint16_t was = atomicCAS(&last[p], seen, (uint16_t)(i + 1));
+            if (was == seen) break;
+            seen = was;
         }
+    }
+    __syncthreads();
+    if (a.copied) {
+        grid_dependency_wait();
+        grid_dependents_go();
+    }
+    // Where out is the input itself, the copy has left a column as it was, or it is not allowed.
+    const T *in = static_cast<const T *>(a.logits) + row * a.stride;
+    T *out = static_cast<T *>(a.out) + row * a.out_stride;
+    const uint32_t *allowed = a.allowed ? a.allowed + row * a.allowed_stride : nullptr;
+    const float *bias_value = a.bias_value + (a.biases > 0 ? row * a.bias_stride : 0);
+    for (int p0 = tid; p0 < a.places; p0 += kBatch * kNameThreads) {
+        uint32_t word[kBatch], c[kBatch], mask[kBatch];
+        T x[kBatch];
+        float bias[kBatch];
+#pragma unroll
+        for (int s = 0; s < kBatch; ++s) {
+            const int p = p0 + s * kNameThreads;
+            word[s] = p < a.places ? words[p] : 0;
+            if (word[s] == 0) continue;
+            c[s] = kHash ? keys[p] : ((uint32_t)p << shift) | share;
+            x[s] = in[c[s]];
+            mask[s] = allowed ? allowed[c[s] >> 5] : kNone;
+            bias[s] = word[s] & kBias ? bias_value[last[p] - 1] : 0.0f;
+        }
+#pragma unroll
+        for (int s = 0; s < kBatch; ++s)
+            if (word[s] != 0 && (mask[s] >> (c[s] & 31) & 1)) out[c[s]] = changed(x[s], word[s], bias[s], r);
     }
 }
 
 // ---------------------------------------------------------------- host side
 
-constexpr size_t smem_bytes(int chunk, bool biases) { return (size_t)(chunk + kPad) * (biases ? 6 : 4); }
+constexpr size_t table_bytes(int places, bool hashed, bool biases)
+{
+    return (size_t)places * (4 + (hashed ? 4 : 0) + (biases ? 2 : 0));
+}
 
 constexpr int kMaxDevices = 64;
 std::atomic<bool> g_ready[kMaxDevices];
@@ -234,11 +291,31 @@ std::mutex g_mutex;
 
 using PenaltyKernel = void (*)(PenaltyArgs);
 
-PenaltyKernel kernel_for(int32_t dtype)
+PenaltyKernel copy_for(int32_t dtype)
 {
-    return dtype == TF_TOPK_DTYPE_F32   ? penalize_kernel<float>
-           : dtype == TF_TOPK_DTYPE_F16 ? penalize_kernel<__half>
-                                        : penalize_kernel<__nv_bfloat16>;
+    return dtype == TF_TOPK_DTYPE_F32 ? copy_kernel<float> : dtype == TF_TOPK_DTYPE_F16 ? copy_kernel<__half> : copy_kernel<__nv_bfloat16>;
+}
+
+PenaltyKernel name_for(int32_t dtype, bool hashed)
+{
+    if (dtype == TF_TOPK_DTYPE_F32) return hashed ? name_kernel<float, true> : name_kernel<float, false>;
+    if (dtype == TF_TOPK_DTYPE_F16) return hashed ? name_kernel<__half, true> : name_kernel<__half, false>;
+    return hashed ? name_kernel<__nv_bfloat16, true> : name_kernel<__nv_bfloat16, false>;
+}
+
+cudaError_t launch(PenaltyKernel kernel, int64_t grid, int threads, size_t smem, const PenaltyArgs &a, void *stream)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
@@ -247,6 +324,8 @@ bool bad_stride(int64_t stride, int64_t width, int64_t rows)
 {
     return stride < width || (rows > 0 && stride > INT64_MAX / 8 / rows);
 }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 } // namespace
 
@@ -260,10 +339,10 @@ extern "C" int tf_topk_penalize(const void *logits, int32_t dtype, int64_t rows,
     if (dtype != TF_TOPK_DTYPE_BF16 && dtype != TF_TOPK_DTYPE_F16 && dtype != TF_TOPK_DTYPE_F32)
         return TF_TOPK_ERR_DTYPE;
     if (rows < 0 || cols < 1 || cols > INT32_MAX || bad_stride(row_stride, cols, rows) ||
-        bad_stride(out_stride, cols, rows) || width < 0 || (width > 0 && bad_stride(token_stride, width, rows)) ||
-        biases < 0 || biases > TF_TOPK_PENALTY_MAX_BIASES || (biases > 0 && bad_stride(bias_stride, biases, rows)) ||
-        (allowed && bad_stride(allowed_stride, (cols + 31) / 32, rows)) ||
-        rows > INT32_MAX / ((cols + kLeastChunk - 1) / kLeastChunk))
+        bad_stride(out_stride, cols, rows) || width < 0 || width > kMostWidth ||
+        (width > 0 && bad_stride(token_stride, width, rows)) || biases < 0 || biases > TF_TOPK_PENALTY_MAX_BIASES ||
+        (biases > 0 && bad_stride(bias_stride, biases, rows)) ||
+        (allowed && bad_stride(allowed_stride, ceil_div(cols, 32), rows)) || rows > INT32_MAX / ceil_div(cols, 1024))
         return TF_TOPK_ERR_SHAPE;
     if (rows == 0) return TF_TOPK_OK;
     if (!logits || !out || (width > 0 && !tokens) || (biases > 0 && (!bias_token || !bias_value))) return TF_TOPK_ERR_NULL;
@@ -280,9 +359,10 @@ extern "C" int tf_topk_penalize(const void *logits, int32_t dtype, int64_t rows,
     if (e == cudaSuccess && !g_ready[dev].load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> lock(g_mutex);
         for (int32_t d : {TF_TOPK_DTYPE_BF16, TF_TOPK_DTYPE_F16, TF_TOPK_DTYPE_F32})
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(kernel_for(d), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem_bytes(kMostChunk, true));
+            for (bool hashed : {false, true})
+                if (e == cudaSuccess)
+                    e = cudaFuncSetAttribute(name_for(d, hashed), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)table_bytes(hashed ? 2 * kHashed : kMostPlaces, hashed, true));
         if (e == cudaSuccess) g_ready[dev].store(true, std::memory_order_release);
     }
     if (e != cudaSuccess) return tf_topk_internal_fail_cuda((int)e);
@@ -306,21 +386,26 @@ extern "C" int tf_topk_penalize(const void *logits, int32_t dtype, int64_t rows,
     a.allowed_stride = allowed_stride;
     a.width = width;
     a.biases = biases;
-    // the widest chunks that still give every SM two CTAs
-    a.chunk = kMostChunk;
-    while (a.chunk > kLeastChunk && rows * ((cols + a.chunk - 1) / a.chunk) < 2 * sm_count) a.chunk /= 2;
-    a.chunks = (int32_t)((cols + a.chunk - 1) / a.chunk);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows * a.chunks), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = width > 0 || biases > 0 ? smem_bytes(a.chunk, biases > 0) : 0;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kernel_for(dtype), a);
+    a.chunks = (int32_t)ceil_div(cols, (int64_t)(kCopyThreads * kStep * 16) / (int64_t)size);
+    // nothing to copy where the logits change in place without a mask
+    a.copied = out != logits || allowed != nullptr;
+    if (a.copied) e = launch(copy_for(dtype), rows * a.chunks, kCopyThreads, 0, a, stream);
+    const bool asked = width > 0 && (repetition || presence || frequency);
+    if (!asked) a.width = 0;
+    const int64_t names = (int64_t)a.width + biases;
+    if (e == cudaSuccess && names > 0) {
+        a.hashed = names <= kHashed;
+        a.shares = 1;
+        a.places = kLeastPlaces;
+        if (a.hashed) {
+            while (a.places < 2 * names) a.places *= 2;
+        } else {
+            // as few CTAs as hold the columns, each of which reads all tokens, but one per SM
+            while (a.shares * (int64_t)kMostPlaces < cols || (rows * a.shares < sm_count && a.shares < kMostShares)) a.shares *= 2;
+            while (a.places * (int64_t)a.shares < cols) a.places *= 2;
+        }
+        e = launch(name_for(dtype, a.hashed), rows * a.shares, kNameThreads, table_bytes(a.places, a.hashed, biases > 0), a, stream);
+    }
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? TF_TOPK_OK : tf_topk_internal_fail_cuda((int)e);
 }

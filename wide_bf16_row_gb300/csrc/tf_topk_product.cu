@@ -59,7 +59,10 @@ constexpr uint32_t kWideRing = kStages * kWideStage, kThinRing = 92 * 1024;
 constexpr int kThinCtas = 2; // of an SM: while one waits for its loads the other's products run
 constexpr int kMaxGroups = TF_TOPK_ROUTE_MAX_EXPERTS;
 constexpr int kEpiWarps = 8;
-constexpr int kWideThreads = 32 * (2 + kEpiWarps);
+// A warpgroup for TMA and MMA and two that scale.  Those hold 128 sums a
+// thread, so registers move over to them: 128 * 72 + 256 * 216 = 384 * 168.
+constexpr int kWideThreads = 32 * (4 + kEpiWarps);
+constexpr int kFrontRegs = 72, kEpiRegs = 216;
 constexpr int kWideTmem = 2 * kMaxWidth;
 constexpr int kChunk = 16;       // accumulator columns a thread takes at a time
 constexpr int kStagingCols = 16; // columns a warp turns round at a time, where its stores need it
@@ -512,78 +515,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     const int units = sm.groups.tiles[a.groups];
     volatile uint32_t *abort = &sm.abort;
 
-    if (warp == 0) {
-        // ---- TMA producer
-        const uint32_t full0 = peer_addr(&sm.full[0], 0); // the leading CTA's barriers
-        uint32_t s = 0, turn = 0;                         // ring stage, times round the ring
-        bool ok = true;
-        for (int u = pair; u < units && ok; u += pairs) {
-            const Tile t = tile_at(sm.groups, a, u, kTileRows, kWidth);
-            const int left = t.end - t.row;
-            const bool few = left <= kRowBox, both = left > kHalf, has_rows = rank == 0 || both;
-            const uint32_t bytes = (few ? kRowBox * kBlock : both ? 2 * kShare : kShare) + kWidth * kBlock;
-            const int wrow = t.group * a.cols + t.col + (int)rank * kShareCols;
-            for (int b = 0; b < a.blocks; ++b) {
-                ok = turn == 0 || mbar_wait_warp(&sm.empty[s], (turn - 1) & 1, abort);
-                if (!ok) break;
-                if (elect_one()) {
-                    if (rank == 0) mbar_expect_tx(&sm.full[s], bytes);
-                    const uint32_t bar = full0 + s * (uint32_t)sizeof(uint64_t);
-                    uint8_t *at = ring + s * kWideStage;
-                    if (has_rows) tma_load(at, few ? &map_few : &map_q, b * kBlock, t.row + (int)rank * kHalf, bar);
-                    tma_load(at + kShare, &map_w, b * kBlock, wrow, bar);
-                }
-                __syncwarp();
-                if (++s == kStages) s = 0, ++turn;
-            }
-        }
-        // both CTAs' copies land before the pair leaves: the last fill of
-        // each stage (the leader's barrier counts both CTAs' bytes)
-        bool landed = rank == 0;
-        for (uint32_t j = 0; j < kStages && landed; ++j) {
-            const uint32_t filled = j < s ? turn + 1 : turn; // times stage j was filled
-            if (filled) landed = mbar_wait(&sm.full[j], (filled - 1) & 1, nullptr);
-        }
-    } else if (warp == 1) {
-        // ---- MMA issuer (the leading CTA's)
-        if (rank == 0) {
-            const uint32_t idesc = instruction_desc(kTileRows, kWidth);
-            uint32_t s = 0, parity = 0, sum = 0;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFrontRegs));
+        if (warp == 0) {
+            // ---- TMA producer
+            const uint32_t full0 = peer_addr(&sm.full[0], 0); // the leading CTA's barriers
+            uint32_t s = 0, turn = 0;                         // ring stage, times round the ring
             bool ok = true;
-#ifdef TF_TOPK_TEST_WAIT_TIMEOUT
-            ok = mbar_wait_warp(&sm.drain, 0, abort); // nothing completes it yet: the wait runs out
-#endif
             for (int u = pair; u < units && ok; u += pairs) {
-                for (int b = 0; b < a.blocks; ++b, ++sum) {
-                    const uint32_t buf = sum & 1, use = sum >> 1;
-                    ok = (use == 0 || mbar_wait_warp(&sm.acc_empty[buf], (use - 1) & 1, abort)) &&
-                         mbar_wait_warp(&sm.full[s], parity, abort);
+                const Tile t = tile_at(sm.groups, a, u, kTileRows, kWidth);
+                const int left = t.end - t.row;
+                const bool few = left <= kRowBox, both = left > kHalf, has_rows = rank == 0 || both;
+                const uint32_t bytes = (few ? kRowBox * kBlock : both ? 2 * kShare : kShare) + kWidth * kBlock;
+                const int wrow = t.group * a.cols + t.col + (int)rank * kShareCols;
+                for (int b = 0; b < a.blocks; ++b) {
+                    ok = turn == 0 || mbar_wait_warp(&sm.empty[s], (turn - 1) & 1, abort);
                     if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t ad = desc_at(ring + s * kWideStage), bd = desc_at(ring + s * kWideStage + kShare);
                     if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < kBlock / 32; ++k) // 32 steps: 32 bytes along a row
-                            mma_pair(tmem + buf * kMaxWidth, ad + k * 2, bd + k * 2, idesc, k != 0);
-                        mma_commit_pair(&sm.empty[s]);
-                        mma_commit_pair(&sm.acc_full[buf]);
+                        if (rank == 0) mbar_expect_tx(&sm.full[s], bytes);
+                        const uint32_t bar = full0 + s * (uint32_t)sizeof(uint64_t);
+                        uint8_t *at = ring + s * kWideStage;
+                        if (has_rows) tma_load(at, few ? &map_few : &map_q, b * kBlock, t.row + (int)rank * kHalf, bar);
+                        tma_load(at + kShare, &map_w, b * kBlock, wrow, bar);
                     }
                     __syncwarp();
-                    if (++s == kStages) s = 0, parity ^= 1;
+                    if (++s == kStages) s = 0, ++turn;
                 }
             }
-            // every product is done before the TMEM is freed
-            if (elect_one())
-                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                                 saddr(&sm.drain))
-                             : "memory");
-            __syncwarp();
-            mbar_wait(&sm.drain, 0, nullptr);
+            // both CTAs' copies land before the pair leaves: the last fill of
+            // each stage (the leader's barrier counts both CTAs' bytes)
+            bool landed = rank == 0;
+            for (uint32_t j = 0; j < kStages && landed; ++j) {
+                const uint32_t filled = j < s ? turn + 1 : turn; // times stage j was filled
+                if (filled) landed = mbar_wait(&sm.full[j], (filled - 1) & 1, nullptr);
+            }
+        } else if (warp == 1) {
+            // ---- MMA issuer (the leading CTA's)
+            if (rank == 0) {
+                const uint32_t idesc = instruction_desc(kTileRows, kWidth);
+                uint32_t s = 0, parity = 0, sum = 0;
+                bool ok = true;
+#ifdef TF_TOPK_TEST_WAIT_TIMEOUT
+                ok = mbar_wait_warp(&sm.drain, 0, abort); // nothing completes it yet: the wait runs out
+#endif
+                for (int u = pair; u < units && ok; u += pairs) {
+                    for (int b = 0; b < a.blocks; ++b, ++sum) {
+                        const uint32_t buf = sum & 1, use = sum >> 1;
+                        ok = (use == 0 || mbar_wait_warp(&sm.acc_empty[buf], (use - 1) & 1, abort)) &&
+                             mbar_wait_warp(&sm.full[s], parity, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t ad = desc_at(ring + s * kWideStage), bd = desc_at(ring + s * kWideStage + kShare);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < kBlock / 32; ++k) // 32 steps: 32 bytes along a row
+                                mma_pair(tmem + buf * kMaxWidth, ad + k * 2, bd + k * 2, idesc, k != 0);
+                            mma_commit_pair(&sm.empty[s]);
+                            mma_commit_pair(&sm.acc_full[buf]);
+                        }
+                        __syncwarp();
+                        if (++s == kStages) s = 0, parity ^= 1;
+                    }
+                }
+                // every product is done before the TMEM is freed
+                if (elect_one())
+                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                     saddr(&sm.drain))
+                                 : "memory");
+                __syncwarp();
+                mbar_wait(&sm.drain, 0, nullptr);
+            }
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         // ---- scaling and sums
         constexpr int kCols = kWidth / (kEpiWarps / 4); // of a thread
-        const int q = warp & 3, h = (warp - 2) >> 2;
+        const int q = warp & 3, h = (warp - 4) >> 2;
         const uint32_t empty0 = peer_addr(&sm.acc_empty[0], 0), empty1 = peer_addr(&sm.acc_empty[1], 0);
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + h * kCols;
         uint32_t done = 0; // accumulators taken
@@ -592,20 +599,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             const Tile t = tile_at(sm.groups, a, u, kTileRows, kWidth);
             const int row0 = t.row + (int)rank * kHalf + 32 * q, col0 = t.col + h * kCols;
             const bool has_rows = row0 < t.end;
-            // a row's scales and the columns' are fetched two blocks ahead
+            // A row's scales and the columns' are fetched four blocks ahead, along the
+            // row: a sector holds those of eight blocks.  (Two ahead, or with the
+            // scales block by block so that a warp reads whole lines, every block
+            // waited: 208 us for 8192 x 7168 x 4096 against 214 and 327; through shared
+            // memory 265.)
             const float *rs = a.scale + (int64_t)min(row0 + lane, a.rows - 1) * a.blocks;
             const float *ws = a.weight_scale +
                               ((int64_t)t.group * a.col_blocks + min(col0 / kBlock, a.col_blocks - 1)) * a.blocks;
-            float r0 = rs[0], w0 = ws[0], r1 = 0.0f, w1 = 0.0f;
+            float r0 = rs[0], w0 = ws[0], r1 = 0.0f, w1 = 0.0f, r2 = 0.0f, w2 = 0.0f, r3 = 0.0f, w3 = 0.0f;
             if (a.blocks > 1) r1 = rs[1], w1 = ws[1];
+            if (a.blocks > 2) r2 = rs[2], w2 = ws[2];
+            if (a.blocks > 3) r3 = rs[3], w3 = ws[3];
             Pair sum[kCols / 2];
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) sum[i] = 0;
             for (int b = 0; b < a.blocks; ++b, ++done) {
                 const uint32_t buf = done & 1;
                 const Pair f = pair_of(r0 * w0);
-                r0 = r1, w0 = w1;
-                if (b + 2 < a.blocks) r1 = rs[b + 2], w1 = ws[b + 2];
+                r0 = r1, w0 = w1, r1 = r2, w1 = w2, r2 = r3, w2 = w3;
+                if (b + 4 < a.blocks) r3 = rs[b + 4], w3 = ws[b + 4];
                 ok = mbar_wait_warp(&sm.acc_full[buf], (done >> 1) & 1, abort);
                 if (!ok) break;
                 tc_fence_after();
@@ -622,9 +635,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(buf ? empty1 : empty0);
             }
-            if (ok && has_rows) put_sums<Out, kCols>(a, sum, sm.staging[warp - 2], row0, t.end, col0);
+            if (ok && has_rows) put_sums<Out, kCols>(a, sum, sm.staging[warp - 4], row0, t.end, col0);
         }
-        zero_unused<Out>(a, sm.groups.begin[a.groups], (int64_t)blockIdx.x * (32 * kEpiWarps) + tid - 64,
+        zero_unused<Out>(a, sm.groups.begin[a.groups], (int64_t)blockIdx.x * (32 * kEpiWarps) + tid - 128,
                          (int64_t)gridDim.x * (32 * kEpiWarps));
     }
     __syncwarp();
