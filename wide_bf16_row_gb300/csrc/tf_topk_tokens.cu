@@ -36,10 +36,15 @@ constexpr int kMaxExperts = TF_TOPK_ROUTE_MAX_EXPERTS;
 constexpr int kMaxK = TF_TOPK_ROUTE_MAX_K;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortChunk = 4096; // choices a CTA sorts at least, where there are several CTAs
+constexpr int kSortChunk = 2048; // choices a CTA sorts at least, where there are several CTAs
+constexpr int kSortKept = 4;     // choices a thread keeps in registers
 constexpr int kSortAlone = 8192; // choices that one CTA sorts by itself
 constexpr int kRowWarps = 8;     // warps per CTA of the kernels over rows
 constexpr int kRowThreads = 32 * kRowWarps;
+// CTAs of an SM for the gradient of combine: so many that their warps hide the
+// latency, as far as the registers go (16384 x 2048 bf16, k 8: 184 us with four,
+// 169 with six; short vectors take more registers, 5001 x 1001 fp32, k 3: 33 with four, 44 with six).
+template <int kBytes> constexpr int kGradCtas = kBytes >= 16 ? 6 : 4;
 constexpr int kScaleBlock = TF_TOPK_FP8_BLOCK;
 
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -77,38 +82,59 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a)
 // that "before" means a lower chunk, a lower warp, an earlier step of 32 or a
 // lower lane, in this order: the counts of the lower chunks, the prefix of the
 // warps' counts, a running count, and the lanes with the same expert
-// (match_any) give the place.  Two readings of 4 bytes per choice; what it
-// takes is the latency of its few steps (a CTA per chunk of 4096 choices).
+// (match_any) give the place.  4 bytes are read per choice and 8 written; what it
+// takes is the latency of its few steps, so a thread's first choices stay in
+// registers, several counts are on their way at a time, and where the counts
+// come from the kernel before, the CTA counts for itself while that runs.
 template <bool kAlone> __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a)
 {
     extern __shared__ int32_t place[]; // [warps][experts]: counts, then the next place of each warp's choices
     __shared__ int32_t warp_sum[kSortWarps];
     __shared__ int32_t used;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (the kernel that counts has waited for what comes before it, idx among it)
+    if (kAlone) {
+        grid_dependency_wait();
+        grid_dependents_go();
+    }
     const int64_t begin = blockIdx.x * a.chunk, end = min(a.n, begin + a.chunk);
     const int64_t share = ((end - begin + kSortWarps - 1) / kSortWarps + 31) / 32 * 32; // of a warp
     const int warps = (int)((end - begin + share - 1) / share);                         // that have any
-    for (int i = tid; i < warps * a.experts; i += kSortThreads) place[i] = 0;
-    grid_dependency_wait();
-    grid_dependents_go();
-    __syncthreads();
     const int64_t w0 = begin + warp * share, w1 = min(end, w0 + share);
-    int32_t *mine = place + warp * a.experts;
-    for (int64_t i = w0; i < w1; i += 32) {
-        const int e = i + lane < w1 ? a.idx[i + lane] : -1;
-        const bool in = (uint32_t)e < (uint32_t)a.experts;
-        const uint32_t same = __match_any_sync(kAll, in ? e : -1);
-        if (in && (same & ((1u << lane) - 1)) == 0) mine[e] += __popc(same);
-        __syncwarp();
-    }
+    int kept[kSortKept];
+#pragma unroll
+    for (int s = 0; s < kSortKept; ++s) kept[s] = w0 + 32 * s + lane < w1 ? a.idx[w0 + 32 * s + lane] : -1;
+    for (int i = tid; i < warps * a.experts; i += kSortThreads) place[i] = 0;
     __syncthreads();
+    int32_t *mine = place + warp * a.experts;
+    // body(place in the order of the choices, expert or -1, lanes with the same) for the warp's choices
+    const auto each_step = [&](auto body) {
+        const auto step = [&](int64_t f, int e) {
+            const int expert = (uint32_t)e < (uint32_t)a.experts ? e : -1;
+            body(f, expert, __match_any_sync(kAll, expert));
+        };
+#pragma unroll
+        for (int s = 0; s < kSortKept; ++s)
+            if (w0 + 32 * s < w1) step(w0 + 32 * s + lane, kept[s]);
+        for (int64_t i = w0 + 32 * kSortKept; i < w1; i += 32) step(i + lane, i + lane < w1 ? a.idx[i + lane] : -1);
+    };
+    const uint32_t lower_lanes = (1u << lane) - 1;
+    each_step([&](int64_t, int e, uint32_t same) {
+        if (e >= 0 && (same & lower_lanes) == 0) mine[e] += __popc(same);
+        __syncwarp();
+    });
+    __syncthreads();
+    if (!kAlone) {
+        grid_dependency_wait();
+        grid_dependents_go();
+    }
     // thread e: the expert's choices in lower chunks and in all
     int32_t before = 0, total = 0;
     if (tid < a.experts) {
         if (kAlone) {
             for (int w = 0; w < warps; ++w) total += place[w * a.experts + tid];
         } else {
-#pragma unroll 8
+#pragma unroll 32
             for (int c = 0; c < (int)gridDim.x; ++c) {
                 const int32_t v = a.counts[(int64_t)c * a.experts + tid];
                 total += v;
@@ -149,19 +175,15 @@ template <bool kAlone> __global__ void __launch_bounds__(kSortThreads) sort_plac
         }
     }
     __syncthreads();
-    for (int64_t i = w0; i < w1; i += 32) {
-        const int64_t f = i + lane;
-        const int e = f < w1 ? a.idx[f] : -1;
-        const bool in = (uint32_t)e < (uint32_t)a.experts;
-        const uint32_t same = __match_any_sync(kAll, in ? e : -1);
-        const int lower = __popc(same & ((1u << lane) - 1));
-        const int32_t s = in ? mine[e] + lower : -1;
+    each_step([&](int64_t f, int e, uint32_t same) {
+        const int lower = __popc(same & lower_lanes);
+        const int32_t s = e >= 0 ? mine[e] + lower : -1;
         __syncwarp();
-        if (in && lower == 0) mine[e] += __popc(same);
+        if (e >= 0 && lower == 0) mine[e] += __popc(same);
         __syncwarp();
         if (f < w1) a.slot[f] = s;
-        if (in) a.source[s] = (int32_t)f;
-    }
+        if (e >= 0) a.source[s] = (int32_t)f;
+    });
     for (int64_t s = begin + tid; s < end; s += kSortThreads)
         if (s >= used) a.source[s] = -1;
 }
@@ -230,7 +252,8 @@ struct GatherArgs {
     int32_t segments; // of a row, kSegment vectors each
 };
 
-constexpr int kStep = 4; // vectors a lane has in flight
+constexpr int kStep = 4;      // vectors a lane has in flight
+constexpr int kQuantVecs = 4; // the same, of rows turned into 8 bits
 
 // A warp copies a segment of a token's row to its k places.
 template <typename T, int kN> __global__ void __launch_bounds__(kRowThreads) gather_kernel(const T *x, T *out, GatherArgs a)
@@ -270,9 +293,9 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
     return r;
 }
 
-// A warp turns 32 * kN values of a token's row (one block of 128, or two) into
-// e4m3 with their scales, and writes them to the row's places, or to the
-// row's own where there is no order.  The largest magnitude is taken on the bits, where NaN is
+// A warp turns kQuantVecs times 32 * kN values of a token's row into e4m3 with
+// their scales, and writes them to the row's places, or to the row's own where
+// there is no order.  The largest magnitude is taken on the bits, where NaN is
 // above infinity above every number: a block that holds one gets a scale of
 // NaN or infinity, and its products are NaN.  The quotient is rounded to 32
 // bits, then to 8: two roundings, so that it is the same wherever it is
@@ -288,43 +311,53 @@ __global__ void __launch_bounds__(kRowThreads) quantize_kernel(const T *x, uint8
     const int64_t units = a.tokens * a.segments, warps = (int64_t)gridDim.x * kRowWarps;
     for (int64_t u = (int64_t)blockIdx.x * kRowWarps + warp; u < units; u += warps) {
         const int64_t t = u / a.segments;
-        const int at = ((int)(u - t * a.segments) * 32 + lane) * kN; // dim is a multiple of 16: whole vectors
-        const bool in = at < a.dim;
+        const int first = ((int)(u - t * a.segments) * 32 * kQuantVecs + lane) * kN; // dim is a multiple of 16: whole vectors
         const int32_t s = a.slot && lane < a.k ? a.slot[t * a.k + lane] : -1;
-        Vec<T, kN> v = zeros<T, kN>();
-        if (in) {
+        Vec<T, kN> v[kQuantVecs];
+#pragma unroll
+        for (int n = 0; n < kQuantVecs; ++n) {
+            const int at = first + 32 * kN * n;
+            v[n] = zeros<T, kN>();
+            if (at >= a.dim) continue;
             const T *p = x + t * a.stride + at;
             if (kVec) {
-                v = load<T, kN>(p);
+                v[n] = load<T, kN>(p);
             } else {
 #pragma unroll
-                for (int i = 0; i < kN; ++i) v.v[i] = p[i];
+                for (int i = 0; i < kN; ++i) v[n].v[i] = p[i];
             }
         }
-        uint32_t most = 0;
+        uint32_t bits[kQuantVecs][kN / 4];
+        float unit[kQuantVecs];
 #pragma unroll
-        for (int i = 0; i < kN; ++i) most = max(most, __float_as_uint(as_float(v.v[i])) & 0x7FFFFFFFu);
+        for (int n = 0; n < kQuantVecs; ++n) {
+            uint32_t most = 0;
 #pragma unroll
-        for (int d = kLanes / 2; d; d >>= 1) most = max(most, __shfl_xor_sync(kAll, most, d));
-        constexpr float kLeast = 7.888609052210118e-31f; // 2^-100
-        const float top = __uint_as_float(most);
-        const float unit = __fmul_rn(top < kLeast ? kLeast : top, 1.0f / 448.0f);
-        uint32_t bits[kN / 4];
+            for (int i = 0; i < kN; ++i) most = max(most, __float_as_uint(as_float(v[n].v[i])) & 0x7FFFFFFFu);
 #pragma unroll
-        for (int i = 0; i < kN / 4; ++i) {
-            float w[4];
+            for (int d = kLanes / 2; d; d >>= 1) most = max(most, __shfl_xor_sync(kAll, most, d));
+            constexpr float kLeast = 7.888609052210118e-31f; // 2^-100
+            const float top = __uint_as_float(most);
+            unit[n] = __fmul_rn(top < kLeast ? kLeast : top, 1.0f / 448.0f);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) w[c] = __fdiv_rn(as_float(v.v[4 * i + c]), unit);
-            bits[i] = e4m3x2(w[0], w[1]) | (e4m3x2(w[2], w[3]) << 16);
+            for (int i = 0; i < kN / 4; ++i) {
+                float w[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) w[c] = __fdiv_rn(as_float(v[n].v[4 * i + c]), unit[n]);
+                bits[n][i] = e4m3x2(w[0], w[1]) | (e4m3x2(w[2], w[3]) << 16);
+            }
         }
         const auto put_row = [&](int64_t row) {
-            if (in) {
+#pragma unroll
+            for (int n = 0; n < kQuantVecs; ++n) {
+                const int at = first + 32 * kN * n;
+                if (at >= a.dim) continue;
                 uint8_t *to = q + row * a.dim + at;
                 if constexpr (kN == 8)
-                    *reinterpret_cast<uint2 *>(to) = make_uint2(bits[0], bits[1]);
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(bits[n][0], bits[n][1]);
                 else
-                    *reinterpret_cast<uint32_t *>(to) = bits[0];
-                if (lane % kLanes == 0) scale[row * blocks + at / kScaleBlock] = unit;
+                    *reinterpret_cast<uint32_t *>(to) = bits[n][0];
+                if (lane % kLanes == 0) scale[row * blocks + at / kScaleBlock] = unit[n];
             }
         };
         if (!a.slot) {
@@ -354,7 +387,7 @@ struct CombineArgs {
     int32_t segments;
 };
 
-constexpr int kCombineVecs = 2; // vectors of a lane
+constexpr int kCombineVecs = 4; // vectors of a lane
 constexpr int kCombineRows = 4; // rows in flight
 
 // A warp adds up a segment of a token's k rows, in the order of its choices, in 32 bits.
@@ -422,29 +455,32 @@ struct CombineGradArgs {
     int32_t token_warps; // warps of a token, a divisor of kRowWarps
 };
 
-constexpr int kGradRows = 8; // choices at a time
+constexpr int kGradRows = 4; // choices at a time
 
-// A token's warps share its dims: each element of d_out is read once for eight
-// choices, whose rows of y are read and whose rows of d_y are written with it;
-// the products' sums are joined through shared memory in the warps' order.
+// A token's warps share its dims: each element of d_out is read once for four
+// choices (more would take registers from the warps that hide the latency), whose rows of y are read and whose rows of d_y are written with it;
+// the products' sums are joined through shared memory in the warps' order.  Where
+// vectors are short a thread has several of them on their way.
 template <typename T, int kN>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, kGradCtas<kN * sizeof(T)>)
     combine_grad_kernel(const T *grad_out, const T *rows, T *grad_rows, CombineGradArgs a)
 {
-    __shared__ float part[kRowWarps][kGradRows];
+    constexpr int kVecs = kN * sizeof(T) >= 16 ? 1 : 4;
+    __shared__ float part[2][kRowWarps][kGradRows];
     grid_dependency_wait();
     grid_dependents_go();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int vecs = a.dim / kN;
     const int per_cta = kRowWarps / a.token_warps;
-    const int of_token = warp % a.token_warps;
+    const int of_token = warp % a.token_warps, stride = 32 * a.token_warps;
+    int turn = 0;
     for (int64_t t0 = (int64_t)blockIdx.x * per_cta; t0 < a.tokens; t0 += (int64_t)gridDim.x * per_cta) {
         const int64_t t = t0 + warp / a.token_warps;
         const bool in = t < a.tokens;
         const int32_t s = in && lane < a.k ? a.slot[t * a.k + lane] : -1;
         const float w = in && lane < a.k ? a.weight[t * a.k + lane] : 0.0f;
-        for (int j0 = 0; j0 < a.k; j0 += kGradRows) {
-            int64_t row[kGradRows];
+        for (int j0 = 0; j0 < a.k; j0 += kGradRows, turn ^= 1) {
+            int32_t row[kGradRows];
             float share[kGradRows], dot[kGradRows];
 #pragma unroll
             for (int j = 0; j < kGradRows; ++j) {
@@ -454,23 +490,34 @@ __global__ void __launch_bounds__(kRowThreads)
                 dot[j] = 0.0f;
             }
             if (in) {
-                for (int c = of_token * 32 + lane; c < vecs; c += 32 * a.token_warps) {
-                    const Vec<T, kN> d = load<T, kN>(grad_out + t * a.grad_stride + (int64_t)c * kN);
-                    Vec<T, kN> y[kGradRows];
+                for (int c0 = of_token * 32 + lane; c0 < vecs; c0 += stride * kVecs) {
+                    Vec<T, kN> d[kVecs], y[kGradRows][kVecs];
+#pragma unroll
+                    for (int n = 0; n < kVecs; ++n)
+                        if (c0 + n * stride < vecs)
+                            d[n] = load<T, kN>(grad_out + t * a.grad_stride + (int64_t)(c0 + n * stride) * kN);
 #pragma unroll
                     for (int j = 0; j < kGradRows; ++j)
-                        if (row[j] >= 0) y[j] = load<T, kN>(rows + row[j] * a.row_stride + (int64_t)c * kN);
+                        if (row[j] >= 0)
+#pragma unroll
+                            for (int n = 0; n < kVecs; ++n)
+                                if (c0 + n * stride < vecs)
+                                    y[j][n] = load<T, kN>(rows + row[j] * a.row_stride + (int64_t)(c0 + n * stride) * kN);
 #pragma unroll
                     for (int j = 0; j < kGradRows; ++j) {
                         if (row[j] < 0) continue;
-                        Vec<T, kN> g;
 #pragma unroll
-                        for (int i = 0; i < kN; ++i) {
-                            const float e = as_float(d.v[i]);
-                            dot[j] = fmaf(e, as_float(y[j].v[i]), dot[j]);
-                            put(g.v[i], e * share[j]);
+                        for (int n = 0; n < kVecs; ++n) {
+                            if (c0 + n * stride >= vecs) continue;
+                            Vec<T, kN> g;
+#pragma unroll
+                            for (int i = 0; i < kN; ++i) {
+                                const float e = as_float(d[n].v[i]);
+                                dot[j] = fmaf(e, as_float(y[j][n].v[i]), dot[j]);
+                                put(g.v[i], e * share[j]);
+                            }
+                            store(grad_rows + (int64_t)row[j] * a.dim + (int64_t)(c0 + n * stride) * kN, g);
                         }
-                        store(grad_rows + row[j] * a.dim + (int64_t)c * kN, g);
                     }
                 }
             }
@@ -478,15 +525,14 @@ __global__ void __launch_bounds__(kRowThreads)
             for (int j = 0; j < kGradRows; ++j) {
 #pragma unroll
                 for (int m = 16; m; m >>= 1) dot[j] += __shfl_xor_sync(kAll, dot[j], m);
-                if (lane == 0) part[warp][j] = dot[j];
+                if (lane == 0) part[turn][warp][j] = dot[j];
             }
-            __syncthreads();
+            __syncthreads(); // the other half is free: all have passed the barrier before
             if (in && of_token == 0 && lane < kGradRows && j0 + lane < a.k) {
                 float sum = 0.0f;
-                for (int i = 0; i < a.token_warps; ++i) sum += part[warp + i][lane];
+                for (int i = 0; i < a.token_warps; ++i) sum += part[turn][warp + i][lane];
                 a.grad_weight[t * a.k + j0 + lane] = sum;
             }
-            __syncthreads();
         }
     }
     unused_rows(a.source, a.n, [&](int64_t s) {
@@ -564,7 +610,7 @@ cudaError_t launch_gather(const void *x, void *out, GatherArgs a, int sm_count, 
 template <typename T, int kN>
 cudaError_t launch_quantize(const void *x, void *q, float *scale, GatherArgs a, int sm_count, void *stream)
 {
-    a.segments = (int32_t)ceil_div(a.dim, 32 * kN);
+    a.segments = (int32_t)ceil_div(a.dim, 32 * kN * kQuantVecs);
     const bool vec = whole(kN * sizeof(T), sizeof(T), a.dim, a.stride, x, nullptr);
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = config(row_grid(a.tokens * a.segments, sm_count), kRowThreads, 0, stream, attr);
