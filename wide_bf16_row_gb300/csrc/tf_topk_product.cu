@@ -50,10 +50,15 @@ constexpr int kHalf = 128;                // wide: one CTA's; thin: columns (M) 
 constexpr int kBlock = TF_TOPK_FP8_BLOCK; // dims of a scale, and of a ring stage: one 128-byte swizzle row
 constexpr int kMaxWidth = 256;
 constexpr uint32_t kShare = kHalf * kBlock; // 16 KB: 128 rows or columns of a block
-constexpr int kStages = 6;                // wide: of the ring
+constexpr int kStages = 4;                // wide: of the ring
 constexpr uint32_t kWideStage = 2 * kShare;
 constexpr int kRowBox = 16;               // rows of a small box
 constexpr int kThinRows = 64;             // thin: rows of a tile at most
+// Rows per group on average up to which the thin kernel takes a product of several
+// groups (one group: kThinRows).  Both (us, thin / wide, 128 experts, 2048 x 1536):
+// 4 rows 62/81, 16 66/91, 32 79/93, 48 99/99, 64 116/102 (groups of more than 64 read
+// their weight twice); one matrix 2048 x 98592: 16 rows 36/54, 48 40/56, 64 43/55.
+constexpr int kThinMostRows = 48;
 constexpr int kThinMostStages = 10;
 constexpr uint32_t kWideRing = kStages * kWideStage, kThinRing = 92 * 1024;
 constexpr int kThinCtas = 2; // of an SM: while one waits for its loads the other's products run
@@ -65,8 +70,11 @@ constexpr int kWideThreads = 32 * (4 + kEpiWarps);
 constexpr int kFrontRegs = 72, kEpiRegs = 216;
 constexpr int kWideTmem = 2 * kMaxWidth;
 constexpr int kChunk = 16;       // accumulator columns a thread takes at a time
-constexpr int kStagingCols = 16; // columns a warp turns round at a time, where its stores need it
-constexpr int kStagingPitch = kStagingCols + 1;
+constexpr uint32_t kBoxBytes = 4096; // wide: 32 rows x 128 bytes on their way out
+constexpr uint32_t kStagingWarp = 2 * kBoxBytes, kStagingBytes = kEpiWarps * kStagingWarp;
+constexpr int kTurnCols = 32;    // columns a warp turns round at a time, where the result's rows are no whole 16 bytes
+constexpr int kTurnPitch = kTurnCols + 1;
+static_assert(32 * kTurnPitch * 4 <= kStagingWarp, "the turned columns fit");
 constexpr int kGroupRows = 16;   // row tiles that share the sweep over the columns
 constexpr int kThinEpiWarps = 8; // two for each 32 columns, which share the rows
 constexpr int kThinThreads = 32 * (2 + kThinEpiWarps);
@@ -101,7 +109,6 @@ struct __align__(16) WideSmem {
     uint32_t tmem_base;
     uint32_t abort;
     Groups groups;
-    float staging[kEpiWarps][32 * kStagingPitch];
 };
 
 struct __align__(16) ThinSmem {
@@ -124,7 +131,7 @@ struct ProductArgs {
     int32_t width; // columns of a tile
     int32_t tile_rows; // thin: rows of a tile
     int32_t stages; // thin: of the ring
-    int32_t wide_stores; // a thread's columns go out in 32-byte stores
+    int32_t boxes; // wide: the result's rows are whole 16 bytes and go out by TMA
 };
 
 // ---------------------------------------------------------------- PTX helpers
@@ -332,12 +339,17 @@ __device__ __forceinline__ Pair mul_pair(Pair a, Pair b)
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
     return p;
 }
-__device__ __forceinline__ void store32(void *to, const uint32_t (&v)[8])
+// Boxes on their way out: from shared memory to the result, cut at its extents.
+__device__ __forceinline__ void send_box(const CUtensorMap *map, const void *box, int32_t x, int32_t y)
 {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                 "r"(saddr(box)), "r"(x), "r"(y)
                  : "memory");
 }
+__device__ __forceinline__ void box_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void box_read_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void box_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---------------------------------------------------------------- the tiles
 
@@ -429,44 +441,74 @@ __device__ __forceinline__ void zero_unused(const ProductArgs &a, int used, int6
     }
 }
 
-// A thread's row of finished sums.  32-byte stores where rows and columns
-// allow them; otherwise the warp turns 16 columns at a time round in shared
-// memory, so that lanes next to each other write columns next to each other.
+// A warp's finished sums, a row per thread.  Whole slices of 32 rows go out as
+// boxes, which the warp does not wait for (with 32-byte stores of its own a
+// thread held up the next tile: 463 us for experts 16384 x 2048 x 1536, k 8,
+// against 411); a group's last rows by themselves; and where rows are no whole 16 bytes
+// the warp turns 32 columns at a time round in shared memory, so that lanes next
+// to each other write columns next to each other.
 template <typename Out, int kCols>
-__device__ __forceinline__ void put_sums(const ProductArgs &a, const Pair (&sum)[kCols / 2], float *staging, int row0, int end,
-                                         int col0)
+__device__ __forceinline__ void put_sums(const ProductArgs &a, const CUtensorMap *map, const Pair (&sum)[kCols / 2],
+                                         uint8_t *staging, int row0, int end, int col0)
 {
     const int lane = threadIdx.x & 31;
     Out *out = static_cast<Out *>(a.out);
-    if (a.wide_stores) {
-        if (row0 + lane >= end) return;
-        Out *to = out + (int64_t)(row0 + lane) * a.cols + col0;
-        constexpr int kEach = 32 / sizeof(Out);
+    constexpr int kEach = 16 / sizeof(Out), kBoxCols = 128 / sizeof(Out);
+    const auto piece = [&](int c) { // kEach columns from c on
+        uint32_t v[4];
 #pragma unroll
-        for (int c = 0; c < kCols; c += kEach) {
-            if (col0 + c >= a.cols) break; // cols is a multiple of kEach
-            uint32_t v[8];
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(Out) == 4)
+                v[i] = __float_as_uint(pair_at(sum[(c + i) / 2], i & 1));
+            else
+                v[i] = pack2(pair_at(sum[c / 2 + i], 0), pair_at(sum[c / 2 + i], 1), Out());
+        }
+        return make_uint4(v[0], v[1], v[2], v[3]);
+    };
+    if (a.boxes && row0 + 32 <= end) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if constexpr (sizeof(Out) == 4)
-                    v[i] = __float_as_uint(pair_at(sum[(c + i) / 2], i & 1));
-                else
-                    v[i] = pack2(pair_at(sum[c / 2 + i], 0), pair_at(sum[c / 2 + i], 1), Out());
+        for (int c0 = 0; c0 < kCols; c0 += 2 * kBoxCols) { // two boxes at a time
+            if (elect_one()) box_read_wait();
+            __syncwarp();
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c0 + b * kBoxCols < kCols)
+                        *reinterpret_cast<uint4 *>(staging + b * kBoxBytes + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                            piece(c0 + b * kBoxCols + j * kEach);
+            fence_async_proxy();
+            __syncwarp();
+            if (elect_one()) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    if (c0 + b * kBoxCols < kCols && col0 + c0 + b * kBoxCols < a.cols)
+                        send_box(map, staging + b * kBoxBytes, col0 + c0 + b * kBoxCols, row0);
+                box_commit();
             }
-            store32(to + c, v);
+            __syncwarp();
         }
         return;
     }
+    if (a.boxes) {
+        Out *to = out + (int64_t)(row0 + lane) * a.cols + col0;
 #pragma unroll
-    for (int c = 0; c < kCols; c += kStagingCols) {
+        for (int c = 0; c < kCols; c += kEach)
+            if (row0 + lane < end && col0 + c < a.cols) *reinterpret_cast<uint4 *>(to + c) = piece(c); // cols: whole pieces
+        return;
+    }
+    float *turn = reinterpret_cast<float *>(staging);
 #pragma unroll
-        for (int i = 0; i < kStagingCols; ++i) staging[lane * kStagingPitch + i] = pair_at(sum[(c + i) / 2], i & 1);
+    for (int c = 0; c < kCols; c += kTurnCols) {
+#pragma unroll
+        for (int i = 0; i < kTurnCols; ++i) turn[lane * kTurnPitch + i] = pair_at(sum[(c + i) / 2], i & 1);
         __syncwarp();
-        const int col = col0 + c + (lane & 15);
-#pragma unroll 4
-        for (int r = lane >> 4; r < 32; r += 2)
-            if (row0 + r < end && col < a.cols)
-                put(out + (int64_t)(row0 + r) * a.cols + col, staging[r * kStagingPitch + (lane & 15)]);
+        const int col = col0 + c + lane;
+        Out *to = out + (int64_t)row0 * a.cols + col;
+        const int rows = col < a.cols ? min(32, end - row0) : 0;
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r)
+            if (r < rows) put(to + (int64_t)r * a.cols, turn[r * kTurnPitch + lane]);
         __syncwarp();
     }
 }
@@ -474,11 +516,13 @@ __device__ __forceinline__ void put_sums(const ProductArgs &a, const Pair (&sum)
 template <typename Out, int kWidth>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     product_wide_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_few,
-                       const __grid_constant__ CUtensorMap map_w, const ProductArgs a)
+                        const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_out,
+                        const ProductArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    WideSmem &sm = *reinterpret_cast<WideSmem *>(ring + kWideRing);
+    uint8_t *staging = ring + kWideRing; // 1024-byte aligned
+    WideSmem &sm = *reinterpret_cast<WideSmem *>(staging + kStagingBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = blockIdx.x & 1; // in the pair; rank 0 leads
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -635,8 +679,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(buf ? empty1 : empty0);
             }
-            if (ok && has_rows) put_sums<Out, kCols>(a, sum, sm.staging[warp - 4], row0, t.end, col0);
+            if (ok && has_rows)
+                put_sums<Out, kCols>(a, &map_out, sum, staging + (warp - 4) * kStagingWarp, row0, t.end, col0);
         }
+        if (elect_one()) box_wait();
+        __syncwarp();
         zero_unused<Out>(a, sm.groups.begin[a.groups], (int64_t)blockIdx.x * (32 * kEpiWarps) + tid - 128,
                          (int64_t)gridDim.x * (32 * kEpiWarps));
     }
@@ -871,7 +918,7 @@ __global__ void __launch_bounds__(kThinThreads, kThinCtas)
 
 // ---------------------------------------------------------------- host side
 
-constexpr size_t kWideSmem = 1024 + kWideRing + sizeof(WideSmem);
+constexpr size_t kWideSmem = 1024 + kWideRing + kStagingBytes + sizeof(WideSmem);
 constexpr size_t kThinSmem = 1024 + kThinRing + sizeof(ThinSmem);
 static_assert(kWideSmem <= 227 * 1024 && kThinCtas * (kThinSmem + 1024) <= 228 * 1024, "the kernels' shared memory fits an SM");
 
@@ -884,7 +931,7 @@ ProductDevice g_product_dev[kMaxDevices];
 std::mutex g_product_mutex;
 PFN_cuTensorMapEncodeTiled_v12000 g_product_encode = nullptr;
 
-using WideKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, ProductArgs);
+using WideKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, ProductArgs);
 using ThinKernel = void (*)(CUtensorMap, CUtensorMap, ProductArgs);
 
 WideKernel wide_kernel(int32_t dtype, int width)
@@ -963,6 +1010,23 @@ bool encode_map(CUtensorMap *map, const void *p, int64_t inner, int64_t outer, i
     cuuint32_t estride[2] = {1, 1};
     return g_product_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), gdim, gstride, box, estride,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The map of the result: boxes of 128 bytes x 32 rows with the 128-byte swizzle.
+bool encode_out(CUtensorMap *map, const void *p, int32_t dtype, int64_t cols, int64_t rows)
+{
+    const size_t size = dtype == TF_TOPK_DTYPE_F32 ? 4 : 2;
+    cuuint64_t gdim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t gstride[1] = {(cuuint64_t)cols * size};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / size), 32};
+    cuuint32_t estride[2] = {1, 1};
+    return g_product_encode(map,
+                            dtype == TF_TOPK_DTYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                            : dtype == TF_TOPK_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                            2, const_cast<void *>(p), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1052,17 +1116,18 @@ extern "C" int tf_topk_product_fp8(const void *q, const float *scale, int64_t ro
     a.groups = groups;
     a.blocks = (dim + kBlock - 1) / kBlock;
     a.col_blocks = (int32_t)((cols + kBlock - 1) / kBlock);
-    a.wide_stores = aligned(out, 32) && (size_t)cols * size % 32 == 0;
+    a.boxes = aligned(out, 16) && (size_t)cols * size % 16 == 0;
     const int64_t active = rows < groups ? rows : groups; // groups that may have rows
-    const bool thin = rows <= kThinRows * active;
+    const bool thin = rows <= active * (active == 1 ? kThinRows : kThinMostRows);
     a.width = thin ? thin_width(active, cols, kThinCtas * sms) : cols <= kHalf ? 128 : 256;
     a.tile_rows = thin ? thin_rows(rows, active) : kTileRows;
     const int fit = (int)(kThinRing / (kShare + a.tile_rows * kBlock));
     a.stages = fit < kThinMostStages ? fit : kThinMostStages;
     a.col_tiles = (int32_t)((cols + a.width - 1) / a.width);
-    CUtensorMap map_q, map_few, map_w;
+    CUtensorMap map_q, map_few, map_w, map_out = {};
     if (!encode_map(&map_few, q, dim, rows, kRowBox) || (!thin && !encode_map(&map_q, q, dim, rows, kHalf)) ||
-        !encode_map(&map_w, weight, dim, (int64_t)groups * cols, thin ? a.width : a.width / 2))
+        !encode_map(&map_w, weight, dim, (int64_t)groups * cols, thin ? a.width : a.width / 2) ||
+        (!thin && a.boxes && !encode_out(&map_out, out, dtype, cols, rows)))
         return tf_topk_internal_fail_cuda((int)cudaErrorInvalidValue);
     cudaLaunchAttribute attr[1];
     cudaError_t e;
@@ -1073,7 +1138,7 @@ extern "C" int tf_topk_product_fp8(const void *q, const float *scale, int64_t ro
     } else {
         const int64_t units = most_units(rows, groups, kTileRows, a.col_tiles);
         const cudaLaunchConfig_t cfg = config(2 * (units < pairs ? units : pairs), kWideThreads, kWideSmem, stream, attr);
-        e = cudaLaunchKernelEx(&cfg, wide_kernel(dtype, a.width), map_q, map_few, map_w, a);
+        e = cudaLaunchKernelEx(&cfg, wide_kernel(dtype, a.width), map_q, map_few, map_w, map_out, a);
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? TF_TOPK_OK : tf_topk_internal_fail_cuda((int)e);
