@@ -532,7 +532,7 @@ size_t tf_topk_sort_experts_workspace(int64_t tokens, int32_t k, int32_t experts
 /*
  * The tokens' rows in the order of tf_topk_sort_experts:
  *   rows[s] = x[source[s] / k], zeros where source[s] is -1.
- *   x            device, [tokens] rows of `dim` elements of `dtype`
+ *   x            device, [tokens] rows of `dim` (1..2^30) elements of `dtype`
  *                (TF_TOPK_DTYPE_*), row_stride elements apart.
  *   slot, source device, as tf_topk_sort_experts wrote them (places outside
  *                [0, tokens * k) are passed over).
@@ -600,7 +600,7 @@ int tf_topk_combine_tokens_grad(const void *grad_out, int32_t dtype, int64_t tok
  *
  *   q            device, [rows][dim] e4m3, packed, 16-byte aligned (as
  *                tf_topk_quantize_tokens writes it); scale float [rows][ceil(dim / 128)].
- *   dim          >= 16, a multiple of 16.
+ *   dim          16..2^30, a multiple of 16.
  *   weight       device, [groups][cols][dim] e4m3, packed, 16-byte aligned;
  *                weight_scale float [groups][ceil(cols / 128)][ceil(dim / 128)].
  *   groups       1..TF_TOPK_ROUTE_MAX_EXPERTS; groups * cols < 2^31 - 1024.
@@ -629,7 +629,7 @@ int tf_topk_product_fp8(const void *q, const float *scale, int64_t rows, int32_t
  *
  *   logits       device, [rows] rows of `cols` elements of `dtype` (TF_TOPK_DTYPE_*),
  *                row_stride elements apart, aligned to the element size.
- *   tokens       device int32, [rows] rows of `width` tokens, token_stride apart: the
+ *   tokens       device int32, [rows] rows of `width` (up to 2^29) tokens, token_stride apart: the
  *                first prompts[r] (NULL: 0) are row r's prompt, those up to lengths[r]
  *                (NULL: width) its answer.  Tokens outside [0, cols) are passed over.
  *                width 0: none.
@@ -641,9 +641,9 @@ int tf_topk_product_fp8(const void *q, const float *scale, int64_t rows, int32_t
  *                % 32 of word c / 32 for column c; or NULL: all.
  *   out          device, rows of `dtype`, out_stride apart; may be logits itself (with
  *                the same stride), and must not overlap it otherwise.
- * Asynchronous on `stream`; allocates nothing; the same inputs give the same
- * bits.  Returns a TF_TOPK_* status: ERR_DTYPE, ERR_SHAPE, ERR_NULL, ERR_ALIGN,
- * ERR_DEVICE or ERR_CUDA.
+ * Asynchronous on `stream` (up to two launches); allocates nothing; the same inputs
+ * give the same bits.  Returns a TF_TOPK_* status: ERR_DTYPE, ERR_SHAPE, ERR_NULL,
+ * ERR_ALIGN, ERR_DEVICE or ERR_CUDA.
  */
 #define TF_TOPK_PENALTY_MAX_BIASES 65535
 int tf_topk_penalize(const void *logits, int32_t dtype, int64_t rows, int64_t cols, int64_t row_stride,

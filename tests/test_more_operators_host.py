@@ -61,7 +61,7 @@ def call_combine_grad(lib, grad=FAKE, dtype=0, tokens=4, dim=64, stride=64, x=FA
 
 ROWS = [(dict(dtype=3), 10), (dict(dtype=-1), 10), (dict(k=0), 3), (dict(k=33), 3), (dict(tokens=-1), 2),
         (dict(tokens=2**31, k=1), 2), (dict(dim=0), 2), (dict(stride=63), 2), (dict(stride=2**62), 2),
-        (dict(tokens=0), 0), (dict(x=None), 1), (dict(slot=FAKE + 2), 4), (dict(out=None), 1), (dict(x=FAKE + 1), 4),
+        (dict(tokens=0), 0), (dict(dim=2**30 + 16, stride=2**31), 2), (dict(x=None), 1), (dict(slot=FAKE + 2), 4), (dict(out=None), 1), (dict(x=FAKE + 1), 4),
         (dict(x=FAKE + 2, dtype=2), 4)]
 
 
@@ -99,6 +99,7 @@ def call_product(lib, q=FAKE, scale=FAKE, rows=4, dim=64, weight=FAKE, wscale=FA
 
 @pytest.mark.parametrize("kwargs,status", [
     (dict(dtype=3), 10), (dict(rows=-1), 2), (dict(rows=2**31 - 1), 2), (dict(dim=0), 2), (dict(dim=24), 2),
+    (dict(dim=2**30 + 16), 2),
     (dict(cols=0), 2), (dict(cols=2**30), 2), (dict(groups=0), 2), (dict(groups=1025), 2),
     (dict(offsets=None), 2), (dict(rows=0, q=None), 0), (dict(q=None), 1), (dict(scale=None), 1),
     (dict(weight=None), 1), (dict(wscale=None), 1), (dict(out=None), 1), (dict(q=FAKE + 8), 4),
@@ -117,7 +118,7 @@ def call_penalize(lib, logits=FAKE, dtype=0, rows=4, cols=100, stride=100, token
 
 @pytest.mark.parametrize("kwargs,status", [
     (dict(dtype=3), 10), (dict(rows=-1), 2), (dict(cols=0), 2), (dict(cols=2**31, stride=2**31, os=2**31), 2),
-    (dict(stride=99), 2), (dict(os=99), 2), (dict(width=-1), 2), (dict(ts=9), 2), (dict(biases=-1), 2),
+    (dict(stride=99), 2), (dict(os=99), 2), (dict(width=-1), 2), (dict(width=2**29 + 1, ts=2**30), 2), (dict(ts=9), 2), (dict(biases=-1), 2),
     (dict(biases=65536, bs=65536, bt=FAKE, bv=FAKE), 2), (dict(biases=3, bs=2, bt=FAKE, bv=FAKE), 2),
     (dict(allowed=FAKE, als=3), 2), (dict(rows=2**31), 2), (dict(rows=2**40, stride=2**30), 2),
     (dict(rows=0, logits=None, out=None, tokens=None), 0), (dict(logits=None), 1), (dict(out=None), 1),

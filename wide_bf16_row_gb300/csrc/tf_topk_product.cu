@@ -1093,7 +1093,8 @@ extern "C" int tf_topk_product_fp8(const void *q, const float *scale, int64_t ro
 {
     if (dtype != TF_TOPK_DTYPE_BF16 && dtype != TF_TOPK_DTYPE_F16 && dtype != TF_TOPK_DTYPE_F32)
         return TF_TOPK_ERR_DTYPE;
-    if (rows < 0 || rows > INT32_MAX - kTileRows || dim < 16 || dim % 16 != 0 || cols < 1 || groups < 1 ||
+    if (rows < 0 || rows > INT32_MAX - kTileRows || dim < 16 || dim > (1 << 30) || dim % 16 != 0 ||
+        cols < 1 || groups < 1 ||
         groups > kMaxGroups || (!offsets && groups != 1) || cols > (INT32_MAX - 1024) / groups ||
         most_units(rows, groups, kRowBox, (cols + 31) / 32) > INT32_MAX / 2)
         return TF_TOPK_ERR_SHAPE;

@@ -34,6 +34,7 @@ namespace {
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kMaxExperts = TF_TOPK_ROUTE_MAX_EXPERTS;
 constexpr int kMaxK = TF_TOPK_ROUTE_MAX_K;
+constexpr int kMaxDim = 1 << 30; // so that the last step past a row's end still fits 32 bits
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortChunk = 2048; // choices a CTA sorts at least, where there are several CTAs
@@ -574,7 +575,7 @@ int check_rows(int32_t dtype, int64_t tokens, int32_t dim, int32_t k)
     if (dtype != TF_TOPK_DTYPE_BF16 && dtype != TF_TOPK_DTYPE_F16 && dtype != TF_TOPK_DTYPE_F32)
         return TF_TOPK_ERR_DTYPE;
     if (k < 1 || k > kMaxK) return TF_TOPK_ERR_K;
-    if (tokens < 0 || dim < 1 || tokens > (int64_t)INT32_MAX / k) return TF_TOPK_ERR_SHAPE;
+    if (tokens < 0 || dim < 1 || dim > kMaxDim || tokens > (int64_t)INT32_MAX / k) return TF_TOPK_ERR_SHAPE;
     return TF_TOPK_OK;
 }
 
