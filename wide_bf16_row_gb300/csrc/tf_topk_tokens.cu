@@ -165,10 +165,15 @@ template <bool kAlone> __global__ void __launch_bounds__(kSortThreads) sort_plac
     const int32_t start = upto - total + (warp ? warp_sum[warp - 1] : 0); // of the expert's rows
     if (tid < a.experts) {
         int32_t at = start + before;
-        for (int w = 0; w < warps; ++w) {
-            const int32_t v = place[w * a.experts + tid];
-            place[w * a.experts + tid] = at;
-            at += v;
+        for (int w0 = 0; w0 < warps; w0 += 8) { // eight counts on their way at a time
+            int32_t v[8];
+#pragma unroll
+            for (int w = 0; w < 8; ++w) v[w] = w0 + w < warps ? place[(w0 + w) * a.experts + tid] : 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                if (w0 + w < warps) place[(w0 + w) * a.experts + tid] = at;
+                at += v[w];
+            }
         }
         if (blockIdx.x == 0) {
             a.offsets[tid] = start;
@@ -253,8 +258,7 @@ struct GatherArgs {
     int32_t segments; // of a row, kSegment vectors each
 };
 
-constexpr int kStep = 4;      // vectors a lane has in flight
-constexpr int kQuantVecs = 4; // the same, of rows turned into 8 bits
+constexpr int kStep = 4; // vectors a lane has in flight
 
 // A warp copies a segment of a token's row to its k places.
 template <typename T, int kN> __global__ void __launch_bounds__(kRowThreads) gather_kernel(const T *x, T *out, GatherArgs a)
@@ -301,7 +305,7 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
 // NaN or infinity, and its products are NaN.  The quotient is rounded to 32
 // bits, then to 8: two roundings, so that it is the same wherever it is
 // computed with IEEE products and divisions.
-template <typename T, int kN, bool kVec>
+template <typename T, int kN, bool kVec, int kQuantVecs>
 __global__ void __launch_bounds__(kRowThreads) quantize_kernel(const T *x, uint8_t *q, float *scale, GatherArgs a)
 {
     grid_dependency_wait();
@@ -611,12 +615,19 @@ cudaError_t launch_gather(const void *x, void *out, GatherArgs a, int sm_count, 
 template <typename T, int kN>
 cudaError_t launch_quantize(const void *x, void *q, float *scale, GatherArgs a, int sm_count, void *stream)
 {
-    a.segments = (int32_t)ceil_div(a.dim, 32 * kN * kQuantVecs);
     const bool vec = whole(kN * sizeof(T), sizeof(T), a.dim, a.stride, x, nullptr);
+    // Four vectors a lane where rows fill them and there are eight warps for each
+    // SM, one otherwise (us, four / one, 2048 dims, k 8: 1 token 4.5/2.9, 64 5.0/3.1,
+    // 512 5.1/5.6, 4096 15.5/20, 16384 56/77; 4001 x 1040, k 1, where a second four
+    // hold 16 of 1024: 14/8.5).
+    const int64_t segments = ceil_div(a.dim, 32 * kN * 4);
+    const bool four = a.tokens * segments >= (int64_t)sm_count * 8 && 4 * (int64_t)a.dim >= 3 * segments * (32 * kN * 4);
+    a.segments = (int32_t)ceil_div(a.dim, 32 * kN * (four ? 4 : 1));
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = config(row_grid(a.tokens * a.segments, sm_count), kRowThreads, 0, stream, attr);
-    return cudaLaunchKernelEx(&cfg, vec ? quantize_kernel<T, kN, true> : quantize_kernel<T, kN, false>,
-                              static_cast<const T *>(x), static_cast<uint8_t *>(q), scale, a);
+    const auto kernel = four ? (vec ? quantize_kernel<T, kN, true, 4> : quantize_kernel<T, kN, false, 4>)
+                             : (vec ? quantize_kernel<T, kN, true, 1> : quantize_kernel<T, kN, false, 1>);
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<const T *>(x), static_cast<uint8_t *>(q), scale, a);
 }
 
 template <typename T, int kN>
