@@ -15,7 +15,7 @@
 // columns a row's tokens and biases name, and how often, while the copy runs; when
 // the copy is done it writes those columns again.  (In one kernel, with every
 // CTA counting for its own columns, the counting took longer than the copy: 99
-// us for 256 x 248320 with 4000 tokens against 60, of which the copy is 40, 0.94
+// us for 256 x 248320 with 4000 tokens against 56, of which the copy is 40, 0.94
 // of the copy bandwidth.)
 //
 // The table: for up to kHashed tokens and biases a hash table of the columns, one
@@ -41,7 +41,7 @@ namespace {
 
 constexpr int kCopyThreads = 256;
 constexpr int kStep = 4; // vectors of a thread
-constexpr int kNameThreads = 1024;
+constexpr int kNameThreads = 1024; // one CTA per SM by its registers; two of fewer registers or threads were slower (55-67 us)
 constexpr int kBatch = 4;              // loads of a thread at once
 constexpr int kHashed = 8192;          // tokens and biases that a hash table holds, in twice the places
 constexpr int kMostPlaces = 32768;     // of a table without a hash: 192 KB with biases
@@ -174,6 +174,11 @@ template <typename T, bool kHash> __global__ void __launch_bounds__(kNameThreads
     uint32_t *words = reinterpret_cast<uint32_t *>(smem);                  // [places]
     uint32_t *keys = words + a.places;                                     // hash: [places], the columns
     uint16_t *last = reinterpret_cast<uint16_t *>(keys + (kHash ? a.places : 0)); // [places]: of a column's last bias, from 1
+    // a thread's first tokens are on their way before their number is known
+    const int32_t *tokens = a.tokens + (a.width > 0 ? row * a.token_stride : 0);
+    const int lead = min(a.width, (int)((4 - (reinterpret_cast<uintptr_t>(tokens) / 4 & 3)) & 3)); // before the first 16 bytes
+    const int4 *vecs = reinterpret_cast<const int4 *>(tokens + lead);
+    const int4 first = tid < (a.width - lead) / 4 ? vecs[tid] : make_int4(-1, -1, -1, -1);
     Request r;
     r.repetition = a.repetition ? a.repetition[row] : 1.0f;
     r.presence = a.presence ? a.presence[row] : 0.0f;
@@ -208,31 +213,30 @@ template <typename T, bool kHash> __global__ void __launch_bounds__(kNameThreads
         return (uint32_t)token < cols && (kHash || ((uint32_t)token & (uint32_t)(a.shares - 1)) == share);
     };
     if (length > 0) {
-        const int32_t *tokens = a.tokens + row * a.token_stride;
         const auto note = [&](int i, int32_t token) {
-            if (!mine(token)) return;
+            if (!mine(token) || i >= length) return;
             const uint32_t p = place_of((uint32_t)token);
             if (i < prompt)
                 atomicOr(&words[p], kPrompt);
             else
                 atomicAdd(&words[p], 1u);
         };
-        const int lead = min(length, (int)((4 - (reinterpret_cast<uintptr_t>(tokens) / 4 & 3)) & 3)); // before the first 16 bytes
-        const int quads = (length - lead) / 4;
-        const int4 *vecs = reinterpret_cast<const int4 *>(tokens + lead);
-        for (int i0 = tid; i0 < quads; i0 += kBatch * kNameThreads) {
+        const auto note4 = [&](int i, const int4 &t) {
+            const int at = lead + 4 * i;
+            note(at, t.x), note(at + 1, t.y), note(at + 2, t.z), note(at + 3, t.w);
+        };
+        note4(tid, first);
+        const int quads = (max(length - lead, 0)) / 4;
+        for (int i0 = tid + kNameThreads; i0 < quads; i0 += kBatch * kNameThreads) {
             int4 t[kBatch];
 #pragma unroll
             for (int s = 0; s < kBatch; ++s)
                 t[s] = i0 + s * kNameThreads < quads ? vecs[i0 + s * kNameThreads] : make_int4(-1, -1, -1, -1);
 #pragma unroll
-            for (int s = 0; s < kBatch; ++s) {
-                const int at = lead + 4 * (i0 + s * kNameThreads);
-                note(at, t[s].x), note(at + 1, t[s].y), note(at + 2, t[s].z), note(at + 3, t[s].w);
-            }
+            for (int s = 0; s < kBatch; ++s) note4(i0 + s * kNameThreads, t[s]);
         }
-        if (tid < lead) note(tid, tokens[tid]);
-        const int rest = lead + 4 * quads + tid;
+        if (tid < min(lead, length)) note(tid, tokens[tid]);
+        const int rest = lead + 4 * max(quads, min(kNameThreads, (a.width - lead) / 4)) + tid;
         if (rest < length) note(rest, tokens[rest]); // up to three
     }
     const int32_t *bias_token = a.bias_token + (a.biases > 0 ? row * a.bias_stride : 0);
