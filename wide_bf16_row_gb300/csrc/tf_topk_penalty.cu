@@ -41,7 +41,8 @@ namespace {
 
 constexpr int kCopyThreads = 256;
 constexpr int kStep = 4; // vectors of a thread
-constexpr int kNameThreads = 1024; // one CTA per SM by its registers; two of fewer registers or threads were slower (55-67 us)
+// One CTA per SM by its registers; two of fewer registers or threads were slower (55-67 us).
+constexpr int kNameThreads = 1024;
 constexpr int kBatch = 4;              // loads of a thread at once
 constexpr int kHashed = 8192;          // tokens and biases that a hash table holds, in twice the places
 constexpr int kMostPlaces = 32768;     // of a table without a hash: 192 KB with biases
@@ -176,7 +177,8 @@ template <typename T, bool kHash> __global__ void __launch_bounds__(kNameThreads
     uint16_t *last = reinterpret_cast<uint16_t *>(keys + (kHash ? a.places : 0)); // [places]: of a column's last bias, from 1
     // a thread's first tokens are on their way before their number is known
     const int32_t *tokens = a.tokens + (a.width > 0 ? row * a.token_stride : 0);
-    const int lead = min(a.width, (int)((4 - (reinterpret_cast<uintptr_t>(tokens) / 4 & 3)) & 3)); // before the first 16 bytes
+    // before the first 16 bytes
+    const int lead = min(a.width, (int)((4 - (reinterpret_cast<uintptr_t>(tokens) / 4 & 3)) & 3));
     const int4 *vecs = reinterpret_cast<const int4 *>(tokens + lead);
     const int4 first = tid < (a.width - lead) / 4 ? vecs[tid] : make_int4(-1, -1, -1, -1);
     Request r;
@@ -297,7 +299,8 @@ using PenaltyKernel = void (*)(PenaltyArgs);
 
 PenaltyKernel copy_for(int32_t dtype)
 {
-    return dtype == TF_TOPK_DTYPE_F32 ? copy_kernel<float> : dtype == TF_TOPK_DTYPE_F16 ? copy_kernel<__half> : copy_kernel<__nv_bfloat16>;
+    if (dtype == TF_TOPK_DTYPE_F32) return copy_kernel<float>;
+    return dtype == TF_TOPK_DTYPE_F16 ? copy_kernel<__half> : copy_kernel<__nv_bfloat16>;
 }
 
 PenaltyKernel name_for(int32_t dtype, bool hashed)
@@ -405,10 +408,12 @@ extern "C" int tf_topk_penalize(const void *logits, int32_t dtype, int64_t rows,
             while (a.places < 2 * names) a.places *= 2;
         } else {
             // as few CTAs as hold the columns, each of which reads all tokens, but one per SM
-            while (a.shares * (int64_t)kMostPlaces < cols || (rows * a.shares < sm_count && a.shares < kMostShares)) a.shares *= 2;
+            while (a.shares * (int64_t)kMostPlaces < cols || (rows * a.shares < sm_count && a.shares < kMostShares))
+                a.shares *= 2;
             while (a.places * (int64_t)a.shares < cols) a.places *= 2;
         }
-        e = launch(name_for(dtype, a.hashed), rows * a.shares, kNameThreads, table_bytes(a.places, a.hashed, biases > 0), a, stream);
+        e = launch(name_for(dtype, a.hashed), rows * a.shares, kNameThreads,
+                   table_bytes(a.places, a.hashed, biases > 0), a, stream);
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? TF_TOPK_OK : tf_topk_internal_fail_cuda((int)e);

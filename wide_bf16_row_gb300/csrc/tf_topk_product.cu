@@ -24,7 +24,7 @@
 // and columns, 128-byte swizzle), an MMA issuer (a block into one of several
 // accumulators in tensor memory), and warps that take each block's sums from
 // there, scale and add them.
-
+//
 // No wait is unbounded: every mbarrier wait gives up after kWaitLimit polls,
 // records a fault code, and the CTA winds down.
 
@@ -767,7 +767,8 @@ __global__ void __launch_bounds__(kThinThreads, kThinCtas)
                     uint8_t *at = ring + s * stage;
                     tma_load_own(at, &map_w, b * kBlock, wrow, &sm.full[s]);
                     for (int i = 0; i < boxes; ++i)
-                        tma_load_own(at + kShare + i * kRowBox * kBlock, &map_rows, b * kBlock, t.row + i * kRowBox, &sm.full[s]);
+                        tma_load_own(at + kShare + i * kRowBox * kBlock, &map_rows, b * kBlock, t.row + i * kRowBox,
+                                     &sm.full[s]);
                 }
                 __syncwarp();
                 if (++s == stages) s = 0, ++turn;
@@ -787,7 +788,8 @@ __global__ void __launch_bounds__(kThinThreads, kThinCtas)
         ok = mbar_wait_warp(&sm.drain, 0, abort); // nothing completes it yet: the wait runs out
 #endif
         for (int u = blockIdx.x; u < units && ok; u += ctas) {
-            const uint32_t idesc = instruction_desc(kHalf, boxes_of(tile_at(sm.groups, a, u, a.tile_rows, a.width)) * kRowBox);
+            const int boxes = boxes_of(tile_at(sm.groups, a, u, a.tile_rows, a.width));
+            const uint32_t idesc = instruction_desc(kHalf, boxes * kRowBox);
             for (int b = 0; b < a.blocks; ++b, ++sum) {
                 const uint32_t buf = sum % kThinAccs, use = sum / kThinAccs;
                 ok = (use == 0 || mbar_wait_warp(&sm.acc_empty[buf], (use - 1) & 1, abort)) &&
@@ -878,7 +880,8 @@ __global__ void __launch_bounds__(kThinThreads, kThinCtas)
 #pragma unroll
                     for (int c = 0; c < kThinRows / kRowBox; ++c) {
                         if (c >= boxes) break;
-                        const ulonglong2 *f = reinterpret_cast<const ulonglong2 *>(&sm.scale[from][b][c * kRowBox + h * kMine]);
+                        const ulonglong2 *f =
+                            reinterpret_cast<const ulonglong2 *>(&sm.scale[from][b][c * kRowBox + h * kMine]);
                         const ulonglong2 f0 = f[0], f1 = f[1];
                         uint32_t x[kMine];
                         tmem_take8(lanes + buf * kThinRows + c * kRowBox, x);
@@ -920,7 +923,8 @@ __global__ void __launch_bounds__(kThinThreads, kThinCtas)
 
 constexpr size_t kWideSmem = 1024 + kWideRing + kStagingBytes + sizeof(WideSmem);
 constexpr size_t kThinSmem = 1024 + kThinRing + sizeof(ThinSmem);
-static_assert(kWideSmem <= 227 * 1024 && kThinCtas * (kThinSmem + 1024) <= 228 * 1024, "the kernels' shared memory fits an SM");
+static_assert(kWideSmem <= 227 * 1024 && kThinCtas * (kThinSmem + 1024) <= 228 * 1024,
+              "the kernels' shared memory fits an SM");
 
 constexpr int kMaxDevices = 64;
 struct ProductDevice {
@@ -1134,7 +1138,8 @@ extern "C" int tf_topk_product_fp8(const void *q, const float *scale, int64_t ro
     cudaError_t e;
     if (thin) {
         const int64_t units = most_units(rows, groups, a.tile_rows, a.col_tiles);
-        const cudaLaunchConfig_t cfg = config(units < kThinCtas * sms ? units : kThinCtas * sms, kThinThreads, kThinSmem, stream, attr);
+        const cudaLaunchConfig_t cfg =
+            config(units < kThinCtas * sms ? units : kThinCtas * sms, kThinThreads, kThinSmem, stream, attr);
         e = cudaLaunchKernelEx(&cfg, thin_kernel(dtype), map_few, map_w, a);
     } else {
         const int64_t units = most_units(rows, groups, kTileRows, a.col_tiles);

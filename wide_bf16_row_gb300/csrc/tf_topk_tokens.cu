@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(kRowThreads) quantize_kernel(const T *x, uint8
     const int64_t units = a.tokens * a.segments, warps = (int64_t)gridDim.x * kRowWarps;
     for (int64_t u = (int64_t)blockIdx.x * kRowWarps + warp; u < units; u += warps) {
         const int64_t t = u / a.segments;
-        const int first = ((int)(u - t * a.segments) * 32 * kQuantVecs + lane) * kN; // dim is a multiple of 16: whole vectors
+        // dim is a multiple of 16: whole vectors
+        const int first = ((int)(u - t * a.segments) * 32 * kQuantVecs + lane) * kN;
         const int32_t s = a.slot && lane < a.k ? a.slot[t * a.k + lane] : -1;
         Vec<T, kN> v[kQuantVecs];
 #pragma unroll
@@ -463,9 +464,10 @@ struct CombineGradArgs {
 constexpr int kGradRows = 4; // choices at a time
 
 // A token's warps share its dims: each element of d_out is read once for four
-// choices (more would take registers from the warps that hide the latency), whose rows of y are read and whose rows of d_y are written with it;
-// the products' sums are joined through shared memory in the warps' order.  Where
-// vectors are short a thread has several of them on their way.
+// choices (more would take registers from the warps that hide the latency), whose
+// rows of y are read and whose rows of d_y are written with it; the products' sums
+// are joined through shared memory in the warps' order.  Where vectors are short a
+// thread has several of them on their way.
 template <typename T, int kN>
 __global__ void __launch_bounds__(kRowThreads, kGradCtas<kN * sizeof(T)>)
     combine_grad_kernel(const T *grad_out, const T *rows, T *grad_rows, CombineGradArgs a)
