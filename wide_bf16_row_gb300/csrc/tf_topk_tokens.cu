@@ -42,10 +42,14 @@ constexpr int kSortKept = 4;     // choices a thread keeps in registers
 constexpr int kSortAlone = 8192; // choices that one CTA sorts by itself
 constexpr int kRowWarps = 8;     // warps per CTA of the kernels over rows
 constexpr int kRowThreads = 32 * kRowWarps;
-// CTAs of an SM for the gradient of combine: so many that their warps hide the
-// latency, as far as the registers go (16384 x 2048 bf16, k 8: 184 us with four,
-// 169 with six; short vectors take more registers, 5001 x 1001 fp32, k 3: 33 with four, 44 with six).
-template <int kBytes> constexpr int kGradCtas = kBytes >= 16 ? 6 : 4;
+// Gradient of combine: vectors that a thread has on their way, and CTAs of an SM, so
+// many that their warps hide the latency as far as the registers go.  Whole vectors
+// (16384 x 2048 bf16, k 8): 184 us with four CTAs, 169 with six.  Pairs (5001 x 1002
+// bf16, k 3): 12.9 with four at a time and four CTAs, 16.2 with two and six.  Single
+// elements (5001 x 1001 fp32; 40000 x 2049 bf16, k 6): 29.4 and 730 with four and
+// four, 27.7 and 646 with two and six.
+template <typename T, int kN> constexpr int kGradVecs = kN * sizeof(T) >= 16 ? 1 : kN > 1 ? 4 : 2;
+template <typename T, int kN> constexpr int kGradCtas = kGradVecs<T, kN> == 4 ? 4 : 6;
 constexpr int kScaleBlock = TF_TOPK_FP8_BLOCK;
 
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -469,10 +473,10 @@ constexpr int kGradRows = 4; // choices at a time
 // are joined through shared memory in the warps' order.  Where vectors are short a
 // thread has several of them on their way.
 template <typename T, int kN>
-__global__ void __launch_bounds__(kRowThreads, kGradCtas<kN * sizeof(T)>)
+__global__ void __launch_bounds__(kRowThreads, kGradCtas<T, kN>)
     combine_grad_kernel(const T *grad_out, const T *rows, T *grad_rows, CombineGradArgs a)
 {
-    constexpr int kVecs = kN * sizeof(T) >= 16 ? 1 : 4;
+    constexpr int kVecs = kGradVecs<T, kN>;
     __shared__ float part[2][kRowWarps][kGradRows];
     grid_dependency_wait();
     grid_dependents_go();
@@ -645,9 +649,13 @@ template <typename T, int kN>
 cudaError_t launch_combine_grad(const void *grad_out, const void *rows, void *grad_rows, CombineGradArgs a,
                                 int sm_count, void *stream)
 {
-    // by the dims alone, so that a token's sums do not depend on the others
+    // By the dims alone, so that a token's sums do not depend on the others.  Short
+    // vectors: a warp takes up to 256 of a token, since more tokens under way hide
+    // more than more warps for each (20000 x 65 fp32, k 6: 67 us with 32 a warp, 25
+    // with 256; 5001 x 1002 bf16, k 3: 23 and 13; a call of 33 tokens 3.3 and 4.3).
+    const int most = kGradVecs<T, kN> == 1 ? 32 : 256;
     a.token_warps = 1;
-    while (a.token_warps < kRowWarps && a.token_warps * 32 < a.dim / kN) a.token_warps *= 2;
+    while (a.token_warps < kRowWarps && a.token_warps * most < a.dim / kN) a.token_warps *= 2;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = config(row_grid(a.tokens * a.token_warps, sm_count), kRowThreads, 0, stream, attr);
     return cudaLaunchKernelEx(&cfg, combine_grad_kernel<T, kN>, static_cast<const T *>(grad_out),
