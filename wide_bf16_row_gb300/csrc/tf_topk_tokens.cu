@@ -538,7 +538,11 @@ __global__ void __launch_bounds__(kRowThreads, kGradCtas<T, kN>)
                 for (int m = 16; m; m >>= 1) dot[j] += __shfl_xor_sync(kAll, dot[j], m);
                 if (lane == 0) part[turn][warp][j] = dot[j];
             }
-            __syncthreads(); // the other half is free: all have passed the barrier before
+            // the other half is free: all have passed the barrier before
+            if (a.token_warps > 1)
+                __syncthreads();
+            else
+                __syncwarp();
             if (in && of_token == 0 && lane < kGradRows && j0 + lane < a.k) {
                 float sum = 0.0f;
                 for (int i = 0; i < a.token_warps; ++i) sum += part[turn][warp + i][lane];
