@@ -24,6 +24,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+#include <mutex>
+
 #include "tf_topk.h"
 
 int tf_topk_internal_fail_cuda(int cuda_error);
@@ -679,6 +682,27 @@ bool bad_sort(int64_t tokens, int32_t k, int32_t experts)
     return tokens < 0 || tokens > (int64_t)INT32_MAX / k || experts < 1 || experts > kMaxExperts;
 }
 
+constexpr int kMaxDevices = 64;
+std::atomic<bool> g_sort_ready[kMaxDevices];
+std::mutex g_sort_mutex;
+
+// Per device, once: the sort's shared memory limit for the most experts.  A
+// constant: the limit is the kernel's, not a call's, and one that a call set for
+// itself another host thread could lower before the launch.
+cudaError_t sort_setup()
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (e != cudaSuccess || g_sort_ready[dev].load(std::memory_order_acquire)) return e;
+    std::lock_guard<std::mutex> lock(g_sort_mutex);
+    constexpr int kMost = kSortWarps * kMaxExperts * (int)sizeof(int32_t);
+    for (const auto kernel : {sort_place_kernel<false>, sort_place_kernel<true>})
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e == cudaSuccess) g_sort_ready[dev].store(true, std::memory_order_release);
+    return e;
+}
+
 } // namespace
 
 extern "C" {
@@ -725,9 +749,7 @@ int tf_topk_sort_experts(const int32_t *idx, int64_t tokens, int32_t k, int32_t 
     const int64_t chunks = ceil_div(a.n, a.chunk); // none of them empty
     const size_t smem = (size_t)kSortWarps * experts * sizeof(int32_t);
     const auto kernel = chunks == 1 ? sort_place_kernel<true> : sort_place_kernel<false>;
-    cudaError_t e = cudaSuccess;
-    if (smem > 40 * 1024)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = sort_setup();
     cudaLaunchAttribute attr[1];
     if (e == cudaSuccess && chunks > 1) {
         const cudaLaunchConfig_t cfg = config(chunks, kSortThreads, 0, stream, attr);
