@@ -640,7 +640,7 @@ int tf_topk_product_fp8(const void *q, const float *scale, int64_t rows, int32_t
  *   allowed      device, [rows] rows of ceil(cols / 32) words, allowed_stride apart, bit c
  *                % 32 of word c / 32 for column c; or NULL: all.
  *   out          device, rows of `dtype`, out_stride apart; may be logits itself (with
- *                the same stride), and must not overlap it otherwise.
+ *                the same stride; ERR_SHAPE if not), and must not overlap it otherwise.
  * Asynchronous on `stream` (up to two launches); allocates nothing; the same inputs
  * give the same bits.  Returns a TF_TOPK_* status: ERR_DTYPE, ERR_SHAPE, ERR_NULL,
  * ERR_ALIGN, ERR_DEVICE or ERR_CUDA.

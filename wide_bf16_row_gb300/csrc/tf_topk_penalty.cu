@@ -349,7 +349,8 @@ extern "C" int tf_topk_penalize(const void *logits, int32_t dtype, int64_t rows,
         bad_stride(out_stride, cols, rows) || width < 0 || width > kMostWidth ||
         (width > 0 && bad_stride(token_stride, width, rows)) || biases < 0 || biases > TF_TOPK_PENALTY_MAX_BIASES ||
         (biases > 0 && bad_stride(bias_stride, biases, rows)) ||
-        (allowed && bad_stride(allowed_stride, ceil_div(cols, 32), rows)) || rows > INT32_MAX / ceil_div(cols, 1024))
+        (allowed && bad_stride(allowed_stride, ceil_div(cols, 32), rows)) || rows > INT32_MAX / ceil_div(cols, 1024) ||
+        (out == logits && rows > 1 && out_stride != row_stride)) // rows of the one would be written over the other's
         return TF_TOPK_ERR_SHAPE;
     if (rows == 0) return TF_TOPK_OK;
     if (!logits || !out || (width > 0 && !tokens) || (biases > 0 && (!bias_token || !bias_value))) return TF_TOPK_ERR_NULL;
