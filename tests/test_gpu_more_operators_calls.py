@@ -54,3 +54,28 @@ def test_orders_from_several_host_threads():
     for idx, experts, out, *_ in work:
         for got, ref in zip(out, oracle.order(idx.cpu().numpy(), experts)):
             assert np.array_equal(got.cpu().numpy(), ref)
+
+
+def test_sizes_past_32_bits_are_refused():
+    """2^32 and a little more: what 32 bits hold of it would be a size that runs."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    idx, logits = tokens._choices(4, 2, 8, 1), tokens._rand((1, 64), "bf16", 2)
+    one = topk.sort_by_expert(idx[:1, :1].contiguous(), 8)
+    raw = torch.zeros(2**32 + 16, dtype=torch.int32, device="cuda")
+    wide = raw.view(torch.bfloat16)[:2**32 + 16].view(1, -1)
+    eight = raw.view(torch.float8_e4m3fn)[:2**32 + 16].view(1, -1)
+    scale, weight = torch.ones(1, 2**25 + 1, device="cuda"), torch.ones(1, 1, device="cuda")
+    many = raw.view(1, -1)
+    for call in (lambda: topk.sort_by_expert(idx, 2**32 + 8), lambda: topk.sort_by_expert(idx, 8 - 2**32),
+                 lambda: topk.gather_tokens(wide, one, out=wide),
+                 lambda: topk.quantize_tokens_fp8(wide, out=(eight, scale)),
+                 lambda: topk.combine_tokens(wide, one, weight, out=wide),
+                 lambda: topk.combine_tokens_grad(wide, wide, one, weight, out=(wide, weight)),
+                 lambda: topk.product_fp8(eight, scale, eight, scale),
+                 lambda: topk.penalize_logits(logits, tokens=many, frequency=weight[0]),
+                 lambda: topk.penalize_logits(logits, bias_tokens=many, bias_values=many.view(torch.float32))):
+        with pytest.raises(topk.TopkError) as e:
+            call()
+        assert e.value.status == topk.ERR_SHAPE

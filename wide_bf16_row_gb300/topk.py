@@ -688,6 +688,11 @@ def route_experts_grad(logits, idx, grad_weight, *, score: str = "softmax", reno
     return out
 
 
+# Sizes that the C calls take as int32 are held against it here: ctypes would hand
+# over the low bits of a larger one, which may be a size that runs.
+_INT32_MAX = 2**31 - 1
+
+
 class ExpertOrder(NamedTuple):
     """The order of routing's choices by expert, as ``sort_by_expert`` gives it."""
 
@@ -727,6 +732,10 @@ def sort_by_expert(idx, experts: int, *, out=None, workspace=None, stream=None) 
         with torch.cuda.device(dev):
             return sort_by_expert(idx, experts, out=out, workspace=workspace, stream=stream)
     tokens, k = idx.shape
+    if k > _INT32_MAX:
+        _check(ERR_K)
+    if not -_INT32_MAX <= experts <= _INT32_MAX:
+        _check(ERR_SHAPE)
     n = tokens * k
     if out is None:
         # a bad count of experts is the library's to refuse
@@ -767,6 +776,8 @@ def _rows_code(x, name):
     stride = x.stride()
     if dim > 1 and stride[1] != 1:
         raise ValueError(f"{name} must have contiguous columns")
+    if dim > _INT32_MAX:
+        _check(ERR_SHAPE)
     return code, rows, dim, stride[0] if rows > 1 else dim
 
 
@@ -776,6 +787,8 @@ def _order_of(order, tokens, dev):
     if slot.dim() != 2 or slot.shape[0] != tokens:
         raise ValueError("the order is not of this many tokens")
     k = slot.shape[1]
+    if k > _INT32_MAX:
+        _check(ERR_K)
     _check_out(slot, (tokens, k), _torch.int32, dev, "slot")
     _check_out(source, (tokens * k,), _torch.int32, dev, "source")
     return slot, source, k
@@ -962,6 +975,8 @@ def product_fp8(q, scale, weight, weight_scale, *, offsets=None, dtype=None, out
     if len(shape) != 3 or shape[2] != dim:
         raise ValueError("weight must be [cols, dim], or with offsets [experts, cols, dim]")
     groups, cols = shape[0], shape[1]
+    if dim > _INT32_MAX or groups > _INT32_MAX:
+        _check(ERR_SHAPE)
     blocks, col_blocks = -(-dim // FP8_BLOCK), -(-cols // FP8_BLOCK)
     _check_out(weight, tuple(weight.shape), f8, dev, "weight")
     _check_out(scale, (rows, blocks), torch.float32, dev, "scale")
@@ -1011,6 +1026,8 @@ def _table(t, rows, dtype, dev, name):
     width, stride = t.shape[1], t.stride()
     if width > 1 and stride[1] != 1:
         raise ValueError(f"{name} must have contiguous columns")
+    if width > _INT32_MAX:
+        _check(ERR_SHAPE)
     return t.data_ptr(), width, stride[0] if rows > 1 else width
 
 
