@@ -2,6 +2,7 @@
 documentation allows and that meet other calls."""
 from __future__ import annotations
 
+import ctypes
 import threading
 
 import numpy as np
@@ -79,3 +80,27 @@ def test_sizes_past_32_bits_are_refused():
         with pytest.raises(topk.TopkError) as e:
             call()
         assert e.value.status == topk.ERR_SHAPE
+
+
+def test_a_failed_call_leaves_nothing_to_the_next():
+    """A call on a stream whose capture has become invalid fails; the calls after it do not report its error."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    x = tokens._rand((50, 32), "bf16", 1)
+    order = topk.sort_by_expert(tokens._choices(50, 2, 8, 1), 8)
+    rows = torch.zeros(100, 32, dtype=x.dtype, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    driver, stream, graph = ctypes.CDLL("libcuda.so.1"), ctypes.c_void_p(side.cuda_stream), ctypes.c_void_p()
+    assert driver.cuStreamBeginCapture_v2(stream, 2) == 0  # relaxed: nothing else is held back
+    assert driver.cuStreamSynchronize(stream) != 0  # not allowed in a capture, and the end of this one
+    try:
+        with pytest.raises(topk.TopkError) as e:
+            topk.gather_tokens(x, order, out=rows, stream=side)
+    finally:
+        assert driver.cuStreamEndCapture(stream, ctypes.byref(graph)) != 0
+    assert e.value.status == topk.ERR_CUDA and not rows.any()
+    topk.gather_tokens(x, order, out=rows)
+    assert np.array_equal(tokens._np(rows), oracle.gather(tokens._np(x), order.source.cpu().numpy(), 2))
+    assert topk.device_fault() == 0

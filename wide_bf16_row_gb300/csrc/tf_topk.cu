@@ -2588,6 +2588,7 @@ thread_local int t_last_cuda_error = 0;
 int fail_cuda(cudaError_t e)
 {
     t_last_cuda_error = (int)e;
+    cudaGetLastError(); // reported with this call: the next one, which asks after its launch, must not find it
     return TF_TOPK_ERR_CUDA;
 }
 
