@@ -605,8 +605,9 @@ int tf_topk_combine_tokens_grad(const void *grad_out, int32_t dtype, int64_t tok
  *                weight_scale float [groups][ceil(cols / 128)][ceil(dim / 128)].
  *   groups       1..TF_TOPK_ROUTE_MAX_EXPERTS; groups * cols < 2^31 - 1024.
  *   offsets      device int32 [groups + 1], ascending from 0, at most rows: group g has the rows
- *                [offsets[g], offsets[g + 1]); as tf_topk_sort_experts wrote it.  NULL:
- *                one group of all rows.
+ *                [offsets[g], offsets[g + 1]); as tf_topk_sort_experts wrote it.  Others are
+ *                made so: the first is 0, each is held to [0, rows], and one below an
+ *                earlier one counts as that one.  NULL: one group of all rows.
  *   dtype        TF_TOPK_DTYPE_* of out: device, [rows][cols], packed, aligned to its
  *                element; must not overlap the inputs.
  * Asynchronous on `stream`; allocates nothing; the same inputs give the same

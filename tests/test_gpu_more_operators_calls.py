@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 
 from oracle import tokens as oracle
+from tests import test_gpu_product as product
 from tests import test_gpu_tokens as tokens
 
 pytestmark = pytest.mark.gpu
@@ -103,4 +104,25 @@ def test_a_failed_call_leaves_nothing_to_the_next():
     assert e.value.status == topk.ERR_CUDA and not rows.any()
     topk.gather_tokens(x, order, out=rows)
     assert np.array_equal(tokens._np(rows), oracle.gather(tokens._np(x), order.source.cpu().numpy(), 2))
+    assert topk.device_fault() == 0
+
+
+@pytest.mark.parametrize("rows,groups,dim,cols", [(100, 4, 272, 136), (400, 4, 128, 264), (3000, 1024, 32, 40),
+                                                  (60000, 1024, 32, 136), (700, 7, 144, 77)])
+def test_offsets_that_run_backwards_give_no_row_to_two_groups(rows, groups, dim, cols):
+    """Each is held to the rows there are, and counts as the largest before it where it is lower."""
+    import torch
+
+    from wide_bf16_row_gb300 import topk
+    args = product.inputs(rows, dim, cols, groups, seed=rows)
+    rng = np.random.default_rng(rows)
+    turns = np.where(np.arange(groups + 1) % 2, rows, 0)
+    for offsets in (turns, turns[::-1], rng.integers(-9, rows + 9, groups + 1), np.sort(rng.integers(0, rows, groups + 1)),
+                    np.full(groups + 1, -2**31), np.full(groups + 1, 2**31 - 1)):
+        held = np.clip(offsets, 0, rows)
+        held[0] = 0
+        held = np.maximum.accumulate(held)
+        y, ref = (topk.product_fp8(*args, offsets=torch.from_numpy(o.astype(np.int32)).cuda()) for o in (offsets, held))
+        assert torch.equal(y, ref) and not y[held[-1]:].any()
+    product.check(args, "bf16", held.tolist())
     assert topk.device_fault() == 0
