@@ -56,11 +56,15 @@ constexpr int kRowBox = 16;               // rows of a small box
 constexpr int kThinRows = 64;             // thin: rows of a tile at most
 // Rows per group on average up to which the thin kernel takes a product of several
 // groups (one group: kThinRows).  Both (us, thin / wide, 128 experts, 2048 x 1536):
-// 4 rows 62/81, 16 66/91, 32 79/93, 48 99/99, 64 116/102 (groups of more than 64 read
-// their weight twice); one matrix 2048 x 98592: 16 rows 36/54, 48 40/56, 64 43/55.
+// 4 rows 62/81, 16 66/91, 32 79/93, 48 99/99, 64 116/102 (routed; groups of more than 64
+// read their weight twice); one matrix 2048 x 98592: 16 rows 36/54, 48 40/56, 64 43/55.
+// Half of all rows at one of the 128: 2048 rows 75/98, 6144 98/103, and over the limit
+// 8192 108/106.  The columns are not looked at, and with few of them the two meet
+// earlier: 8 groups of 48 rows 14.7/12.8 (4096 columns 15.2/21.7), one matrix of 64 rows
+// 7168 x 8192 43/30 (7168 x 24576 44/59).
 constexpr int kThinMostRows = 48;
-constexpr int kThinMostStages = 10;
 constexpr uint32_t kWideRing = kStages * kWideStage, kThinRing = 92 * 1024;
+constexpr int kThinMostStages = kThinRing / (kShare + kRowBox * kBlock); // with the fewest rows a tile has
 constexpr int kThinCtas = 2; // of an SM: while one waits for its loads the other's products run
 constexpr int kMaxGroups = TF_TOPK_ROUTE_MAX_EXPERTS;
 constexpr int kEpiWarps = 8;
@@ -1079,7 +1083,9 @@ int thin_width(int64_t groups, int64_t cols, int ctas)
 
 // Rows of a thin tile: all there can be, or for several groups what four times
 // the average needs, in sixteens: a group beyond reads its weight again, from
-// the L2, and rows that are not there take room from the ring.
+// the L2, and rows that are not there take room from the ring.  (Twice, four and eight
+// times, us, 128 groups of 2048 x 1536: 1024 rows, half of them of one group, 77, 72
+// and 71, evenly 67, 67 and 66; 512 rows, nine tenths of eight groups, 45, 45 and 42.)
 int thin_rows(int64_t rows, int64_t groups)
 {
     const int64_t want = groups == 1 ? rows : (4 * rows + groups - 1) / groups;
@@ -1150,8 +1156,7 @@ extern "C" int tf_topk_product_fp8(const void *q, const float *scale, int64_t ro
     const bool thin = rows <= active * (active == 1 ? kThinRows : kThinMostRows);
     a.width = thin ? thin_width(active, cols, kThinCtas * sms) : cols <= kHalf ? 128 : 256;
     a.tile_rows = thin ? thin_rows(rows, active) : kTileRows;
-    const int fit = (int)(kThinRing / (kShare + a.tile_rows * kBlock));
-    a.stages = fit < kThinMostStages ? fit : kThinMostStages;
+    a.stages = (int32_t)(kThinRing / (kShare + a.tile_rows * kBlock)); // thin
     a.col_tiles = (int32_t)((cols + a.width - 1) / a.width);
     CUtensorMap map_q, map_few, map_w, map_out = {};
     if (!encode_map(&map_few, q, dim, rows, kRowBox) || (!thin && !encode_map(&map_q, q, dim, rows, kHalf)) ||
