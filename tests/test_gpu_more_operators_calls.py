@@ -126,3 +126,64 @@ def test_offsets_that_run_backwards_give_no_row_to_two_groups(rows, groups, dim,
         assert torch.equal(y, ref) and not y[held[-1]:].any()
     product.check(args, "bf16", held.tolist())
     assert topk.device_fault() == 0
+
+
+@pytest.mark.parametrize("rows,hot,share", [(512, 8, 0.9), (4096, 1, 0.5), (6000, 3, 0.7), (8192, 1, 0.6)])
+def test_routing_that_favours_few_experts(rows, hot, share):
+    """Groups of many times the average, in tiles of either kernel."""
+    rng = np.random.default_rng(rows)
+    counts = rng.multinomial(rows - hot * int(rows * share / hot), np.ones(128) / 128)
+    counts[rng.permutation(128)[:hot]] += int(rows * share / hot)
+    product.check(product.inputs(rows + 5, 272, 392, 128, seed=rows), "bf16", np.concatenate([[0], np.cumsum(counts)]).tolist())
+
+
+def test_a_layer_from_several_host_threads():
+    """Each thread's calls on its own stream give the bits that they give alone."""
+    import torch
+
+    from tests import test_gpu_penalty as penalty
+    from wide_bf16_row_gb300 import topk
+
+    def of(seed):
+        experts, stream = (16, 500, 1000, 64)[seed], torch.cuda.Stream()
+        idx, x = tokens._choices(700 * (seed + 1), 4, experts, seed, 0.1), tokens._rand((700 * (seed + 1), 256), "bf16", seed)
+        _, _, w, ws = product.inputs(1, 256, 136 + seed, experts, seed=seed)
+        logits, r = penalty.logits_of(9, 20001, "bf16", seed), penalty.request(9, 20001, 300 * 10**(seed % 3), 5, True, seed)
+
+        def run():
+            order = topk.sort_by_expert(idx, experts, stream=stream)
+            q, s = topk.quantize_tokens_fp8(x, order, stream=stream)
+            y = topk.product_fp8(q, s, w, ws, offsets=order.offsets, stream=stream)
+            out = topk.combine_tokens(y, order, stream=stream)
+            grads = topk.combine_tokens_grad(out, y, order, share, stream=stream)
+            return (*order, y, out, *grads, topk.gather_tokens_grad(grads[0], order, stream=stream),
+                    topk.penalize_logits(logits, **r, stream=stream))
+
+        share = torch.ones(idx.shape, device="cuda")
+        return run, stream
+
+    work = [of(seed) for seed in range(4)]
+    torch.cuda.synchronize()
+    alone = []
+    for run, stream in work:
+        alone.append(run())
+        stream.synchronize()
+    start, got = threading.Barrier(len(work)), [[] for _ in work]
+
+    def calls(i):
+        run, stream = work[i]
+        start.wait()
+        for _ in range(50):
+            last = run()
+        stream.synchronize()
+        got[i].extend(last)
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for a, b in zip(alone, got):
+        assert len(a) == len(b) and all(torch.equal(p, q) for p, q in zip(a, b))
+    assert topk.device_fault() == 0
