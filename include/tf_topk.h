@@ -603,7 +603,8 @@ int tf_topk_combine_tokens_grad(const void *grad_out, int32_t dtype, int64_t tok
  *   dim          16..2^30, a multiple of 16.
  *   weight       device, [groups][cols][dim] e4m3, packed, 16-byte aligned;
  *                weight_scale float [groups][ceil(cols / 128)][ceil(dim / 128)].
- *   groups       1..TF_TOPK_ROUTE_MAX_EXPERTS; groups * cols < 2^31 - 1024.
+ *   groups       1..TF_TOPK_ROUTE_MAX_EXPERTS; groups * cols < 2^31 - 1024, and
+ *                (rows / 16 + min(rows, groups)) * ceil(cols / 32) < 2^30.
  *   offsets      device int32 [groups + 1], ascending from 0, at most rows: group g has the rows
  *                [offsets[g], offsets[g + 1]); as tf_topk_sort_experts wrote it.  Others are
  *                made so: the first is 0, each is held to [0, rows], and one below an

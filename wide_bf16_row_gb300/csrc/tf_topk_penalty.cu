@@ -14,14 +14,17 @@
 // what bounds the whole.  name_kernel counts, in a table in shared memory, which
 // columns a row's tokens and biases name, and how often, while the copy runs; when
 // the copy is done it writes those columns again.  (In one kernel, with every
-// CTA counting for its own columns, the counting took longer than the copy: 99
-// us for 256 x 248320 with 4000 tokens against 56, of which the copy is 40, 0.94
+// CTA counting for its own columns, the counting took longer than the copy: 113
+// us for 256 x 248320 with 4000 tokens against 56, of which the copy is 40, 0.95
 // of the copy bandwidth.)
 //
 // The table: for up to kHashed tokens and biases a hash table of the columns, one
-// CTA per row; for more, one word per column, the columns dealt out to several
-// CTAs in turn (common tokens are neighbours), each of which reads all of the
-// row's tokens.
+// CTA per row (16384 places of 10 bytes; twice as many do not fit an SM); for more,
+// one word per column, the columns dealt out to several CTAs in turn (common tokens
+// are neighbours), each of which reads all of the row's tokens.  Both (us, hash / words,
+// 248320 columns, in place): 4000 tokens, 1 row 11.5/5.6, 33 rows 14/16, 256 rows 26/106;
+// 8192 tokens 26/6.8, 31/20, 66/137: many rows want the hash, few rows, whose columns
+// are shared out over the SMs, would not.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,7 +50,10 @@ constexpr int kBatch = 4;              // loads of a thread at once
 constexpr int kHashed = 8192;          // tokens and biases that a hash table holds, in twice the places
 constexpr int kMostPlaces = 32768;     // of a table without a hash: 192 KB with biases
 constexpr int kLeastPlaces = 256;
-constexpr int kMostShares = 16;        // of a row's columns, for the sake of the SMs
+// CTAs that share a row's columns for the sake of the SMs, at most.  With 4, 16 and
+// 64 (us, 40000 tokens): 1 x 248320 15.4 (8 for the table's size), 10.7 and 6.8; 1 x 32771
+// 9.1, 6.8 and 6.6; 33 x 32771 9.5, 15.2 and 15.2, where eight a row are more than one an SM.
+constexpr int kMostShares = 16;
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr uint32_t kPrompt = 1u << 31, kBias = 1u << 30; // of a column's word; the answer's count below
 constexpr int kMostWidth = 1 << 29;

@@ -42,7 +42,10 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortChunk = 2048; // choices a CTA sorts at least, where there are several CTAs
 constexpr int kSortKept = 4;     // choices a thread keeps in registers
-constexpr int kSortAlone = 8192; // choices that one CTA sorts by itself
+// Choices that one CTA sorts by itself, in one launch and without a workspace.  One
+// CTA / several (us, 256 experts): 2048 choices 7.4 (one chunk), 4096 11.3/8.1, 8192
+// 19.5/8.5, 16384 35.5/9.7; with 16 experts 7.0/5.8, 10.9/6.0 and 18.8/7.2.
+constexpr int kSortAlone = 8192;
 constexpr int kRowWarps = 8;     // warps per CTA of the kernels over rows
 constexpr int kRowThreads = 32 * kRowWarps;
 // Gradient of combine: vectors that a thread has on their way, and CTAs of an SM, so

@@ -909,7 +909,7 @@ def tf_topk_quantize_tokens(x: int, dtype: int, tokens: int, dim: int, row_strid
 
 def quantize_tokens_fp8(x, order: ExpertOrder | None = None, *, out=None, stream=None):
     """Rows in 8 bits: e4m3 values with a scale for each 128 of a row, the
-    scale being the largest magnitude over 448.
+    scale being the largest magnitude (2^-100 at least) times 1/448 in 32 bits.
 
     ``x``: CUDA bf16 / fp16 / fp32 [tokens, dim], contiguous columns, dim a
     multiple of 16.  With ``order`` the rows come in the order of
